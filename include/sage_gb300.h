@@ -44,8 +44,9 @@ enum sage_status {
     SAGE_ERR_LAUNCH = -3,       /* CUDA reported an error at launch */
     SAGE_ERR_TIMEOUT = -4,      /* device: a bounded wait inside a kernel ran out */
     SAGE_ERR_DRIVER = -5,       /* driver entry point for TMA descriptors missing */
-    SAGE_ERR_SCRATCH = -6       /* problem needs more scratch than the fixed buffer
+    SAGE_ERR_SCRATCH = -6,      /* problem needs more scratch than the fixed buffer
                                    of sage_prep_qkv_noalloc holds */
+    SAGE_ERR_PAGE = -7          /* device: a page or slot outside the page cache */
 };
 
 /* Logical [B, H, N, D] BF16 tensor given by its element strides; the D stride
@@ -295,6 +296,102 @@ int sage_attention_host_overlapped(const sage_tensor* q_host, const sage_tensor*
                                    const int32_t* q_len, const int32_t* kv_len,
                                    float sm_scale, int causal, int head_groups,
                                    const sage_prep_buffers* buf, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * Serving from a page cache.  (The pages describe no cache; these entries give
+ * the attention path the single-token and piecewise forms that follow a
+ * prompt, in exact BF16.)  Keys and values of all requests lie in a pool of
+ * pages of page_size tokens.  A request owns the pages that its row of the
+ * page table lists in order: its token t is row t % page_size of page
+ * table[b][t / page_size].  One step of a serving loop is sage_page_tables
+ * (pages and slots for the new tokens), sage_cache_append (their keys and
+ * values into the slots) and sage_attn_paged (the new tokens' attention).
+ * ------------------------------------------------------------------------- */
+
+/* A pool of pages.  k, v : BF16 [num_pages, heads, page_size, D] views by
+ * element strides (stride_b is the page stride, stride_n the token stride;
+ * pages may hold their heads token by token or one after another); pointer
+ * and strides as for every sage_tensor.  page_size is 16, 32, 64 or 128, D is
+ * 64 or 128, and num_pages * page_size is below 2^31. */
+typedef struct {
+    sage_tensor k;
+    sage_tensor v;
+    int num_pages;
+    int page_size;
+    int heads;
+    int D;
+} sage_page_cache;
+
+/* Page tables and slot maps from lengths, on the GPU: request b grows from
+ * old_len[b] to new_len[b] tokens.
+ *  old_len, new_len : device int32 [B]; old_len may be NULL (all 0).  Both are
+ *            clamped to [0, table_width * page_size]; a new_len below old_len
+ *            counts as old_len (pages are not given back here).
+ *  free_pages : device int32 [n_free], page numbers to take, in order: first
+ *            those request 0 needs, then request 1's, ...
+ *  table   : device int32, B rows of table_width entries, table_stride apart.
+ *            Entries of the pages that old_len covers are kept, those of the
+ *            pages taken are written, all others become -1.
+ *  slots   : device int32, B rows of n_slots entries, slots_stride apart (NULL
+ *            when n_slots is 0).  slots[b][i] = page * page_size + offset of
+ *            token old_len[b] + i, or -1 when that token is not below
+ *            new_len[b], has no page, or its slot number passes 2^31 - 1.
+ *  taken   : device int32 [1]: the number of pages the call needs.  When it is
+ *            above n_free, the requests that came too late have -1 entries
+ *            and -1 slots, and their tokens are not held.
+ * One launch.  A call repeated on its own output with the same lengths and
+ * free list writes the same values. */
+int sage_page_tables(const int32_t* old_len, const int32_t* new_len, int B, int page_size,
+                     const int32_t* free_pages, int n_free, int32_t* table, int64_t table_stride, int table_width,
+                     int32_t* slots, int64_t slots_stride, int n_slots, int32_t* taken, void* stream);
+
+/* Write the keys and values of new tokens into their slots.
+ *  k, v    : BF16 [B, heads, N, D] views (device), as for every sage_tensor;
+ *            they must not overlap the cache.
+ *  slots   : device int32, B rows of N entries, slots_stride apart.  A negative
+ *            slot skips its token; a slot outside the cache is skipped too and
+ *            recorded as SAGE_ERR_PAGE in the device status.  A slot that
+ *            occurs twice holds either token's rows, or parts of both.
+ * Rows of the cache that no slot names are left as they are.  One launch. */
+int sage_cache_append(const sage_tensor* k, const sage_tensor* v, int B, int N, const int32_t* slots,
+                      int64_t slots_stride, const sage_page_cache* cache, void* stream);
+
+/* Bytes of workspace sage_attn_paged needs for a shape, with or without a
+ * prefix (H query heads, Hkv key heads). */
+int sage_paged_workspace(int B, int H, int Hkv, int Nq, int D, size_t* bytes);
+
+/* Attention of new tokens over the page cache, for a batch whose requests may
+ * share a prefix.  Query row i of request b and head h sees, in key head
+ * h / (H / cache->heads), the first prefix_len tokens of prefix_table (the
+ * same for all requests) and tokens j < kv_len[b] of table row b; causal = 1:
+ * only those with j <= i + kv_len[b] - q_len[b], so that the last query row
+ * sees the last key.  Its output is the softmax-weighted sum of the values
+ * over both together; a row that sees no key is written as zero.
+ *  q, o    : BF16 [B, H, Nq, D] views (device); rows >= q_len[b] of o are not
+ *            written.  H is a multiple of cache->heads; D is cache->D.
+ *  q_len   : device int32 [B], or NULL for Nq; kv_len : device int32 [B], or
+ *            NULL for table_width * page_size; prefix_len : device int32 [1],
+ *            or NULL for prefix_width * page_size.  Out-of-range lengths are
+ *            clamped.  kv_len counts a request's own tokens, the new ones
+ *            included, without the prefix.
+ *  table   : device int32, B rows of table_width entries, table_stride apart;
+ *            prefix_table : device int32 [prefix_width].  A width may be 0 and
+ *            its pointer NULL.  Entries behind a length are not read.  A
+ *            listed page outside the cache reads as zeros and is recorded as
+ *            SAGE_ERR_PAGE in the device status.
+ *  sm_scale <= 0 selects 1/sqrt(D).
+ *  workspace : device scratch of at least sage_paged_workspace bytes, 16-byte
+ *            aligned, whose contents do not matter before or after.  Calls on
+ *            the same workspace must be ordered.
+ * Cache rows behind a length are never used, whatever they hold; the rows
+ * within the lengths must be finite, hidden ones included.  Scores, maxima,
+ * sums and outputs are FP32, the weights are rounded to BF16 for the product
+ * with the values.  Results do not depend on the workspace or on earlier
+ * calls: equal inputs give equal bits on the same device. */
+int sage_attn_paged(const sage_tensor* q, const sage_tensor* o, const sage_page_cache* cache, int B, int H, int Nq,
+                    const int32_t* q_len, const int32_t* table, int64_t table_stride, int table_width,
+                    const int32_t* kv_len, const int32_t* prefix_table, int prefix_width, const int32_t* prefix_len,
+                    float sm_scale, int causal, void* workspace, size_t workspace_bytes, void* stream);
 
 /* Synchronizes the device, returns the first error a kernel recorded since
  * the last call (SAGE_OK if none) and clears it. */

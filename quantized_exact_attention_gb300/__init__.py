@@ -25,9 +25,11 @@ SAGE_ERR_LAUNCH = -3
 SAGE_ERR_TIMEOUT = -4
 SAGE_ERR_DRIVER = -5
 SAGE_ERR_SCRATCH = -6
+SAGE_ERR_PAGE = -7
 
 D_HEAD = 128
 HEAD_DIMS = (64, 128)       # head dimensions the kernels are built for
+PAGE_SIZES = (16, 32, 64, 128)   # tokens per page of a page cache
 
 # Names the header declares (checked by the CPU tests against the .so exports).
 EXPORTED = ("sage_buffer_sizes", "sage_prep_qkv", "sage_attn_fwd", "sage_attn_fwd_causal", "sage_attention",
@@ -37,7 +39,8 @@ EXPORTED = ("sage_buffer_sizes", "sage_prep_qkv", "sage_attn_fwd", "sage_attn_fw
             "sage_attention_host", "sage_get_device_status", "sage_status_string",
             "sage_last_launch_count", "sage_debug_inject_fault", "sage_debug_prep_mode",
             "sage_debug_epilogue_mode", "sage_prep_qkv_noalloc",
-            "sage_prep_noalloc_capacity")
+            "sage_prep_noalloc_capacity", "sage_page_tables", "sage_cache_append",
+            "sage_paged_workspace", "sage_attn_paged")
 
 
 class SageError(RuntimeError):
@@ -71,6 +74,11 @@ class sage_checkpoints(ctypes.Structure):
 
 class sage_copy(ctypes.Structure):
     _fields_ = [("host", ctypes.c_void_p), ("device", ctypes.c_void_p), ("bytes", ctypes.c_size_t)]
+
+
+class sage_page_cache(ctypes.Structure):
+    _fields_ = [("k", sage_tensor), ("v", sage_tensor), ("num_pages", ctypes.c_int), ("page_size", ctypes.c_int),
+                ("heads", ctypes.c_int), ("D", ctypes.c_int)]
 
 
 _lib = None
@@ -115,6 +123,12 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
                                                                           P(sage_prep_buffers), vp]
     lib.sage_prep_qkv_noalloc.argtypes = lib.sage_prep_qkv.argtypes
     lib.sage_prep_noalloc_capacity.argtypes = []
+    i64, sz = ctypes.c_int64, ctypes.c_size_t
+    lib.sage_page_tables.argtypes = [vp, vp, i, i, vp, i, vp, i64, i, vp, i64, i, vp, vp]
+    lib.sage_cache_append.argtypes = [P(sage_tensor), P(sage_tensor), i, i, vp, i64, P(sage_page_cache), vp]
+    lib.sage_paged_workspace.argtypes = [i, i, i, i, i, P(sz)]
+    lib.sage_attn_paged.argtypes = [P(sage_tensor), P(sage_tensor), P(sage_page_cache), i, i, i, vp, vp, i64, i, vp,
+                                    vp, i, vp, f, i, vp, sz, vp]
     for name in EXPORTED:
         if name not in ("sage_status_string", "sage_prep_noalloc_capacity"):
             getattr(lib, name).restype = ctypes.c_int
@@ -406,3 +420,167 @@ def attention(q, k, v, q_len=None, kv_len=None, sm_scale: float = 0.0, out=None,
         sage_prep_qkv(q, k, v, bufs, q_len, kv_len, stream)
         sage_attn_fwd(bufs, out, q_len, kv_len, sm_scale, stream, Nkv=Nkv, causal=causal)
     return out, bufs
+
+
+# ---------------------------------------------------------------------------
+# Serving from a page cache
+# ---------------------------------------------------------------------------
+@dataclass(frozen=True)
+class PageCache:
+    """A pool of pages of keys and values: BF16 [num_pages, heads, page_size, D]
+    views with unit D stride (see sage_page_cache in the header).  Frozen: the
+    C struct is built once and reused by every call."""
+    k: torch.Tensor
+    v: torch.Tensor
+
+    def __post_init__(self):
+        if self.k.shape != self.v.shape or self.k.device != self.v.device:
+            raise ValueError("k and v of a page cache have one shape and device")
+        self._c                                            # checks type, dimensions and unit stride
+
+    @property
+    def num_pages(self) -> int:
+        return self.k.shape[0]
+
+    @property
+    def heads(self) -> int:
+        return self.k.shape[1]
+
+    @property
+    def page_size(self) -> int:
+        return self.k.shape[2]
+
+    @functools.cached_property
+    def _c(self) -> sage_page_cache:
+        n, h, page, d = self.k.shape
+        return sage_page_cache(tensor_desc(self.k), tensor_desc(self.v), n, page, h, d)
+
+    @functools.cached_property
+    def _ref(self):
+        return ctypes.byref(self._c)
+
+    @functools.cached_property
+    def _device(self) -> int:
+        return self.k.get_device()
+
+
+def alloc_page_cache(num_pages: int, page_size: int, heads: int, D: int = D_HEAD, device="cuda") -> PageCache:
+    """A page cache whose pages hold their tokens one after another, all heads
+    of a token together; its contents are undefined."""
+    if page_size not in PAGE_SIZES:
+        raise ValueError(f"page_size is one of {PAGE_SIZES}")
+    e = lambda: torch.empty((num_pages, page_size, heads, D), dtype=torch.bfloat16, device=device).permute(0, 2, 1, 3)  # noqa: E731
+    return PageCache(e(), e())
+
+
+def _on(dev: int, *tensors):
+    """Refuse tensors that do not live on CUDA device `dev`, or a call while another device is current."""
+    for t in tensors:
+        if t is not None and t.get_device() != dev:
+            raise ValueError("all tensors of a call live on one CUDA device")
+    if dev < 0 or torch.cuda.current_device() != dev:
+        raise ValueError("the tensors of a call live on the current CUDA device")
+
+
+def _ints(t, what: str, dim: int = 1):
+    """Data pointer of an int32 tensor with unit stride along its last dimension (None stays None)."""
+    if t is None:
+        return None
+    if t.dtype != torch.int32 or t.dim() != dim or (t.shape[-1] > 1 and t.stride(-1) != 1):
+        raise ValueError(f"{what}: expected a {dim}-dimensional int32 tensor, contiguous along its last dimension")
+    return t.data_ptr()
+
+
+def _count(t, n: int, what: str):
+    if t is not None and t.shape[0] != n:
+        raise ValueError(f"{what}: expected {n} entries, got {t.shape[0]}")
+
+
+def sage_page_tables(new_len, page_size: int, free_pages, table, slots=None, taken=None, old_len=None, stream=None):
+    """Enqueue the page tables and slot maps of requests that grow from old_len
+    (None: 0) to new_len tokens, with pages taken from free_pages in order.
+    table: int32 [B, W], updated in place; slots: int32 [B, N] or None; taken:
+    int32 [1], the number of pages needed.  Returns taken (allocated if None)."""
+    B, W = table.shape
+    if taken is None:
+        with torch.cuda.stream(stream):
+            taken = torch.empty((1,), dtype=torch.int32, device=table.device)
+    _on(table.get_device(), new_len, free_pages, slots, taken, old_len)
+    ptrs = [_ints(t, n, d) for t, n, d in ((old_len, "old_len", 1), (new_len, "new_len", 1),
+                                           (free_pages, "free_pages", 1), (table, "table", 2),
+                                           (slots, "slots", 2), (taken, "taken", 1))]
+    _count(new_len, B, "new_len")
+    _count(old_len, B, "old_len")
+    _count(slots, B, "slots")
+    _count(taken, 1, "taken")
+    rc = load_library().sage_page_tables(ptrs[0], ptrs[1], B, int(page_size), ptrs[2], free_pages.shape[0], ptrs[3],
+                                         table.stride(0), W, ptrs[4], slots.stride(0) if slots is not None else 0,
+                                         slots.shape[1] if slots is not None else 0, ptrs[5], _stream_ptr(stream))
+    _check(rc, "sage_page_tables")
+    return taken
+
+
+def sage_cache_append(k, v, slots, cache: PageCache, stream=None):
+    """Enqueue the copy of new keys and values ([B, heads, N, D] BF16 views) into
+    their cache slots (int32 [B, N]; a negative slot skips its token)."""
+    B, h, N, D = k.shape
+    if v.shape != k.shape or h != cache.heads or D != cache.k.shape[3]:
+        raise ValueError("k and v are [B, heads, N, D] with the cache's heads and D")
+    _on(cache._device, k, v, slots)
+    sp = _ints(slots, "slots", 2)
+    if slots.shape[0] != B or slots.shape[1] != N:
+        raise ValueError(f"slots: expected [{B}, {N}]")
+    ks, vs = tensor_desc(k), tensor_desc(v)
+    rc = load_library().sage_cache_append(ctypes.byref(ks), ctypes.byref(vs), B, N, sp, slots.stride(0), cache._ref,
+                                          _stream_ptr(stream))
+    _check(rc, "sage_cache_append")
+
+
+def paged_workspace_bytes(B: int, H: int, Hkv: int, Nq: int, D: int = D_HEAD) -> int:
+    n = ctypes.c_size_t()
+    _check(load_library().sage_paged_workspace(B, H, Hkv, Nq, D, ctypes.byref(n)), "sage_paged_workspace")
+    return n.value
+
+
+def alloc_paged_workspace(B: int, H: int, Hkv: int, Nq: int, D: int = D_HEAD, device="cuda") -> torch.Tensor:
+    """Workspace of sage_attn_paged for this shape, with or without a prefix."""
+    return torch.empty((paged_workspace_bytes(B, H, Hkv, Nq, D),), dtype=torch.uint8, device=device)
+
+
+def sage_attn_paged(q, o, cache: PageCache, table, workspace, q_len=None, kv_len=None, prefix_table=None,
+                    prefix_len=None, sm_scale: float = 0.0, causal: bool = True, stream=None):
+    """Enqueue attention of the new tokens q ([B, H, Nq, D] BF16 view, output
+    view o) over the page cache: table int32 [B, W] (or None: no own keys) with
+    kv_len own tokens each, and the pages of prefix_table (int32 [Wp], prefix_len
+    int32 [1]) that all requests share.  See the header for the masks."""
+    B, H, Nq, D = q.shape
+    if o.shape != q.shape or D != cache.k.shape[3]:
+        raise ValueError("q and o are [B, H, Nq, D] with the cache's D")
+    _on(cache._device, q, o, table, workspace, q_len, kv_len, prefix_table, prefix_len)
+    tp, pp = _ints(table, "table", 2), _ints(prefix_table, "prefix_table")
+    ql, kl, pl = _ints(q_len, "q_len"), _ints(kv_len, "kv_len"), _ints(prefix_len, "prefix_len")
+    _count(table, B, "table")
+    _count(q_len, B, "q_len")
+    _count(kv_len, B, "kv_len")
+    _count(prefix_len, 1, "prefix_len")
+    if not workspace.is_contiguous():
+        raise ValueError("workspace is contiguous")
+    qs, os_ = tensor_desc(q), tensor_desc(o)
+    rc = load_library().sage_attn_paged(
+        ctypes.byref(qs), ctypes.byref(os_), cache._ref, B, H, Nq, ql, tp, table.stride(0) if tp else 0,
+        table.shape[1] if tp else 0, kl, pp, prefix_table.shape[0] if pp else 0, pl, float(sm_scale),
+        1 if causal else 0, workspace.data_ptr(), workspace.numel() * workspace.element_size(), _stream_ptr(stream))
+    _check(rc, "sage_attn_paged")
+
+
+def attention_paged(q, cache: PageCache, table, q_len=None, kv_len=None, prefix_table=None, prefix_len=None,
+                    sm_scale: float = 0.0, causal: bool = True, out=None, stream=None):
+    """sage_attn_paged with its own workspace and, unless `out` is given, output
+    (rows at or beyond q_len are zero); returns the output."""
+    B, H, Nq, D = q.shape
+    with torch.cuda.stream(stream):                        # what is allocated here belongs to the stream that uses it
+        if out is None:
+            out = torch.zeros((B, Nq, H, D), dtype=torch.bfloat16, device=q.device).permute(0, 2, 1, 3)
+        ws = alloc_paged_workspace(B, H, cache.heads, Nq, D, q.device)
+        sage_attn_paged(q, out, cache, table, ws, q_len, kv_len, prefix_table, prefix_len, sm_scale, causal)
+    return out

@@ -1,0 +1,574 @@
+// sage_paged.cu - attention over a page cache, for a batch that may share a
+// prefix: the kernel for few query rows, the kernel that joins partial
+// results, and the C entry points.
+//
+// Row (b, h, i) sees the prefix's keys and its request's own keys j < kv_len[b]
+// (causal: j <= i + kv_len[b] - q_len[b]):
+//     o = sum_j softmax_j(sm_scale * q.k_j) v_j        (no key: 0)
+// The softmax runs online: per key tile the running maximum m, the sum
+// l = sum 2^(s - m) and O = sum 2^(s - m) v are updated in FP32 (s in the log2
+// domain).  Results over disjoint key sets join exactly the same way:
+//     M = max m_p,  o = (sum_p 2^(m_p - M) O_p) / (sum_p 2^(m_p - M) l_p),
+// which is what lets one request's keys be split among workers and the
+// prefix be read once for the rows of all requests.
+#include <algorithm>
+#include <cmath>
+
+#include "sage_gb300.h"
+#include "sage_internal.h"
+#include "sage_paged.h"
+#include "sage_paged_sched.cuh"
+#include "sage_ptx.cuh"
+#include "sage_quant.cuh"
+
+namespace sage {
+namespace {
+
+// ---------------------------------------------------------------------------
+// Few rows: one warp is one worker.
+//
+// Reading the keys and values bounds this form (per key 4*D bytes, and only
+// 4*D operations for each of a few rows), so the work of a warp is a stream
+// of 16-key steps through its own ring of shared-memory stages, filled by
+// 16-byte asynchronous copies; no barrier joins the warps of a CTA.
+// S^T = K Q^T and O^T = V^T P^T, i.e. the keys (then the channels) are the
+// 16 rows of the matrix instruction and the query rows its 8 columns, so 8
+// query rows waste nothing, and the rescale factor of a query row multiplies
+// whole accumulator columns.  P is rounded to BF16 (relative error at most 2^-8) for
+// the second product, as its other operand V is BF16; l sums it unrounded.
+// A step never crosses a page: pages hold a multiple of 16 tokens.
+// ---------------------------------------------------------------------------
+constexpr int kRowWarps = 4;             // warps of a CTA
+constexpr int kStep = 16;                // keys of a step
+
+template <int D>
+struct RowsShape {
+    static constexpr int kStages = D == 128 ? 3 : 6;
+    static constexpr int kChunks = D / 8;                          // 16-byte chunks of a row
+    static constexpr uint32_t kTile = kStep * D * 2;               // K (or V) bytes of a stage
+    static constexpr uint32_t kStage = 2 * kTile;
+    static constexpr uint32_t kSmem = kRowWarps * kStages * kStage;
+};
+
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, uint32_t bytes) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ void ldsm_x4(uint32_t (&r)[4], uint32_t a) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(a) : "memory");
+}
+__device__ __forceinline__ void ldsm_x4_t(uint32_t (&r)[4], uint32_t a) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(a) : "memory");
+}
+__device__ __forceinline__ void mma_bf16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
+    uint32_t y;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+    return y;
+}
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+    uint32_t r;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+__device__ __forceinline__ void record_page(const PagedParams& p, int page) {
+    if (atomicCAS(p.status, 0, kErrPage) == 0) p.status[3] = page;
+}
+
+// A step as the loading side leaves it for the computing side.
+struct StepNote {
+    int b, h, rt, item;                  // of its item
+    int key0, nkeys;
+    int own, first;                      // own keys; first step of its item in this warp
+};
+
+template <int D, int NR>
+__global__ void __launch_bounds__(kRowWarps * 32, 2) paged_rows_kernel(const PagedParams p) {
+    using Sh = RowsShape<D>;
+    constexpr int M = 8 * NR, S = Sh::kStages;
+    constexpr int kRowsPerPass = 32 / Sh::kChunks;
+    extern __shared__ __align__(128) uint8_t smem[];
+    __shared__ int chunk[kRowWarps * 32];
+    __shared__ int warp_sums[kRowWarps];
+    __shared__ StepNote notes[kRowWarps][S];
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const PagedSched<M, kStep> sched(p);
+    const int total = paged_scan<M, kStep, kRowWarps * 32>(sched, chunk, warp_sums, blockIdx.x == 0);
+    const int per = sched.per_worker(total);
+    // workers next to each other in the list sit on different SMs: a CTA's
+    // warps are a grid apart, so a short list still uses every SM
+    const int worker = warp * gridDim.x + blockIdx.x;
+    if ((int64_t)worker * per >= total || worker >= p.workers) return;
+    const int t0 = worker * per;
+    const int count = min(per, total - t0);
+
+    const uint32_t ring = smem_u32(smem) + warp * S * Sh::kStage;
+    PagedPlace at = paged_find<M, kStep, kRowWarps * 32>(sched, chunk, t0);
+    int left = count;                                     // steps not yet fetched
+    bool first = true;
+    PagedSpan span{};
+    int page = 0;
+    // Read the page number of the next step (one step before its copies, so
+    // that the table's latency lies behind a step of computing).
+    auto fetch = [&]() {
+        span = paged_span(sched, at);
+        const int j = span.key0 >> p.page_shift;
+        page = span.own ? __ldg(p.table + (int64_t)at.b * p.table_stride + j) : __ldg(p.ptable + j);
+    };
+    auto issue = [&](int stage) {
+        const bool ok = (unsigned)page < (unsigned)p.num_pages;
+        if (!ok && lane == 0) record_page(p, page);
+        const int nk = ok ? span.nkeys : 0;               // rows of a page outside the cache read as zero
+        const int64_t pg = ok ? page : 0;
+        const int off = span.key0 & (p.page - 1);
+        const int r0 = lane / Sh::kChunks, c = lane % Sh::kChunks;
+        const uint16_t* kp = p.k + pg * p.ksp + at.h * p.ksh + (int64_t)(off + r0) * p.kst + c * 8;
+        const uint16_t* vp = p.v + pg * p.vsp + at.h * p.vsh + (int64_t)(off + r0) * p.vst + c * 8;
+        const uint32_t base = ring + stage * Sh::kStage;
+#pragma unroll
+        for (int i = 0; i < kStep / kRowsPerPass; ++i) {
+            const int r = r0 + i * kRowsPerPass;
+            const uint32_t d = base + r * (D * 2) + ((c ^ (r & 7)) << 4);
+            const bool in = r < nk;
+            cp_async16(d, in ? kp + (int64_t)i * kRowsPerPass * p.kst : p.k, in ? 16u : 0u);
+            cp_async16(d + Sh::kTile, in ? vp + (int64_t)i * kRowsPerPass * p.vst : p.v, in ? 16u : 0u);
+        }
+        if (lane == 0) {
+            StepNote& nt = notes[warp][stage];
+            nt.b = at.b; nt.h = at.h; nt.rt = at.rt; nt.item = at.item;
+            nt.key0 = span.key0; nt.nkeys = span.nkeys;
+            nt.own = span.own; nt.first = first;
+        }
+        if (--left > 0) {
+            const int item = at.item;
+            paged_next(sched, at);
+            first = at.item != item;
+            fetch();
+        }
+    };
+
+    fetch();
+#pragma unroll
+    for (int s = 0; s < S - 1; ++s) {
+        if (left > 0) issue(s);
+        cp_async_commit();
+    }
+
+    uint32_t qf[NR][D / 16][2];                           // Q^T fragments
+    float o[NR][D / 16][4];                               // O^T: channels x query rows
+    float m[NR][2], l[NR][2];                             // of the two query rows this lane's columns are
+    int lim[NR][2];                                       // own keys each of them sees
+    int item = -1, ib = 0, ih = 0, irt = 0;               // the item these belong to
+
+    // Leave the item's partial result.
+    auto leave = [&]() {
+        const int64_t slot = (int64_t)worker + item;
+        PagedPlace x{};
+        x.b = ib; x.h = ih; x.rt = irt;
+        if (ib >= 0) x.n = sched.q_rows(ib);
+#pragma unroll
+        for (int nr = 0; nr < NR; ++nr) {
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                float s = l[nr][e];
+                s += __shfl_xor_sync(0xffffffffu, s, 4);
+                s += __shfl_xor_sync(0xffffffffu, s, 8);
+                s += __shfl_xor_sync(0xffffffffu, s, 16);
+                const int r = nr * 8 + (lane & 3) * 2 + e;
+                int b, i, hq;
+                if (!paged_row(sched, x, r, b, i, hq)) continue;
+                if (lane < 4) p.part_ml[slot * M + r] = make_float2(m[nr][e], s);
+                float* dst = p.part_o + (slot * M + r) * D + (lane >> 2);
+#pragma unroll
+                for (int j = 0; j < D / 16; ++j) {
+                    dst[j * 16] = o[nr][j][e];
+                    dst[j * 16 + 8] = o[nr][j][2 + e];
+                }
+            }
+        }
+    };
+    auto enter = [&](const StepNote& nt) {
+        item = nt.item; ib = nt.b; ih = nt.h; irt = nt.rt;
+        PagedPlace x{};
+        x.b = ib; x.h = ih; x.rt = irt;
+        if (ib >= 0) { x.n = sched.q_rows(ib); x.len = sched.own_keys(ib); }
+#pragma unroll
+        for (int nr = 0; nr < NR; ++nr) {
+            int b, i, hq;
+            const bool in = paged_row(sched, x, nr * 8 + (lane >> 2), b, i, hq);
+            const uint16_t* qp = p.q + (in ? b * p.qsb + hq * p.qsh + i * p.qsn : 0) + (lane & 3) * 2;
+#pragma unroll
+            for (int j = 0; j < D / 16; ++j) {
+                qf[nr][j][0] = in ? __ldg(reinterpret_cast<const uint32_t*>(qp + j * 16)) : 0u;
+                qf[nr][j][1] = in ? __ldg(reinterpret_cast<const uint32_t*>(qp + j * 16 + 8)) : 0u;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) o[nr][j][e] = 0.f;
+            }
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                m[nr][e] = -INFINITY;
+                l[nr][e] = 0.f;
+                lim[nr][e] = x.len;
+                if (ib >= 0 && p.causal) {
+                    const int rr = irt * M + nr * 8 + (lane & 3) * 2 + e;
+                    lim[nr][e] = min(x.len, x.len - x.n + rr / p.G + 1);
+                }
+            }
+        }
+    };
+
+    for (int it = 0; it < count; ++it) {
+        const int stage = it % S;
+        cp_async_wait<S - 2>();
+        __syncwarp();
+        const StepNote nt = notes[warp][stage];
+        if (left > 0) issue((it + S - 1) % S);            // its stage was read in the step before
+        cp_async_commit();
+        if (nt.first) {
+            if (it > 0) leave();
+            enter(nt);
+        }
+        const uint32_t kb = ring + stage * Sh::kStage, vb = kb + Sh::kTile;
+        float sacc[NR][4];
+#pragma unroll
+        for (int nr = 0; nr < NR; ++nr)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) sacc[nr][e] = 0.f;
+        {
+            const int r = lane & 15;
+#pragma unroll
+            for (int j = 0; j < D / 16; ++j) {
+                uint32_t a[4];
+                ldsm_x4(a, kb + r * (D * 2) + (((2 * j + (lane >> 4)) ^ (r & 7)) << 4));
+#pragma unroll
+                for (int nr = 0; nr < NR; ++nr) mma_bf16(sacc[nr], a, qf[nr][j][0], qf[nr][j][1]);
+            }
+        }
+        uint32_t pf[NR][2];
+        const int k0 = nt.key0 + (lane >> 2);             // this lane's keys: k0 and k0 + 8
+#pragma unroll
+        for (int nr = 0; nr < NR; ++nr) {
+            float f[2];
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const int end = nt.own ? min(lim[nr][e], nt.key0 + nt.nkeys) : nt.key0 + nt.nkeys;
+                if (k0 >= end) sacc[nr][e] = -INFINITY;
+                if (k0 + 8 >= end) sacc[nr][2 + e] = -INFINITY;
+                float mx = fmaxf(sacc[nr][e], sacc[nr][2 + e]);
+                mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
+                mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
+                mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
+                const float mn = fmaxf(m[nr][e], mx * p.sc);
+                const float ms = mn == -INFINITY ? 0.f : mn;      // no visible key yet: every weight is 0
+                f[e] = ex2_approx(m[nr][e] - ms);
+                m[nr][e] = mn;
+                sacc[nr][e] = ex2_approx(fmaf(sacc[nr][e], p.sc, -ms));
+                sacc[nr][2 + e] = ex2_approx(fmaf(sacc[nr][2 + e], p.sc, -ms));
+                l[nr][e] = l[nr][e] * f[e] + (sacc[nr][e] + sacc[nr][2 + e]);
+            }
+            pf[nr][0] = transpose8x8(pack_bf16(sacc[nr][0], sacc[nr][1]));
+            pf[nr][1] = transpose8x8(pack_bf16(sacc[nr][2], sacc[nr][3]));
+            if (!__all_sync(0xffffffffu, f[0] == 1.f && f[1] == 1.f)) {
+#pragma unroll
+                for (int j = 0; j < D / 16; ++j) {
+                    o[nr][j][0] *= f[0]; o[nr][j][1] *= f[1];
+                    o[nr][j][2] *= f[0]; o[nr][j][3] *= f[1];
+                }
+            }
+        }
+        {
+            const int r = (lane & 7) + ((lane >> 4) << 3), hc = (lane >> 3) & 1;
+#pragma unroll
+            for (int j = 0; j < D / 16; ++j) {
+                uint32_t a[4];
+                ldsm_x4_t(a, vb + r * (D * 2) + (((2 * j + hc) ^ (r & 7)) << 4));
+#pragma unroll
+                for (int nr = 0; nr < NR; ++nr) mma_bf16(o[nr][j], a, pf[nr][0], pf[nr][1]);
+            }
+        }
+    }
+    leave();
+    cp_async_wait<0>();
+}
+
+// ---------------------------------------------------------------------------
+// Join the partial results of each output row.  WPR warps share a row.
+// ---------------------------------------------------------------------------
+struct RowParts {
+    int64_t slot0;                       // slots slot0, slot0 + 1, ... (one per worker in order)
+    int n;
+};
+
+// Parts of the item of `nt` tiles that starts at list position `start`.
+__device__ __forceinline__ RowParts parts_of(int start, int nt, int per, int item) {
+    RowParts r{0, 0};
+    if (nt > 0) {
+        const int w0 = start / per, w1 = (start + nt - 1) / per;
+        r.slot0 = (int64_t)w0 + item;
+        r.n = w1 - w0 + 1;
+    }
+    return r;
+}
+
+template <int D, int M, int TK, int WPR>
+__global__ void __launch_bounds__(256) paged_join_kernel(const PagedParams p) {
+    constexpr int V = D / 32;                              // channels of a lane
+    __shared__ float red_o[8][D];
+    __shared__ float2 red_ml[8];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int64_t row = (int64_t)blockIdx.x * (8 / WPR) + warp / WPR;
+    const int sub = warp % WPR;
+    const bool in = row < (int64_t)p.B * p.H * p.Nq;
+    const PagedSched<M, TK> s(p);
+    int b = 0, i = 0, hq = 0;
+    if (in) {
+        i = (int)(row % p.Nq);
+        const int64_t bh = row / p.Nq;
+        hq = (int)(bh % p.H);
+        b = (int)(bh / p.H);
+    }
+    const int n = s.q_rows(b), len = s.own_keys(b);
+    const bool live = in && i < n;
+    float acc[V], m = -INFINITY, l = 0.f;
+#pragma unroll
+    for (int v = 0; v < V; ++v) acc[v] = 0.f;
+    if (live) {
+        const int h = hq / p.G, g = hq - h * p.G;
+        const int per = s.per_worker(p.start[p.B]);
+        const int r = i * p.G + g, rt = r / M;
+        int at = p.start[b], before = 0, per_head = 0;
+        for (int x = 0; x < p.rt; ++x) {
+            const int nt = s.item_tiles(n, len, x);
+            if (x < rt) before += nt;
+            per_head += nt;
+        }
+        at += h * per_head + before;
+        const RowParts own = parts_of(at, s.item_tiles(n, len, rt), per, p.pre_rt * p.Hkv + (b * p.Hkv + h) * p.rt + rt);
+        RowParts pre{0, 0};
+        int pr = 0;
+        if (p.pre_rt > 0) {
+            const int rr = (b * p.Nq + i) * p.G + g;
+            const int it = h * p.pre_rt + rr / M;
+            pr = rr % M;
+            pre = parts_of(it * s.pre_tiles(), s.pre_tiles(), per, it);
+        }
+        const int parts = own.n + pre.n;
+#pragma unroll 4
+        for (int x = sub; x < parts; x += WPR) {
+            const int64_t q = x < pre.n ? (pre.slot0 + x) * M + pr : (own.slot0 + (x - pre.n)) * M + r % M;
+            const float2 ml = __ldcg(p.part_ml + q);
+            float w[V];
+            if (V == 4) {
+                const float4 t = __ldcg(reinterpret_cast<const float4*>(p.part_o + q * D) + lane);
+                w[0] = t.x; w[1] = t.y; w[V - 2] = t.z; w[V - 1] = t.w;
+            } else {
+                const float2 t = __ldcg(reinterpret_cast<const float2*>(p.part_o + q * D) + lane);
+                w[0] = t.x; w[1] = t.y;
+            }
+            const float mn = fmaxf(m, ml.x);
+            const float ms = mn == -INFINITY ? 0.f : mn;
+            const float fa = ex2_approx(m - ms), fb = ex2_approx(ml.x - ms);
+            l = l * fa + ml.y * fb;
+#pragma unroll
+            for (int v = 0; v < V; ++v) acc[v] = acc[v] * fa + w[v] * fb;
+            m = mn;
+        }
+    }
+    if (WPR > 1) {
+#pragma unroll
+        for (int v = 0; v < V; ++v) red_o[warp][lane * V + v] = acc[v];
+        if (lane == 0) red_ml[warp] = make_float2(m, l);
+        __syncthreads();
+        if (sub != 0) return;
+#pragma unroll
+        for (int x = 1; x < WPR; ++x) {
+            const float2 ml = red_ml[warp + x];
+            const float mn = fmaxf(m, ml.x);
+            const float ms = mn == -INFINITY ? 0.f : mn;
+            const float fa = ex2_approx(m - ms), fb = ex2_approx(ml.x - ms);
+            l = l * fa + ml.y * fb;
+#pragma unroll
+            for (int v = 0; v < V; ++v) acc[v] = acc[v] * fa + red_o[warp + x][lane * V + v] * fb;
+            m = mn;
+        }
+    }
+    if (!live) return;
+    // l is 0 exactly when the row saw no key (its largest weight is 1); a NaN
+    // in l stays in the output
+    const float inv = l == 0.f ? 0.f : __fdiv_rn(1.f, l);
+    uint32_t out[V / 2];
+#pragma unroll
+    for (int v = 0; v < V / 2; ++v) out[v] = pack_bf16(acc[2 * v] * inv, acc[2 * v + 1] * inv);
+    uint16_t* dst = p.o + b * p.osb + hq * p.osh + (int64_t)i * p.osn + lane * V;
+    if (V == 4) *reinterpret_cast<uint2*>(dst) = make_uint2(out[0], out[V / 2 - 1]);
+    else *reinterpret_cast<uint32_t*>(dst) = out[0];
+}
+
+// ---------------------------------------------------------------------------
+// Host side: which rows go together.
+// ---------------------------------------------------------------------------
+struct Plan {
+    int nr;                              // 8-row groups of an item: 1, 2 or 4
+    int M, rt, pre_rt, join;
+    int64_t items, slots;
+};
+
+Plan make_plan(int B, int Hkv, int G, int Nq, bool prefix) {
+    Plan x{};
+    const int64_t rows = (int64_t)Nq * G;
+    // One pass over the prefix for all requests' rows pays when the rows of
+    // one request leave a row tile partly empty.
+    const bool shared = prefix && B > 1 && rows < 32;
+    const int64_t most = shared ? rows * B : rows;
+    x.nr = most <= 8 ? 1 : (most <= 16 ? 2 : 4);
+    x.M = 8 * x.nr;
+    x.rt = (int)ceil_div(rows, x.M);
+    x.pre_rt = shared ? (int)ceil_div(rows * B, x.M) : 0;
+    x.join = prefix && !shared;
+    x.items = (int64_t)Hkv * x.pre_rt + (int64_t)B * Hkv * x.rt;
+    x.slots = x.items + kMaxRowWorkers;
+    return x;
+}
+
+size_t plan_bytes(const Plan& x, int B, int D) {
+    const size_t o = (size_t)x.slots * x.M * D * 4, ml = (size_t)x.slots * x.M * 8;
+    return o + ml + (((size_t)B + 1) * 4 + 15) / 16 * 16;
+}
+
+bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+
+int check_view(const sage_tensor* t) {
+    if (t == nullptr || t->ptr == nullptr) return SAGE_ERR_ARG;
+    if (!aligned16(t->ptr) || (t->stride_b % 8) || (t->stride_h % 8) || (t->stride_n % 8) ||
+        t->stride_b < 0 || t->stride_h < 0 || t->stride_n < 0)
+        return SAGE_ERR_UNSUPPORTED;
+    return SAGE_OK;
+}
+
+int check_batch(int B, int H, int Hkv, int Nq, int D) {
+    if (B <= 0 || H <= 0 || Hkv <= 0 || Nq <= 0 || H % Hkv != 0) return SAGE_ERR_ARG;
+    if (B > 65535 || H > 65535 || Nq > (1 << 24)) return SAGE_ERR_ARG;
+    if (D != 64 && D != 128) return SAGE_ERR_UNSUPPORTED;
+    if ((int64_t)B * Nq * (H / Hkv) > INT32_MAX / 2) return SAGE_ERR_UNSUPPORTED;   // row numbers stay in int
+    return SAGE_OK;
+}
+
+int sm_count() {
+    static int n[64] = {};
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
+    if (n[dev] == 0 && cudaDeviceGetAttribute(&n[dev], cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 0;
+    return n[dev];
+}
+
+template <int D, int NR>
+cudaError_t launch_rows(PagedParams& p, int sms, cudaStream_t s) {
+    using Sh = RowsShape<D>;
+    cudaError_t e = cudaFuncSetAttribute(paged_rows_kernel<D, NR>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         (int)Sh::kSmem);
+    if (e != cudaSuccess) return e;
+    const int ctas = std::min(2 * sms, kMaxRowWorkers / kRowWarps);
+    p.workers = ctas * kRowWarps;
+    paged_rows_kernel<D, NR><<<ctas, kRowWarps * 32, Sh::kSmem, s>>>(p);
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    const int64_t rows = (int64_t)p.B * p.H * p.Nq;
+    if (rows <= 1024) paged_join_kernel<D, 8 * NR, kStep, 8><<<(unsigned)rows, 256, 0, s>>>(p);
+    else paged_join_kernel<D, 8 * NR, kStep, 1><<<(unsigned)ceil_div(rows, 8), 256, 0, s>>>(p);
+    return cudaGetLastError();
+}
+
+}  // namespace
+}  // namespace sage
+
+using namespace sage;
+
+extern "C" {
+
+int sage_paged_workspace(int B, int H, int Hkv, int Nq, int D, size_t* bytes) {
+    if (bytes == nullptr) return SAGE_ERR_ARG;
+    const int rc = check_batch(B, H, Hkv, Nq, D);
+    if (rc != SAGE_OK) return rc;
+    const size_t a = plan_bytes(make_plan(B, Hkv, H / Hkv, Nq, false), B, D);
+    const size_t b = plan_bytes(make_plan(B, Hkv, H / Hkv, Nq, true), B, D);
+    *bytes = a > b ? a : b;
+    return SAGE_OK;
+}
+
+int sage_attn_paged(const sage_tensor* q, const sage_tensor* o, const sage_page_cache* cache, int B, int H, int Nq,
+                    const int32_t* q_len, const int32_t* table, int64_t table_stride, int table_width,
+                    const int32_t* kv_len, const int32_t* prefix_table, int prefix_width, const int32_t* prefix_len,
+                    float sm_scale, int causal, void* workspace, size_t workspace_bytes, void* stream) {
+    int rc = check_page_cache(cache);
+    if (rc != SAGE_OK) return rc;
+    const int D = cache->D;
+    if ((rc = check_batch(B, H, cache->heads, Nq, D)) != SAGE_OK) return rc;
+    if ((rc = check_view(q)) != SAGE_OK || (rc = check_view(o)) != SAGE_OK) return rc;
+    if (table_width < 0 || prefix_width < 0 || (table_width > 0 && table == nullptr) ||
+        (prefix_width > 0 && prefix_table == nullptr) || table_stride < 0)
+        return SAGE_ERR_ARG;
+    if ((int64_t)table_width * cache->page_size > INT32_MAX - 128 ||
+        (int64_t)prefix_width * cache->page_size > INT32_MAX - 128)
+        return SAGE_ERR_UNSUPPORTED;
+    const int G = H / cache->heads;
+    const Plan plan = make_plan(B, cache->heads, G, Nq, prefix_width > 0);
+    const size_t need = plan_bytes(plan, B, D);
+    if (workspace == nullptr || !aligned16(workspace) || workspace_bytes < need) return SAGE_ERR_ARG;
+    // list positions and slot numbers stay in int
+    const int64_t keys = ((int64_t)table_width + (plan.join ? prefix_width : 0)) * cache->page_size;
+    const int64_t tiles = (int64_t)B * cache->heads * plan.rt * (keys / kStep + 2) +
+                          (int64_t)cache->heads * plan.pre_rt * ((int64_t)prefix_width * cache->page_size / kStep + 1);
+    if (tiles > INT32_MAX / 2 || plan.slots > INT32_MAX / 2) return SAGE_ERR_UNSUPPORTED;
+
+    PagedParams p{};
+    p.status = device_status_ptr();
+    const int sms = sm_count();
+    if (p.status == nullptr || sms == 0) return SAGE_ERR_LAUNCH;
+    p.q = static_cast<const uint16_t*>(q->ptr);
+    p.o = static_cast<uint16_t*>(const_cast<void*>(o->ptr));
+    p.k = static_cast<const uint16_t*>(cache->k.ptr);
+    p.v = static_cast<const uint16_t*>(cache->v.ptr);
+    p.qsb = q->stride_b; p.qsh = q->stride_h; p.qsn = q->stride_n;
+    p.osb = o->stride_b; p.osh = o->stride_h; p.osn = o->stride_n;
+    p.ksp = cache->k.stride_b; p.ksh = cache->k.stride_h; p.kst = cache->k.stride_n;
+    p.vsp = cache->v.stride_b; p.vsh = cache->v.stride_h; p.vst = cache->v.stride_n;
+    p.q_len = q_len; p.kv_len = kv_len; p.prefix_len = prefix_len;
+    p.table = table; p.table_stride = table_stride; p.ptable = prefix_table;
+    p.B = B; p.H = H; p.Hkv = cache->heads; p.G = G; p.Nq = Nq;
+    p.W = table_width; p.Wp = prefix_width;
+    p.num_pages = cache->num_pages; p.page = cache->page_size;
+    p.page_shift = 31 - __builtin_clz((unsigned)cache->page_size);
+    p.causal = causal != 0;
+    const double scale = sm_scale > 0.f ? (double)sm_scale : 1.0 / std::sqrt((double)D);
+    p.sc = (float)(scale * (1.0 / std::log(2.0)));
+    p.rt = plan.rt; p.pre_rt = plan.pre_rt; p.join = plan.join;
+    char* w = static_cast<char*>(workspace);
+    p.part_o = reinterpret_cast<float*>(w);
+    w += (size_t)plan.slots * plan.M * D * 4;
+    p.part_ml = reinterpret_cast<float2*>(w);
+    w += (size_t)plan.slots * plan.M * 8;
+    p.start = reinterpret_cast<int32_t*>(w);
+    const cudaStream_t s = static_cast<cudaStream_t>(stream);
+    cudaError_t e;
+    if (D == 64)
+        e = plan.nr == 1 ? launch_rows<64, 1>(p, sms, s)
+                         : (plan.nr == 2 ? launch_rows<64, 2>(p, sms, s) : launch_rows<64, 4>(p, sms, s));
+    else
+        e = plan.nr == 1 ? launch_rows<128, 1>(p, sms, s)
+                         : (plan.nr == 2 ? launch_rows<128, 2>(p, sms, s) : launch_rows<128, 4>(p, sms, s));
+    if (e != cudaSuccess) return SAGE_ERR_LAUNCH;
+    set_last_launch_count(2);
+    return SAGE_OK;
+}
+
+}  // extern "C"

@@ -1,0 +1,49 @@
+// sage_paged.h - parameter blocks of the paged serving kernels, shared by
+// their translation units (host and device).
+#pragma once
+
+#include <cstdint>
+#include <cuda_runtime.h>
+
+#include "sage_gb300.h"
+#include "sage_internal.h"
+
+namespace sage {
+
+constexpr int kErrPage = -7;             // SAGE_ERR_PAGE as the kernels record it
+constexpr int kMaxRowWorkers = 1280;     // warps of the few-rows kernel that take work (8 per SM, 160 SMs at most)
+
+struct PagedParams {
+    const uint16_t* q;                   // BF16 bit patterns
+    uint16_t* o;
+    const uint16_t* k;                   // page caches [page][head][token][channel] by strides
+    const uint16_t* v;
+    int64_t qsb, qsh, qsn, osb, osh, osn;            // element strides
+    int64_t ksp, ksh, kst, vsp, vsh, vst;            // page, head, token strides
+    const int32_t* q_len;                // device [B] or null
+    const int32_t* kv_len;               // device [B] or null: own tokens of each request
+    const int32_t* prefix_len;           // device [1] or null
+    const int32_t* table;                // device [B][table_stride], W entries used
+    const int32_t* ptable;               // device [Wp]
+    int64_t table_stride;
+    int B, H, Hkv, G, Nq;                // G = H / Hkv query heads to a key head
+    int W, Wp;                           // table widths in pages (Wp = 0: no prefix)
+    int num_pages, page, page_shift;     // tokens per page: a power of two
+    int causal;
+    float sc;                            // sm_scale * log2(e)
+    int* status;
+    // schedule (see sage_paged_sched.cuh)
+    int rt;                              // row tiles of a request's rows
+    int pre_rt;                          // row tiles of all requests' rows against the prefix (0: not in this list)
+    int join;                            // 1: a request's key sequence is the prefix followed by its own keys
+    int workers;                         // workers the list is shared among
+    // workspace
+    float* part_o;                       // [slot][M][D]
+    float2* part_ml;                     // [slot][M] running maximum (log2 domain) and sum
+    int32_t* start;                      // [B + 1] list position of each request's first tile; [B] = total
+};
+
+// Checks of a page cache's description that need no GPU (sage_tables.cu).
+int check_page_cache(const sage_page_cache* c);
+
+}  // namespace sage

@@ -1,0 +1,228 @@
+// sage_tables.cu - the bookkeeping of a page cache on the GPU: page tables and
+// slot maps from request lengths, and the append of new keys and values.
+#include <algorithm>
+
+#include "sage_gb300.h"
+#include "sage_internal.h"
+#include "sage_paged.h"
+
+namespace sage {
+namespace {
+
+// ---------------------------------------------------------------------------
+// Page tables and slots.
+//
+// Request b holds p(old) = ceil(old / P) pages and needs p(new); it takes the
+// pages free[first .. first + need) with first = sum of the needs before it.
+// One launch: every block sums the needs in front of its first request itself
+// (8 bytes per request, from L2 for all blocks but the first), which costs
+// less than a second launch or a wait between blocks.
+// ---------------------------------------------------------------------------
+struct TableParams {
+    const int32_t* old_len;              // or null: 0
+    const int32_t* new_len;
+    const int32_t* free_pages;
+    int32_t* table;
+    int32_t* slots;
+    int32_t* taken;
+    int64_t table_stride, slots_stride;
+    int B, W, N, n_free, page, page_shift;
+};
+
+struct Held { int old_len, new_len, old_pages, new_pages; };
+
+__device__ __forceinline__ Held held(const TableParams& p, int b) {
+    Held x;
+    const int cap = p.W << p.page_shift;
+    x.old_len = p.old_len == nullptr ? 0 : min(max(__ldg(p.old_len + b), 0), cap);
+    x.new_len = max(x.old_len, min(max(__ldg(p.new_len + b), 0), cap));
+    x.old_pages = (int)(((int64_t)x.old_len + p.page - 1) >> p.page_shift);
+    x.new_pages = (int)(((int64_t)x.new_len + p.page - 1) >> p.page_shift);
+    return x;
+}
+
+constexpr int kTableThreads = 256;
+
+__device__ __forceinline__ int block_sum(int v, int* red) {
+    v = __reduce_add_sync(0xffffffffu, v);
+    __syncthreads();                     // an earlier sum's reads of red are done
+    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
+    __syncthreads();
+    int s = 0;
+#pragma unroll
+    for (int i = 0; i < kTableThreads / 32; ++i) s += red[i];
+    return s;
+}
+
+__global__ void __launch_bounds__(kTableThreads) page_tables_kernel(const TableParams p) {
+    __shared__ int red[kTableThreads / 32];
+    const int per = (p.B + gridDim.x - 1) / gridDim.x;
+    const int b0 = min((int)blockIdx.x * per, p.B), b1 = min(b0 + per, p.B);
+    int sum = 0;
+    for (int b = threadIdx.x; b < b0; b += kTableThreads) {
+        const Held x = held(p, b);
+        sum += x.new_pages - x.old_pages;
+    }
+    int first = block_sum(sum, red);
+    for (int b = b0; b < b1; ++b) {
+        const Held x = held(p, b);
+        int32_t* row = p.table + (int64_t)b * p.table_stride;
+        // page of entry j of this request after the call
+        auto entry = [&](int j) -> int {
+            if (j < x.old_pages) return row[j];
+            const int f = first + (j - x.old_pages);
+            return j < x.new_pages && f < p.n_free ? __ldg(p.free_pages + f) : -1;
+        };
+        for (int j = x.old_pages + (int)threadIdx.x; j < p.W; j += kTableThreads) row[j] = entry(j);
+        if (p.slots != nullptr) {
+            int32_t* out = p.slots + (int64_t)b * p.slots_stride;
+            for (int i = threadIdx.x; i < p.N; i += kTableThreads) {
+                int64_t slot = -1;
+                if (i < x.new_len - x.old_len) {
+                    const int t = x.old_len + i;
+                    const int pg = entry(t >> p.page_shift);
+                    slot = pg < 0 ? -1 : ((int64_t)pg << p.page_shift) + (t & (p.page - 1));
+                    if (slot > INT32_MAX) slot = -1;
+                }
+                out[i] = (int32_t)slot;
+            }
+        }
+        first += x.new_pages - x.old_pages;
+    }
+    if (b1 == p.B && b0 < p.B && threadIdx.x == 0) *p.taken = first;
+}
+
+// ---------------------------------------------------------------------------
+// Append: one warp copies the K and V rows of one token, 16 bytes a lane.
+// Reads and writes each row once; HBM bounds it.
+// ---------------------------------------------------------------------------
+struct AppendParams {
+    const uint16_t* k;
+    const uint16_t* v;
+    uint16_t* ck;
+    uint16_t* cv;
+    const int32_t* slots;
+    int* status;
+    int64_t ksb, ksh, ksn, vsb, vsh, vsn;
+    int64_t ckp, ckh, ckt, cvp, cvh, cvt;
+    int64_t slots_stride, capacity;
+    int64_t tokens;                      // B * N
+    int N, heads, chunk_shift;           // chunk_shift: log2 of the 16-byte chunks of a head's row
+    int page, page_shift;
+};
+
+constexpr int kAppendThreads = 256;
+
+__global__ void __launch_bounds__(kAppendThreads) cache_append_kernel(const AppendParams p) {
+    const int lane = threadIdx.x & 31;
+    const int64_t warps = (int64_t)gridDim.x * (kAppendThreads / 32);
+    const int chunks = p.heads << p.chunk_shift;
+    for (int64_t t = (int64_t)blockIdx.x * (kAppendThreads / 32) + (threadIdx.x >> 5); t < p.tokens; t += warps) {
+        const int b = (int)(t / p.N), i = (int)(t % p.N);
+        const int slot = __ldg(p.slots + b * p.slots_stride + i);
+        if (slot < 0) continue;
+        if (slot >= p.capacity) {
+            if (lane == 0 && atomicCAS(p.status, 0, kErrPage) == 0) p.status[3] = slot >> p.page_shift;
+            continue;
+        }
+        const int64_t pg = slot >> p.page_shift;
+        const int off = slot & (p.page - 1);
+        const uint16_t* k = p.k + b * p.ksb + i * p.ksn;
+        const uint16_t* v = p.v + b * p.vsb + i * p.vsn;
+        uint16_t* ck = p.ck + pg * p.ckp + off * p.ckt;
+        uint16_t* cv = p.cv + pg * p.cvp + off * p.cvt;
+#pragma unroll 4
+        for (int c = lane; c < chunks; c += 32) {
+            const int h = c >> p.chunk_shift, x = (c - (h << p.chunk_shift)) * 8;
+            const uint4 a = __ldg(reinterpret_cast<const uint4*>(k + h * p.ksh + x));
+            const uint4 d = __ldg(reinterpret_cast<const uint4*>(v + h * p.vsh + x));
+            *reinterpret_cast<uint4*>(ck + h * p.ckh + x) = a;
+            *reinterpret_cast<uint4*>(cv + h * p.cvh + x) = d;
+        }
+    }
+}
+
+bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+
+int check_view(const sage_tensor* t) {
+    if (t == nullptr || t->ptr == nullptr) return SAGE_ERR_ARG;
+    if (!aligned16(t->ptr) || (t->stride_b % 8) || (t->stride_h % 8) || (t->stride_n % 8) ||
+        t->stride_b < 0 || t->stride_h < 0 || t->stride_n < 0)
+        return SAGE_ERR_UNSUPPORTED;
+    return SAGE_OK;
+}
+
+bool page_size_ok(int page) { return page == 16 || page == 32 || page == 64 || page == 128; }
+
+}  // namespace
+
+int check_page_cache(const sage_page_cache* c) {
+    if (c == nullptr || c->num_pages <= 0 || c->heads <= 0 || c->heads > 65535) return SAGE_ERR_ARG;
+    if ((c->D != 64 && c->D != 128) || !page_size_ok(c->page_size)) return SAGE_ERR_UNSUPPORTED;
+    if ((int64_t)c->num_pages * c->page_size > INT32_MAX) return SAGE_ERR_UNSUPPORTED;
+    int rc = check_view(&c->k);
+    return rc != SAGE_OK ? rc : check_view(&c->v);
+}
+
+}  // namespace sage
+
+using namespace sage;
+
+extern "C" {
+
+int sage_page_tables(const int32_t* old_len, const int32_t* new_len, int B, int page_size,
+                     const int32_t* free_pages, int n_free, int32_t* table, int64_t table_stride, int table_width,
+                     int32_t* slots, int64_t slots_stride, int n_slots, int32_t* taken, void* stream) {
+    if (B <= 0 || new_len == nullptr || taken == nullptr || table == nullptr || table_width <= 0) return SAGE_ERR_ARG;
+    if (n_free < 0 || (n_free > 0 && free_pages == nullptr) || n_slots < 0 || (n_slots > 0 && slots == nullptr))
+        return SAGE_ERR_ARG;
+    if ((B > 1 && table_stride < table_width) || (B > 1 && n_slots > 0 && slots_stride < n_slots)) return SAGE_ERR_ARG;
+    if (!page_size_ok(page_size)) return SAGE_ERR_UNSUPPORTED;
+    // lengths and the count of pages taken stay in int
+    if ((int64_t)table_width * page_size > INT32_MAX - page_size || (int64_t)B * table_width > INT32_MAX)
+        return SAGE_ERR_UNSUPPORTED;
+    TableParams p{};
+    p.old_len = old_len; p.new_len = new_len; p.free_pages = free_pages; p.n_free = n_free;
+    p.table = table; p.table_stride = table_stride; p.W = table_width;
+    p.slots = n_slots > 0 ? slots : nullptr; p.slots_stride = slots_stride; p.N = n_slots;
+    p.taken = taken; p.B = B; p.page = page_size;
+    p.page_shift = 31 - __builtin_clz((unsigned)page_size);
+    const int grid = std::min(B, 152 * 8);
+    page_tables_kernel<<<grid, kTableThreads, 0, static_cast<cudaStream_t>(stream)>>>(p);
+    if (cudaGetLastError() != cudaSuccess) return SAGE_ERR_LAUNCH;
+    set_last_launch_count(1);
+    return SAGE_OK;
+}
+
+int sage_cache_append(const sage_tensor* k, const sage_tensor* v, int B, int N, const int32_t* slots,
+                      int64_t slots_stride, const sage_page_cache* cache, void* stream) {
+    int rc = check_page_cache(cache);
+    if (rc != SAGE_OK) return rc;
+    if (B <= 0 || N <= 0 || slots == nullptr || slots_stride < 0) return SAGE_ERR_ARG;
+    if ((rc = check_view(k)) != SAGE_OK || (rc = check_view(v)) != SAGE_OK) return rc;
+    AppendParams p{};
+    p.status = device_status_ptr();
+    if (p.status == nullptr) return SAGE_ERR_LAUNCH;
+    p.k = static_cast<const uint16_t*>(k->ptr);
+    p.v = static_cast<const uint16_t*>(v->ptr);
+    p.ck = static_cast<uint16_t*>(const_cast<void*>(cache->k.ptr));
+    p.cv = static_cast<uint16_t*>(const_cast<void*>(cache->v.ptr));
+    p.slots = slots; p.slots_stride = slots_stride;
+    p.ksb = k->stride_b; p.ksh = k->stride_h; p.ksn = k->stride_n;
+    p.vsb = v->stride_b; p.vsh = v->stride_h; p.vsn = v->stride_n;
+    p.ckp = cache->k.stride_b; p.ckh = cache->k.stride_h; p.ckt = cache->k.stride_n;
+    p.cvp = cache->v.stride_b; p.cvh = cache->v.stride_h; p.cvt = cache->v.stride_n;
+    p.capacity = (int64_t)cache->num_pages * cache->page_size;
+    p.tokens = (int64_t)B * N; p.N = N; p.heads = cache->heads;
+    p.chunk_shift = cache->D == 128 ? 4 : 3;
+    p.page = cache->page_size;
+    p.page_shift = 31 - __builtin_clz((unsigned)cache->page_size);
+    const int64_t blocks = ceil_div(p.tokens, kAppendThreads / 32);
+    const int grid = (int)std::min<int64_t>(blocks, 152 * 8);
+    cache_append_kernel<<<grid, kAppendThreads, 0, static_cast<cudaStream_t>(stream)>>>(p);
+    if (cudaGetLastError() != cudaSuccess) return SAGE_ERR_LAUNCH;
+    set_last_launch_count(1);
+    return SAGE_OK;
+}
+
+}  // extern "C"

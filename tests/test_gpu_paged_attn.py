@@ -1,0 +1,261 @@
+"""Attention over a page cache against its definition in 64 bits.  Rows of the
+cache that no length covers are NaN and unused table entries lie outside the
+cache, so reading either shows."""
+import pytest
+import torch
+
+import quantized_exact_attention_gb300 as S
+from tests import gpu_support as G
+from tests import paged_support as P
+
+pytestmark = pytest.mark.gpu
+
+
+def go(**kw):
+    G.ensure_built()
+    p = P.make(**kw)
+    P.check(p, P.run(p))
+    return p
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("page", [16, 32, 64, 128])
+@pytest.mark.parametrize("n", [1, 15, 16, 17, 63, 64, 65, 127, 128, 129, 500])
+def test_one_token_one_request(D, page, n):
+    go(B=1, H=2, Hkv=2, D=D, Nq=1, page=page, kv_len=[n], seed=n)
+
+
+@pytest.mark.parametrize("H,Hkv", [(1, 1), (4, 4), (6, 2), (8, 1), (24, 8), (16, 1), (9, 3), (20, 1), (33, 1)])
+@pytest.mark.parametrize("D", [64, 128])
+def test_heads(H, Hkv, D):
+    go(B=3, H=H, Hkv=Hkv, D=D, Nq=1, page=16, kv_len=[70, 1, 333], seed=H)
+
+
+@pytest.mark.parametrize("layout", ["nhd", "hnd"])
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("Nq,G", [(2, 1), (5, 2), (3, 8), (17, 3), (40, 1), (129, 2)])
+def test_several_tokens(layout, causal, Nq, G):
+    kv = [Nq, Nq + 100, Nq + 1, Nq + 37]
+    go(B=4, H=2 * G, Hkv=2, D=128, Nq=Nq, page=32, kv_len=kv, q_len=[Nq, 1, Nq - 1, Nq], causal=causal, layout=layout,
+       seed=Nq)
+
+
+@pytest.mark.parametrize("prefix", [1, 16, 100, 128, 777])
+@pytest.mark.parametrize("B,Nq,G", [(1, 1, 1), (3, 1, 2), (5, 1, 8), (20, 1, 4), (4, 3, 2), (2, 30, 2), (70, 1, 8)])
+@pytest.mark.parametrize("D", [64, 128])
+def test_shared_prefix(prefix, B, Nq, G, D):
+    kv = [Nq + (37 * b) % 90 for b in range(B)]
+    go(B=B, H=2 * G, Hkv=2, D=D, Nq=Nq, page=16, kv_len=kv, prefix=prefix, seed=prefix + B)
+
+
+@pytest.mark.parametrize("prefix", [0, 50])
+@pytest.mark.parametrize("Nq", [1, 4, 40])
+@pytest.mark.parametrize("causal", [True, False])
+def test_rows_without_keys(prefix, Nq, causal):
+    """No own keys, no query rows, and (causal) fewer keys than query rows: rows that see nothing are zero."""
+    p = go(B=5, H=4, Hkv=2, D=64, Nq=Nq, page=16, q_len=[Nq, 0, Nq, Nq, 0], kv_len=[0, 5, max(Nq - 2, 0), Nq + 3, 0],
+           prefix=prefix, causal=causal, seed=Nq)
+    if prefix == 0:
+        o = P.run(p)
+        torch.cuda.synchronize()
+        assert int(o[0].count_nonzero()) == 0
+
+
+def test_everything_empty():
+    go(B=2, H=2, Hkv=2, D=128, Nq=3, page=16, q_len=[0, 0], kv_len=[0, 0])
+    go(B=2, H=2, Hkv=2, D=128, Nq=3, page=16, q_len=[3, 1], kv_len=[0, 0])
+
+
+@pytest.mark.parametrize("causal", [True, False])
+def test_lengths_left_out_and_out_of_range(causal):
+    """None means all; what is out of range is clamped."""
+    G.ensure_built()
+    page, W, N = 16, 5, 3
+    p = P.make(B=2, H=4, Hkv=2, D=64, Nq=N, page=page, kv_len=[W * page] * 2, prefix=2 * page, causal=causal,
+               table_pad=0, seed=3)
+    ref = P.run(p)
+    o = torch.full_like(ref, 7.0)
+    cache = S.PageCache(p.cache_k, p.cache_v)
+    ws = S.alloc_paged_workspace(2, 4, 2, N, 64)
+    S.sage_attn_paged(p.q, o, cache, p.table, ws, prefix_table=p.prefix_table, causal=causal)
+    P.check(p, o)
+    assert torch.equal(o, ref)
+    far = torch.tensor([1 << 30, W * page + 1], dtype=torch.int32, device="cuda")
+    o2 = torch.full_like(ref, 7.0)
+    S.sage_attn_paged(p.q, o2, cache, p.table, ws, q_len=far, kv_len=far, prefix_table=p.prefix_table,
+                      prefix_len=far[:1], causal=causal)
+    torch.cuda.synchronize()
+    assert torch.equal(o2, ref)
+    neg = torch.tensor([-1, -2], dtype=torch.int32, device="cuda")
+    o3 = torch.full_like(ref, 7.0)
+    S.sage_attn_paged(p.q, o3, cache, p.table, ws, kv_len=neg, prefix_table=p.prefix_table, prefix_len=neg[:1],
+                      causal=causal)
+    torch.cuda.synchronize()
+    assert int(o3.count_nonzero()) == 0
+
+
+@pytest.mark.parametrize("Nq,H", [(1, 8), (1, 128), (60, 8)])
+def test_prefix_without_own_table(Nq, H):
+    G.ensure_built()
+    p = P.make(B=6, H=H, Hkv=4, D=128, Nq=Nq, page=32, kv_len=[0] * 6, prefix=300, seed=5)
+    p.table = None
+    P.check(p, P.run(p))
+
+
+@pytest.mark.parametrize("scale,sm_scale", [(30.0, 0.0), (1.0, 2.0), (0.01, 0.0), (1.0, 1e-6)])
+@pytest.mark.parametrize("Nq", [1, 64])
+def test_sharp_and_flat_softmax(scale, sm_scale, Nq):
+    go(B=2, H=8, Hkv=2, D=128, Nq=Nq, page=16, kv_len=[Nq + 300, Nq + 41], prefix=77, scale=scale, sm_scale=sm_scale,
+       seed=11)
+
+
+@pytest.mark.parametrize("poison", [float("inf"), -float("inf"), 3e38])
+def test_other_values_behind_the_lengths(poison):
+    go(B=3, H=4, Hkv=2, D=64, Nq=1, page=128, kv_len=[5, 129, 300], prefix=130, poison=poison, seed=12)
+    go(B=3, H=4, Hkv=2, D=128, Nq=70, page=128, kv_len=[75, 129, 300], prefix=130, poison=poison, seed=13)
+
+
+@pytest.mark.parametrize("B,H,Hkv,D,Nq,n,prefix", [
+    (1, 4, 2, 128, 1, 40000, 0), (2, 8, 1, 64, 1, 20000, 9000), (40, 8, 2, 128, 1, 1500, 5000),
+    (1, 2, 1, 128, 700, 3000, 2000), (3, 6, 2, 64, 300, 900, 0), (16, 8, 2, 128, 4, 300, 3000)])
+def test_long_and_many(B, H, Hkv, D, Nq, n, prefix):
+    kv = [max(Nq, n - 313 * b % n) for b in range(B)]
+    go(B=B, H=H, Hkv=Hkv, D=D, Nq=Nq, page=64, kv_len=kv, prefix=prefix, seed=n)
+
+
+@pytest.mark.parametrize("Nq,prefix", [(1, 0), (1, 500), (100, 500)])
+def test_strided_views(Nq, prefix):
+    """q inside a fused projection, o inside a wider buffer, table rows apart."""
+    G.ensure_built()
+    B, H, Hkv, D = 4, 8, 2, 64
+    p = P.make(B=B, H=H, Hkv=Hkv, D=D, Nq=Nq, page=16, kv_len=[Nq + 9, Nq, Nq + 200, Nq + 31], prefix=prefix, seed=21)
+    fused = torch.zeros((B, Nq, H + 2 * Hkv, D), dtype=torch.bfloat16, device="cuda")
+    fused[:, :, :H] = p.q.permute(0, 2, 1, 3)
+    p.q = fused[:, :, :H].permute(0, 2, 1, 3)
+    wide = torch.full((B, p.table.shape[1] + 5), 1 << 30, dtype=torch.int32, device="cuda")
+    wide[:, :p.table.shape[1]] = p.table
+    p.table = wide[:, :p.table.shape[1]]
+    buf = torch.full((B, H, Nq + 2, D + 8), 7.0, dtype=torch.bfloat16, device="cuda")
+    P.check(p, P.run(p, o=buf[:, :, 1:Nq + 1, :D]))
+    assert bool((buf[:, :, 0] == 7).all()) and bool((buf[:, :, -1] == 7).all()) and bool((buf[..., D:] == 7).all())
+
+
+@pytest.mark.parametrize("Nq,H,prefix", [(1, 4, 0), (1, 4, 100), (90, 4, 0), (1, 128, 100)])
+def test_a_page_outside_the_cache_reads_as_zeros_and_is_reported(Nq, H, prefix):
+    G.ensure_built()
+    p = P.make(B=2, H=H, Hkv=2, D=128, Nq=Nq, page=16, kv_len=[Nq + 100, Nq + 60], prefix=prefix, poison=0.0, seed=31)
+    zero = p.cache_k.shape[0]                              # a page of zeros, added to the definition's cache only
+    good = P.Paged(**{**p.__dict__})
+    good.cache_k = torch.cat((p.cache_k, torch.zeros_like(p.cache_k[:1])))
+    good.cache_v = torch.cat((p.cache_v, torch.zeros_like(p.cache_v[:1])))
+    for bad in (zero, -1, 2 ** 31 - 1, -2 ** 31):
+        p.table[1, 2] = bad
+        good.table = p.table.clone()
+        good.table[1, 2] = zero
+        if prefix:
+            p.prefix_table[3] = bad
+            good.prefix_table = p.prefix_table.clone()
+            good.prefix_table[3] = zero
+        o = P.run(p)
+        torch.cuda.synchronize()
+        assert S.sage_get_device_status() == S.SAGE_ERR_PAGE
+        P.check(good, o)
+
+
+@pytest.mark.parametrize("B,H,Hkv,Nq,n,prefix", [(8, 8, 2, 1, 3000, 0), (40, 8, 2, 1, 500, 3000), (2, 4, 2, 200, 2000, 700)])
+def test_equal_inputs_give_equal_bits(B, H, Hkv, Nq, n, prefix):
+    G.ensure_built()
+    p = P.make(B=B, H=H, Hkv=Hkv, D=128, Nq=Nq, page=32, kv_len=[Nq + max(0, n - 71 * b) for b in range(B)], prefix=prefix,
+               seed=41)
+    first = P.run(p).clone()
+    ws = S.alloc_paged_workspace(B, H, Hkv, Nq, 128)
+    for fill in (0, 0x7F, 0xFF):                           # whatever the workspace held
+        ws.fill_(fill)
+        assert torch.equal(P.run(p, workspace=ws), first)
+
+
+@pytest.mark.parametrize("Nq,prefix", [(1, 0), (1, 700), (130, 700)])
+def test_captured_and_replayed_with_growing_lengths(Nq, prefix):
+    """One graph, captured once, serves every later length: the lengths are read on the device."""
+    G.ensure_built()
+    B, H, Hkv, D = 3, 8, 2, 128
+    long = [Nq + 400, Nq + 17, Nq + 250]
+    p = P.make(B=B, H=H, Hkv=Hkv, D=D, Nq=Nq, page=16, kv_len=long, prefix=prefix, seed=51)
+    cache = S.PageCache(p.cache_k, p.cache_v)
+    ws = S.alloc_paged_workspace(B, H, Hkv, Nq, D)
+    o = torch.zeros((B, Nq, H, D), dtype=torch.bfloat16, device="cuda").permute(0, 2, 1, 3)
+    q_len = torch.tensor([Nq] * B, dtype=torch.int32, device="cuda")
+    kv_len = torch.tensor(long, dtype=torch.int32, device="cuda")
+    plen = torch.tensor([prefix], dtype=torch.int32, device="cuda") if prefix else None
+
+    def call():
+        S.sage_attn_paged(p.q, o, cache, p.table, ws, q_len=q_len, kv_len=kv_len, prefix_table=p.prefix_table,
+                          prefix_len=plen)
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        call()
+    torch.cuda.current_stream().wait_stream(side)
+    graphs = [torch.cuda.CUDAGraph() for _ in range(2)]    # two graphs over one workspace, replayed in order
+    for g in graphs:
+        with torch.cuda.graph(g):
+            call()
+    for k, lens in enumerate(([Nq, Nq, Nq], [Nq + 400, Nq + 3, Nq + 99], long)):
+        kv_len.copy_(torch.tensor(lens, dtype=torch.int32))
+        o.fill_(7.0)
+        graphs[k % 2].replay()
+        p.kv_len = lens
+        P.check(p, o)
+        graphs[1 - k % 2].replay()
+        P.check(p, o)
+
+
+def test_two_streams_with_their_own_workspaces():
+    G.ensure_built()
+    ps = [P.make(B=6, H=8, Hkv=2, D=128, Nq=1, page=16, kv_len=[900 - 100 * b for b in range(6)], prefix=pre, seed=61 + pre)
+          for pre in (0, 400)]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in ps]
+    wss = [S.alloc_paged_workspace(6, 8, 2, 1, 128) for _ in ps]
+    outs = [torch.full((6, 1, 8, 128), 7.0, dtype=torch.bfloat16, device="cuda").permute(0, 2, 1, 3) for _ in ps]
+    lens = [torch.tensor(p.kv_len, dtype=torch.int32, device="cuda") for p in ps]
+    pl = torch.tensor([400], dtype=torch.int32, device="cuda")
+    caches = [S.PageCache(p.cache_k, p.cache_v) for p in ps]
+    torch.cuda.synchronize()
+    for _ in range(10):
+        for p, s, ws, o, n, c in zip(ps, streams, wss, outs, lens, caches):
+            S.sage_attn_paged(p.q, o, c, p.table, ws, kv_len=n, prefix_table=p.prefix_table,
+                              prefix_len=pl if p.prefix_table is not None else None, stream=s)
+    for p, o in zip(ps, outs):
+        P.check(p, o)
+
+
+def test_cache_offsets_behind_two_to_the_32_elements():
+    G.ensure_built()
+    heads, D, page = 32, 128, 128
+    pages = 2 ** 32 // (heads * D * page) + 4
+    k = torch.zeros((pages, page, heads, D), dtype=torch.bfloat16, device="cuda").permute(0, 2, 1, 3)
+    v = torch.zeros((pages, page, heads, D), dtype=torch.bfloat16, device="cuda").permute(0, 2, 1, 3)
+    g = torch.Generator(device="cuda").manual_seed(5)
+    for Nq in (1, 40):
+        n = [Nq + 200, Nq + 90]
+        last = torch.tensor([[pages - 1, pages - 3, pages - 2], [0, pages - 4, 5]], dtype=torch.int32, device="cuda")
+        for pg in last.unique().tolist():
+            k[pg] = torch.randn((heads, page, D), device="cuda", generator=g).to(torch.bfloat16)
+            v[pg] = torch.randn((heads, page, D), device="cuda", generator=g).to(torch.bfloat16)
+        q = torch.randn((2, heads, Nq, D), device="cuda", generator=g).to(torch.bfloat16)
+        p = P.Paged(q, k, v, last, [Nq, Nq], n, None, 0, True)
+        P.check(p, P.run(p))
+
+
+def test_convenience_call_and_launch_count():
+    G.ensure_built()
+    p = P.make(B=2, H=4, Hkv=2, D=64, Nq=2, page=16, kv_len=[50, 3], seed=71)
+    kv = torch.tensor(p.kv_len, dtype=torch.int32, device="cuda")
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    o = S.attention_paged(p.q, S.PageCache(p.cache_k, p.cache_v), p.table, kv_len=kv, stream=s)
+    s.synchronize()
+    assert 1 <= S.sage_last_launch_count() <= 3
+    P.check(p, o)

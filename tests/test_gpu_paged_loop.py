@@ -1,0 +1,74 @@
+"""The page-cache operators together, as a serving loop runs them: prompts in
+pieces, then single tokens, the pages and slots of every step made on the GPU
+from the lengths, and every step's output against plain attention over the
+tokens so far."""
+import math
+import random
+
+import pytest
+import torch
+
+import quantized_exact_attention_gb300 as S
+from tests import gpu_support as G
+from tests import paged_support as P
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("B,H,Hkv,D,page,prefix", [(3, 8, 2, 128, 16, 0), (5, 4, 4, 64, 32, 75), (12, 16, 2, 128, 64, 200)])
+def test_serving_loop(B, H, Hkv, D, page, prefix):
+    G.ensure_built()
+    r = random.Random(B)
+    g = torch.Generator(device="cuda").manual_seed(B)
+    pieces = [[r.choice((0, 1, 17, 70)) for _ in range(B)] for _ in range(3)] + [[r.choice((0, 1)) for _ in range(B)]
+                                                                                 for _ in range(6)]
+    longest = sum(max(p) for p in pieces)
+    W = -(-longest // page)
+    n_pages = B * W + -(-prefix // page) + 5
+    cache = S.alloc_page_cache(n_pages, page, Hkv, D)
+    cache.k.fill_(float("nan"))
+    cache.v.fill_(float("nan"))
+    order = torch.randperm(n_pages, generator=torch.Generator().manual_seed(1)).to(torch.int32).cuda()
+    randn = lambda *s: torch.randn(s, device="cuda", generator=g).to(torch.bfloat16)  # noqa: E731
+    i32 = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")  # noqa: E731
+
+    ptable, plen, used = None, None, 0
+    pk = pv = torch.empty((0, Hkv, D), dtype=torch.bfloat16, device="cuda")
+    if prefix:                                             # the shared prompt: one request's tables, kept as the prefix
+        t = torch.empty((1, -(-prefix // page)), dtype=torch.int32, device="cuda")
+        s = torch.empty((1, prefix), dtype=torch.int32, device="cuda")
+        taken = S.sage_page_tables(i32([prefix]), page, order, t, s)
+        pk, pv = randn(prefix, Hkv, D), randn(prefix, Hkv, D)
+        S.sage_cache_append(pk[None].transpose(1, 2), pv[None].transpose(1, 2), s, cache)
+        ptable, plen, used = t[0], i32([prefix]), int(taken)
+    table = torch.empty((B, W), dtype=torch.int32, device="cuda")
+    have = [0] * B
+    ks, vs = ([torch.empty((0, Hkv, D), dtype=torch.bfloat16, device="cuda")] * B for _ in range(2))
+    for new in pieces:
+        N = max(max(new), 1)
+        slots = torch.empty((B, N), dtype=torch.int32, device="cuda")
+        old, have = have, [a + n for a, n in zip(have, new)]
+        taken = S.sage_page_tables(i32(have), page, order[used:], table, slots, old_len=i32(old))
+        q, k, v = randn(B, H, N, D), randn(B, Hkv, N, D), randn(B, Hkv, N, D)
+        S.sage_cache_append(k, v, slots, cache)
+        o = S.attention_paged(q, cache, table, q_len=i32(new), kv_len=i32(have), prefix_table=ptable, prefix_len=plen)
+        torch.cuda.synchronize()
+        used += int(taken)
+        assert S.sage_get_device_status() == S.SAGE_OK
+        ks = [torch.cat((a, k[b, :, :n].transpose(0, 1))) for b, (a, n) in enumerate(zip(ks, new))]
+        vs = [torch.cat((a, v[b, :, :n].transpose(0, 1))) for b, (a, n) in enumerate(zip(vs, new))]
+        for b, n in enumerate(new):
+            assert int(o[b, :, n:].count_nonzero()) == 0
+            kk = torch.cat((pk, ks[b])).double().repeat_interleave(H // Hkv, 1).transpose(0, 1)
+            vv = torch.cat((pv, vs[b])).double().repeat_interleave(H // Hkv, 1).transpose(0, 1)
+            L = kk.shape[1]
+            if n == 0:
+                continue
+            s = q[b, :, :n].double() @ kk.transpose(1, 2) / math.sqrt(D)
+            i, j = torch.arange(n, device="cuda")[:, None], torch.arange(L, device="cuda")[None]
+            w = torch.softmax(s.masked_fill(j > i + (L - n), -math.inf), -1)
+            want, size = w @ vv, w @ vv.abs()
+            # output rounding, weight rounding, and 2^-11 for the FP32 scores (|s| stays below 2^4 here)
+            tol = P.U_BF16 * want.abs() + (P.U_BF16 * 1.01 + 2.0 ** -11) * size
+            assert bool(((o[b, :, :n].double() - want).abs() <= tol).all())
+    assert used <= n_pages
