@@ -8,6 +8,7 @@
 
 #include "sage_gb300.h"
 #include "sage_internal.h"
+#include "sage_paged.h"
 
 namespace sage {
 
@@ -124,6 +125,28 @@ int* device_status_ptr() {
 }
 
 void set_last_launch_count(int n) { g_last_launches = n; }
+
+int take_fault_mode() {
+    const int mode = fault_mode_for_next_launch;
+    fault_mode_for_next_launch = 0;
+    return mode;
+}
+
+int encode_pages(CUtensorMap* m, const sage_tensor& t, int D, int page, int heads, int pages) {
+    EncodeTiledFn fn = encode_fn();
+    if (!fn) return SAGE_ERR_DRIVER;
+    cuuint64_t dims[4] = {(cuuint64_t)D, (cuuint64_t)page, (cuuint64_t)heads, (cuuint64_t)pages};
+    // the stride of an axis of one entry is never used; any legal value does
+    cuuint64_t strides[3] = {(cuuint64_t)t.stride_n * 2, heads > 1 ? (cuuint64_t)t.stride_h * 2 : (cuuint64_t)D * 2,
+                             pages > 1 ? (cuuint64_t)t.stride_b * 2 : (cuuint64_t)D * 2};
+    cuuint32_t box[4] = {64, (cuuint32_t)page, 1, 1};
+    cuuint32_t estr[4] = {1, 1, 1, 1};
+    return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(t.ptr), dims, strides, box, estr,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
+               ? SAGE_OK
+               : SAGE_ERR_UNSUPPORTED;
+}
 
 }  // namespace sage
 

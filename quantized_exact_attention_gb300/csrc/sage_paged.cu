@@ -357,23 +357,28 @@ __global__ void __launch_bounds__(256) paged_join_kernel(const PagedParams p) {
         const RowParts own = parts_of(at, s.item_tiles(n, len, rt), per, p.pre_rt * p.Hkv + (b * p.Hkv + h) * p.rt + rt);
         RowParts pre{0, 0};
         int pr = 0;
-        if (p.pre_rt > 0) {
+        if (p.pre_items_rt > 0) {
             const int rr = (b * p.Nq + i) * p.G + g;
-            const int it = h * p.pre_rt + rr / M;
-            pr = rr % M;
-            pre = parts_of(it * s.pre_tiles(), s.pre_tiles(), per, it);
+            const int it = h * p.pre_items_rt + rr / p.pre_m;
+            const int nt = (s.lp + p.pre_tk - 1) / p.pre_tk;
+            pr = rr % p.pre_m;
+            // alone in its list, or at the front of this one
+            const int pre_per = p.pre_rt > 0 ? per : max(1, (p.Hkv * p.pre_items_rt * nt + p.pre_workers - 1) / p.pre_workers);
+            pre = parts_of(it * nt, nt, pre_per, it);
         }
         const int parts = own.n + pre.n;
 #pragma unroll 4
         for (int x = sub; x < parts; x += WPR) {
-            const int64_t q = x < pre.n ? (pre.slot0 + x) * M + pr : (own.slot0 + (x - pre.n)) * M + r % M;
-            const float2 ml = __ldcg(p.part_ml + q);
+            const bool from_pre = x < pre.n;
+            const int64_t q = from_pre ? (pre.slot0 + x) * p.pre_m + pr : (own.slot0 + (x - pre.n)) * M + r % M;
+            const float2 ml = __ldcg((from_pre ? p.pre_ml : p.part_ml) + q);
+            const float* po = (from_pre ? p.pre_o : p.part_o) + q * D;
             float w[V];
             if (V == 4) {
-                const float4 t = __ldcg(reinterpret_cast<const float4*>(p.part_o + q * D) + lane);
+                const float4 t = __ldcg(reinterpret_cast<const float4*>(po) + lane);
                 w[0] = t.x; w[1] = t.y; w[V - 2] = t.z; w[V - 1] = t.w;
             } else {
-                const float2 t = __ldcg(reinterpret_cast<const float2*>(p.part_o + q * D) + lane);
+                const float2 t = __ldcg(reinterpret_cast<const float2*>(po) + lane);
                 w[0] = t.x; w[1] = t.y;
             }
             const float mn = fmaxf(m, ml.x);
@@ -416,34 +421,69 @@ __global__ void __launch_bounds__(256) paged_join_kernel(const PagedParams p) {
 }
 
 // ---------------------------------------------------------------------------
-// Host side: which rows go together.
+// Host side: which kernel reads which keys for which rows.
+//
+// A request brings rows = Nq * G query rows to a key head.
+//  - rows > 32: the many-rows kernel, each request's keys behind the prefix
+//    (one list; the prefix is read again for every request, mostly from L2).
+//  - rows <= 32: the few-rows kernel for the own keys.  The prefix, when
+//    several requests share it, is read once for all their rows: by the
+//    few-rows kernel in the same list when all rows together are 32 or
+//    fewer, else by the many-rows kernel in a list of its own.
 // ---------------------------------------------------------------------------
-struct Plan {
-    int nr;                              // 8-row groups of an item: 1, 2 or 4
-    int M, rt, pre_rt, join;
-    int64_t items, slots;
+constexpr int kFewRows = 32;
+
+struct Lists {
+    // the list with the own keys
+    bool tiles;                          // many-rows kernel
+    bool split;                          // ... in its form for 128 rows
+    int nr;                              // few-rows kernel: 8-row groups of an item
+    int M, rt, join;
+    int pre_rt;                          // shared prefix items in this list
+    int64_t slots;
+    // the prefix's own list (many-rows kernel)
+    bool pre;
+    bool pre_split;
+    int pre_M, pre_items_rt;
+    int64_t pre_slots;
 };
 
-Plan make_plan(int B, int Hkv, int G, int Nq, bool prefix) {
-    Plan x{};
-    const int64_t rows = (int64_t)Nq * G;
-    // One pass over the prefix for all requests' rows pays when the rows of
-    // one request leave a row tile partly empty.
-    const bool shared = prefix && B > 1 && rows < 32;
-    const int64_t most = shared ? rows * B : rows;
+Lists make_lists(int B, int Hkv, int G, int Nq, bool prefix) {
+    Lists x{};
+    const int64_t rows = (int64_t)Nq * G, all = rows * B;
+    if (rows > kFewRows) {
+        x.tiles = true;
+        x.split = rows <= 128;
+        x.M = x.split ? 128 : 256;
+        x.rt = (int)ceil_div(rows, x.M);
+        x.join = prefix;
+        x.slots = 2 * kMaxTileWorkers;
+        return x;
+    }
+    const bool shared = prefix && B > 1;
+    const int64_t most = shared && all <= kFewRows ? all : rows;
     x.nr = most <= 8 ? 1 : (most <= 16 ? 2 : 4);
     x.M = 8 * x.nr;
     x.rt = (int)ceil_div(rows, x.M);
-    x.pre_rt = shared ? (int)ceil_div(rows * B, x.M) : 0;
     x.join = prefix && !shared;
-    x.items = (int64_t)Hkv * x.pre_rt + (int64_t)B * Hkv * x.rt;
-    x.slots = x.items + kMaxRowWorkers;
+    x.slots = (int64_t)B * Hkv * x.rt + kMaxRowWorkers;
+    if (shared && all <= kFewRows) {
+        x.pre_rt = x.pre_items_rt = (int)ceil_div(all, x.M);
+        x.pre_M = x.M;
+        x.slots += (int64_t)Hkv * x.pre_rt;
+    } else if (shared) {
+        x.pre = true;
+        x.pre_split = all <= 128;
+        x.pre_M = x.pre_split ? 128 : 256;
+        x.pre_items_rt = (int)ceil_div(all, x.pre_M);
+        x.pre_slots = (int64_t)Hkv * x.pre_items_rt + kMaxTileWorkers;
+    }
     return x;
 }
 
-size_t plan_bytes(const Plan& x, int B, int D) {
-    const size_t o = (size_t)x.slots * x.M * D * 4, ml = (size_t)x.slots * x.M * 8;
-    return o + ml + (((size_t)B + 1) * 4 + 15) / 16 * 16;
+size_t slot_bytes(int64_t slots, int M, int D) { return (size_t)slots * M * (D * 4 + 8); }
+size_t lists_bytes(const Lists& x, int B, int D) {
+    return slot_bytes(x.slots, x.M, D) + slot_bytes(x.pre_slots, x.pre_M, D) + (((size_t)B + 1) * 4 + 15) / 16 * 16;
 }
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
@@ -473,19 +513,27 @@ int sm_count() {
 }
 
 template <int D, int NR>
-cudaError_t launch_rows(PagedParams& p, int sms, cudaStream_t s) {
+cudaError_t launch_rows(const PagedParams& p, cudaStream_t s) {
     using Sh = RowsShape<D>;
-    cudaError_t e = cudaFuncSetAttribute(paged_rows_kernel<D, NR>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         (int)Sh::kSmem);
-    if (e != cudaSuccess) return e;
-    const int ctas = std::min(2 * sms, kMaxRowWorkers / kRowWarps);
-    p.workers = ctas * kRowWarps;
-    paged_rows_kernel<D, NR><<<ctas, kRowWarps * 32, Sh::kSmem, s>>>(p);
+    static bool attr_set[64] = {};
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess || dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+    if (!attr_set[dev]) {
+        e = cudaFuncSetAttribute(paged_rows_kernel<D, NR>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Sh::kSmem);
+        if (e != cudaSuccess) return e;
+        attr_set[dev] = true;
+    }
+    paged_rows_kernel<D, NR><<<p.workers / kRowWarps, kRowWarps * 32, Sh::kSmem, s>>>(p);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
     const int64_t rows = (int64_t)p.B * p.H * p.Nq;
     if (rows <= 1024) paged_join_kernel<D, 8 * NR, kStep, 8><<<(unsigned)rows, 256, 0, s>>>(p);
     else paged_join_kernel<D, 8 * NR, kStep, 1><<<(unsigned)ceil_div(rows, 8), 256, 0, s>>>(p);
     return cudaGetLastError();
+}
+template <int D>
+cudaError_t launch_rows_d(const PagedParams& p, int nr, cudaStream_t s) {
+    return nr == 1 ? launch_rows<D, 1>(p, s) : (nr == 2 ? launch_rows<D, 2>(p, s) : launch_rows<D, 4>(p, s));
 }
 
 }  // namespace
@@ -499,8 +547,8 @@ int sage_paged_workspace(int B, int H, int Hkv, int Nq, int D, size_t* bytes) {
     if (bytes == nullptr) return SAGE_ERR_ARG;
     const int rc = check_batch(B, H, Hkv, Nq, D);
     if (rc != SAGE_OK) return rc;
-    const size_t a = plan_bytes(make_plan(B, Hkv, H / Hkv, Nq, false), B, D);
-    const size_t b = plan_bytes(make_plan(B, Hkv, H / Hkv, Nq, true), B, D);
+    const size_t a = lists_bytes(make_lists(B, Hkv, H / Hkv, Nq, false), B, D);
+    const size_t b = lists_bytes(make_lists(B, Hkv, H / Hkv, Nq, true), B, D);
     *bytes = a > b ? a : b;
     return SAGE_OK;
 }
@@ -517,23 +565,28 @@ int sage_attn_paged(const sage_tensor* q, const sage_tensor* o, const sage_page_
     if (table_width < 0 || prefix_width < 0 || (table_width > 0 && table == nullptr) ||
         (prefix_width > 0 && prefix_table == nullptr) || table_stride < 0)
         return SAGE_ERR_ARG;
-    if ((int64_t)table_width * cache->page_size > INT32_MAX - 128 ||
-        (int64_t)prefix_width * cache->page_size > INT32_MAX - 128)
-        return SAGE_ERR_UNSUPPORTED;
-    const int G = H / cache->heads;
-    const Plan plan = make_plan(B, cache->heads, G, Nq, prefix_width > 0);
-    const size_t need = plan_bytes(plan, B, D);
-    if (workspace == nullptr || !aligned16(workspace) || workspace_bytes < need) return SAGE_ERR_ARG;
+    const int64_t own_keys = (int64_t)table_width * cache->page_size;
+    const int64_t pre_keys = (int64_t)prefix_width * cache->page_size;
+    if (own_keys > INT32_MAX - 256 || pre_keys > INT32_MAX - 256) return SAGE_ERR_UNSUPPORTED;
+    const Lists x = make_lists(B, cache->heads, H / cache->heads, Nq, prefix_width > 0);
+    if (workspace == nullptr || !aligned16(workspace) || workspace_bytes < lists_bytes(x, B, D)) return SAGE_ERR_ARG;
     // list positions and slot numbers stay in int
-    const int64_t keys = ((int64_t)table_width + (plan.join ? prefix_width : 0)) * cache->page_size;
-    const int64_t tiles = (int64_t)B * cache->heads * plan.rt * (keys / kStep + 2) +
-                          (int64_t)cache->heads * plan.pre_rt * ((int64_t)prefix_width * cache->page_size / kStep + 1);
-    if (tiles > INT32_MAX / 2 || plan.slots > INT32_MAX / 2) return SAGE_ERR_UNSUPPORTED;
+    const int tk = x.tiles ? 128 : kStep;
+    const int64_t tiles = (int64_t)B * cache->heads * x.rt * ((own_keys + (x.join ? pre_keys : 0)) / tk + 2) +
+                          (int64_t)cache->heads * x.pre_items_rt * (pre_keys / tk + 2);
+    if (tiles > INT32_MAX / 2 || x.slots + x.pre_slots > INT32_MAX / 2) return SAGE_ERR_UNSUPPORTED;
 
     PagedParams p{};
     p.status = device_status_ptr();
     const int sms = sm_count();
     if (p.status == nullptr || sms == 0) return SAGE_ERR_LAUNCH;
+    CUtensorMap mk, mv;
+    if (x.tiles || x.pre) {
+        if ((rc = encode_pages(&mk, cache->k, D, cache->page_size, cache->heads, cache->num_pages)) != SAGE_OK ||
+            (rc = encode_pages(&mv, cache->v, D, cache->page_size, cache->heads, cache->num_pages)) != SAGE_OK)
+            return rc;
+        p.fault_mode = take_fault_mode();
+    }
     p.q = static_cast<const uint16_t*>(q->ptr);
     p.o = static_cast<uint16_t*>(const_cast<void*>(o->ptr));
     p.k = static_cast<const uint16_t*>(cache->k.ptr);
@@ -544,30 +597,48 @@ int sage_attn_paged(const sage_tensor* q, const sage_tensor* o, const sage_page_
     p.vsp = cache->v.stride_b; p.vsh = cache->v.stride_h; p.vst = cache->v.stride_n;
     p.q_len = q_len; p.kv_len = kv_len; p.prefix_len = prefix_len;
     p.table = table; p.table_stride = table_stride; p.ptable = prefix_table;
-    p.B = B; p.H = H; p.Hkv = cache->heads; p.G = G; p.Nq = Nq;
+    p.B = B; p.H = H; p.Hkv = cache->heads; p.G = H / cache->heads; p.Nq = Nq;
     p.W = table_width; p.Wp = prefix_width;
     p.num_pages = cache->num_pages; p.page = cache->page_size;
     p.page_shift = 31 - __builtin_clz((unsigned)cache->page_size);
     p.causal = causal != 0;
     const double scale = sm_scale > 0.f ? (double)sm_scale : 1.0 / std::sqrt((double)D);
     p.sc = (float)(scale * (1.0 / std::log(2.0)));
-    p.rt = plan.rt; p.pre_rt = plan.pre_rt; p.join = plan.join;
+    p.rt = x.rt; p.pre_rt = x.pre_rt; p.join = x.join;
     char* w = static_cast<char*>(workspace);
-    p.part_o = reinterpret_cast<float*>(w);
-    w += (size_t)plan.slots * plan.M * D * 4;
-    p.part_ml = reinterpret_cast<float2*>(w);
-    w += (size_t)plan.slots * plan.M * 8;
+    auto take = [&](size_t n) { char* at = w; w += n; return at; };
+    p.part_o = reinterpret_cast<float*>(take((size_t)x.slots * x.M * D * 4));
+    p.part_ml = reinterpret_cast<float2*>(take((size_t)x.slots * x.M * 8));
+    p.pre_o = p.part_o;
+    p.pre_ml = p.part_ml;
+    if (x.pre) {
+        p.pre_o = reinterpret_cast<float*>(take((size_t)x.pre_slots * x.pre_M * D * 4));
+        p.pre_ml = reinterpret_cast<float2*>(take((size_t)x.pre_slots * x.pre_M * 8));
+    }
     p.start = reinterpret_cast<int32_t*>(w);
+    const int ctas = std::min(sms, kMaxTileWorkers);
+    p.pre_items_rt = x.pre_items_rt; p.pre_m = x.pre_M; p.pre_tk = x.pre ? 128 : kStep; p.pre_workers = ctas;
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
     cudaError_t e;
-    if (D == 64)
-        e = plan.nr == 1 ? launch_rows<64, 1>(p, sms, s)
-                         : (plan.nr == 2 ? launch_rows<64, 2>(p, sms, s) : launch_rows<64, 4>(p, sms, s));
-    else
-        e = plan.nr == 1 ? launch_rows<128, 1>(p, sms, s)
-                         : (plan.nr == 2 ? launch_rows<128, 2>(p, sms, s) : launch_rows<128, 4>(p, sms, s));
+    int launches = 0;
+    if (x.tiles) {
+        p.workers = ctas;
+        e = launch_paged_tiles(p, D, x.split, mk, mv, s);
+        launches = 2;
+    } else {
+        if (x.pre) {
+            PagedParams pp = p;
+            pp.part_o = p.pre_o; pp.part_ml = p.pre_ml; pp.start = nullptr;
+            pp.rt = 0; pp.pre_rt = x.pre_items_rt; pp.workers = ctas;
+            if (launch_paged_tiles(pp, D, x.pre_split, mk, mv, s) != cudaSuccess) return SAGE_ERR_LAUNCH;
+            ++launches;
+        }
+        p.workers = std::min(2 * sms, kMaxRowWorkers / kRowWarps) * kRowWarps;
+        e = D == 64 ? launch_rows_d<64>(p, x.nr, s) : launch_rows_d<128>(p, x.nr, s);
+        launches += 2;
+    }
     if (e != cudaSuccess) return SAGE_ERR_LAUNCH;
-    set_last_launch_count(2);
+    set_last_launch_count(launches);
     return SAGE_OK;
 }
 

@@ -12,6 +12,7 @@ namespace sage {
 
 constexpr int kErrPage = -7;             // SAGE_ERR_PAGE as the kernels record it
 constexpr int kMaxRowWorkers = 1280;     // warps of the few-rows kernel that take work (8 per SM, 160 SMs at most)
+constexpr int kMaxTileWorkers = 160;     // CTAs of the many-rows kernel (1 per SM)
 
 struct PagedParams {
     const uint16_t* q;                   // BF16 bit patterns
@@ -37,11 +38,27 @@ struct PagedParams {
     int pre_rt;                          // row tiles of all requests' rows against the prefix (0: not in this list)
     int join;                            // 1: a request's key sequence is the prefix followed by its own keys
     int workers;                         // workers the list is shared among
+    int fault_mode;                      // test hook: 0 = none
     // workspace
     float* part_o;                       // [slot][M][D]
     float2* part_ml;                     // [slot][M] running maximum (log2 domain) and sum
     int32_t* start;                      // [B + 1] list position of each request's first tile; [B] = total
+    // the list that holds the shared prefix's items, for the join
+    float* pre_o;
+    float2* pre_ml;
+    int pre_items_rt, pre_m, pre_tk, pre_workers;    // row tiles (0: none), rows of an item, keys of a tile, workers
 };
+
+// The many-rows kernel (sage_paged_tiles.cu): workers = CTAs; split: items of
+// at most 128 rows.  Writes whole rows unless the list holds shared prefix
+// items; then every result is partial.
+cudaError_t launch_paged_tiles(const PagedParams& p, int D, bool split, const CUtensorMap& tk, const CUtensorMap& tv,
+                               cudaStream_t s);
+
+// Tensor map over one tensor of a page cache, box: one page of one head, 64 channels (sage_api.cu).
+int encode_pages(CUtensorMap* m, const sage_tensor& t, int D, int page, int heads, int pages);
+// The fault the next launch has to make (test hook), taken once (sage_api.cu).
+int take_fault_mode();
 
 // Checks of a page cache's description that need no GPU (sage_tables.cu).
 int check_page_cache(const sage_page_cache* c);

@@ -28,6 +28,9 @@ __device__ __forceinline__ int paged_clamp(const int32_t* lens, int b, int n) {
 
 template <int M, int TK>
 struct PagedSched {
+    // The 128-key lists' worker writes whole rows itself, so rows that see no
+    // key have a tile too (with no visible key: zeros).
+    static constexpr bool kWholeRows = TK == 128;
     const PagedParams& p;
     int lp;                              // prefix length
     __device__ explicit PagedSched(const PagedParams& pp) : p(pp) {
@@ -47,7 +50,8 @@ struct PagedSched {
     }
     __device__ int item_tiles(int n, int len, int rt) const {
         if (rt * M >= n * p.G) return 0;
-        return (own_end(n, len, rt) + TK - 1) / TK + (p.join ? pre_tiles() : 0);
+        const int nt = (own_end(n, len, rt) + TK - 1) / TK + (p.join ? pre_tiles() : 0);
+        return kWholeRows ? max(nt, 1) : nt;
     }
     // tiles of one key head of request b
     __device__ int head_tiles(int b) const {

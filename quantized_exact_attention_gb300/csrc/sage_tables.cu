@@ -160,8 +160,16 @@ int check_page_cache(const sage_page_cache* c) {
     if (c == nullptr || c->num_pages <= 0 || c->heads <= 0 || c->heads > 65535) return SAGE_ERR_ARG;
     if ((c->D != 64 && c->D != 128) || !page_size_ok(c->page_size)) return SAGE_ERR_UNSUPPORTED;
     if ((int64_t)c->num_pages * c->page_size > INT32_MAX) return SAGE_ERR_UNSUPPORTED;
-    int rc = check_view(&c->k);
-    return rc != SAGE_OK ? rc : check_view(&c->v);
+    for (const sage_tensor* t : {&c->k, &c->v}) {
+        const int rc = check_view(t);
+        if (rc != SAGE_OK) return rc;
+        // rows apart (no broadcast axis), and byte strides that a tensor map holds
+        if (t->stride_n < c->D || (c->heads > 1 && t->stride_h < c->D) || (c->num_pages > 1 && t->stride_b < c->D))
+            return SAGE_ERR_UNSUPPORTED;
+        for (int64_t s : {t->stride_b, t->stride_h, t->stride_n})
+            if (s >= (int64_t(1) << 38)) return SAGE_ERR_UNSUPPORTED;
+    }
+    return SAGE_OK;
 }
 
 }  // namespace sage
