@@ -11,7 +11,7 @@
 //     tile; their results join in shared memory when the item ends.  It keeps
 //     two units in flight where there are only rows for one.
 //
-// Warp roles (320 threads):
+// Warp roles (384 threads):
 //   warps 0-3, 4-7  softmax of group 0 and 1, one thread per row: S from tensor
 //                   memory, mask, online maximum and sum, P in BF16 over the
 //                   columns of its S; at an item's ends Q into shared memory
@@ -19,8 +19,15 @@
 //   warp 8          TMA producer: the pages of a K and of a V tile through
 //                   rings of stages; it alone walks the list and leaves a note
 //                   for each tile
-//   warp 9          tensor-memory allocator and single-thread tcgen05 issuer
-// Tensor memory: S/P of group X at column 128 X, O of group X at 256 + 128 X.
+//   warp 9          tensor-memory allocator; one thread issues S = Q K^T
+//   warp 10         one thread issues O += P V
+//   warp 11         idle; it completes the warpgroup whose registers go to the
+//                   softmax (setmaxnreg: 2 x 128 x 224 + 128 x 56 = 384 x 168)
+// Tensor memory: O of group X in the top 2 D columns, P of group X beside its
+// S.  D = 128: [S 128 | P0 64 | P1 64 | O0 128 | O1 128], one S for both
+// groups: a group loads its scores into registers at once and frees it, so the
+// next scores are computed while both groups' exponentials run, and a group
+// never waits for its own P V.  D = 64: [S0 128 | S1 128 | P0 | P1 | O0 | O1].
 //
 // The reference of the exponentials follows the row maximum lazily: O is
 // rescaled only when the maximum has grown by more than 2^8 since the last
@@ -40,13 +47,13 @@
 namespace sage {
 namespace {
 
-constexpr int kTileThreads = 320;
+constexpr int kTileThreads = 384;
 constexpr int kWarpLoad = 8;
-constexpr int kWarpIssue = 9;
+constexpr int kWarpS = 9;
+constexpr int kWarpPV = 10;
 constexpr int kNotes = 8;
 constexpr float kLazy = 8.f;                              // log2 of the weights' bound
 constexpr uint32_t kBlk = 128 * 128;                      // 128 rows x 64 channels
-constexpr uint32_t TM_O = 256;
 
 enum TileRole { R_ROWS = 6, R_LOAD = 7, R_ISSUE = 8 };
 
@@ -67,13 +74,18 @@ struct TilesShape {
     static constexpr int kNB = D / 64;                    // 64-channel blocks of a row
     static constexpr uint32_t kTile = kNB * kBlk;         // bytes of a K (or V) tile
     static constexpr int kNS = D == 128 ? 2 : 4;          // K and V stages
+    static constexpr int kSBufs = D == 128 ? 1 : 2;       // S buffers in tensor memory
+    static constexpr uint32_t TM_P = 128 * kSBufs;        // + 64 X
+    static constexpr uint32_t TM_O = TM_P + 128;          // + D X
     static constexpr uint32_t OFF_Q = 0;                  // two groups' Q; split: one Q, later the join buffer
     static constexpr uint32_t OFF_K = 2 * kTile;
     static constexpr uint32_t OFF_V = OFF_K + kNS * kTile;
-    static constexpr uint32_t OFF_BAR = OFF_V + kNS * kTile;
+    static constexpr uint32_t OFF_STAGE = OFF_V + kNS * kTile;                    // split: rows on their way out
+    static constexpr uint32_t OFF_BAR = OFF_STAGE + (kSplit ? 4 * 4096 : 0);
     // barriers
-    static constexpr int B_Q = 0, B_ITEM = 1, B_JOIN = 2, B_ODONE = 3, B_DRAIN = 4, B_S = 5, B_P = 7;
-    static constexpr int B_KF = 9, B_KE = B_KF + kNS, B_VF = B_KE + kNS, B_VE = B_VF + kNS, B_NOTE = B_VE + kNS;
+    static constexpr int B_Q = 0, B_ITEM = 1, B_JOIN = 2, B_ODONE = 3, B_DRAIN = 4;
+    static constexpr int B_S = 6, B_SFREE = 8, B_P = 10, B_PV = 12;               // one of each per group
+    static constexpr int B_KF = 14, B_KE = B_KF + kNS, B_VF = B_KE + kNS, B_VE = B_VF + kNS, B_NOTE = B_VE + kNS;
     static constexpr int kBars = B_NOTE + kNotes;
     static constexpr uint32_t OFF_NOTE = OFF_BAR + (kBars * 8 + 15) / 16 * 16;
     static constexpr uint32_t OFF_ML = OFF_NOTE + kNotes * sizeof(TileNote);      // float2 [128]
@@ -99,28 +111,75 @@ __device__ __forceinline__ uint64_t sdesc_n_major(uint32_t saddr) {
     d |= static_cast<uint64_t>(2) << 61;
     return d;
 }
-// D[tmem] (+)= A[tmem] * B[smem], 16-bit inputs, FP32 accumulate.
-__device__ __forceinline__ void mma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
-                                           uint32_t accumulate) {
+// One elected lane of a converged warp issues; the operands are warp-uniform.
+// D[tmem] (+)= A[smem] * B[smem]^T, 16-bit inputs, FP32 accumulate.
+__device__ __forceinline__ void mma_ss_elect(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                             uint32_t accumulate) {
     asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}"
+        "{\n\t.reg .pred p, e;\n\tsetp.ne.b32 p, %4, 0;\n\telect.sync _|e, 0xffffffff;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}"
+        ::"r"(d_tmem), "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate) : "memory");
+}
+// D[tmem] (+)= A[tmem] * B[smem]
+__device__ __forceinline__ void mma_ts_elect(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
+                                             uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p, e;\n\tsetp.ne.b32 p, %4, 0;\n\telect.sync _|e, 0xffffffff;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}"
         ::"r"(d_tmem), "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate) : "memory");
 }
-// Whether the phase with the given parity is complete; never suspends.
-__device__ __forceinline__ bool mbar_test_wait(uint32_t bar, uint32_t parity) {
-    uint32_t ok;
+// The same lane is elected each time, so it is the thread that issued the products.
+__device__ __forceinline__ void commit_elect(uint32_t bar) {
     asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(ok) : "r"(bar), "r"(parity) : "memory");
-    return ok != 0;
+        "{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\t"
+        "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}"
+        ::"r"(bar) : "memory");
+}
+// The bounded wait of the hand-offs between softmax and issuers.  It polls with
+// test_wait, which never suspends the warp (a suspended try_wait adds its
+// wake-up to the hand-off), and looks at the clock only every 1,024 polls.
+// All 32 lanes call it together.
+__device__ __forceinline__ bool mbar_spin_warp(uint32_t bar, uint32_t parity, const volatile int* abort_flag) {
+    unsigned long long t0 = 0;
+    for (uint32_t i = 1;; ++i) {
+        uint32_t ok;
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+            "selp.u32 %0, 1, 0, p;\n\t}"
+            : "=r"(ok) : "r"(bar), "r"(parity) : "memory");
+        if (__all_sync(0xffffffffu, ok != 0)) return true;
+        if ((i & 1023u) == 0) {
+            if (__any_sync(0xffffffffu, *abort_flag != 0)) return false;
+            const unsigned long long now = globaltimer();
+            if (t0 == 0) t0 = now;
+            if (__any_sync(0xffffffffu, now - t0 > kWaitLimitNs)) return false;
+        }
+    }
 }
 __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
     uint32_t r;
     asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
     return r;
+}
+
+// Store kC 16-byte chunks of each lane's row (at base + at; at < 0: no row)
+// through 32 staged rows of 128 bytes.  All 32 lanes call it together.
+template <int kC, class T>
+__device__ __forceinline__ void stage_out(uint8_t* stage, const uint32_t (&o)[32], int64_t at, T* base, int lane) {
+#pragma unroll
+    for (int i = 0; i < kC; ++i)
+        *reinterpret_cast<uint4*>(stage + lane * 128 + ((i ^ (lane & 7)) << 4)) =
+            make_uint4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < kC; ++i) {
+        const int r = i * (32 / kC) + lane / kC, c = lane % kC;
+        const int64_t a = __shfl_sync(0xffffffffu, at, r);
+        const uint4 w = *reinterpret_cast<const uint4*>(stage + r * 128 + ((c ^ (r & 7)) << 4));
+        if (a >= 0) reinterpret_cast<uint4*>(base + a)[c] = w;
+    }
+    __syncwarp();
 }
 
 template <int D, bool kSplit>
@@ -163,16 +222,18 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
         mbar_init(bar(L::B_ITEM), 256);
         mbar_init(bar(L::B_JOIN), 128);
         mbar_init(bar(L::B_ODONE), 1);
-        mbar_init(bar(L::B_DRAIN), 1);
         for (int i = 0; i < 2; ++i) {
+            mbar_init(bar(L::B_DRAIN + i), 1);
             mbar_init(bar(L::B_S + i), 1);
-            mbar_init(bar(L::B_P + i), 128);
+            mbar_init(bar(L::B_SFREE + i), 4);            // one arrival a warp
+            mbar_init(bar(L::B_P + i), 4);
+            mbar_init(bar(L::B_PV + i), 1);
         }
         for (int i = 0; i < 4 * NS; ++i) mbar_init(bar(L::B_KF + i), 1);
         for (int i = 0; i < kNotes; ++i) mbar_init(bar(L::B_NOTE + i), 1);
         fence_mbar_init();
     }
-    if (warp == kWarpIssue) {
+    if (warp == kWarpS) {
         tmem_alloc(sbase + L::OFF_TMEM, 512);
         tmem_relinquish();
     }
@@ -187,18 +248,21 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
 
     if (warp < 8) {
         // ===================================================== softmax
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 224;");
         const int X = warp >> 2, row = threadIdx.x & 127;
         const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
-        const uint32_t tS = tmem + lane_base + 128u * X, tO = tmem + lane_base + TM_O + 128u * X;
+        const uint32_t tS = tmem + lane_base + (L::kSBufs == 2 ? 128u * X : 0u);
+        const uint32_t tP = tmem + lane_base + L::TM_P + 64u * X, tO = tmem + lane_base + L::TM_O + (uint32_t)D * X;
         float2* ml_s = reinterpret_cast<float2*>(sgen + L::OFF_ML);
         float m = -INFINITY, l = 0.f;                      // reference of the exponentials (log2 domain), sum
         bool fresh = true;                                // no tile of this item yet: O holds nothing
         bool valid = false, active = false;               // this row exists; some row of this warp does
         int rb = 0, ri = 0, rh = 0, lim_own = 0;
+        int64_t o_at = -1;                                // offset of this row's output, -1: none
         int units = 0, items = 0;
         bool ok = true;
         for (int t = 0; t < count && ok; ++t) {
-            if (!mbar_wait_warp(bar(L::B_NOTE + t % kNotes), (t / kNotes) & 1, abort_flag)) {
+            if (!mbar_spin_warp(bar(L::B_NOTE + t % kNotes), (t / kNotes) & 1, abort_flag)) {
                 if (lane == 0) fail(R_ROWS, t);
                 break;
             }
@@ -215,23 +279,35 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
                 lim_own = nt.len;
                 if (p.causal && nt.b >= 0) lim_own = min(nt.len, nt.len - nt.n + ri + 1);
                 m = -INFINITY; l = 0.f; fresh = true;
-                // Q rows in the K-major 128-byte swizzle; split: each group half of the channels
-                constexpr int kC = kSplit ? D / 16 : D / 8;
+                // Q in the K-major 128-byte swizzle.  A warp fetches its 32 rows with
+                // neighbouring lanes on neighbouring chunks of a row (one row a lane
+                // would touch 32 lines with each load); split: each group half of
+                // the channels.
+                constexpr int kC = kSplit ? D / 16 : D / 8;           // 16-byte chunks of a row
+                constexpr int kR = 32 / kC;                           // rows a load covers
+                constexpr int kQ = kC < 8 ? kC : 8;                   // loads in flight
                 const int c0 = kSplit ? X * kC : 0;
-                const uint16_t* qp = p.q + (valid ? rb * p.qsb + rh * p.qsh + ri * p.qsn : 0);
-                uint4 qv[kC];
-#pragma unroll
-                for (int c = 0; c < kC; ++c)
-                    qv[c] = valid ? __ldg(reinterpret_cast<const uint4*>(qp) + c0 + c) : make_uint4(0, 0, 0, 0);
+                const int64_t q_at = valid ? rb * p.qsb + rh * p.qsh + ri * p.qsn : -1;
+                o_at = valid ? rb * p.osb + rh * p.osh + ri * p.osn : -1;
                 if (!mbar_wait_warp(bar(L::B_ITEM), items & 1, abort_flag)) {
                     if (lane == 0) fail(R_ROWS, t);
                     break;
                 }
-                uint8_t* qs = sgen + L::OFF_Q + (kSplit ? 0 : X * L::kTile) + row * 128;
+                uint8_t* qs = sgen + L::OFF_Q + (kSplit ? 0 : X * L::kTile);
+#pragma unroll 1
+                for (int i0 = 0; i0 < kC; i0 += kQ) {
+                    uint4 qv[kQ];
 #pragma unroll
-                for (int c = 0; c < kC; ++c) {
-                    const int cc = c0 + c;
-                    *reinterpret_cast<uint4*>(qs + (cc >> 3) * kBlk + (((cc & 7) ^ (row & 7)) << 4)) = qv[c];
+                    for (int i = 0; i < kQ; ++i) {
+                        const int64_t at = __shfl_sync(0xffffffffu, q_at, (i0 + i) * kR + lane / kC);
+                        qv[i] = at >= 0 ? __ldg(reinterpret_cast<const uint4*>(p.q + at) + c0 + lane % kC)
+                                        : make_uint4(0, 0, 0, 0);
+                    }
+#pragma unroll
+                    for (int i = 0; i < kQ; ++i) {
+                        const int r = (warp & 3) * 32 + (i0 + i) * kR + lane / kC, c = c0 + lane % kC;
+                        *reinterpret_cast<uint4*>(qs + (c >> 3) * kBlk + r * 128 + (((c & 7) ^ (r & 7)) << 4)) = qv[i];
+                    }
                 }
                 fence_proxy_async_smem();
                 mbar_arrive(bar(L::B_Q));
@@ -240,71 +316,96 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
                 const int nkeys = nt.nkeys;
                 int lim = nkeys;
                 if (flags & N_OWN) lim = min(lim, lim_own - nt.key0);
-                if (!mbar_wait_warp(bar(L::B_S + X), units & 1, abort_flag)) {
+                if (!mbar_spin_warp(bar(L::B_S + X), units & 1, abort_flag)) {
                     if (lane == 0) fail(R_ROWS, t);
                     break;
                 }
-                ++units;
                 tc_fence_after();
+                // Keys that some row of this warp does not see: -inf over their scores
+                // in tensor memory.  This and the other seldom-run parts are rolled
+                // loops: what is run once for an item is fetched from far away, at
+                // about 100 cycles for 8 instructions.
+                if (active && !__all_sync(0xffffffffu, lim >= 128)) {
+#pragma unroll 1
+                    for (int c = 0; c < 128; c += 32) {
+                        if (__all_sync(0xffffffffu, lim >= c + 32)) continue;
+                        uint32_t w[32];
+                        tmem_ld32(tS + c, w);
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int i = 0; i < 32; ++i)
+                            if (c + i >= lim) w[i] = 0xFF800000u;
+                        tmem_st32(tS + c, w);
+                    }
+                    tmem_wait_st();
+                }
+                uint32_t s[4][32];
+                float mx0 = 0.f, mx1 = 0.f;
                 if (active) {
-                    uint32_t s[4][32];
-                    float mx0, mx1;
                     tmem_ld64_max(tS, s[0], s[1], mx0);
                     tmem_ld64_max(tS + 64, s[2], s[3], mx1);
                     tmem_wait_ld();
-                    float mx = fmaxf(mx0, mx1);
-                    if (!__all_sync(0xffffffffu, lim >= 128)) {
-                        mx = -INFINITY;
-#pragma unroll
-                        for (int a = 0; a < 4; ++a)
-#pragma unroll
-                            for (int i = 0; i < 32; ++i) {
-                                if (a * 32 + i >= lim) s[a][i] = 0xFF800000u;    // -inf
-                                mx = fmaxf(mx, __uint_as_float(s[a][i]));
-                            }
-                    }
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar(L::B_SFREE + X));
+                float f = 1.f;
+                bool rescale = false;
+                if (active) {
+                    const float mx = fmaxf(mx0, mx1);
                     const float mt = mx * p.sc;
                     const bool grow = mt > m + kLazy;      // also the first visible key: m = -inf
-                    if (__any_sync(0xffffffffu, grow)) {
-                        const float mn = grow ? mt : m;
-                        const float f = grow ? ex2_approx(m - mn) : 1.f;
+                    if (grow) {
+                        f = ex2_approx(m - mt);
                         l *= f;
-                        m = mn;
-                        if (!fresh) {
-                            // the products of this group's earlier tiles are done:
-                            // its scores were issued behind them
-#pragma unroll
-                            for (int c = 0; c < D / 32; ++c) {
-                                uint32_t o[32];
-                                tmem_ld32(tO + c * 32, o);
-                                tmem_wait_ld();
-#pragma unroll
-                                for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
-                                tmem_st32(tO + c * 32, o);
-                            }
-                        }
+                        m = mt;
                     }
                     const float neg = m == -INFINITY ? 0.f : -m;
-                    float l0 = 0.f, l1 = 0.f;
+                    float la[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-                    for (int a = 0; a < 2; ++a) {
-                        uint32_t w[32];
+                    for (int a = 0; a < 4; ++a)
 #pragma unroll
-                        for (int i = 0; i < 32; ++i) {
-                            const int b = a * 64 + 2 * i;
+                        for (int i = 0; i < 32; i += 2) {
                             float x0, x1;
-                            fma2_bc(x0, x1, __uint_as_float(s[b / 32][b % 32]), __uint_as_float(s[b / 32][b % 32 + 1]),
-                                    p.sc, neg);
+                            fma2_bc(x0, x1, __uint_as_float(s[a][i]), __uint_as_float(s[a][i + 1]), p.sc, neg);
                             x0 = ex2_approx(x0);
                             x1 = ex2_approx(x1);
-                            add2(l0, l1, x0, x1);
-                            w[i] = pack2(x0, x1);
+                            add2(la[i & 2], la[(i & 2) + 1], x0, x1);
+                            s[a][i / 2] = pack2(x0, x1);
                         }
-                        tmem_st32(tS + a * 32, w);
+                    l += (la[0] + la[1]) + (la[2] + la[3]);
+                    rescale = !fresh && __any_sync(0xffffffffu, grow);
+                }
+                // This group's product before is done: it has read P, and O may be
+                // rescaled.  Warps without rows wait too: an arrival for the next
+                // product before this one was issued would be lost.
+                if (units > 0 && !mbar_spin_warp(bar(L::B_PV + X), (units - 1) & 1, abort_flag)) {
+                    if (lane == 0) fail(R_ROWS, t);
+                    break;
+                }
+                tc_fence_after();
+                if (active) {
+                    if (rescale) {
+#pragma unroll 1
+                        for (int c = 0; c < D / 32; ++c) {
+                            uint32_t o[32];
+                            tmem_ld32(tO + c * 32, o);
+                            tmem_wait_ld();
+#pragma unroll
+                            for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+                            tmem_st32(tO + c * 32, o);
+                        }
                     }
-                    l += l0 + l1;
+#pragma unroll
+                    for (int a = 0; a < 4; ++a) {
+                        uint32_t w[16];
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) w[i] = s[a][i];
+                        tmem_st16(tP + a * 16, w);
+                    }
                     tmem_wait_st();
                 }
+                ++units;
                 fresh = false;
                 tc_fence_before();
                 // V rows behind the last key: whatever they hold times a weight
@@ -316,13 +417,14 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
                     }
                     if (row >= nkeys) {
                         uint8_t* vr = sgen + L::OFF_V + (t % NS) * L::kTile + row * 128;
-#pragma unroll
+#pragma unroll 1
                         for (int c = 0; c < D / 8; ++c)
                             *reinterpret_cast<uint4*>(vr + (c >> 3) * kBlk + ((c & 7) << 4)) = make_uint4(0, 0, 0, 0);
                     }
                     fence_proxy_async_smem();
                 }
-                mbar_arrive(bar(L::B_P + X));
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar(L::B_P + X));
             }
             if (flags & N_LAST) {
                 if (!mbar_wait_warp(bar(L::B_ODONE), items & 1, abort_flag)) {
@@ -337,7 +439,7 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
                     if (X == 1) {
                         ml_s[row] = make_float2(m, l);
                         if (active && !fresh) {
-#pragma unroll
+#pragma unroll 1
                             for (int c = 0; c < D / 32; ++c) {
                                 uint32_t o[32];
                                 tmem_ld32(tO + c * 32, o);
@@ -364,21 +466,20 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
                     }
                 }
                 if (active && (!kSplit || X == 0)) {
+                    // 32 channels at a time.  They leave through shared memory (Q's
+                    // place: its products are done), so that a store's lanes share
+                    // lines; a warp stages its own 32 rows.
                     const bool whole = (flags & N_WHOLE) != 0;
-                    const float inv = whole ? (l == 0.f ? 0.f : __fdiv_rn(1.f, l)) : 1.f;
-                    const int r = kSplit ? row : X * 128 + row;
-                    const int64_t slot_row = (int64_t)nt.slot * M + r;
-                    if (valid && !whole) p.part_ml[slot_row] = make_float2(m, l);
-                    uint16_t* dst = p.o + rb * p.osb + rh * p.osh + (int64_t)ri * p.osn;
-                    float* part = p.part_o + slot_row * D;
-#pragma unroll
+                    const float inv = l == 0.f ? 0.f : __fdiv_rn(1.f, l);
+                    const int64_t row0 = (int64_t)nt.slot * M + (kSplit ? 0 : X * 128) + (warp & 3) * 32;
+                    const int64_t at = whole ? o_at : (valid ? (row0 + lane) * D : -1);
+                    if (valid && !whole) p.part_ml[row0 + lane] = make_float2(m, l);
+                    uint8_t* stage = sgen + (kSplit ? L::OFF_STAGE : L::OFF_Q + X * L::kTile) + (warp & 3) * 4096;
+#pragma unroll 1
                     for (int c = 0; c < D / 32; ++c) {
                         uint32_t o[32];
                         tmem_ld32(tO + c * 32, o);
                         tmem_wait_ld();
-                        float x[32];
-#pragma unroll
-                        for (int i = 0; i < 32; ++i) x[i] = __uint_as_float(o[i]);
                         if constexpr (kSplit) {
                             // a group without a tile, or without a visible key, adds nothing
                             // (its O may hold anything)
@@ -387,32 +488,29 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
                                 const float4 y = *reinterpret_cast<const float4*>(jr + (((c * 8 + i) ^ (row & kSw)) << 4));
                                 const float yy[4] = {y.x, y.y, y.z, y.w};
 #pragma unroll
-                                for (int e = 0; e < 4; ++e)
-                                    x[4 * i + e] = (fa == 0.f ? 0.f : x[4 * i + e] * fa) + (fb == 0.f ? 0.f : yy[e] * fb);
+                                for (int e = 0; e < 4; ++e) {
+                                    const float z = __uint_as_float(o[4 * i + e]);
+                                    o[4 * i + e] = __float_as_uint((fa == 0.f ? 0.f : z * fa) + (fb == 0.f ? 0.f : yy[e] * fb));
+                                }
                             }
                         }
-                        if (valid && whole) {
+                        if (whole) {
 #pragma unroll
-                            for (int i = 0; i < 4; ++i) {
-                                uint32_t w[4];
-#pragma unroll
-                                for (int e = 0; e < 4; ++e) w[e] = pack2(x[8 * i + 2 * e] * inv, x[8 * i + 2 * e + 1] * inv);
-                                reinterpret_cast<uint4*>(dst)[c * 4 + i] = make_uint4(w[0], w[1], w[2], w[3]);
-                            }
-                        } else if (valid) {
-#pragma unroll
-                            for (int i = 0; i < 8; ++i)
-                                reinterpret_cast<float4*>(part)[c * 8 + i] =
-                                    make_float4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
+                            for (int i = 0; i < 16; ++i)
+                                o[i] = pack2(__uint_as_float(o[2 * i]) * inv, __uint_as_float(o[2 * i + 1]) * inv);
                         }
-                        __syncwarp();
+                        if (whole) stage_out<4>(stage, o, at, p.o + c * 32, lane);
+                        else stage_out<8>(stage, o, at, p.part_o + c * 32, lane);
                     }
                 }
                 tc_fence_before();
                 ++items;
             }
         }
-    } else if (warp == kWarpLoad) {
+    } else {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+    }
+    if (warp == kWarpLoad) {
         // ===================================================== TMA producer
         PagedPlace at = paged_find<M, 128, kTileThreads>(sched, chunk, t0);
         const int per_tile = 128 >> p.page_shift;         // pages of a whole tile
@@ -483,96 +581,87 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
             if (tk >= 0) mbar_wait_warp(bar(L::B_KF + tk % NS), (tk / NS) & 1, &zero);
             if (tv >= 0 && p.fault_mode != 1) mbar_wait_warp(bar(L::B_VF + tv % NS), (tv / NS) & 1, &zero);
         }
-    } else if (lane == 0) {
-        // ===================================================== MMA issuer
-        constexpr uint32_t kIdescQK = idesc_bf16(128, false);
-        constexpr uint32_t kIdescPV = idesc_bf16(D, true);
+    } else if (warp == kWarpS || warp == kWarpPV) {
+        // ===================================================== MMA issuers
+        // Issuing takes about 48 cycles of a thread per instruction and 45 per
+        // wait or commit: one thread for both products needs longer than the
+        // 1,024 cycles that a unit's products take.  The two touch different
+        // tensor memory, so each has a thread of its own.
         constexpr int kUnitsPerTile = kSplit ? 1 : 2;
-        const uint64_t dQ = sdesc_sw128(sbase + L::OFF_Q);
-        const uint64_t dK = sdesc_sw128(sbase + L::OFF_K);
-        const uint64_t dV = sdesc_n_major(sbase + L::OFF_V);
         const int U = count * kUnitsPerTile;
-        int s = 0, v = 0;                                 // next unit whose S, whose PV is issued
-        int noted = 0;                                    // tiles whose note has been read
-        uint32_t firsts = 0, lasts = 0;                   // their flags, bit tile % 32
-        int items = 0;                                    // items whose first S has been issued
-        uint32_t summed = 0;                              // bit X: group X has a product in this item
         bool ok = true;
-        unsigned long long since = 0;
-        uint32_t polls = 0;
-        while (v < U) {
-            bool moved = false;
-            // S of unit s: at most two units ahead (its columns hold the P of
-            // unit s - 2), and into a new item only when the item before it is
-            // through (its Q is overwritten, and its output read, after that).
-            if (s < U && s < v + 2) {
-                const int t = s / kUnitsPerTile, st = t % NS;
-                bool ready = true;
-                if (t == noted) {
-                    ready = mbar_test_wait(bar(L::B_KF + st), (t / NS) & 1);
-                    if (ready) {
-                        const int f = notes[t % kNotes].flags;
-                        firsts = (firsts & ~(1u << (t & 31))) | ((f & N_FIRST ? 1u : 0u) << (t & 31));
-                        lasts = (lasts & ~(1u << (t & 31))) | ((f & N_LAST ? 1u : 0u) << (t & 31));
-                        ++noted;
+        int u = 0;
+        if (warp == kWarpS) {
+            constexpr uint32_t kIdescQK = idesc_bf16(128, false);
+            const uint64_t dQ = sdesc_sw128(sbase + L::OFF_Q);
+            const uint64_t dK = sdesc_sw128(sbase + L::OFF_K);
+            int items = 0;
+            for (; u < U; ++u) {
+                const int t = u / kUnitsPerTile, st = t % NS, X = u & 1;
+                if (u % kUnitsPerTile == 0) {
+                    if (!mbar_spin_warp(bar(L::B_KF + st), (t / NS) & 1, abort_flag)) { ok = false; break; }
+                    // a new item's Q: written when the item before is through
+                    if (notes[t % kNotes].flags & N_FIRST) {
+                        if (!mbar_spin_warp(bar(L::B_Q), items & 1, abort_flag)) { ok = false; break; }
+                        ++items;
                     }
                 }
-                const bool opens = ready && ((firsts >> (t & 31)) & 1u) && s % kUnitsPerTile == 0;
-                if (opens) ready = v == s && mbar_test_wait(bar(L::B_Q), items & 1);
-                if (ready) {
-                    if (opens) ++items;
-                    const int X = s & 1;
-                    tc_fence_after();
-                    const uint64_t a = dQ + (uint64_t)((kSplit ? 0 : X * L::kTile) >> 4);
-                    const uint64_t b = dK + (uint64_t)((st * L::kTile) >> 4);
+                const int before = u - L::kSBufs;          // the unit that used the buffer last: its scores are in registers
+                if (before >= 0 && !mbar_spin_warp(bar(L::B_SFREE + (before & 1)), (before >> 1) & 1, abort_flag)) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+                const uint64_t a = dQ + (uint64_t)((kSplit ? 0 : X * L::kTile) >> 4);
+                const uint64_t b = dK + (uint64_t)((st * L::kTile) >> 4);
+                const uint32_t d = tmem + (L::kSBufs == 2 ? 128u * X : 0u);
 #pragma unroll
-                    for (int kk = 0; kk < D / 16; ++kk) {
-                        const uint32_t o = ((kk >> 2) * kBlk + (kk & 3) * 32) >> 4;
-                        mma_f16_ss(tmem + 128u * X, a + o, b + o, kIdescQK, kk > 0 ? 1u : 0u);
-                    }
-                    mma_commit(bar(L::B_S + X));
-                    if (s % kUnitsPerTile == kUnitsPerTile - 1) mma_commit(bar(L::B_KE + st));
-                    ++s;
-                    moved = true;
+                for (int kk = 0; kk < D / 16; ++kk) {
+                    const uint32_t o = ((kk >> 2) * kBlk + (kk & 3) * 32) >> 4;
+                    mma_ss_elect(d, a + o, b + o, kIdescQK, kk > 0 ? 1u : 0u);
                 }
+                commit_elect(bar(L::B_S + X));
+                if (u % kUnitsPerTile == kUnitsPerTile - 1) commit_elect(bar(L::B_KE + st));
             }
-            if (v < s) {
-                const int t = v / kUnitsPerTile, st = t % NS, X = v & 1;
-                if (mbar_test_wait(bar(L::B_P + X), (v >> 1) & 1) && mbar_test_wait(bar(L::B_VF + st), (t / NS) & 1)) {
-                    tc_fence_after();
-                    if (((firsts >> (t & 31)) & 1u) && v % kUnitsPerTile == 0) summed = 0;
-                    const uint64_t b = dV + (uint64_t)((st * L::kTile) >> 4);
+        } else {
+            constexpr uint32_t kIdescPV = idesc_bf16(D, true);
+            const uint64_t dV = sdesc_n_major(sbase + L::OFF_V);
+            uint32_t summed = 0;                          // bit X: group X has a product in this item
+            bool last = false;
+            for (; u < U; ++u) {
+                const int t = u / kUnitsPerTile, st = t % NS, X = u & 1;
+                if (u % kUnitsPerTile == 0) {
+                    if (!mbar_spin_warp(bar(L::B_VF + st), (t / NS) & 1, abort_flag)) { ok = false; break; }
+                    const int f = notes[t % kNotes].flags;
+                    if (f & N_FIRST) summed = 0;
+                    last = (f & N_LAST) != 0;
+                }
+                if (!mbar_spin_warp(bar(L::B_P + X), (u >> 1) & 1, abort_flag)) { ok = false; break; }
+                tc_fence_after();
+                const uint64_t b = dV + (uint64_t)((st * L::kTile) >> 4);
+                const uint32_t dO = tmem + L::TM_O + (uint32_t)D * X, aP = tmem + L::TM_P + 64u * X;
 #pragma unroll
-                    for (int kk = 0; kk < 8; ++kk)
-                        mma_f16_ts(tmem + TM_O + 128u * X, tmem + 128u * X + kk * 8, b + (uint64_t)(kk * (2048 >> 4)),
-                                   kIdescPV, kk > 0 || ((summed >> X) & 1u) ? 1u : 0u);
-                    summed |= 1u << X;
-                    if (v % kUnitsPerTile == kUnitsPerTile - 1) {
-                        mma_commit(bar(L::B_VE + st));
-                        if ((lasts >> (t & 31)) & 1u) mma_commit(bar(L::B_ODONE));
-                    }
-                    ++v;
-                    moved = true;
+                for (int kk = 0; kk < 8; ++kk)
+                    mma_ts_elect(dO, aP + kk * 8, b + (uint64_t)(kk * (2048 >> 4)), kIdescPV,
+                               kk > 0 || ((summed >> X) & 1u) ? 1u : 0u);
+                summed |= 1u << X;
+                commit_elect(bar(L::B_PV + X));
+                if (u % kUnitsPerTile == kUnitsPerTile - 1) {
+                    commit_elect(bar(L::B_VE + st));
+                    if (last) commit_elect(bar(L::B_ODONE));
                 }
-            }
-            if (moved) {
-                polls = 0;
-            } else if ((++polls & 63u) == 0) {
-                if (*abort_flag) { ok = false; break; }
-                const unsigned long long now = globaltimer();
-                if (polls == 64) since = now;
-                else if (now - since > kWaitLimitNs) { ok = false; break; }
             }
         }
-        if (!ok) fail(R_ISSUE, v);
-        mma_commit(bar(L::B_DRAIN));                       // all products done before teardown
+        if (!ok && lane == 0) fail(R_ISSUE, u);
+        const int drain = L::B_DRAIN + (warp == kWarpS ? 0 : 1);
+        commit_elect(bar(drain));                           // all products done before teardown
         const int zero = 0;
-        mbar_wait(bar(L::B_DRAIN), 0, &zero);
+        mbar_wait_warp(bar(drain), 0, &zero);
     }
 
     tc_fence_before();
     __syncthreads();
-    if (warp == kWarpIssue) {
+    if (warp == kWarpS) {
         __syncwarp();
         tc_fence_after();
         tmem_dealloc(tmem, 512);
