@@ -98,23 +98,24 @@ __global__ void __launch_bounds__(kRowWarps * 32, 2) paged_rows_kernel(const Pag
     constexpr int M = 8 * NR, S = Sh::kStages;
     constexpr int kRowsPerPass = 32 / Sh::kChunks;
     extern __shared__ __align__(128) uint8_t smem[];
-    __shared__ int chunk[kRowWarps * 32];
+    __shared__ int2 found[kRowWarps];
     __shared__ int warp_sums[kRowWarps];
     __shared__ StepNote notes[kRowWarps][S];
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const PagedSched<M, kStep> sched(p);
-    const int total = paged_scan<M, kStep, kRowWarps * 32>(sched, chunk, warp_sums, blockIdx.x == 0);
-    const int per = sched.per_worker(total);
     // workers next to each other in the list sit on different SMs: a CTA's
     // warps are a grid apart, so a short list still uses every SM
     const int worker = warp * gridDim.x + blockIdx.x;
+    const int total = paged_scan<M, kStep, kRowWarps * 32, kRowWarps>(sched, blockIdx.x, gridDim.x, found, warp_sums,
+                                                                      blockIdx.x == 0);
+    const int per = sched.per_worker(total);
     if ((int64_t)worker * per >= total || worker >= p.workers) return;
     const int t0 = worker * per;
     const int count = min(per, total - t0);
 
     const uint32_t ring = smem_u32(smem) + warp * S * Sh::kStage;
-    PagedPlace at = paged_find<M, kStep, kRowWarps * 32>(sched, chunk, t0);
+    PagedPlace at = paged_place(sched, found[warp], t0);
     int left = count;                                     // steps not yet fetched
     bool first = true;
     PagedSpan span{};
@@ -159,11 +160,6 @@ __global__ void __launch_bounds__(kRowWarps * 32, 2) paged_rows_kernel(const Pag
     };
 
     fetch();
-#pragma unroll
-    for (int s = 0; s < S - 1; ++s) {
-        if (left > 0) issue(s);
-        cp_async_commit();
-    }
 
     uint32_t qf[NR][D / 16][2];                           // Q^T fragments
     float o[NR][D / 16][4];                               // O^T: channels x query rows
@@ -228,18 +224,24 @@ __global__ void __launch_bounds__(kRowWarps * 32, 2) paged_rows_kernel(const Pag
         }
     };
 
-    for (int it = 0; it < count; ++it) {
-        const int stage = it % S;
+    // The ring is filled by the same loop (one copy of its code): S - 1 steps
+    // that only load.
+    int stage = 0, fill = 0;                              // stages to compute from and to load into
+#pragma unroll 1
+    for (int it = 1 - S; it < count; ++it) {
         cp_async_wait<S - 2>();
         __syncwarp();
         const StepNote nt = notes[warp][stage];
-        if (left > 0) issue((it + S - 1) % S);            // its stage was read in the step before
+        if (left > 0) issue(fill);                        // its stage was read in the step before
+        fill = fill + 1 == S ? 0 : fill + 1;
         cp_async_commit();
+        if (it < 0) continue;
         if (nt.first) {
             if (it > 0) leave();
             enter(nt);
         }
         const uint32_t kb = ring + stage * Sh::kStage, vb = kb + Sh::kTile;
+        stage = stage + 1 == S ? 0 : stage + 1;
         float sacc[NR][4];
 #pragma unroll
         for (int nr = 0; nr < NR; ++nr)
@@ -436,14 +438,14 @@ constexpr int kFewRows = 32;
 struct Lists {
     // the list with the own keys
     bool tiles;                          // many-rows kernel
-    bool split;                          // ... in its form for 128 rows
+    int groups;                          // ... 128-row groups of an item
     int nr;                              // few-rows kernel: 8-row groups of an item
     int M, rt, join;
     int pre_rt;                          // shared prefix items in this list
     int64_t slots;
     // the prefix's own list (many-rows kernel)
     bool pre;
-    bool pre_split;
+    int pre_groups;
     int pre_M, pre_items_rt;
     int64_t pre_slots;
 };
@@ -453,11 +455,11 @@ Lists make_lists(int B, int Hkv, int G, int Nq, bool prefix) {
     const int64_t rows = (int64_t)Nq * G, all = rows * B;
     if (rows > kFewRows) {
         x.tiles = true;
-        x.split = rows <= 128;
-        x.M = x.split ? 128 : 256;
+        x.groups = rows <= 128 ? 1 : 2;
+        x.M = 128 * x.groups;
         x.rt = (int)ceil_div(rows, x.M);
         x.join = prefix;
-        x.slots = 2 * kMaxTileWorkers;
+        x.slots = 2 * kMaxTileWorkers * (3 - x.groups);
         return x;
     }
     const bool shared = prefix && B > 1;
@@ -473,17 +475,18 @@ Lists make_lists(int B, int Hkv, int G, int Nq, bool prefix) {
         x.slots += (int64_t)Hkv * x.pre_rt;
     } else if (shared) {
         x.pre = true;
-        x.pre_split = all <= 128;
-        x.pre_M = x.pre_split ? 128 : 256;
+        x.pre_groups = all <= 128 ? 1 : 2;
+        x.pre_M = 128 * x.pre_groups;
         x.pre_items_rt = (int)ceil_div(all, x.pre_M);
-        x.pre_slots = (int64_t)Hkv * x.pre_items_rt + kMaxTileWorkers;
+        x.pre_slots = (int64_t)Hkv * x.pre_items_rt + kMaxTileWorkers * (3 - x.pre_groups);
     }
     return x;
 }
 
 size_t slot_bytes(int64_t slots, int M, int D) { return (size_t)slots * M * (D * 4 + 8); }
 size_t lists_bytes(const Lists& x, int B, int D) {
-    return slot_bytes(x.slots, x.M, D) + slot_bytes(x.pre_slots, x.pre_M, D) + (((size_t)B + 1) * 4 + 15) / 16 * 16;
+    const size_t index = x.tiles ? 2 * kMaxTileWorkers * sizeof(int4) : (((size_t)B + 1) * 4 + 15) / 16 * 16;
+    return slot_bytes(x.slots, x.M, D) + slot_bytes(x.pre_slots, x.pre_M, D) + index;
 }
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
@@ -615,22 +618,24 @@ int sage_attn_paged(const sage_tensor* q, const sage_tensor* o, const sage_page_
         p.pre_o = reinterpret_cast<float*>(take((size_t)x.pre_slots * x.pre_M * D * 4));
         p.pre_ml = reinterpret_cast<float2*>(take((size_t)x.pre_slots * x.pre_M * 8));
     }
-    p.start = reinterpret_cast<int32_t*>(w);
-    const int ctas = std::min(sms, kMaxTileWorkers);
-    p.pre_items_rt = x.pre_items_rt; p.pre_m = x.pre_M; p.pre_tk = x.pre ? 128 : kStep; p.pre_workers = ctas;
+    if (x.tiles) p.cuts = reinterpret_cast<int4*>(w);
+    else p.start = reinterpret_cast<int32_t*>(w);
+    const int ctas = std::min(sms, kMaxTileWorkers);       // one per SM; of one row group: two
+    p.pre_items_rt = x.pre_items_rt; p.pre_m = x.pre_M; p.pre_tk = x.pre ? 128 : kStep;
+    p.pre_workers = ctas * (3 - x.pre_groups);
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
     cudaError_t e;
     int launches = 0;
     if (x.tiles) {
-        p.workers = ctas;
-        e = launch_paged_tiles(p, D, x.split, mk, mv, s);
+        p.workers = ctas * (3 - x.groups);
+        e = launch_paged_tiles(p, D, x.groups, mk, mv, s);
         launches = 2;
     } else {
         if (x.pre) {
             PagedParams pp = p;
-            pp.part_o = p.pre_o; pp.part_ml = p.pre_ml; pp.start = nullptr;
-            pp.rt = 0; pp.pre_rt = x.pre_items_rt; pp.workers = ctas;
-            if (launch_paged_tiles(pp, D, x.pre_split, mk, mv, s) != cudaSuccess) return SAGE_ERR_LAUNCH;
+            pp.part_o = p.pre_o; pp.part_ml = p.pre_ml; pp.start = nullptr; pp.cuts = nullptr;
+            pp.rt = 0; pp.pre_rt = x.pre_items_rt; pp.workers = p.pre_workers;
+            if (launch_paged_tiles(pp, D, x.pre_groups, mk, mv, s) != cudaSuccess) return SAGE_ERR_LAUNCH;
             ++launches;
         }
         p.workers = std::min(2 * sms, kMaxRowWorkers / kRowWarps) * kRowWarps;

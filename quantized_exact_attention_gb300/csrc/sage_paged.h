@@ -12,7 +12,7 @@ namespace sage {
 
 constexpr int kErrPage = -7;             // SAGE_ERR_PAGE as the kernels record it
 constexpr int kMaxRowWorkers = 1280;     // warps of the few-rows kernel that take work (8 per SM, 160 SMs at most)
-constexpr int kMaxTileWorkers = 160;     // CTAs of the many-rows kernel (1 per SM)
+constexpr int kMaxTileWorkers = 160;     // CTAs of the many-rows kernel with two row groups (1 per SM); with one: twice that
 
 struct PagedParams {
     const uint16_t* q;                   // BF16 bit patterns
@@ -42,6 +42,7 @@ struct PagedParams {
     // workspace
     float* part_o;                       // [slot][M][D]
     float2* part_ml;                     // [slot][M] running maximum (log2 domain) and sum
+    int4* cuts;                          // [workers] items that a worker boundary cuts (null: not wanted)
     int32_t* start;                      // [B + 1] list position of each request's first tile; [B] = total
     // the list that holds the shared prefix's items, for the join
     float* pre_o;
@@ -49,10 +50,10 @@ struct PagedParams {
     int pre_items_rt, pre_m, pre_tk, pre_workers;    // row tiles (0: none), rows of an item, keys of a tile, workers
 };
 
-// The many-rows kernel (sage_paged_tiles.cu): workers = CTAs; split: items of
-// at most 128 rows.  Writes whole rows unless the list holds shared prefix
-// items; then every result is partial.
-cudaError_t launch_paged_tiles(const PagedParams& p, int D, bool split, const CUtensorMap& tk, const CUtensorMap& tv,
+// The many-rows kernel (sage_paged_tiles.cu): workers = CTAs, groups: row groups
+// of 128 of an item (1 or 2).  Writes whole rows unless the list holds shared
+// prefix items; then every result is partial.
+cudaError_t launch_paged_tiles(const PagedParams& p, int D, int groups, const CUtensorMap& tk, const CUtensorMap& tv,
                                cudaStream_t s);
 
 // Tensor map over one tensor of a page cache, box: one page of one head, 64 channels (sage_api.cu).

@@ -56,52 +56,15 @@ struct PagedSched {
     // tiles of one key head of request b
     __device__ int head_tiles(int b) const {
         const int n = q_rows(b), len = own_keys(b);
+        if (p.rt == 1) return item_tiles(n, len, 0);
         int s = 0;
+#pragma unroll 1
         for (int rt = 0; rt < p.rt; ++rt) s += item_tiles(n, len, rt);
         return s;
     }
     // tiles of one worker, given the length of the list
     __device__ int per_worker(int total) const { return max(1, (total + p.workers - 1) / p.workers); }
 };
-
-// Exclusive prefix sums of the requests' tiles by a block of THREADS threads:
-// thread t owns requests [t*cb, (t+1)*cb); chunk[t] receives the list
-// position of its first tile and the return value is the list's length.
-// With `publish` the positions of all requests go to p.start as well.
-template <int M, int TK, int THREADS>
-__device__ __forceinline__ int paged_scan(const PagedSched<M, TK>& s, int* chunk, int* warp_sums, bool publish) {
-    const PagedParams& p = s.p;
-    const int t = threadIdx.x, lane = t & 31, w = t >> 5;
-    const int cb = (p.B + THREADS - 1) / THREADS;
-    const int b0 = min(t * cb, p.B), b1 = min(b0 + cb, p.B);
-    int mine = 0;
-    for (int b = b0; b < b1; ++b) mine += s.head_tiles(b) * p.Hkv;
-    int inc = mine;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const int x = __shfl_up_sync(0xffffffffu, inc, o);
-        if (lane >= o) inc += x;
-    }
-    if (lane == 31) warp_sums[w] = inc;
-    __syncthreads();
-    int base = s.pre_total(), total = base;
-#pragma unroll
-    for (int i = 0; i < THREADS / 32; ++i) {
-        if (i < w) base += warp_sums[i];
-        total += warp_sums[i];
-    }
-    chunk[t] = base + inc - mine;
-    if (publish) {
-        int at = base + inc - mine;
-        for (int b = b0; b < b1; ++b) {
-            p.start[b] = at;
-            at += s.head_tiles(b) * p.Hkv;
-        }
-        if (t == 0) p.start[p.B] = total;
-    }
-    __syncthreads();
-    return total;
-}
 
 // A place in the list.  b = -1: a prefix item (rt counts its row tiles).
 struct PagedPlace {
@@ -123,15 +86,72 @@ __device__ __forceinline__ void paged_enter(const PagedSched<M, TK>& s, PagedPla
     }
 }
 
-// The place of list position t (t < total).  Same result in every thread.
-template <int M, int TK, int THREADS>
-__device__ __forceinline__ PagedPlace paged_find(const PagedSched<M, TK>& s, const int* chunk, int t) {
+// The length of the list, and where the CTA's workers begin.  A block of
+// THREADS threads sums the requests' tiles, thread t those of requests
+// [t*cb, (t+1)*cb); the thread whose requests hold the first tile of worker
+// first_worker + w*worker_step (w < NW) leaves {request, list position of its
+// first tile} in found[w] ({-1, 0}: among the prefix items).  With `publish`
+// the positions of all requests go to p.start as well.  `red` holds THREADS/32
+// ints.  Ends with a barrier.
+template <int M, int TK, int THREADS, int NW>
+__device__ __forceinline__ int paged_scan(const PagedSched<M, TK>& s, int first_worker, int worker_step, int2* found,
+                                          int* red, bool publish) {
+    const PagedParams& p = s.p;
+    const int t = threadIdx.x, lane = t & 31, w = t >> 5;
+    const int cb = (p.B + THREADS - 1) / THREADS;
+    const int b0 = min(t * cb, p.B), b1 = min(b0 + cb, p.B);
+    int mine = 0;
+#pragma unroll 1
+    for (int b = b0; b < b1; ++b) mine += s.head_tiles(b) * p.Hkv;
+    int inc = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int x = __shfl_up_sync(0xffffffffu, inc, o);
+        if (lane >= o) inc += x;
+    }
+    if (lane == 31) red[w] = inc;
+    if (t < NW) found[t] = make_int2(-1, 0);
+    __syncthreads();
+    int base = s.pre_total(), total = base;
+#pragma unroll
+    for (int i = 0; i < THREADS / 32; ++i) {
+        if (i < w) base += red[i];
+        total += red[i];
+    }
+    base += inc - mine;
+    const int per = s.per_worker(total);
+    if (cb == 1 && !publish) {
+#pragma unroll
+        for (int k = 0; k < NW; ++k) {
+            const int at = (first_worker + k * worker_step) * per;
+            if (at >= base && at - base < mine) found[k] = make_int2(b0, base);
+        }
+    } else {
+#pragma unroll 1
+        for (int b = b0; b < b1; ++b) {
+            const int n = s.head_tiles(b) * p.Hkv;
+#pragma unroll 1
+            for (int k = 0; k < NW; ++k) {
+                const int at = (first_worker + k * worker_step) * per;
+                if (at >= base && at - base < n) found[k] = make_int2(b, base);
+            }
+            if (publish) p.start[b] = base;
+            base += n;
+        }
+        if (publish && t == 0) p.start[p.B] = total;
+    }
+    __syncthreads();
+    return total;
+}
+
+// The place of list position t (t < total), with paged_scan's finding.
+template <int M, int TK>
+__device__ __forceinline__ PagedPlace paged_place(const PagedSched<M, TK>& s, int2 found, int t) {
     const PagedParams& p = s.p;
     PagedPlace x{};
-    const int pre = s.pre_total();
-    if (t < pre) {
+    x.b = found.x;
+    if (x.b < 0) {
         const int nt = s.pre_tiles();
-        x.b = -1;
         x.item = t / nt;
         x.tile = t - x.item * nt;
         x.h = x.item / p.pre_rt;
@@ -139,31 +159,21 @@ __device__ __forceinline__ PagedPlace paged_find(const PagedSched<M, TK>& s, con
         x.ntiles = nt;
         return x;
     }
-    int lo = 0, hi = THREADS - 1;                          // last chunk that starts at or before t
-    while (lo < hi) {
-        const int mid = (lo + hi + 1) >> 1;
-        if (chunk[mid] <= t) lo = mid; else hi = mid - 1;
-    }
-    const int cb = (p.B + THREADS - 1) / THREADS;
-    int at = chunk[lo];
-    for (x.b = lo * cb; x.b < p.B; ++x.b) {
-        x.n = s.q_rows(x.b);
-        x.len = s.own_keys(x.b);
-        int per_head = 0;
-        for (int rt = 0; rt < p.rt; ++rt) per_head += s.item_tiles(x.n, x.len, rt);
-        if (t < at + per_head * p.Hkv) {
-            x.h = (t - at) / per_head;
-            at += x.h * per_head;
-            break;
-        }
-        at += per_head * p.Hkv;
-    }
+    x.n = s.q_rows(x.b);
+    x.len = s.own_keys(x.b);
+    int per_head = 0;
+#pragma unroll 1
+    for (int rt = 0; rt < p.rt; ++rt) per_head += s.item_tiles(x.n, x.len, rt);
+    int at = t - found.y;
+    x.h = at / per_head;
+    at -= x.h * per_head;
+#pragma unroll 1
     for (x.rt = 0; x.rt < p.rt; ++x.rt) {
         const int nt = s.item_tiles(x.n, x.len, x.rt);
-        if (t < at + nt) break;
-        at += nt;
+        if (at < nt) break;
+        at -= nt;
     }
-    x.tile = t - at;
+    x.tile = at;
     paged_enter(s, x);
     return x;
 }
