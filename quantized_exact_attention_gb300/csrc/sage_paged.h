@@ -64,4 +64,30 @@ int take_fault_mode();
 // Checks of a page cache's description that need no GPU (sage_tables.cu).
 int check_page_cache(const sage_page_cache* c);
 
+#ifdef __CUDACC__
+// Programmatic dependent launch: a kernel launched with `overlap` may start
+// once every CTA of the kernel before it has called pdl_trigger (or ended),
+// which hides its launch and its prologue; pdl_wait returns when that kernel
+// is complete and its writes are visible.
+__device__ __forceinline__ void pdl_trigger() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
+template <class... P, class... A>
+cudaError_t launch_after(void (*kernel)(P...), dim3 grid, dim3 block, size_t smem, cudaStream_t s, bool overlap,
+                         const A&... args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = block;
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = overlap ? 1 : 0;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, args...);
+    return e != cudaSuccess ? e : cudaGetLastError();
+}
+#endif
+
 }  // namespace sage

@@ -202,6 +202,7 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
     uint8_t* sgen = smem_raw + (sbase - raw_base);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
+    pdl_trigger();
     auto bar = [&](int i) -> uint32_t { return sbase + L::OFF_BAR + 8u * (uint32_t)i; };
     TileNote* notes = reinterpret_cast<TileNote*>(sgen + L::OFF_NOTE);
     volatile uint32_t* tmem_slot = reinterpret_cast<volatile uint32_t*>(sgen + L::OFF_TMEM);
@@ -642,10 +643,11 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
 // the worker behind the boundary, blockIdx.y a group of 32 rows.
 // ---------------------------------------------------------------------------
 template <int D, int M>
-__global__ void __launch_bounds__(256) paged_cuts_kernel(const PagedParams p) {
+__global__ void __launch_bounds__(256) paged_cuts_kernel(const __grid_constant__ PagedParams p) {
     constexpr int V = D / 32;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int w = blockIdx.x + 1;
+    pdl_wait();
     const int4 cut = __ldcg(p.cuts + w);
     if (cut.x < 0) return;
     const PagedSched<M, 128> s(p);
@@ -709,10 +711,8 @@ cudaError_t launch_one(const PagedParams& p, const CUtensorMap& tk, const CUtens
     }
     paged_tiles_kernel<D, kGroups><<<p.workers, L::kThreads, L::kSmem, s>>>(tk, tv, p);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
-    if (p.pre_rt == 0 && p.workers > 1) {
-        paged_cuts_kernel<D, L::M><<<dim3((unsigned)p.workers - 1, L::M / 32), 256, 0, s>>>(p);
-        e = cudaGetLastError();
-    }
+    if (p.pre_rt == 0 && p.workers > 1)
+        e = launch_after(paged_cuts_kernel<D, L::M>, dim3((unsigned)p.workers - 1, L::M / 32), dim3(256), 0, s, true, p);
     return e;
 }
 

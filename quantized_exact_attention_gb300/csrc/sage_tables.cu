@@ -41,11 +41,10 @@ __device__ __forceinline__ Held held(const TableParams& p, int b) {
     return x;
 }
 
-constexpr int kTableThreads = 256;
+constexpr int kTableThreads = 128;
 
 __device__ __forceinline__ int block_sum(int v, int* red) {
     v = __reduce_add_sync(0xffffffffu, v);
-    __syncthreads();                     // an earlier sum's reads of red are done
     if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
     __syncthreads();
     int s = 0;
@@ -54,18 +53,26 @@ __device__ __forceinline__ int block_sum(int v, int* red) {
     return s;
 }
 
+// kQuads: rows of the table and of the slots are 16-byte aligned and a
+// multiple of 4 long, and leave in 16-byte stores.
+template <bool kQuads>
 __global__ void __launch_bounds__(kTableThreads) page_tables_kernel(const TableParams p) {
     __shared__ int red[kTableThreads / 32];
     const int per = (p.B + gridDim.x - 1) / gridDim.x;
     const int b0 = min((int)blockIdx.x * per, p.B), b1 = min(b0 + per, p.B);
+    Held x{};
+    if (b0 < p.B) x = held(p, b0);
     int sum = 0;
+#pragma unroll 4
     for (int b = threadIdx.x; b < b0; b += kTableThreads) {
-        const Held x = held(p, b);
-        sum += x.new_pages - x.old_pages;
+        const Held y = held(p, b);
+        sum += y.new_pages - y.old_pages;
     }
     int first = block_sum(sum, red);
+    constexpr int kE = kQuads ? 4 : 1;                     // entries of a store
+#pragma unroll 1
     for (int b = b0; b < b1; ++b) {
-        const Held x = held(p, b);
+        if (b > b0) x = held(p, b);
         int32_t* row = p.table + (int64_t)b * p.table_stride;
         // page of entry j of this request after the call
         auto entry = [&](int j) -> int {
@@ -73,18 +80,32 @@ __global__ void __launch_bounds__(kTableThreads) page_tables_kernel(const TableP
             const int f = first + (j - x.old_pages);
             return j < x.new_pages && f < p.n_free ? __ldg(p.free_pages + f) : -1;
         };
-        for (int j = x.old_pages + (int)threadIdx.x; j < p.W; j += kTableThreads) row[j] = entry(j);
+#pragma unroll 2
+        for (int j = (x.old_pages & ~(kE - 1)) + (int)threadIdx.x * kE; j < p.W; j += kTableThreads * kE) {
+            if constexpr (kQuads) {
+                // kept entries of the first quad are written back as they are
+                *reinterpret_cast<int4*>(row + j) = make_int4(entry(j), entry(j + 1), entry(j + 2), entry(j + 3));
+            } else {
+                row[j] = entry(j);
+            }
+        }
         if (p.slots != nullptr) {
             int32_t* out = p.slots + (int64_t)b * p.slots_stride;
-            for (int i = threadIdx.x; i < p.N; i += kTableThreads) {
-                int64_t slot = -1;
-                if (i < x.new_len - x.old_len) {
-                    const int t = x.old_len + i;
-                    const int pg = entry(t >> p.page_shift);
-                    slot = pg < 0 ? -1 : ((int64_t)pg << p.page_shift) + (t & (p.page - 1));
-                    if (slot > INT32_MAX) slot = -1;
-                }
-                out[i] = (int32_t)slot;
+            // the page of token t is read where it comes from, not from the row
+            // that other threads are writing
+            auto slot = [&](int i) -> int {
+                if (i >= x.new_len - x.old_len) return -1;
+                const int t = x.old_len + i;
+                const int pg = entry(t >> p.page_shift);
+                const int64_t sl = ((int64_t)pg << p.page_shift) + (t & (p.page - 1));
+                return pg < 0 || sl > INT32_MAX ? -1 : (int)sl;
+            };
+#pragma unroll 2
+            for (int i = (int)threadIdx.x * kE; i < p.N; i += kTableThreads * kE) {
+                if constexpr (kQuads)
+                    *reinterpret_cast<int4*>(out + i) = make_int4(slot(i), slot(i + 1), slot(i + 2), slot(i + 3));
+                else
+                    out[i] = slot(i);
             }
         }
         first += x.new_pages - x.old_pages;
@@ -195,8 +216,12 @@ int sage_page_tables(const int32_t* old_len, const int32_t* new_len, int B, int 
     p.slots = n_slots > 0 ? slots : nullptr; p.slots_stride = slots_stride; p.N = n_slots;
     p.taken = taken; p.B = B; p.page = page_size;
     p.page_shift = 31 - __builtin_clz((unsigned)page_size);
-    const int grid = std::min(B, 152 * 8);
-    page_tables_kernel<<<grid, kTableThreads, 0, static_cast<cudaStream_t>(stream)>>>(p);
+    // one wave: sixteen blocks on each of 152 SMs
+    const int grid = std::min(B, 152 * 16);
+    const bool quads = aligned16(table) && table_stride % 4 == 0 && table_width % 4 == 0 &&
+                       (n_slots == 0 || (aligned16(slots) && slots_stride % 4 == 0 && n_slots % 4 == 0));
+    if (quads) page_tables_kernel<true><<<grid, kTableThreads, 0, static_cast<cudaStream_t>(stream)>>>(p);
+    else page_tables_kernel<false><<<grid, kTableThreads, 0, static_cast<cudaStream_t>(stream)>>>(p);
     if (cudaGetLastError() != cudaSuccess) return SAGE_ERR_LAUNCH;
     set_last_launch_count(1);
     return SAGE_OK;
