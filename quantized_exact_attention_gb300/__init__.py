@@ -456,8 +456,8 @@ class PageCache:
         return sage_page_cache(tensor_desc(self.k), tensor_desc(self.v), n, page, h, d)
 
     @functools.cached_property
-    def _ref(self):
-        return ctypes.byref(self._c)
+    def _address(self) -> int:
+        return ctypes.addressof(self._c)
 
     @functools.cached_property
     def _device(self) -> int:
@@ -473,27 +473,19 @@ def alloc_page_cache(num_pages: int, page_size: int, heads: int, D: int = D_HEAD
     return PageCache(e(), e())
 
 
-def _on(dev: int, *tensors):
-    """Refuse tensors that do not live on CUDA device `dev`, or a call while another device is current."""
-    for t in tensors:
-        if t is not None and t.get_device() != dev:
-            raise ValueError("all tensors of a call live on one CUDA device")
-    if dev < 0 or torch.cuda.current_device() != dev:
-        raise ValueError("the tensors of a call live on the current CUDA device")
+_paged = None
 
 
-def _ints(t, what: str, dim: int = 1):
-    """Data pointer of an int32 tensor with unit stride along its last dimension (None stays None)."""
-    if t is None:
-        return None
-    if t.dtype != torch.int32 or t.dim() != dim or (t.shape[-1] > 1 and t.stride(-1) != 1):
-        raise ValueError(f"{what}: expected a {dim}-dimensional int32 tensor, contiguous along its last dimension")
-    return t.data_ptr()
-
-
-def _count(t, n: int, what: str):
-    if t is not None and t.shape[0] != n:
-        raise ValueError(f"{what}: expected {n} entries, got {t.shape[0]}")
+def _paged_binding():
+    """The module that hands torch tensors to the page-cache entries (see csrc/sage_binding.cpp)."""
+    global _paged
+    if _paged is None:
+        lib = load_library()
+        from . import _sage_binding
+        _sage_binding.bind(*[ctypes.cast(f, ctypes.c_void_p).value
+                             for f in (lib.sage_page_tables, lib.sage_cache_append, lib.sage_attn_paged)])
+        _paged = _sage_binding
+    return _paged
 
 
 def sage_page_tables(new_len, page_size: int, free_pages, table, slots=None, taken=None, old_len=None, stream=None):
@@ -501,39 +493,23 @@ def sage_page_tables(new_len, page_size: int, free_pages, table, slots=None, tak
     (None: 0) to new_len tokens, with pages taken from free_pages in order.
     table: int32 [B, W], updated in place; slots: int32 [B, N] or None; taken:
     int32 [1], the number of pages needed.  Returns taken (allocated if None)."""
-    B, W = table.shape
     if taken is None:
-        with torch.cuda.stream(stream):
+        with torch.cuda.stream(stream):                    # what is allocated here belongs to the stream that uses it
             taken = torch.empty((1,), dtype=torch.int32, device=table.device)
-    _on(table.get_device(), new_len, free_pages, slots, taken, old_len)
-    ptrs = [_ints(t, n, d) for t, n, d in ((old_len, "old_len", 1), (new_len, "new_len", 1),
-                                           (free_pages, "free_pages", 1), (table, "table", 2),
-                                           (slots, "slots", 2), (taken, "taken", 1))]
-    _count(new_len, B, "new_len")
-    _count(old_len, B, "old_len")
-    _count(slots, B, "slots")
-    _count(taken, 1, "taken")
-    rc = load_library().sage_page_tables(ptrs[0], ptrs[1], B, int(page_size), ptrs[2], free_pages.shape[0], ptrs[3],
-                                         table.stride(0), W, ptrs[4], slots.stride(0) if slots is not None else 0,
-                                         slots.shape[1] if slots is not None else 0, ptrs[5], _stream_ptr(stream))
-    _check(rc, "sage_page_tables")
+    rc = (_paged or _paged_binding()).page_tables(new_len, page_size, free_pages, table, slots, taken, old_len,
+                                                  None if stream is None else stream.cuda_stream)
+    if rc:
+        _check(rc, "sage_page_tables")
     return taken
 
 
 def sage_cache_append(k, v, slots, cache: PageCache, stream=None):
     """Enqueue the copy of new keys and values ([B, heads, N, D] BF16 views) into
     their cache slots (int32 [B, N]; a negative slot skips its token)."""
-    B, h, N, D = k.shape
-    if v.shape != k.shape or h != cache.heads or D != cache.k.shape[3]:
-        raise ValueError("k and v are [B, heads, N, D] with the cache's heads and D")
-    _on(cache._device, k, v, slots)
-    sp = _ints(slots, "slots", 2)
-    if slots.shape[0] != B or slots.shape[1] != N:
-        raise ValueError(f"slots: expected [{B}, {N}]")
-    ks, vs = tensor_desc(k), tensor_desc(v)
-    rc = load_library().sage_cache_append(ctypes.byref(ks), ctypes.byref(vs), B, N, sp, slots.stride(0), cache._ref,
-                                          _stream_ptr(stream))
-    _check(rc, "sage_cache_append")
+    rc = (_paged or _paged_binding()).cache_append(k, v, slots, cache._address, cache._device,
+                                                   None if stream is None else stream.cuda_stream)
+    if rc:
+        _check(rc, "sage_cache_append")
 
 
 def paged_workspace_bytes(B: int, H: int, Hkv: int, Nq: int, D: int = D_HEAD) -> int:
@@ -553,24 +529,11 @@ def sage_attn_paged(q, o, cache: PageCache, table, workspace, q_len=None, kv_len
     view o) over the page cache: table int32 [B, W] (or None: no own keys) with
     kv_len own tokens each, and the pages of prefix_table (int32 [Wp], prefix_len
     int32 [1]) that all requests share.  See the header for the masks."""
-    B, H, Nq, D = q.shape
-    if o.shape != q.shape or D != cache.k.shape[3]:
-        raise ValueError("q and o are [B, H, Nq, D] with the cache's D")
-    _on(cache._device, q, o, table, workspace, q_len, kv_len, prefix_table, prefix_len)
-    tp, pp = _ints(table, "table", 2), _ints(prefix_table, "prefix_table")
-    ql, kl, pl = _ints(q_len, "q_len"), _ints(kv_len, "kv_len"), _ints(prefix_len, "prefix_len")
-    _count(table, B, "table")
-    _count(q_len, B, "q_len")
-    _count(kv_len, B, "kv_len")
-    _count(prefix_len, 1, "prefix_len")
-    if not workspace.is_contiguous():
-        raise ValueError("workspace is contiguous")
-    qs, os_ = tensor_desc(q), tensor_desc(o)
-    rc = load_library().sage_attn_paged(
-        ctypes.byref(qs), ctypes.byref(os_), cache._ref, B, H, Nq, ql, tp, table.stride(0) if tp else 0,
-        table.shape[1] if tp else 0, kl, pp, prefix_table.shape[0] if pp else 0, pl, float(sm_scale),
-        1 if causal else 0, workspace.data_ptr(), workspace.numel() * workspace.element_size(), _stream_ptr(stream))
-    _check(rc, "sage_attn_paged")
+    rc = (_paged or _paged_binding()).attn_paged(q, o, cache._address, cache._device, table, workspace, q_len, kv_len,
+                                                 prefix_table, prefix_len, sm_scale, causal,
+                                                 None if stream is None else stream.cuda_stream)
+    if rc:
+        _check(rc, "sage_attn_paged")
 
 
 def attention_paged(q, cache: PageCache, table, q_len=None, kv_len=None, prefix_table=None, prefix_len=None,

@@ -27,90 +27,85 @@ struct TableParams {
     int32_t* taken;
     int64_t table_stride, slots_stride;
     int B, W, N, n_free, page, page_shift;
+    bool len_quads;                      // the lengths are 16-byte aligned
 };
 
 struct Held { int old_len, new_len, old_pages, new_pages; };
 
-__device__ __forceinline__ Held held(const TableParams& p, int b) {
+__device__ __forceinline__ Held held(const TableParams& p, int o, int n) {
     Held x;
-    const int cap = p.W << p.page_shift;
-    x.old_len = p.old_len == nullptr ? 0 : min(max(__ldg(p.old_len + b), 0), cap);
-    x.new_len = max(x.old_len, min(max(__ldg(p.new_len + b), 0), cap));
-    x.old_pages = (int)(((int64_t)x.old_len + p.page - 1) >> p.page_shift);
-    x.new_pages = (int)(((int64_t)x.new_len + p.page - 1) >> p.page_shift);
+    const int cap = p.W << p.page_shift;                   // at most 2^31 - 1 - page
+    x.old_len = min(max(o, 0), cap);
+    x.new_len = max(x.old_len, min(max(n, 0), cap));
+    x.old_pages = (x.old_len + p.page - 1) >> p.page_shift;
+    x.new_pages = (x.new_len + p.page - 1) >> p.page_shift;
     return x;
 }
-
-constexpr int kTableThreads = 128;
-
-__device__ __forceinline__ int block_sum(int v, int* red) {
-    v = __reduce_add_sync(0xffffffffu, v);
-    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
-    __syncthreads();
-    int s = 0;
-#pragma unroll
-    for (int i = 0; i < kTableThreads / 32; ++i) s += red[i];
-    return s;
+__device__ __forceinline__ Held held(const TableParams& p, int b) {
+    return held(p, p.old_len == nullptr ? 0 : __ldg(p.old_len + b), __ldg(p.new_len + b));
 }
 
-// kQuads: rows of the table and of the slots are 16-byte aligned and a
-// multiple of 4 long, and leave in 16-byte stores.
-template <bool kQuads>
-__global__ void __launch_bounds__(kTableThreads) page_tables_kernel(const TableParams p) {
+constexpr int kTableThreads = 256;
+
+__global__ void __launch_bounds__(kTableThreads, 8) page_tables_kernel(const __grid_constant__ TableParams p) {
     __shared__ int red[kTableThreads / 32];
     const int per = (p.B + gridDim.x - 1) / gridDim.x;
     const int b0 = min((int)blockIdx.x * per, p.B), b1 = min(b0 + per, p.B);
-    Held x{};
-    if (b0 < p.B) x = held(p, b0);
+    if (b0 == b1) return;
+    Held x = held(p, b0);
     int sum = 0;
-#pragma unroll 4
-    for (int b = threadIdx.x; b < b0; b += kTableThreads) {
+    int quads = 0;                                         // requests counted four at a time
+    if (p.len_quads) {
+        quads = b0 & ~3;
+#pragma unroll 2
+        for (int b = 4 * (int)threadIdx.x; b < quads; b += 4 * kTableThreads) {
+            const int4 n = __ldg(reinterpret_cast<const int4*>(p.new_len + b));
+            const int4 o = p.old_len == nullptr ? make_int4(0, 0, 0, 0) : __ldg(reinterpret_cast<const int4*>(p.old_len + b));
+            const int nn[4] = {n.x, n.y, n.z, n.w}, oo[4] = {o.x, o.y, o.z, o.w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const Held y = held(p, oo[e], nn[e]);
+                sum += y.new_pages - y.old_pages;
+            }
+        }
+    }
+    for (int b = quads + (int)threadIdx.x; b < b0; b += kTableThreads) {
         const Held y = held(p, b);
         sum += y.new_pages - y.old_pages;
     }
-    int first = block_sum(sum, red);
-    constexpr int kE = kQuads ? 4 : 1;                     // entries of a store
+    sum = __reduce_add_sync(0xffffffffu, sum);
+    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = sum;
+    __syncthreads();
+    int first = 0;
+#pragma unroll
+    for (int i = 0; i < kTableThreads / 32; ++i) first += red[i];
 #pragma unroll 1
     for (int b = b0; b < b1; ++b) {
         if (b > b0) x = held(p, b);
         int32_t* row = p.table + (int64_t)b * p.table_stride;
-        // page of entry j of this request after the call
+        // page of entry j of this request after the call, read where it comes
+        // from: other threads are writing the row
         auto entry = [&](int j) -> int {
             if (j < x.old_pages) return row[j];
             const int f = first + (j - x.old_pages);
             return j < x.new_pages && f < p.n_free ? __ldg(p.free_pages + f) : -1;
         };
 #pragma unroll 2
-        for (int j = (x.old_pages & ~(kE - 1)) + (int)threadIdx.x * kE; j < p.W; j += kTableThreads * kE) {
-            if constexpr (kQuads) {
-                // kept entries of the first quad are written back as they are
-                *reinterpret_cast<int4*>(row + j) = make_int4(entry(j), entry(j + 1), entry(j + 2), entry(j + 3));
-            } else {
-                row[j] = entry(j);
-            }
-        }
-        if (p.slots != nullptr) {
-            int32_t* out = p.slots + (int64_t)b * p.slots_stride;
-            // the page of token t is read where it comes from, not from the row
-            // that other threads are writing
-            auto slot = [&](int i) -> int {
-                if (i >= x.new_len - x.old_len) return -1;
-                const int t = x.old_len + i;
-                const int pg = entry(t >> p.page_shift);
-                const int64_t sl = ((int64_t)pg << p.page_shift) + (t & (p.page - 1));
-                return pg < 0 || sl > INT32_MAX ? -1 : (int)sl;
-            };
+        for (int j = x.old_pages + (int)threadIdx.x; j < p.W; j += kTableThreads) row[j] = entry(j);
+        int32_t* out = p.slots + (int64_t)b * p.slots_stride;
 #pragma unroll 2
-            for (int i = (int)threadIdx.x * kE; i < p.N; i += kTableThreads * kE) {
-                if constexpr (kQuads)
-                    *reinterpret_cast<int4*>(out + i) = make_int4(slot(i), slot(i + 1), slot(i + 2), slot(i + 3));
-                else
-                    out[i] = slot(i);
+        for (int i = threadIdx.x; i < p.N; i += kTableThreads) {
+            int slot = -1;
+            if (i < x.new_len - x.old_len) {
+                const int t = x.old_len + i, pg = entry(t >> p.page_shift);
+                // a page whose slots pass 2^31 - 1 has none
+                if (pg >= 0 && pg <= (INT32_MAX >> p.page_shift)) slot = (pg << p.page_shift) + (t & (p.page - 1));
             }
+            out[i] = slot;
         }
         first += x.new_pages - x.old_pages;
     }
-    if (b1 == p.B && b0 < p.B && threadIdx.x == 0) *p.taken = first;
+    if (b1 == p.B && threadIdx.x == 0) *p.taken = first;
 }
 
 // ---------------------------------------------------------------------------
@@ -127,7 +122,7 @@ struct AppendParams {
     int64_t ksb, ksh, ksn, vsb, vsh, vsn;
     int64_t ckp, ckh, ckt, cvp, cvh, cvt;
     int64_t slots_stride, capacity;
-    int64_t tokens;                      // B * N
+    int64_t tokens;                      // B * N, below 2^31
     int N, heads, chunk_shift;           // chunk_shift: log2 of the 16-byte chunks of a head's row
     int page, page_shift;
 };
@@ -139,7 +134,7 @@ __global__ void __launch_bounds__(kAppendThreads) cache_append_kernel(const Appe
     const int64_t warps = (int64_t)gridDim.x * (kAppendThreads / 32);
     const int chunks = p.heads << p.chunk_shift;
     for (int64_t t = (int64_t)blockIdx.x * (kAppendThreads / 32) + (threadIdx.x >> 5); t < p.tokens; t += warps) {
-        const int b = (int)(t / p.N), i = (int)(t % p.N);
+        const int b = (int)((uint32_t)t / (uint32_t)p.N), i = (int)t - b * p.N;
         const int slot = __ldg(p.slots + b * p.slots_stride + i);
         if (slot < 0) continue;
         if (slot >= p.capacity) {
@@ -213,15 +208,12 @@ int sage_page_tables(const int32_t* old_len, const int32_t* new_len, int B, int 
     TableParams p{};
     p.old_len = old_len; p.new_len = new_len; p.free_pages = free_pages; p.n_free = n_free;
     p.table = table; p.table_stride = table_stride; p.W = table_width;
-    p.slots = n_slots > 0 ? slots : nullptr; p.slots_stride = slots_stride; p.N = n_slots;
+    p.slots = slots; p.slots_stride = slots_stride; p.N = n_slots;
     p.taken = taken; p.B = B; p.page = page_size;
     p.page_shift = 31 - __builtin_clz((unsigned)page_size);
-    // one wave: sixteen blocks on each of 152 SMs
-    const int grid = std::min(B, 152 * 16);
-    const bool quads = aligned16(table) && table_stride % 4 == 0 && table_width % 4 == 0 &&
-                       (n_slots == 0 || (aligned16(slots) && slots_stride % 4 == 0 && n_slots % 4 == 0));
-    if (quads) page_tables_kernel<true><<<grid, kTableThreads, 0, static_cast<cudaStream_t>(stream)>>>(p);
-    else page_tables_kernel<false><<<grid, kTableThreads, 0, static_cast<cudaStream_t>(stream)>>>(p);
+    p.len_quads = aligned16(new_len) && (old_len == nullptr || aligned16(old_len));
+    // one wave: eight blocks on each of 152 SMs
+    page_tables_kernel<<<std::min(B, 152 * 8), kTableThreads, 0, static_cast<cudaStream_t>(stream)>>>(p);
     if (cudaGetLastError() != cudaSuccess) return SAGE_ERR_LAUNCH;
     set_last_launch_count(1);
     return SAGE_OK;
@@ -232,6 +224,7 @@ int sage_cache_append(const sage_tensor* k, const sage_tensor* v, int B, int N, 
     int rc = check_page_cache(cache);
     if (rc != SAGE_OK) return rc;
     if (B <= 0 || N <= 0 || slots == nullptr || slots_stride < 0) return SAGE_ERR_ARG;
+    if ((int64_t)B * N > INT32_MAX) return SAGE_ERR_UNSUPPORTED;
     if ((rc = check_view(k)) != SAGE_OK || (rc = check_view(v)) != SAGE_OK) return rc;
     AppendParams p{};
     p.status = device_status_ptr();

@@ -78,6 +78,7 @@ def test_cache_append_refuses(lib):
     assert lib.sage_cache_append(None, R(t), 1, 1, 0x20000, 1, R(c), None) == S.SAGE_ERR_ARG
     assert lib.sage_cache_append(R(t), R(tensor(ptr=0x10002)), 1, 1, 0x20000, 1, R(c), None) == S.SAGE_ERR_UNSUPPORTED
     assert lib.sage_cache_append(R(t), R(t), 1, 1, 0x20000, 1, None, None) == S.SAGE_ERR_ARG
+    assert lib.sage_cache_append(R(t), R(t), 1 << 16, 1 << 15, 0x20000, 1, R(c), None) == S.SAGE_ERR_UNSUPPORTED
 
 
 def test_page_tables_refuses(lib):
