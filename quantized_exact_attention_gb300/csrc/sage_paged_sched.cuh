@@ -236,4 +236,9 @@ __device__ __forceinline__ bool paged_row(const PagedSched<M, TK>& s, const Page
     return i < (x.b < 0 ? s.q_rows(b) : x.n);
 }
 
+// 16 bytes to shared memory, the first `bytes` of them from src, zeros behind.
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, uint32_t bytes) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+
 }  // namespace sage

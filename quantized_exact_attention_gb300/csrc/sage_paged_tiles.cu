@@ -14,19 +14,19 @@
 // Warp roles.  kGroups = 2: 384 threads, kGroups = 1: 192.
 //   warps 0-3 (4-7)  softmax of group 0 (1), one thread per row: S from tensor
 //                    memory, mask, online maximum and sum, P in BF16 back to
-//                    tensor memory; at an item's ends Q into shared memory and
-//                    the output from tensor memory
+//                    tensor memory; the output from tensor memory
 //   loader           the pages of a K and of a V tile by TMA through rings of
 //                    stages; it alone walks the list and leaves a note for
 //                    each tile
+//   Q loader         the rows of the next item as soon as the last scores of
+//                    this one are computed (kGroups = 1: the loader)
 //   issuers          kGroups = 2: one thread for S = Q K^T and one for O += P V
 //                    (issuing takes about 48 cycles of a thread per
 //                    instruction and 45 per wait or commit, so one thread
 //                    would need longer than the 1,024 cycles of a unit's
 //                    products); kGroups = 1: one thread for both
-//   kGroups = 2 has one more warp, idle: it completes the warpgroup whose
-//   registers go to the softmax (setmaxnreg: 2 x 128 x 224 + 128 x 56 =
-//   384 x 168).
+//   kGroups = 2: the last four warps' registers go to the softmax (setmaxnreg:
+//   2 x 128 x 224 + 128 x 56 = 384 x 168).
 // Tensor memory, kGroups = 2: O of both groups in the top 2 D columns, P of
 // each group beside its S.  D = 128: [S 128 | P0 64 | P1 64 | O0 | O1], one S
 // for both groups: a group loads its scores into registers at once and frees
@@ -56,6 +56,7 @@ namespace sage {
 namespace {
 
 constexpr int kNotes = 8;
+constexpr int kItemNotes = 8;
 constexpr float kLazy = 8.f;                              // log2 of the weights' bound
 constexpr uint32_t kBlk = 128 * 128;                      // 128 rows x 64 channels
 
@@ -70,6 +71,12 @@ struct TileNote {
     int flags;
     int pad[3];
 };
+// ... and about an item, to the Q loader.
+struct ItemNote {
+    int b, h, rt, n;
+    int tile;                                             // its first tile in this worker
+    int pad[3];
+};
 enum { N_FIRST = 1, N_LAST = 2, N_OWN = 4, N_WHOLE = 8 };  // of its item in this worker; own keys; item not shared
 
 template <int D, int kGroups>
@@ -77,6 +84,7 @@ struct TilesShape {
     static constexpr int M = 128 * kGroups;
     static constexpr int kThreads = kGroups == 2 ? 384 : 192;
     static constexpr int kWarpLoad = 4 * kGroups, kWarpS = kWarpLoad + 1, kWarpPV = kGroups == 2 ? kWarpS + 1 : kWarpS;
+    static constexpr int kWarpQ = kGroups == 2 ? kWarpPV + 1 : kWarpLoad;
     static constexpr int kCtasPerSm = kGroups == 2 ? 1 : 2;
     static constexpr int kNB = D / 64;                    // 64-channel blocks of a row
     static constexpr uint32_t kTile = kNB * kBlk;         // bytes of a K (or V) tile, and of a group's Q
@@ -88,16 +96,19 @@ struct TilesShape {
     static constexpr uint32_t TM_P = kAlias ? 0 : 128 * kSBufs;    // + 64 X
     static constexpr uint32_t TM_O = kAlias ? 128 : TM_P + 64 * kGroups;   // + D X
     // shared memory
-    static constexpr uint32_t OFF_Q = 0;                  // at an item's end: rows on their way out
+    static constexpr uint32_t OFF_Q = 0;
     static constexpr uint32_t OFF_K = kGroups * kTile;
     static constexpr uint32_t OFF_V = OFF_K + kNS * kTile;
-    static constexpr uint32_t OFF_BAR = OFF_V + kNS * kTile;
-    static constexpr int B_Q = 0, B_ITEM = 1, B_ODONE = 2, B_DRAIN = 3;
-    static constexpr int B_S = 5, B_SFREE = 7, B_P = 9, B_PV = 11;                // one of each per group
-    static constexpr int B_KF = 13, B_KE = B_KF + kNS, B_VF = B_KE + kNS, B_VE = B_VF + kNS, B_NOTE = B_VE + kNS;
-    static constexpr int kBars = B_NOTE + kNotes;
+    static constexpr uint32_t OFF_STAGE = OFF_V + kNS * kTile;     // rows on their way out, 2 KB a warp
+    static constexpr uint32_t OFF_BAR = OFF_STAGE + kGroups * 4 * 2048;
+    static constexpr int B_Q = 0, B_ODONE = 1, B_DRAIN = 2;
+    static constexpr int B_S = 4, B_SFREE = 6, B_P = 8, B_PV = 10;                // one of each per group
+    static constexpr int B_KF = 12, B_KE = B_KF + kNS, B_VF = B_KE + kNS, B_VE = B_VF + kNS, B_NOTE = B_VE + kNS;
+    static constexpr int B_ITEM = B_NOTE + kNotes;
+    static constexpr int kBars = B_ITEM + kItemNotes;
     static constexpr uint32_t OFF_NOTE = OFF_BAR + (kBars * 8 + 15) / 16 * 16;
-    static constexpr uint32_t OFF_SCAN = OFF_NOTE + kNotes * sizeof(TileNote);    // int [16], int2
+    static constexpr uint32_t OFF_ITEM = OFF_NOTE + kNotes * sizeof(TileNote);
+    static constexpr uint32_t OFF_SCAN = OFF_ITEM + kItemNotes * sizeof(ItemNote);    // int [16], int2
     static constexpr uint32_t OFF_TMEM = OFF_SCAN + 80;
     static constexpr uint32_t OFF_ABORT = OFF_TMEM + 16;
     static constexpr uint32_t kSmem = OFF_ABORT + 16 + 1024;                      // + alignment slack
@@ -171,21 +182,21 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
     return r;
 }
 
-// Store kC 16-byte chunks of each lane's row (at base + at; at < 0: no row)
-// through 32 staged rows of 128 bytes.  All 32 lanes call it together.
-template <int kC, class T>
-__device__ __forceinline__ void stage_out(uint8_t* stage, const uint32_t (&o)[32], int64_t at, T* base, int lane) {
+// Store 64 bytes of each lane's row (at base + at; at < 0: no row) through 32
+// staged rows.  All 32 lanes call it together.
+template <class T>
+__device__ __forceinline__ void stage_out(uint8_t* stage, const uint32_t (&w)[16], int64_t at, T* base, int lane) {
 #pragma unroll
-    for (int i = 0; i < kC; ++i)
-        *reinterpret_cast<uint4*>(stage + lane * 128 + ((i ^ (lane & 7)) << 4)) =
-            make_uint4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+    for (int i = 0; i < 4; ++i)
+        *reinterpret_cast<uint4*>(stage + lane * 64 + ((i ^ ((lane >> 1) & 3)) << 4)) =
+            make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
     __syncwarp();
 #pragma unroll
-    for (int i = 0; i < kC; ++i) {
-        const int r = i * (32 / kC) + lane / kC, c = lane % kC;
+    for (int i = 0; i < 4; ++i) {
+        const int r = i * 8 + (lane >> 2), c = lane & 3;
         const int64_t a = __shfl_sync(0xffffffffu, at, r);
-        const uint4 w = *reinterpret_cast<const uint4*>(stage + r * 128 + ((c ^ (r & 7)) << 4));
-        if (a >= 0) reinterpret_cast<uint4*>(base + a)[c] = w;
+        const uint4 v = *reinterpret_cast<const uint4*>(stage + r * 64 + ((c ^ ((r >> 1) & 3)) << 4));
+        if (a >= 0) reinterpret_cast<uint4*>(base + a)[c] = v;
     }
     __syncwarp();
 }
@@ -205,6 +216,7 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
     pdl_trigger();
     auto bar = [&](int i) -> uint32_t { return sbase + L::OFF_BAR + 8u * (uint32_t)i; };
     TileNote* notes = reinterpret_cast<TileNote*>(sgen + L::OFF_NOTE);
+    ItemNote* item_notes = reinterpret_cast<ItemNote*>(sgen + L::OFF_ITEM);
     volatile uint32_t* tmem_slot = reinterpret_cast<volatile uint32_t*>(sgen + L::OFF_TMEM);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(sgen + L::OFF_ABORT);
     auto fail = [&](int role, int tile) {
@@ -218,8 +230,7 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
 
     if (threadIdx.x == 0) {
         *abort_flag = 0;
-        mbar_init(bar(L::B_Q), 128 * kGroups);
-        mbar_init(bar(L::B_ITEM), 128 * kGroups);
+        mbar_init(bar(L::B_Q), 1);
         mbar_init(bar(L::B_ODONE), 1);
         for (int i = 0; i < 2; ++i) {
             mbar_init(bar(L::B_DRAIN + i), 1);
@@ -229,7 +240,7 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
             mbar_init(bar(L::B_PV + i), 1);
         }
         for (int i = 0; i < 4 * NS; ++i) mbar_init(bar(L::B_KF + i), 1);
-        for (int i = 0; i < kNotes; ++i) mbar_init(bar(L::B_NOTE + i), 1);
+        for (int i = 0; i < kNotes + kItemNotes; ++i) mbar_init(bar(L::B_NOTE + i), 1);
         fence_mbar_init();
     }
     if (warp == L::kWarpS) {
@@ -273,9 +284,6 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
             const TileNote& nt = notes[t % kNotes];
             const int flags = nt.flags;
             if (flags & N_FIRST) {
-                // All groups have left the item before: its products are done (each
-                // waited for them) and its rows have left Q's place.
-                mbar_arrive(bar(L::B_ITEM));
                 PagedPlace x{};
                 x.b = nt.b; x.h = nt.h; x.rt = nt.rt; x.n = nt.n; x.len = nt.len;
                 int rb, ri, rh;
@@ -283,34 +291,8 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
                 active = __any_sync(0xffffffffu, valid);
                 lim_own = nt.len;
                 if (p.causal && nt.b >= 0) lim_own = min(nt.len, nt.len - nt.n + ri + 1);
-                m = -INFINITY; l = 0.f; fresh = true;
-                // Q in the K-major 128-byte swizzle.  A warp fetches its 32 rows with
-                // neighbouring lanes on neighbouring chunks of a row (one row a lane
-                // would touch 32 lines with each load).
-                constexpr int kC = D / 8, kR = 32 / kC;   // 16-byte chunks of a row, rows a load covers
-                const int64_t q_at = valid ? rb * p.qsb + rh * p.qsh + ri * p.qsn : -1;
                 o_at = valid ? rb * p.osb + rh * p.osh + ri * p.osn : -1;
-                if (!mbar_wait_warp(bar(L::B_ITEM), items & 1, abort_flag)) {
-                    if (lane == 0) fail(R_ROWS, t);
-                    break;
-                }
-                uint8_t* qs = sgen + L::OFF_Q + X * L::kTile;
-#pragma unroll 1
-                for (int i0 = 0; i0 < kC; i0 += 8) {
-                    uint4 qv[8];
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        const int64_t at = __shfl_sync(0xffffffffu, q_at, (i0 + i) * kR + lane / kC);
-                        qv[i] = at >= 0 ? __ldg(reinterpret_cast<const uint4*>(p.q + at) + lane % kC) : make_uint4(0, 0, 0, 0);
-                    }
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        const int r = (warp & 3) * 32 + (i0 + i) * kR + lane / kC, c = lane % kC;
-                        *reinterpret_cast<uint4*>(qs + (c >> 3) * kBlk + r * 128 + (((c & 7) ^ (r & 7)) << 4)) = qv[i];
-                    }
-                }
-                fence_proxy_async_smem();
-                mbar_arrive(bar(L::B_Q));
+                m = -INFINITY; l = 0.f; fresh = true;
             }
             const int nkeys = nt.nkeys;
             int lim = nkeys;                              // keys of the tile this row sees (may be negative)
@@ -431,25 +413,29 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
                 }
                 tc_fence_after();
                 if (active) {
-                    // 32 channels at a time.  They leave through shared memory (Q's
-                    // place: its products are done), so that a store's lanes share
-                    // lines; a warp stages its own 32 rows.
-                    const float inv = l == 0.f ? 0.f : __fdiv_rn(1.f, l);
-                    const int64_t at = whole ? o_at : (valid ? (row0 + lane) * D : -1);
-                    if (valid && !whole) p.part_ml[row0 + lane] = make_float2(m, l);
-                    uint8_t* stage = sgen + L::OFF_Q + X * L::kTile + (warp & 3) * 4096;
+                    // 64 bytes of each row at a time leave through shared memory, so
+                    // that a store's lanes share lines; a warp stages its own rows.
+                    uint8_t* stage = sgen + L::OFF_STAGE + warp * 2048;
+                    if (whole) {
+                        const float inv = l == 0.f ? 0.f : __fdiv_rn(1.f, l);
 #pragma unroll 1
-                    for (int c = 0; c < D / 32; ++c) {
-                        uint32_t o[32];
-                        tmem_ld32(tO + c * 32, o);
-                        tmem_wait_ld();
-                        if (whole) {
+                        for (int c = 0; c < D / 32; ++c) {
+                            uint32_t o[32], w[16];
+                            tmem_ld32(tO + c * 32, o);
+                            tmem_wait_ld();
 #pragma unroll
                             for (int i = 0; i < 16; ++i)
-                                o[i] = pack2(__uint_as_float(o[2 * i]) * inv, __uint_as_float(o[2 * i + 1]) * inv);
-                            stage_out<4>(stage, o, at, p.o + c * 32, lane);
-                        } else {
-                            stage_out<8>(stage, o, at, p.part_o + c * 32, lane);
+                                w[i] = pack2(__uint_as_float(o[2 * i]) * inv, __uint_as_float(o[2 * i + 1]) * inv);
+                            stage_out(stage, w, o_at, p.o + c * 32, lane);
+                        }
+                    } else {
+                        if (valid) p.part_ml[row0 + lane] = make_float2(m, l);
+#pragma unroll 1
+                        for (int c = 0; c < D / 16; ++c) {
+                            uint32_t o[16];
+                            tmem_ld16(tO + c * 16, o);
+                            tmem_wait_ld();
+                            stage_out(stage, o, valid ? (row0 + lane) * D : -1, p.part_o + c * 16, lane);
                         }
                     }
                 }
@@ -460,7 +446,56 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
     } else if constexpr (kGroups == 2) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
     }
-    if (warp == L::kWarpLoad) {
+    // Fetch an item's Q rows by 16-byte copies,
+    // neighbouring lanes on neighbouring chunks of a row, into the K-major 128-byte
+    // swizzle.  Its place is free once the scores of the tile before are computed,
+    // which is well before that item's output is written.  One warp.
+    auto load_q = [&](const ItemNote& nt) -> bool {
+        const int t = nt.tile;
+        PagedPlace x{};
+        x.b = nt.b; x.h = nt.h; x.rt = nt.rt; x.n = nt.n;
+        if (t > 0 && !mbar_wait_warp(bar(L::B_KE + (t - 1) % NS), ((t - 1) / NS) & 1, abort_flag)) return false;
+        constexpr int kC = D / 8, kR = 32 / kC;           // 16-byte chunks of a row, rows a copy covers
+#pragma unroll 1
+        for (int r0 = 0; r0 < M; r0 += 32) {
+            int rb, ri, rh;
+            const bool in = paged_row(sched, x, r0 + lane, rb, ri, rh);
+            const int64_t q_at = in ? rb * p.qsb + rh * p.qsh + ri * p.qsn : -1;
+#pragma unroll 4
+            for (int i = 0; i < kC; ++i) {
+                const int r = r0 + i * kR + lane / kC, c = lane % kC;
+                const int64_t at = __shfl_sync(0xffffffffu, q_at, i * kR + lane / kC);
+                cp_async16(sbase + L::OFF_Q + (r >> 7) * L::kTile + (c >> 3) * kBlk + (r & 127) * 128 + (((c & 7) ^ (r & 7)) << 4),
+                           at >= 0 ? p.q + at + c * 8 : p.q, at >= 0 ? 16u : 0u);
+            }
+        }
+        return true;
+    };
+    auto q_ready = [&]() {
+        asm volatile("cp.async.wait_all;" ::: "memory");
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(L::B_Q));
+    };
+    if (kGroups == 2 && warp == L::kWarpQ) {
+        // ===================================================== Q loader
+        // Slots of notes are not overrun: item k + 8 begins 8 tiles or more behind
+        // item k, and the loader is at most its stages ahead of the scores.
+        for (int k = 0;; ++k) {
+            const ItemNote& nt = item_notes[k % kItemNotes];
+            if (!mbar_wait_warp(bar(L::B_ITEM + k % kItemNotes), (k / kItemNotes) & 1, abort_flag)) {
+                if (lane == 0) fail(R_LOAD, -1);
+                break;
+            }
+            if (nt.tile >= count) break;                  // no more items
+            if (!load_q(nt)) {
+                if (lane == 0) fail(R_LOAD, nt.tile);
+                break;
+            }
+            q_ready();
+        }
+        asm volatile("cp.async.wait_all;" ::: "memory");
+    } else if (warp == L::kWarpLoad) {
         // ===================================================== TMA producer
         // Whether this worker's run opens inside an item and is the first to do
         // so: then the item is joined from its parts afterwards.
@@ -489,6 +524,12 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
         bool first = true;
         int run0 = at.tile;                               // the item's first tile in this worker
         int loaded_k = 0, loaded_v = 0;                   // tiles whose copies were issued
+        int items = 0;                                    // items noted
+        auto post_item = [&](int t) {                     // lane 0
+            ItemNote& in = item_notes[items % kItemNotes];
+            in.b = at.b; in.h = at.h; in.rt = at.rt; in.n = at.n; in.tile = t;
+            if (kGroups == 2) mbar_arrive(bar(L::B_ITEM + items % kItemNotes));
+        };
         bool ok = true;
 #pragma unroll 1
         for (int t = 0; t < count; ++t) {
@@ -496,8 +537,6 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
             const bool mine = lane < per_tile && (lane << p.page_shift) < span.nkeys;
             const uint32_t bytes = (uint32_t)((span.nkeys + p.page - 1) >> p.page_shift) * (uint32_t)(p.page * 128 * L::kNB);
             const uint32_t off = (uint32_t)(lane * p.page) * 128u;
-            // a page outside the cache: the copy reads zeros there
-            if (mine && (unsigned)page >= (unsigned)p.num_pages && atomicCAS(p.status, 0, kErrPage) == 0) p.status[3] = page;
             if (t >= NS && !mbar_wait_warp(bar(L::B_KE + st), ph ^ 1, abort_flag)) { ok = false; break; }
             if (lane == 0) {
                 TileNote& nt = notes[t % kNotes];
@@ -508,10 +547,14 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
                 nt.slot = p.pre_rt > 0 ? worker + at.item : 2 * worker + (run0 == 0 ? 1 : 0);
                 nt.flags = (first ? N_FIRST : 0) | (last ? N_LAST : 0) | (span.own ? N_OWN : 0) |
                            (p.pre_rt == 0 && run0 == 0 && at.tile + 1 == at.ntiles ? N_WHOLE : 0);
+                if (first) post_item(t);
                 mbar_arrive(bar(L::B_NOTE + t % kNotes));
                 mbar_arrive_expect_tx(bar(L::B_KF + st), bytes);
             }
+            if (first) ++items;
             __syncwarp();
+            // a page outside the cache: the copy reads zeros there
+            if (mine && (unsigned)page >= (unsigned)p.num_pages && atomicCAS(p.status, 0, kErrPage) == 0) p.status[3] = page;
             if (mine) {
 #pragma unroll
                 for (int hb = 0; hb < L::kNB; ++hb)
@@ -519,6 +562,7 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
                                 bar(L::B_KF + st));
             }
             loaded_k = t + 1;
+            if (kGroups == 1 && first && !load_q(item_notes[(items - 1) % kItemNotes])) { ok = false; break; }
             if (t >= NS && !mbar_wait_warp(bar(L::B_VE + st), ph ^ 1, abort_flag)) { ok = false; break; }
             if (lane == 0) mbar_arrive_expect_tx(bar(L::B_VF + st), bytes);
             __syncwarp();
@@ -529,6 +573,7 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
                                 bar(L::B_VF + st));
             }
             loaded_v = t + 1;
+            if (kGroups == 1 && first) q_ready();
             if (t + 1 < count) {
                 const int item = at.item;
                 paged_next(sched, at);
@@ -540,6 +585,9 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
         }
         if (!ok && lane == 0) fail(R_LOAD, loaded_v);
         __syncwarp();
+        // (its slot is free for the same reason)
+        if (kGroups == 2 && ok && lane == 0) post_item(count);
+        asm volatile("cp.async.wait_all;" ::: "memory");
         // every copy issued lands before the CTA may exit
         const int zero = 0;
         for (int i = 0; i < NS; ++i) {
@@ -562,7 +610,7 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
             const int t = u / kGroups, st = t % NS, X = u % kGroups;
             if (X == 0) {
                 if (!mbar_spin_warp(bar(L::B_KF + st), (t / NS) & 1, abort_flag)) return false;
-                // a new item's Q: written when the item before is through
+                // a new item's Q
                 if (notes[t % kNotes].flags & N_FIRST) {
                     if (!mbar_spin_warp(bar(L::B_Q), items & 1, abort_flag)) return false;
                     ++items;
