@@ -132,20 +132,31 @@ int take_fault_mode() {
     return mode;
 }
 
-int encode_pages(CUtensorMap* m, const sage_tensor& t, int D, int page, int heads, int pages) {
+static int encode_4d(CUtensorMap* m, const void* base, const uint64_t (&dims)[4], const int64_t (&strides)[3],
+                     const uint32_t (&box)[4]) {
     EncodeTiledFn fn = encode_fn();
     if (!fn) return SAGE_ERR_DRIVER;
-    cuuint64_t dims[4] = {(cuuint64_t)D, (cuuint64_t)page, (cuuint64_t)heads, (cuuint64_t)pages};
+    cuuint64_t dm[4], st[3];
+    cuuint32_t bx[4], estr[4] = {1, 1, 1, 1};
+    for (int i = 0; i < 4; ++i) { dm[i] = dims[i]; bx[i] = box[i]; }
     // the stride of an axis of one entry is never used; any legal value does
-    cuuint64_t strides[3] = {(cuuint64_t)t.stride_n * 2, heads > 1 ? (cuuint64_t)t.stride_h * 2 : (cuuint64_t)D * 2,
-                             pages > 1 ? (cuuint64_t)t.stride_b * 2 : (cuuint64_t)D * 2};
-    cuuint32_t box[4] = {64, (cuuint32_t)page, 1, 1};
-    cuuint32_t estr[4] = {1, 1, 1, 1};
-    return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(t.ptr), dims, strides, box, estr,
+    for (int i = 0; i < 3; ++i) st[i] = dims[i + 1] > 1 ? (cuuint64_t)strides[i] * 2 : (cuuint64_t)dims[0] * 2;
+    return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base), dm, st, bx, estr,
               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
                ? SAGE_OK
                : SAGE_ERR_UNSUPPORTED;
+}
+
+int encode_pages(CUtensorMap* m, const sage_tensor& t, int D, int page, int heads, int pages) {
+    return encode_4d(m, t.ptr, {(uint64_t)D, (uint64_t)page, (uint64_t)heads, (uint64_t)pages},
+                     {t.stride_n, t.stride_h, t.stride_b}, {64u, (uint32_t)page, 1u, 1u});
+}
+
+int encode_rows(CUtensorMap* m, const sage_tensor& t, int D, int H, int Nq, int B, int heads, int tokens, int requests) {
+    return encode_4d(m, t.ptr, {(uint64_t)D, (uint64_t)H, (uint64_t)Nq, (uint64_t)B},
+                     {t.stride_h, t.stride_n, t.stride_b},
+                     {64u, (uint32_t)heads, (uint32_t)tokens, (uint32_t)requests});
 }
 
 }  // namespace sage

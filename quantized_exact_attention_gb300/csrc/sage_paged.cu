@@ -107,7 +107,7 @@ __global__ void __launch_bounds__(kRowWarps * 32, 2) paged_rows_kernel(const __g
     const int worker = warp * gridDim.x + blockIdx.x;
     const int total = paged_scan<M, kStep, kRowWarps * 32, kRowWarps>(sched, blockIdx.x, gridDim.x, found, warp_sums,
                                                                       blockIdx.x == 0);
-    const int per = sched.per_worker(total);
+    const int per = paged_per_worker(p, total);
     if ((int64_t)worker * per >= total || worker >= p.workers) {
         pdl_wait();
         return;
@@ -124,7 +124,7 @@ __global__ void __launch_bounds__(kRowWarps * 32, 2) paged_rows_kernel(const __g
     // Read the page number of the next step (one step before its copies, so
     // that the table's latency lies behind a step of computing).
     auto fetch = [&]() {
-        span = paged_span(sched, at);
+        span = paged_span(sched, at.b, at.len, at.tile);
         const int j = span.key0 >> p.page_shift;
         page = span.own ? __ldg(p.table + (int64_t)at.b * p.table_stride + j) : __ldg(p.ptable + j);
     };
@@ -171,9 +171,7 @@ __global__ void __launch_bounds__(kRowWarps * 32, 2) paged_rows_kernel(const __g
     // Leave the item's partial result.
     auto leave = [&]() {
         const int64_t slot = (int64_t)worker + item;
-        PagedPlace x{};
-        x.b = ib; x.h = ih; x.rt = irt;
-        if (ib >= 0) x.n = sched.q_rows(ib);
+        const int n = ib >= 0 ? sched.q_rows(ib) : 0;
 #pragma unroll
         for (int nr = 0; nr < NR; ++nr) {
 #pragma unroll
@@ -184,7 +182,7 @@ __global__ void __launch_bounds__(kRowWarps * 32, 2) paged_rows_kernel(const __g
                 s += __shfl_xor_sync(0xffffffffu, s, 16);
                 const int r = nr * 8 + (lane & 3) * 2 + e;
                 int b, i, hq;
-                if (!paged_row(sched, x, r, b, i, hq)) continue;
+                if (!paged_row(sched, ib, ih, irt, n, r, b, i, hq)) continue;
                 if (lane < 4) p.part_ml[slot * M + r] = make_float2(m[nr][e], s);
                 float* dst = p.part_o + (slot * M + r) * D + (lane >> 2);
 #pragma unroll
@@ -197,13 +195,11 @@ __global__ void __launch_bounds__(kRowWarps * 32, 2) paged_rows_kernel(const __g
     };
     auto enter = [&](const StepNote& nt) {
         item = nt.item; ib = nt.b; ih = nt.h; irt = nt.rt;
-        PagedPlace x{};
-        x.b = ib; x.h = ih; x.rt = irt;
-        if (ib >= 0) { x.n = sched.q_rows(ib); x.len = sched.own_keys(ib); }
+        const int n = ib >= 0 ? sched.q_rows(ib) : 0, len = ib >= 0 ? sched.own_keys(ib) : 0;
 #pragma unroll
         for (int nr = 0; nr < NR; ++nr) {
             int b, i, hq;
-            const bool in = paged_row(sched, x, nr * 8 + (lane >> 2), b, i, hq);
+            const bool in = paged_row(sched, ib, ih, irt, n, nr * 8 + (lane >> 2), b, i, hq);
             const uint16_t* qp = p.q + (in ? b * p.qsb + hq * p.qsh + i * p.qsn : 0) + (lane & 3) * 2;
 #pragma unroll
             for (int j = 0; j < D / 16; ++j) {
@@ -216,10 +212,10 @@ __global__ void __launch_bounds__(kRowWarps * 32, 2) paged_rows_kernel(const __g
             for (int e = 0; e < 2; ++e) {
                 m[nr][e] = -INFINITY;
                 l[nr][e] = 0.f;
-                lim[nr][e] = x.len;
+                lim[nr][e] = len;
                 if (ib >= 0 && p.causal) {
                     const int rr = irt * M + nr * 8 + (lane & 3) * 2 + e;
-                    lim[nr][e] = min(x.len, x.len - x.n + rr / p.G + 1);
+                    lim[nr][e] = min(len, len - n + fast_div(rr, p.by_G) + 1);
                 }
             }
         }
@@ -338,33 +334,36 @@ __global__ void __launch_bounds__(256) paged_join_kernel(const __grid_constant__
     const int hq = row / p.Nq, i = row - hq * p.Nq;
     const int n = s.q_rows(b), len = s.own_keys(b);
     const bool live = hq < p.H && i < n;
-    const int h = hq / p.G, r = i * p.G + (hq - h * p.G), rt = r / M;
+    const int h = fast_div(hq, p.by_G), r = i * p.G + (hq - h * p.G), rt = r / M;
     pdl_wait();                                            // the parts are written
     float acc[V], m = -INFINITY, l = 0.f;
 #pragma unroll
     for (int v = 0; v < V; ++v) acc[v] = 0.f;
     if (live) {
-        const int per = s.per_worker(__ldcg(p.start + p.B));
-        int at = __ldcg(p.start + b), per_head = 0, nt = 0;
-#pragma unroll 1
-        for (int x = 0; x < p.rt; ++x) {
-            const int k = s.item_tiles(n, len, x);
-            if (x < rt) at += k;
-            if (x == rt) nt = k;
-            per_head += k;
-        }
-        const RowParts own = parts_of(at + h * per_head, nt, per, p.pre_rt * p.Hkv + (b * p.Hkv + h) * p.rt + rt);
+        const int per = paged_per_worker(p, __ldcg(p.start + p.B * p.rt));
+        const int nt = s.item_tiles(n, len, rt), pair = b * p.rt + rt;
+        const RowParts own = parts_of(__ldcg(p.start + pair) + h * nt, nt, per, (p.pre_rt + pair) * p.Hkv + h);
         const int64_t own_q = own.slot0 * M + (r - rt * M);
         RowParts pre{0, 0};
         int64_t pre_q = 0;
         if (p.pre_items_rt > 0) {
-            const int rr = (b * p.Nq + i) * p.G + (hq - h * p.G), prt = rr / p.pre_m;
-            const int it = h * p.pre_items_rt + prt;
-            const int pt = (s.lp + p.pre_tk - 1) / p.pre_tk;
+            // the row set of the prefix's list that holds this row, and its place there
+            const int rest = r, pt = (s.lp + p.pre_tk - 1) / p.pre_tk;
+            int set, place;
+            if (p.pre_tok > 0) {
+                const int group = b / p.pre_tok;
+                set = group * 128 / p.pre_m;
+                place = group * 128 - set * p.pre_m + (b - group * p.pre_tok) * p.Nq * p.G + rest;
+            } else {
+                const int rr = b * p.Nq * p.G + rest;
+                set = rr / p.pre_m;
+                place = rr - set * p.pre_m;
+            }
+            const int it = set * p.Hkv + h;
             // alone in its list, or at the front of this one
             const int pre_per = p.pre_rt > 0 ? per : max(1, (p.Hkv * p.pre_items_rt * pt + p.pre_workers - 1) / p.pre_workers);
             pre = parts_of(it * pt, pt, pre_per, it);
-            pre_q = pre.slot0 * p.pre_m + (rr - prt * p.pre_m);
+            pre_q = pre.slot0 * p.pre_m + place;
         }
         const int parts = own.n + pre.n;
 #pragma unroll 1
@@ -448,6 +447,8 @@ __global__ void __launch_bounds__(256) paged_join_kernel(const __grid_constant__
 // A request brings rows = Nq * G query rows to a key head.
 //  - rows > 32: the many-rows kernel, each request's keys behind the prefix
 //    (one list; the prefix is read again for every request, mostly from L2).
+//    More than 128 query heads to a key head leave no whole token in a group:
+//    these, which no model is known to have, stay with the few-rows kernel.
 //  - rows <= 32: the few-rows kernel for the own keys.  The prefix, when
 //    several requests share it, is read once for all their rows: by the
 //    few-rows kernel in the same list when all rows together are 32 or
@@ -461,30 +462,33 @@ struct Lists {
     int groups;                          // ... 128-row groups of an item
     int nr;                              // few-rows kernel: 8-row groups of an item
     int M, rt, join;
+    int tok, unit;                       // many-rows kernel: tokens of a 128-row group, rows of a token
     int pre_rt;                          // shared prefix items in this list
     int64_t slots;
     // the prefix's own list (many-rows kernel)
     bool pre;
     int pre_groups;
-    int pre_M, pre_items_rt;
+    int pre_M, pre_items_rt, pre_tok, pre_unit;
     int64_t pre_slots;
 };
 
 Lists make_lists(int B, int Hkv, int G, int Nq, bool prefix) {
     Lists x{};
     const int64_t rows = (int64_t)Nq * G, all = rows * B;
-    if (rows > kFewRows) {
+    if (rows > kFewRows && G <= 128) {
         x.tiles = true;
-        x.groups = rows <= 128 ? 1 : 2;
+        x.unit = G;
+        x.tok = 128 / G;
+        x.groups = Nq <= x.tok ? 1 : 2;
         x.M = 128 * x.groups;
-        x.rt = (int)ceil_div(rows, x.M);
+        x.rt = (int)ceil_div(Nq, x.tok * x.groups);
         x.join = prefix;
         x.slots = 2 * kMaxTileWorkers * (3 - x.groups);
         return x;
     }
-    const bool shared = prefix && B > 1;
+    const bool shared = prefix && B > 1 && rows <= kFewRows;
     const int64_t most = shared && all <= kFewRows ? all : rows;
-    x.nr = most <= 8 ? 1 : (most <= 16 ? 2 : 4);
+    x.nr = most <= 8 ? 1 : (most <= 16 ? 2 : 4);             // more than 32 rows: several sets
     x.M = 8 * x.nr;
     x.rt = (int)ceil_div(rows, x.M);
     x.join = prefix && !shared;
@@ -495,9 +499,11 @@ Lists make_lists(int B, int Hkv, int G, int Nq, bool prefix) {
         x.slots += (int64_t)Hkv * x.pre_rt;
     } else if (shared) {
         x.pre = true;
-        x.pre_groups = all <= 128 ? 1 : 2;
+        x.pre_unit = (int)rows;
+        x.pre_tok = 128 / x.pre_unit;
+        x.pre_groups = B <= x.pre_tok ? 1 : 2;
         x.pre_M = 128 * x.pre_groups;
-        x.pre_items_rt = (int)ceil_div(all, x.pre_M);
+        x.pre_items_rt = (int)ceil_div(B, x.pre_tok * x.pre_groups);
         x.pre_slots = (int64_t)Hkv * x.pre_items_rt + kMaxTileWorkers * (3 - x.pre_groups);
     }
     return x;
@@ -505,7 +511,7 @@ Lists make_lists(int B, int Hkv, int G, int Nq, bool prefix) {
 
 size_t slot_bytes(int64_t slots, int M, int D) { return (size_t)slots * M * (D * 4 + 8); }
 size_t lists_bytes(const Lists& x, int B, int D) {
-    const size_t index = x.tiles ? 2 * kMaxTileWorkers * sizeof(int4) : (((size_t)B + 1) * 4 + 15) / 16 * 16;
+    const size_t index = x.tiles ? (size_t)2 * kMaxTileWorkers * sizeof(int4) : (((size_t)B * x.rt + 1) * 4 + 15) / 16 * 16;
     return slot_bytes(x.slots, x.M, D) + slot_bytes(x.pre_slots, x.pre_M, D) + index;
 }
 
@@ -589,7 +595,14 @@ int sage_attn_paged(const sage_tensor* q, const sage_tensor* o, const sage_page_
     if (rc != SAGE_OK) return rc;
     const int D = cache->D;
     if ((rc = check_batch(B, H, cache->heads, Nq, D)) != SAGE_OK) return rc;
-    if ((rc = check_view(q)) != SAGE_OK || (rc = check_view(o)) != SAGE_OK) return rc;
+    for (const sage_tensor* t : {q, o}) {
+        if ((rc = check_view(t)) != SAGE_OK) return rc;
+        // rows apart (no broadcast axis), and byte strides that a tensor map holds
+        if ((B > 1 && t->stride_b < D) || (H > 1 && t->stride_h < D) || (Nq > 1 && t->stride_n < D))
+            return SAGE_ERR_UNSUPPORTED;
+        for (int64_t st : {t->stride_b, t->stride_h, t->stride_n})
+            if (st >= (int64_t(1) << 38)) return SAGE_ERR_UNSUPPORTED;
+    }
     if (table_width < 0 || prefix_width < 0 || (table_width > 0 && table == nullptr) ||
         (prefix_width > 0 && prefix_table == nullptr) || table_stride < 0)
         return SAGE_ERR_ARG;
@@ -608,9 +621,12 @@ int sage_attn_paged(const sage_tensor* q, const sage_tensor* o, const sage_page_
     p.status = device_status_ptr();
     const int sms = sm_count();
     if (p.status == nullptr || sms == 0) return SAGE_ERR_LAUNCH;
-    CUtensorMap mk, mv;
+    CUtensorMap mq, mk, mv;
     if (x.tiles || x.pre) {
-        if ((rc = encode_pages(&mk, cache->k, D, cache->page_size, cache->heads, cache->num_pages)) != SAGE_OK ||
+        // q in boxes of whole tokens; for the prefix's items, of whole requests
+        const int heads = H / cache->heads;
+        if ((rc = encode_rows(&mq, *q, D, H, Nq, B, heads, x.tiles ? x.tok : Nq, x.tiles ? 1 : x.pre_tok)) != SAGE_OK ||
+            (rc = encode_pages(&mk, cache->k, D, cache->page_size, cache->heads, cache->num_pages)) != SAGE_OK ||
             (rc = encode_pages(&mv, cache->v, D, cache->page_size, cache->heads, cache->num_pages)) != SAGE_OK)
             return rc;
         p.fault_mode = take_fault_mode();
@@ -633,6 +649,11 @@ int sage_attn_paged(const sage_tensor* q, const sage_tensor* o, const sage_page_
     const double scale = sm_scale > 0.f ? (double)sm_scale : 1.0 / std::sqrt((double)D);
     p.sc = (float)(scale * (1.0 / std::log(2.0)));
     p.rt = x.rt; p.pre_rt = x.pre_rt; p.join = x.join;
+    p.tok = x.tok; p.unit = x.unit;
+    p.by_G = make_fast_div(p.G);
+    p.by_rows = make_fast_div(Nq * p.G);
+    p.by_rt = make_fast_div(x.rt);
+    p.by_unit = make_fast_div(x.unit > 0 ? x.unit : 1);
     char* w = static_cast<char*>(workspace);
     auto take = [&](size_t n) { char* at = w; w += n; return at; };
     p.part_o = reinterpret_cast<float*>(take((size_t)x.slots * x.M * D * 4));
@@ -647,20 +668,21 @@ int sage_attn_paged(const sage_tensor* q, const sage_tensor* o, const sage_page_
     else p.start = reinterpret_cast<int32_t*>(w);
     const int ctas = std::min(sms, kMaxTileWorkers);       // one per SM; of one row group: two
     p.pre_items_rt = x.pre_items_rt; p.pre_m = x.pre_M; p.pre_tk = x.pre ? 128 : kStep;
-    p.pre_workers = ctas * (3 - x.pre_groups);
+    p.pre_workers = ctas * (3 - x.pre_groups); p.pre_tok = x.pre_tok;
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
     cudaError_t e;
     int launches = 0;
     if (x.tiles) {
         p.workers = ctas * (3 - x.groups);
-        e = launch_paged_tiles(p, D, x.groups, mk, mv, s);
+        e = launch_paged_tiles(p, D, x.groups, mq, mk, mv, s);
         launches = 2;
     } else {
         if (x.pre) {
             PagedParams pp = p;
             pp.part_o = p.pre_o; pp.part_ml = p.pre_ml; pp.start = nullptr; pp.cuts = nullptr;
+            pp.tok = x.pre_tok; pp.unit = x.pre_unit; pp.by_unit = make_fast_div(x.pre_unit);
             pp.rt = 0; pp.pre_rt = x.pre_items_rt; pp.workers = p.pre_workers;
-            if (launch_paged_tiles(pp, D, x.pre_groups, mk, mv, s) != cudaSuccess) return SAGE_ERR_LAUNCH;
+            if (launch_paged_tiles(pp, D, x.pre_groups, mq, mk, mv, s) != cudaSuccess) return SAGE_ERR_LAUNCH;
             ++launches;
         }
         p.workers = std::min(2 * sms, kMaxRowWorkers / kRowWarps) * kRowWarps;

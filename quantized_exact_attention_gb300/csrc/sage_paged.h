@@ -14,6 +14,18 @@ constexpr int kErrPage = -7;             // SAGE_ERR_PAGE as the kernels record 
 constexpr int kMaxRowWorkers = 1280;     // warps of the few-rows kernel that take work (8 per SM, 160 SMs at most)
 constexpr int kMaxTileWorkers = 160;     // CTAs of the many-rows kernel with two row groups (1 per SM); with one: twice that
 
+// Division by a constant the host knows: (umulhi(n, m) + n) >> s = n / d for
+// 0 <= n < 2^31, with s = ceil(log2 d) and m = floor(2^32 (2^s - d) / d) + 1
+// (Granlund and Montgomery's round-up reciprocal).
+struct FastDiv {
+    uint32_t m, s;
+};
+inline FastDiv make_fast_div(uint32_t d) {
+    uint32_t s = 0;
+    while ((uint64_t(1) << s) < d) ++s;
+    return FastDiv{(uint32_t)(((((uint64_t(1) << s) - d) << 32) / d) + 1), s};
+}
+
 struct PagedParams {
     const uint16_t* q;                   // BF16 bit patterns
     uint16_t* o;
@@ -34,8 +46,10 @@ struct PagedParams {
     float sc;                            // sm_scale * log2(e)
     int* status;
     // schedule (see sage_paged_sched.cuh)
-    int rt;                              // row tiles of a request's rows
-    int pre_rt;                          // row tiles of all requests' rows against the prefix (0: not in this list)
+    int rt;                              // row sets of a request
+    int pre_rt;                          // row sets of all requests against the prefix (0: not in this list)
+    int tok, unit;                       // tiles kernel: tokens (prefix items: requests) of a group, rows of one
+    FastDiv by_G, by_rows, by_rt, by_unit;           // G, Nq * G, rt, unit
     int join;                            // 1: a request's key sequence is the prefix followed by its own keys
     int workers;                         // workers the list is shared among
     int fault_mode;                      // test hook: 0 = none
@@ -43,21 +57,25 @@ struct PagedParams {
     float* part_o;                       // [slot][M][D]
     float2* part_ml;                     // [slot][M] running maximum (log2 domain) and sum
     int4* cuts;                          // [workers] items that a worker boundary cuts (null: not wanted)
-    int32_t* start;                      // [B + 1] list position of each request's first tile; [B] = total
+    int32_t* start;                      // [B rt + 1] list position of each (request, row set); last: the length
     // the list that holds the shared prefix's items, for the join
     float* pre_o;
     float2* pre_ml;
-    int pre_items_rt, pre_m, pre_tk, pre_workers;    // row tiles (0: none), rows of an item, keys of a tile, workers
+    int pre_items_rt, pre_m, pre_tk, pre_workers;    // row sets (0: none), rows of an item, keys of a tile, workers
+    int pre_tok;                         // requests of a 128-row group (0: rows after one another)
 };
 
 // The many-rows kernel (sage_paged_tiles.cu): workers = CTAs, groups: row groups
 // of 128 of an item (1 or 2).  Writes whole rows unless the list holds shared
 // prefix items; then every result is partial.
-cudaError_t launch_paged_tiles(const PagedParams& p, int D, int groups, const CUtensorMap& tk, const CUtensorMap& tv,
-                               cudaStream_t s);
+cudaError_t launch_paged_tiles(const PagedParams& p, int D, int groups, const CUtensorMap& tq, const CUtensorMap& tk,
+                               const CUtensorMap& tv, cudaStream_t s);
 
 // Tensor map over one tensor of a page cache, box: one page of one head, 64 channels (sage_api.cu).
 int encode_pages(CUtensorMap* m, const sage_tensor& t, int D, int page, int heads, int pages);
+// Tensor map over q [B, H, Nq, D] as (channel, head, token, request), box: 64
+// channels of `heads` heads, `tokens` tokens and `requests` requests.
+int encode_rows(CUtensorMap* m, const sage_tensor& t, int D, int H, int Nq, int B, int heads, int tokens, int requests);
 // The fault the next launch has to make (test hook), taken once (sage_api.cu).
 int take_fault_mode();
 

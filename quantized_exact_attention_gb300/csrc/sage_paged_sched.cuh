@@ -1,19 +1,25 @@
 // sage_paged_sched.cuh - how the paged attention kernels share their work.
 //
-// The work is a list of items.  An item is a set of up to M query rows of one
-// key head and the key sequence they read, cut into tiles of TK keys.  The
-// list holds, in this order,
-//   (1) for each key head and each M rows of ALL requests' rows: the shared
-//       prefix (only when the prefix is computed once for all: pre_rt > 0);
-//   (2) for each request, key head and M rows of that request: its own keys,
-//       preceded by the prefix when join = 1.
+// The work is a list of items.  An item is a set of query rows of one key head
+// and the key sequence they read, cut into tiles of TK keys.  The list holds,
+// in this order,
+//   (1) for each set of rows out of ALL requests' rows, and each key head: the
+//       shared prefix (only when the prefix is computed once for all);
+//   (2) for each request, each set of its rows, and each key head: its own
+//       keys, preceded by the prefix when join = 1.
 // The tiles of the list, numbered through, are cut into equal runs, one for
 // each worker (a warp or a CTA).  So the split follows the lengths that the
 // device holds: a long sequence is shared among many workers, several short
 // ones fall to a single worker, and no host value depends on the lengths.
 // A worker leaves a partial result (running maximum, sum and unnormalised
-// output) for each item it touches, in slot worker + item: along the list
-// either the worker or the item advances by one, so the slots are distinct.
+// output) for an item it shares, in slot worker + item: along the list either
+// the worker or the item advances by one, so the slots are distinct.
+//
+// Sets of rows, in the order of query token, then query head of the key head:
+//   rows kernel (TK = 16): M rows after one another;
+//   tiles kernel (TK = 128): groups of 128 rows that hold whole tokens (of the
+//   shared prefix's items: whole requests), `tok` of them, so that a group is
+//   one box of a tensor map; the rows left over stay empty.
 #pragma once
 
 #include "sage_paged.h"
@@ -26,11 +32,14 @@ __device__ __forceinline__ int paged_clamp(const int32_t* lens, int b, int n) {
     return v < 0 ? 0 : (v > n ? n : v);
 }
 
+// n / d for 0 <= n < 2^31 (FastDiv, made by the host).
+__device__ __forceinline__ int fast_div(int n, const FastDiv& f) {
+    return (int)((__umulhi((uint32_t)n, f.m) + (uint32_t)n) >> f.s);
+}
+
 template <int M, int TK>
 struct PagedSched {
-    // The 128-key lists' worker writes whole rows itself, so rows that see no
-    // key have a tile too (with no visible key: zeros).
-    static constexpr bool kWholeRows = TK == 128;
+    static constexpr bool kTiles = TK == 128;
     const PagedParams& p;
     int lp;                              // prefix length
     __device__ explicit PagedSched(const PagedParams& pp) : p(pp) {
@@ -40,69 +49,49 @@ struct PagedSched {
     __device__ int own_keys(int b) const { return paged_clamp(p.kv_len, b, p.W * p.page); }
     __device__ int pre_tiles() const { return (lp + TK - 1) / TK; }
     __device__ int pre_total() const { return p.pre_rt * p.Hkv * pre_tiles(); }
-    // own keys that some row of row tile rt sees (n query tokens, len own keys)
-    __device__ int own_end(int n, int len, int rt) const {
-        const int rows = n * p.G;
-        if (rt * M >= rows) return 0;
-        if (!p.causal) return len;
-        const int last = (min(rt * M + M, rows) - 1) / p.G;
-        return max(0, min(len, len - n + last + 1));
-    }
+    // Tiles of row set rt of a request with n query tokens and len own keys.
     __device__ int item_tiles(int n, int len, int rt) const {
-        if (rt * M >= n * p.G) return 0;
-        const int nt = (own_end(n, len, rt) + TK - 1) / TK + (p.join ? pre_tiles() : 0);
-        return kWholeRows ? max(nt, 1) : nt;
+        int last;                        // last token of the set that exists
+        if constexpr (kTiles) {
+            const int toks = p.tok * (M / 128);
+            if (rt * toks >= n) return 0;
+            last = min((rt + 1) * toks, n) - 1;
+        } else {
+            if (rt * M >= n * p.G) return 0;
+            last = rt + 1 == p.rt ? n - 1 : min(fast_div(rt * M + M - 1, p.by_G), n - 1);
+        }
+        const int end = p.causal ? max(0, min(len, len - n + last + 1)) : len;      // own keys that some row sees
+        const int nt = (end + TK - 1) / TK + (p.join ? pre_tiles() : 0);
+        // the tiles kernel writes whole rows itself, so rows that see no key
+        // have a tile too (with no visible key: zeros)
+        return kTiles ? max(nt, 1) : nt;
     }
-    // tiles of one key head of request b
-    __device__ int head_tiles(int b) const {
-        const int n = q_rows(b), len = own_keys(b);
-        if (p.rt == 1) return item_tiles(n, len, 0);
-        int s = 0;
-#pragma unroll 1
-        for (int rt = 0; rt < p.rt; ++rt) s += item_tiles(n, len, rt);
-        return s;
-    }
-    // tiles of one worker, given the length of the list
-    __device__ int per_worker(int total) const { return max(1, (total + p.workers - 1) / p.workers); }
 };
-
-// A place in the list.  b = -1: a prefix item (rt counts its row tiles).
-struct PagedPlace {
-    int b, h, rt;
-    int tile, ntiles;                    // tile of the item, tiles of the item
-    int n, len;                          // the request's query tokens and own keys
-    int item;                            // number of the item in the list
-};
-
-template <int M, int TK>
-__device__ __forceinline__ void paged_enter(const PagedSched<M, TK>& s, PagedPlace& x) {
-    const PagedParams& p = s.p;
-    if (x.b < 0) {
-        x.ntiles = s.pre_tiles();
-        x.item = x.h * p.pre_rt + x.rt;
-    } else {
-        x.ntiles = s.item_tiles(x.n, x.len, x.rt);
-        x.item = p.pre_rt * p.Hkv + (x.b * p.Hkv + x.h) * p.rt + x.rt;
-    }
-}
 
 // The length of the list, and where the CTA's workers begin.  A block of
-// THREADS threads sums the requests' tiles, thread t those of requests
-// [t*cb, (t+1)*cb); the thread whose requests hold the first tile of worker
-// first_worker + w*worker_step (w < NW) leaves {request, list position of its
-// first tile} in found[w] ({-1, 0}: among the prefix items).  With `publish`
-// the positions of all requests go to p.start as well.  `red` holds THREADS/32
-// ints.  Ends with a barrier.
+// THREADS threads sums the tiles of the (request, row set) pairs; the thread
+// whose pairs hold the first tile of worker first_worker + w*worker_step
+// (w < NW) leaves {pair, list position of its first tile} in found[w]
+// ({-1, 0}: among the prefix items).  With `publish` the positions of all
+// pairs go to p.start as well.  `red` holds THREADS/32 ints.  Ends with a
+// barrier.
 template <int M, int TK, int THREADS, int NW>
 __device__ __forceinline__ int paged_scan(const PagedSched<M, TK>& s, int first_worker, int worker_step, int2* found,
                                           int* red, bool publish) {
     const PagedParams& p = s.p;
     const int t = threadIdx.x, lane = t & 31, w = t >> 5;
-    const int cb = (p.B + THREADS - 1) / THREADS;
-    const int b0 = min(t * cb, p.B), b1 = min(b0 + cb, p.B);
+    const int pairs = p.B * p.rt, cb = (pairs + THREADS - 1) / THREADS;
+    const int u0 = min(t * cb, pairs), u1 = min(u0 + cb, pairs);
+    const int b0 = p.rt > 1 ? fast_div(u0, p.by_rt) : u0;
     int mine = 0;
+    {
+        int b = b0, rt = u0 - b0 * p.rt;
 #pragma unroll 1
-    for (int b = b0; b < b1; ++b) mine += s.head_tiles(b) * p.Hkv;
+        for (int u = u0; u < u1; ++u) {
+            mine += s.item_tiles(s.q_rows(b), s.own_keys(b), rt) * p.Hkv;
+            if (++rt == p.rt) { rt = 0; ++b; }
+        }
+    }
     int inc = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -119,62 +108,60 @@ __device__ __forceinline__ int paged_scan(const PagedSched<M, TK>& s, int first_
         total += red[i];
     }
     base += inc - mine;
-    const int per = s.per_worker(total);
-    if (cb == 1 && !publish) {
+    const int per = max(1, (total + p.workers - 1) / p.workers);
+    int b = b0, rt = u0 - b0 * p.rt;
+#pragma unroll 1
+    for (int u = u0; u < u1; ++u) {
+        const int n = cb == 1 ? mine : s.item_tiles(s.q_rows(b), s.own_keys(b), rt) * p.Hkv;
 #pragma unroll
         for (int k = 0; k < NW; ++k) {
             const int at = (first_worker + k * worker_step) * per;
-            if (at >= base && at - base < mine) found[k] = make_int2(b0, base);
+            if (at >= base && at - base < n) found[k] = make_int2(u, base);
         }
-    } else {
-#pragma unroll 1
-        for (int b = b0; b < b1; ++b) {
-            const int n = s.head_tiles(b) * p.Hkv;
-#pragma unroll 1
-            for (int k = 0; k < NW; ++k) {
-                const int at = (first_worker + k * worker_step) * per;
-                if (at >= base && at - base < n) found[k] = make_int2(b, base);
-            }
-            if (publish) p.start[b] = base;
-            base += n;
-        }
-        if (publish && t == 0) p.start[p.B] = total;
+        if (publish) p.start[u] = base;
+        base += n;
+        if (++rt == p.rt) { rt = 0; ++b; }
     }
+    if (publish && t == 0) p.start[pairs] = total;
     __syncthreads();
     return total;
 }
+
+// Tiles of one worker, given the length of the list.
+__device__ __forceinline__ int paged_per_worker(const PagedParams& p, int total) {
+    return max(1, (total + p.workers - 1) / p.workers);
+}
+
+// A place in the list.  b = -1: a prefix item (rt counts its row sets).
+struct PagedPlace {
+    int b, h, rt;
+    int tile, ntiles;                    // tile of the item, tiles of the item
+    int n, len;                          // the request's query tokens and own keys
+    int item;                            // number of the item in the list
+};
 
 // The place of list position t (t < total), with paged_scan's finding.
 template <int M, int TK>
 __device__ __forceinline__ PagedPlace paged_place(const PagedSched<M, TK>& s, int2 found, int t) {
     const PagedParams& p = s.p;
     PagedPlace x{};
-    x.b = found.x;
-    if (x.b < 0) {
-        const int nt = s.pre_tiles();
-        x.item = t / nt;
-        x.tile = t - x.item * nt;
-        x.h = x.item / p.pre_rt;
-        x.rt = x.item - x.h * p.pre_rt;
-        x.ntiles = nt;
+    if (found.x < 0) {
+        x.b = -1;
+        x.ntiles = s.pre_tiles();
+        x.item = t / x.ntiles;
+        x.tile = t - x.item * x.ntiles;
+        x.rt = x.item / p.Hkv;
+        x.h = x.item - x.rt * p.Hkv;
         return x;
     }
+    x.b = p.rt > 1 ? fast_div(found.x, p.by_rt) : found.x;
+    x.rt = found.x - x.b * p.rt;
     x.n = s.q_rows(x.b);
     x.len = s.own_keys(x.b);
-    int per_head = 0;
-#pragma unroll 1
-    for (int rt = 0; rt < p.rt; ++rt) per_head += s.item_tiles(x.n, x.len, rt);
-    int at = t - found.y;
-    x.h = at / per_head;
-    at -= x.h * per_head;
-#pragma unroll 1
-    for (x.rt = 0; x.rt < p.rt; ++x.rt) {
-        const int nt = s.item_tiles(x.n, x.len, x.rt);
-        if (at < nt) break;
-        at -= nt;
-    }
-    x.tile = at;
-    paged_enter(s, x);
+    x.ntiles = s.item_tiles(x.n, x.len, x.rt);
+    x.h = (t - found.y) / x.ntiles;
+    x.tile = t - found.y - x.h * x.ntiles;
+    x.item = (p.pre_rt + found.x) * p.Hkv + x.h;
     return x;
 }
 
@@ -184,22 +171,20 @@ __device__ __forceinline__ void paged_next(const PagedSched<M, TK>& s, PagedPlac
     const PagedParams& p = s.p;
     if (++x.tile < x.ntiles) return;
     x.tile = 0;
-    do {
-        if (x.b < 0) {
-            if (++x.rt == p.pre_rt) {
-                x.rt = 0;
-                if (++x.h == p.Hkv) { x.h = 0; x.b = 0; x.n = s.q_rows(0); x.len = s.own_keys(0); }
-            }
-        } else if (++x.rt == p.rt) {
+    ++x.item;
+    if (++x.h < p.Hkv) return;
+    x.h = 0;
+    x.item -= p.Hkv;
+    do {                                 // the next row set that has tiles
+        x.item += p.Hkv;
+        if (x.b < 0 && ++x.rt < p.pre_rt) return;
+        if (x.b < 0 || ++x.rt == p.rt) {
             x.rt = 0;
-            if (++x.h == p.Hkv) {
-                x.h = 0;
-                if (++x.b >= p.B) { x.ntiles = 0; return; }
-                x.n = s.q_rows(x.b);
-                x.len = s.own_keys(x.b);
-            }
+            if (++x.b >= p.B) { x.ntiles = 0; return; }
+            x.n = s.q_rows(x.b);
+            x.len = s.own_keys(x.b);
         }
-        paged_enter(s, x);
+        x.ntiles = s.item_tiles(x.n, x.len, x.rt);
     } while (x.ntiles == 0);
 }
 
@@ -207,33 +192,50 @@ __device__ __forceinline__ void paged_next(const PagedSched<M, TK>& s, PagedPlac
 struct PagedSpan {
     bool own;                            // own keys of request b, else the prefix
     int key0;                            // first key, in its sequence
-    int nkeys;                           // keys of the tile that exist (<= TK)
+    int nkeys;                           // keys of the tile that exist (<= TK; 0 in an item without keys)
 };
 template <int M, int TK>
-__device__ __forceinline__ PagedSpan paged_span(const PagedSched<M, TK>& s, const PagedPlace& x) {
+__device__ __forceinline__ PagedSpan paged_span(const PagedSched<M, TK>& s, int b, int len, int tile) {
     PagedSpan r;
-    const int np = (x.b < 0 || s.p.join) ? s.pre_tiles() : 0;
-    r.own = x.tile >= np;
-    r.key0 = (r.own ? x.tile - np : x.tile) * TK;
-    r.nkeys = min(TK, (r.own ? x.len : s.lp) - r.key0);
+    const int np = b < 0 || s.p.join ? s.pre_tiles() : 0;
+    r.own = b >= 0 && tile >= np;
+    r.key0 = (r.own ? tile - np : tile) * TK;
+    r.nkeys = min(TK, (r.own ? len : s.lp) - r.key0);
     return r;
 }
 
-// Row r of an item: its request, query token and query head (false: no such row).
+// Row r of an item: its request, query token and query head (false: no such
+// row).  n: query tokens of the item's request.
 template <int M, int TK>
-__device__ __forceinline__ bool paged_row(const PagedSched<M, TK>& s, const PagedPlace& x, int r, int& b, int& i, int& hq) {
+__device__ __forceinline__ bool paged_row(const PagedSched<M, TK>& s, int ib, int ih, int irt, int n, int r, int& b, int& i,
+                                          int& hq) {
     const PagedParams& p = s.p;
-    int row = x.rt * M + r;
-    b = x.b;
-    if (x.b < 0) {
-        const int per = p.Nq * p.G;
-        b = row / per;
-        row -= b * per;
-        if (b >= p.B) return false;
+    if constexpr (PagedSched<M, TK>::kTiles) {
+        const int group = irt * (M / 128) + (r >> 7);      // of `tok` tokens (requests)
+        const int rr = r & 127, u = fast_div(rr, p.by_unit);
+        const int at = group * p.tok + u, rest = rr - u * p.unit;
+        if (ib < 0) {
+            b = at;
+            i = fast_div(rest, p.by_G);
+            hq = ih * p.G + rest - i * p.G;
+            return u < p.tok && b < p.B && i < s.q_rows(b);
+        }
+        b = ib;
+        i = at;
+        hq = ih * p.G + rest;
+        return u < p.tok && i < n;
+    } else {
+        int row = irt * M + r;
+        b = ib;
+        if (ib < 0) {
+            b = fast_div(row, p.by_rows);
+            row -= b * p.Nq * p.G;
+            if (b >= p.B) return false;
+        }
+        i = fast_div(row, p.by_G);
+        hq = ih * p.G + row - i * p.G;
+        return i < (ib < 0 ? s.q_rows(b) : n);
     }
-    i = row / p.G;
-    hq = x.h * p.G + (row - i * p.G);
-    return i < (x.b < 0 ? s.q_rows(b) : x.n);
 }
 
 // 16 bytes to shared memory, the first `bytes` of them from src, zeros behind.
