@@ -108,16 +108,16 @@ __global__ void __launch_bounds__(kRowWarps * 32, 2) paged_rows_kernel(const __g
     const int total = paged_scan<M, kStep, kRowWarps * 32, kRowWarps>(sched, blockIdx.x, gridDim.x, found, warp_sums,
                                                                       blockIdx.x == 0);
     const int per = paged_per_worker(p, total);
-    if ((int64_t)worker * per >= total || worker >= p.workers) {
+    const int t0 = min(worker * per, total), t1 = min(t0 + per, total);   // this worker's run of the list
+    PagedPlace at{};
+    at.pos = t1;
+    if (t0 < t1) at = paged_place(sched, found[warp], t0);
+    if (at.pos >= t1) {
         pdl_wait();
         return;
     }
-    const int t0 = worker * per;
-    const int count = min(per, total - t0);
-
     const uint32_t ring = smem_u32(smem) + warp * S * Sh::kStage;
-    PagedPlace at = paged_place(sched, found[warp], t0);
-    int left = count;                                     // steps not yet fetched
+    int issued = 0;                                       // steps whose copies were issued
     bool first = true;
     PagedSpan span{};
     int page = 0;
@@ -152,12 +152,11 @@ __global__ void __launch_bounds__(kRowWarps * 32, 2) paged_rows_kernel(const __g
             nt.key0 = span.key0; nt.nkeys = span.nkeys;
             nt.own = span.own; nt.first = first;
         }
-        if (--left > 0) {
-            const int item = at.item;
-            paged_next(sched, at);
-            first = at.item != item;
-            fetch();
-        }
+        ++issued;
+        const int item = at.item;
+        paged_next(sched, at);
+        first = at.item != item;
+        if (at.pos < t1) fetch();
     };
 
     fetch();
@@ -225,11 +224,11 @@ __global__ void __launch_bounds__(kRowWarps * 32, 2) paged_rows_kernel(const __g
     // that only load.
     int stage = 0, fill = 0;                              // stages to compute from and to load into
 #pragma unroll 1
-    for (int it = 1 - S; it < count; ++it) {
+    for (int it = 1 - S; it < 0 || it < issued; ++it) {
         cp_async_wait<S - 2>();
         __syncwarp();
         const StepNote nt = notes[warp][stage];
-        if (left > 0) issue(fill);                        // its stage was read in the step before
+        if (at.pos < t1) issue(fill);                        // its stage was read in the step before
         fill = fill + 1 == S ? 0 : fill + 1;
         cp_async_commit();
         if (it < 0) continue;
@@ -310,7 +309,7 @@ struct RowParts {
     int n;
 };
 
-// Parts of the item of `nt` tiles that starts at list position `start`.
+// Parts of the item whose `nt` tiles lie from place `start` on.
 __device__ __forceinline__ RowParts parts_of(int start, int nt, int per, int item) {
     RowParts r{0, 0};
     if (nt > 0) {
@@ -342,7 +341,8 @@ __global__ void __launch_bounds__(256) paged_join_kernel(const __grid_constant__
     if (live) {
         const int per = paged_per_worker(p, __ldcg(p.start + p.B * p.rt));
         const int nt = s.item_tiles(n, len, rt), pair = b * p.rt + rt;
-        const RowParts own = parts_of(__ldcg(p.start + pair) + h * nt, nt, per, (p.pre_rt + pair) * p.Hkv + h);
+        const RowParts own = parts_of(__ldcg(p.start + pair) + h * s.places(nt) + s.kItemCost, nt, per,
+                                      (p.pre_rt + pair) * p.Hkv + h);
         const int64_t own_q = own.slot0 * M + (r - rt * M);
         RowParts pre{0, 0};
         int64_t pre_q = 0;
@@ -361,8 +361,10 @@ __global__ void __launch_bounds__(256) paged_join_kernel(const __grid_constant__
             }
             const int it = set * p.Hkv + h;
             // alone in its list, or at the front of this one
-            const int pre_per = p.pre_rt > 0 ? per : max(1, (p.Hkv * p.pre_items_rt * pt + p.pre_workers - 1) / p.pre_workers);
-            pre = parts_of(it * pt, pt, pre_per, it);
+            const int cost = p.pre_rt > 0 ? s.kItemCost : PagedSched<128, 128>::kItemCost;
+            const int pre_per =
+                p.pre_rt > 0 ? per : max(1, (p.Hkv * p.pre_items_rt * (pt + cost) + p.pre_workers - 1) / p.pre_workers);
+            pre = parts_of(it * (pt + cost) + cost, pt, pre_per, it);
             pre_q = pre.slot0 * p.pre_m + place;
         }
         const int parts = own.n + pre.n;
@@ -613,8 +615,8 @@ int sage_attn_paged(const sage_tensor* q, const sage_tensor* o, const sage_page_
     if (workspace == nullptr || !aligned16(workspace) || workspace_bytes < lists_bytes(x, B, D)) return SAGE_ERR_ARG;
     // list positions and slot numbers stay in int
     const int tk = x.tiles ? 128 : kStep;
-    const int64_t tiles = (int64_t)B * cache->heads * x.rt * ((own_keys + (x.join ? pre_keys : 0)) / tk + 2) +
-                          (int64_t)cache->heads * x.pre_items_rt * (pre_keys / tk + 2);
+    const int64_t tiles = (int64_t)B * cache->heads * x.rt * ((own_keys + (x.join ? pre_keys : 0)) / tk + 6) +
+                          (int64_t)cache->heads * x.pre_items_rt * (pre_keys / tk + 6);
     if (tiles > INT32_MAX / 2 || x.slots + x.pre_slots > INT32_MAX / 2) return SAGE_ERR_UNSUPPORTED;
 
     PagedParams p{};

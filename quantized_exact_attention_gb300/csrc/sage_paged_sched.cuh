@@ -7,8 +7,10 @@
 //       shared prefix (only when the prefix is computed once for all);
 //   (2) for each request, each set of its rows, and each key head: its own
 //       keys, preceded by the prefix when join = 1.
-// The tiles of the list, numbered through, are cut into equal runs, one for
-// each worker (a warp or a CTA).  So the split follows the lengths that the
+// Each item takes as many places in the list as it has tiles, and kItemCost in
+// front of them, which stand for what an item costs a worker besides its tiles
+// (fetching its rows, writing its output).  The places are cut into equal
+// runs, one for each worker (a warp or a CTA).  So the split follows the lengths that the
 // device holds: a long sequence is shared among many workers, several short
 // ones fall to a single worker, and no host value depends on the lengths.
 // A worker leaves a partial result (running maximum, sum and unnormalised
@@ -40,6 +42,7 @@ __device__ __forceinline__ int fast_div(int n, const FastDiv& f) {
 template <int M, int TK>
 struct PagedSched {
     static constexpr bool kTiles = TK == 128;
+    static constexpr int kItemCost = kTiles ? 3 : 1;
     const PagedParams& p;
     int lp;                              // prefix length
     __device__ explicit PagedSched(const PagedParams& pp) : p(pp) {
@@ -48,7 +51,9 @@ struct PagedSched {
     __device__ int q_rows(int b) const { return paged_clamp(p.q_len, b, p.Nq); }
     __device__ int own_keys(int b) const { return paged_clamp(p.kv_len, b, p.W * p.page); }
     __device__ int pre_tiles() const { return (lp + TK - 1) / TK; }
-    __device__ int pre_total() const { return p.pre_rt * p.Hkv * pre_tiles(); }
+    // places of an item of nt tiles
+    __device__ static int places(int nt) { return nt > 0 ? nt + kItemCost : 0; }
+    __device__ int pre_total() const { return p.pre_rt * p.Hkv * places(pre_tiles()); }
     // Tiles of row set rt of a request with n query tokens and len own keys.
     __device__ int item_tiles(int n, int len, int rt) const {
         int last;                        // last token of the set that exists
@@ -69,10 +74,10 @@ struct PagedSched {
 };
 
 // The length of the list, and where the CTA's workers begin.  A block of
-// THREADS threads sums the tiles of the (request, row set) pairs; the thread
-// whose pairs hold the first tile of worker first_worker + w*worker_step
-// (w < NW) leaves {pair, list position of its first tile} in found[w]
-// ({-1, 0}: among the prefix items).  With `publish` the positions of all
+// THREADS threads sums the places of the (request, row set) pairs; the thread
+// whose pairs hold the first place of worker first_worker + w*worker_step
+// (w < NW) leaves {pair, the pair's first place} in found[w] ({-1, 0}: among
+// the prefix items).  With `publish` the positions of all
 // pairs go to p.start as well.  `red` holds THREADS/32 ints.  Ends with a
 // barrier.
 template <int M, int TK, int THREADS, int NW>
@@ -88,7 +93,7 @@ __device__ __forceinline__ int paged_scan(const PagedSched<M, TK>& s, int first_
         int b = b0, rt = u0 - b0 * p.rt;
 #pragma unroll 1
         for (int u = u0; u < u1; ++u) {
-            mine += s.item_tiles(s.q_rows(b), s.own_keys(b), rt) * p.Hkv;
+            mine += s.places(s.item_tiles(s.q_rows(b), s.own_keys(b), rt)) * p.Hkv;
             if (++rt == p.rt) { rt = 0; ++b; }
         }
     }
@@ -112,7 +117,7 @@ __device__ __forceinline__ int paged_scan(const PagedSched<M, TK>& s, int first_
     int b = b0, rt = u0 - b0 * p.rt;
 #pragma unroll 1
     for (int u = u0; u < u1; ++u) {
-        const int n = cb == 1 ? mine : s.item_tiles(s.q_rows(b), s.own_keys(b), rt) * p.Hkv;
+        const int n = cb == 1 ? mine : s.places(s.item_tiles(s.q_rows(b), s.own_keys(b), rt)) * p.Hkv;
 #pragma unroll
         for (int k = 0; k < NW; ++k) {
             const int at = (first_worker + k * worker_step) * per;
@@ -127,49 +132,55 @@ __device__ __forceinline__ int paged_scan(const PagedSched<M, TK>& s, int first_
     return total;
 }
 
-// Tiles of one worker, given the length of the list.
+// Places of one worker, given the length of the list.
 __device__ __forceinline__ int paged_per_worker(const PagedParams& p, int total) {
     return max(1, (total + p.workers - 1) / p.workers);
 }
 
-// A place in the list.  b = -1: a prefix item (rt counts its row sets).
+// A tile in the list.  b = -1: a prefix item (rt counts its row sets).
 struct PagedPlace {
     int b, h, rt;
     int tile, ntiles;                    // tile of the item, tiles of the item
     int n, len;                          // the request's query tokens and own keys
     int item;                            // number of the item in the list
+    int pos;                             // the tile's place
 };
 
-// The place of list position t (t < total), with paged_scan's finding.
+// The first tile at or behind place t (t < total), with paged_scan's finding.
 template <int M, int TK>
 __device__ __forceinline__ PagedPlace paged_place(const PagedSched<M, TK>& s, int2 found, int t) {
     const PagedParams& p = s.p;
     PagedPlace x{};
+    int o;                               // place within the item
     if (found.x < 0) {
         x.b = -1;
         x.ntiles = s.pre_tiles();
-        x.item = t / x.ntiles;
-        x.tile = t - x.item * x.ntiles;
+        x.item = t / s.places(x.ntiles);
+        o = t - x.item * s.places(x.ntiles);
         x.rt = x.item / p.Hkv;
         x.h = x.item - x.rt * p.Hkv;
-        return x;
+    } else {
+        x.b = p.rt > 1 ? fast_div(found.x, p.by_rt) : found.x;
+        x.rt = found.x - x.b * p.rt;
+        x.n = s.q_rows(x.b);
+        x.len = s.own_keys(x.b);
+        x.ntiles = s.item_tiles(x.n, x.len, x.rt);
+        x.h = (t - found.y) / s.places(x.ntiles);
+        o = t - found.y - x.h * s.places(x.ntiles);
+        x.item = (p.pre_rt + found.x) * p.Hkv + x.h;
     }
-    x.b = p.rt > 1 ? fast_div(found.x, p.by_rt) : found.x;
-    x.rt = found.x - x.b * p.rt;
-    x.n = s.q_rows(x.b);
-    x.len = s.own_keys(x.b);
-    x.ntiles = s.item_tiles(x.n, x.len, x.rt);
-    x.h = (t - found.y) / x.ntiles;
-    x.tile = t - found.y - x.h * x.ntiles;
-    x.item = (p.pre_rt + found.x) * p.Hkv + x.h;
+    x.tile = max(0, o - s.kItemCost);
+    x.pos = t - o + s.kItemCost + x.tile;
     return x;
 }
 
-// The next tile of the list (the caller knows that there is one).
+// The next tile of the list (its place is behind the list when there is none).
 template <int M, int TK>
 __device__ __forceinline__ void paged_next(const PagedSched<M, TK>& s, PagedPlace& x) {
     const PagedParams& p = s.p;
+    ++x.pos;
     if (++x.tile < x.ntiles) return;
+    x.pos += s.kItemCost;
     x.tile = 0;
     ++x.item;
     if (++x.h < p.Hkv) return;
@@ -178,9 +189,10 @@ __device__ __forceinline__ void paged_next(const PagedSched<M, TK>& s, PagedPlac
     do {                                 // the next row set that has tiles
         x.item += p.Hkv;
         if (x.b < 0 && ++x.rt < p.pre_rt) return;
+        if (x.b < 0 && p.rt == 0) { x.pos = INT32_MAX; return; }      // a list of prefix items only
         if (x.b < 0 || ++x.rt == p.rt) {
             x.rt = 0;
-            if (++x.b >= p.B) { x.ntiles = 0; return; }
+            if (++x.b >= p.B) { x.ntiles = 0; x.pos = INT32_MAX; return; }
             x.n = s.q_rows(x.b);
             x.len = s.own_keys(x.b);
         }

@@ -57,7 +57,7 @@
 namespace sage {
 namespace {
 
-constexpr int kItemNotes = 8;
+constexpr int kItemNotes = 16;
 constexpr float kLazy = 8.f;                              // log2 of the weights' bound
 constexpr uint32_t kBlk = 128 * 128;                      // 128 rows x 64 channels
 
@@ -67,7 +67,7 @@ enum TileRole { R_ROWS = 6, R_LOAD = 7, R_ISSUE = 8 };
 struct ItemNote {
     int b, h, rt;
     int n, len;                                           // the request's query tokens and own keys
-    int tile, run;                                        // its first tile in this worker, and how many
+    int tile, run;                                        // its first tile in this worker, and how many (0: no item)
     int slot;                                             // of a partial result
     int whole;                                            // no other worker shares it: the output is final
     int pad[3];
@@ -146,28 +146,6 @@ __device__ __forceinline__ void commit_elect(uint32_t bar) {
         "{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\t"
         "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}"
         ::"r"(bar) : "memory");
-}
-// The bounded wait of the hand-offs between softmax and issuers.  It polls with
-// test_wait, which never suspends the warp (a suspended try_wait adds its
-// wake-up to the hand-off), and looks at the clock only every 1,024 polls.
-// All 32 lanes call it together.
-__device__ __forceinline__ bool mbar_spin_warp(uint32_t bar, uint32_t parity, const volatile int* abort_flag) {
-    unsigned long long t0 = 0;
-    for (uint32_t i = 1;; ++i) {
-        uint32_t ok;
-        asm volatile(
-            "{\n\t.reg .pred p;\n\t"
-            "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-            "selp.u32 %0, 1, 0, p;\n\t}"
-            : "=r"(ok) : "r"(bar), "r"(parity) : "memory");
-        if (__all_sync(0xffffffffu, ok != 0)) return true;
-        if ((i & 1023u) == 0) {
-            if (__any_sync(0xffffffffu, *abort_flag != 0)) return false;
-            const unsigned long long now = globaltimer();
-            if (t0 == 0) t0 = now;
-            if (__any_sync(0xffffffffu, now - t0 > kWaitLimitNs)) return false;
-        }
-    }
 }
 __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
     uint32_t r;
@@ -253,8 +231,7 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
     const int per = paged_per_worker(p, total);
-    const int t0 = min(worker * per, total);
-    const int count = min(per, total - t0);               // tiles of this worker, perhaps none
+    const int t0 = min(worker * per, total), t1 = min(t0 + per, total);   // this worker's run of the list
 
     if (warp < 8 * kGroups) {
         // ===================================================== softmax
@@ -273,12 +250,13 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
         int turn = 0;                                     // exchanges so far
         int t = 0;
         bool ok = true;
-        for (int k = 0; t < count && ok; ++k) {
-            if (!mbar_spin_warp(bar(L::B_ITEM + k % kItemNotes), (k / kItemNotes) & 1, abort_flag)) {
+        for (int k = 0; ok; ++k) {
+            if (!mbar_wait_warp(bar(L::B_ITEM + k % kItemNotes), (k / kItemNotes) & 1, abort_flag)) {
                 if (lane == 0) fail(R_ROWS, t);
                 break;
             }
             const ItemNote& nt = notes[k % kItemNotes];
+            if (nt.run == 0) break;
             const int ib = nt.b, len = nt.len, end = t + nt.run;
             int lim_own, rb, ri, rh;
             const bool valid = paged_row(sched, ib, nt.h, nt.rt, nt.n, X * 128 + row, rb, ri, rh);
@@ -292,7 +270,7 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                 const PagedSpan span = paged_span(sched, ib, len, tile);
                 // keys of this half that this row sees (may be negative)
                 const int lim = (span.own ? min(span.nkeys, lim_own - span.key0) : span.nkeys) - half * 64;
-                if (!mbar_spin_warp(bar(L::B_S + X), t & 1, abort_flag)) { ok = false; break; }
+                if (!mbar_wait_warp(bar(L::B_S + X), t & 1, abort_flag)) { ok = false; break; }
                 tc_fence_after();
                 uint32_t s[2][32];
                 float mx = 0.f;
@@ -320,7 +298,7 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                     *at = mx;
                     __syncwarp();
                     if (lane == 0) mbar_arrive(bx);
-                    if (!mbar_spin_warp(bx, turn & 1, abort_flag)) { ok = false; break; }
+                    if (!mbar_wait_warp(bx, turn & 1, abort_flag)) { ok = false; break; }
                     tc_fence_after();                     // the other half has its scores: P may lie over S
                     ++turn;
                     const float mt = fmaxf(mx, at[other]) * p.sc;
@@ -350,7 +328,7 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                 // rescaled.  (P over S: these scores were issued behind it.)  Warps
                 // without rows wait too: an arrival for the next product before
                 // this one was issued would be lost.
-                if (!L::kAlias && t > 0 && !mbar_spin_warp(bar(L::B_PV + X), (t - 1) & 1, abort_flag)) { ok = false; break; }
+                if (!L::kAlias && t > 0 && !mbar_wait_warp(bar(L::B_PV + X), (t - 1) & 1, abort_flag)) { ok = false; break; }
                 tc_fence_after();
                 if (active) {
                     if (rescale) {
@@ -398,10 +376,10 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                 __syncwarp();
                 if (lane == 0) mbar_arrive(bx);
             }
-            if (!mbar_spin_warp(bar(L::B_ODONE + X), k & 1, abort_flag)) { ok = false; break; }
+            if (!mbar_wait_warp(bar(L::B_ODONE + X), k & 1, abort_flag)) { ok = false; break; }
             tc_fence_after();
             if (active) {
-                if (!mbar_spin_warp(bx, turn & 1, abort_flag)) { ok = false; break; }
+                if (!mbar_wait_warp(bx, turn & 1, abort_flag)) { ok = false; break; }
                 ++turn;
                 l += at[other];
                 uint8_t* stage = sgen + L::OFF_STAGE + warp * 1024;
@@ -443,12 +421,11 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
         // so: then the item is joined from its parts afterwards.
         int4 cut = make_int4(-1, 0, 0, 0);                // request, key head, row set, parts
         PagedPlace at{};
-        if (count > 0) {
-            at = paged_place(sched, found[0], t0);
-            if (p.cuts != nullptr && at.tile > 0) {
-                const int start = t0 - at.tile, w0 = start / per;
-                if (w0 == worker - 1) cut = make_int4(at.b, at.h, at.rt, (start + at.ntiles - 1) / per - w0 + 1);
-            }
+        at.pos = t1;
+        if (t0 < t1) at = paged_place(sched, found[0], t0);
+        if (at.pos < t1 && p.cuts != nullptr && at.tile > 0) {
+            const int start = at.pos - at.tile, w0 = start / per;
+            if (w0 == worker - 1) cut = make_int4(at.b, at.h, at.rt, (start + at.ntiles - 1) / per - w0 + 1);
         }
         if (p.cuts != nullptr && lane == 0) p.cuts[worker] = cut;
         const int per_tile = 128 >> p.page_shift;         // pages of a whole tile
@@ -463,13 +440,13 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                 page = span.own ? __ldg(p.table + (int64_t)at.b * p.table_stride + j) : __ldg(p.ptable + j);
             }
         };
-        if (count > 0) look_up();
+        if (at.pos < t1) look_up();
         bool first = true;
         int items = 0;                                    // items noted
         int loaded_k = 0, loaded_v = 0;                   // tiles whose copies were issued
         bool ok = true;
 #pragma unroll 1
-        for (int t = 0; t < count; ++t) {
+        for (int t = 0; at.pos < t1; ++t) {
             const int st = t % NS, ph = (t / NS) & 1;
             const bool mine = lane < per_tile && (lane << p.page_shift) < span.nkeys;
             const uint32_t bytes = (uint32_t)((span.nkeys + p.page - 1) >> p.page_shift) * (uint32_t)(p.page * 128 * L::kNB);
@@ -477,12 +454,12 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
             if (t >= NS && !mbar_wait_warp(bar(L::B_KE + st), ph ^ 1, abort_flag)) { ok = false; break; }
             if (lane == 0) {
                 if (first) {
-                    // Slots of notes are not overrun: item k + 8 begins 8 tiles or more
+                    // Slots of notes are not overrun: item k + 16 begins 16 tiles or more
                     // behind item k, and the stages keep the loader that close.
                     ItemNote& nt = notes[items % kItemNotes];
                     nt.b = at.b; nt.h = at.h; nt.rt = at.rt;
                     nt.n = at.n; nt.len = at.len;
-                    nt.tile = at.tile; nt.run = min(at.ntiles - at.tile, count - t);
+                    nt.tile = at.tile; nt.run = min(at.ntiles - at.tile, t1 - at.pos);
                     nt.slot = p.pre_rt > 0 ? worker + at.item : 2 * worker + (at.tile == 0 ? 1 : 0);
                     nt.whole = p.pre_rt == 0 && nt.run == at.ntiles;
                     mbar_arrive(bar(L::B_ITEM + items % kItemNotes));
@@ -526,14 +503,16 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                                 bar(L::B_VF + st));
             }
             loaded_v = t + 1;
-            if (t + 1 < count) {
-                const int item = at.item;
-                paged_next(sched, at);
-                first = at.item != item;
-                look_up();
-            }
+            const int item = at.item;
+            paged_next(sched, at);
+            first = at.item != item;
+            if (at.pos < t1) look_up();
         }
         if (!ok && lane == 0) fail(R_LOAD, loaded_v);
+        if (ok && lane == 0) {                            // no more items
+            notes[items % kItemNotes].run = 0;
+            mbar_arrive(bar(L::B_ITEM + items % kItemNotes));
+        }
         __syncwarp();
         // every copy issued lands before the CTA may exit
         const int zero = 0;
@@ -552,20 +531,22 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
         const uint64_t dV = sdesc_n_major(sbase + L::OFF_V);
         // an item's first tile and the one behind its last, as S and as PV see them
         int s_items = 0, s_end = 0, v_items = 0, v_first = 0, v_end = 0;
+        bool s_done = false, v_done = false;              // no more items
         auto issue_s = [&](int t) -> bool {
             if (t == s_end) {
-                if (!mbar_spin_warp(bar(L::B_ITEM + s_items % kItemNotes), (s_items / kItemNotes) & 1, abort_flag)) return false;
+                if (!mbar_wait_warp(bar(L::B_ITEM + s_items % kItemNotes), (s_items / kItemNotes) & 1, abort_flag)) return false;
                 s_end = t + notes[s_items % kItemNotes].run;
-                if (!mbar_spin_warp(bar(L::B_Q), s_items & 1, abort_flag)) return false;
+                if (s_end == t) { s_done = true; return true; }
+                if (!mbar_wait_warp(bar(L::B_Q), s_items & 1, abort_flag)) return false;
                 ++s_items;
             }
             const int st = t % NS;
-            if (!mbar_spin_warp(bar(L::B_KF + st), (t / NS) & 1, abort_flag)) return false;
+            if (!mbar_wait_warp(bar(L::B_KF + st), (t / NS) & 1, abort_flag)) return false;
 #pragma unroll 1
             for (int X = 0; X < kGroups; ++X) {
                 if constexpr (!L::kAlias) {               // the unit that used the buffer last has its scores in registers
                     const int before = t * kGroups + X - L::kSBufs;
-                    if (before >= 0 && !mbar_spin_warp(bar(L::B_SFREE + before % kGroups), (before / kGroups) & 1, abort_flag))
+                    if (before >= 0 && !mbar_wait_warp(bar(L::B_SFREE + before % kGroups), (before / kGroups) & 1, abort_flag))
                         return false;
                 }
                 tc_fence_after();
@@ -583,16 +564,17 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
         };
         auto issue_pv = [&](int t) -> bool {
             if (t == v_end) {
-                if (!mbar_spin_warp(bar(L::B_ITEM + v_items % kItemNotes), (v_items / kItemNotes) & 1, abort_flag)) return false;
+                if (!mbar_wait_warp(bar(L::B_ITEM + v_items % kItemNotes), (v_items / kItemNotes) & 1, abort_flag)) return false;
                 v_first = t;
                 v_end = t + notes[v_items % kItemNotes].run;
+                if (v_end == t) { v_done = true; return true; }
                 ++v_items;
             }
             const int st = t % NS;
-            if (!mbar_spin_warp(bar(L::B_VF + st), (t / NS) & 1, abort_flag)) return false;
+            if (!mbar_wait_warp(bar(L::B_VF + st), (t / NS) & 1, abort_flag)) return false;
 #pragma unroll 1
             for (int X = 0; X < kGroups; ++X) {
-                if (!mbar_spin_warp(bar(L::B_P + X), t & 1, abort_flag)) return false;
+                if (!mbar_wait_warp(bar(L::B_P + X), t & 1, abort_flag)) return false;
                 tc_fence_after();
                 const uint64_t b = dV + (uint64_t)((st * L::kTile) >> 4);
 #pragma unroll
@@ -609,15 +591,16 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
         int t = 0;
         if constexpr (kGroups == 2) {
             if (warp == L::kWarpIssue) {
-                for (; t < count && ok; ++t) ok = issue_s(t);
+                for (; ok && !s_done; ++t) ok = issue_s(t);
             } else {
-                for (; t < count && ok; ++t) ok = issue_pv(t);
+                for (; ok && !v_done; ++t) ok = issue_pv(t);
             }
         } else if constexpr (L::kAlias) {
-            for (; t < count && ok; ++t) ok = issue_s(t) && issue_pv(t);
+            for (; ok && !v_done; ++t) ok = issue_s(t) && issue_pv(t);
         } else {
-            if (count > 0) ok = issue_s(0);
-            for (; t < count && ok; ++t) ok = (t + 1 == count || issue_s(t + 1)) && issue_pv(t);
+            // the scores of the next tile before this one's product
+            ok = issue_s(0);
+            for (; ok && !v_done; ++t) ok = (s_done || issue_s(t + 1)) && issue_pv(t);
         }
         if (!ok && lane == 0) fail(R_ISSUE, t);
         const int drain = L::B_DRAIN + warp - L::kWarpIssue;
