@@ -100,6 +100,7 @@ __global__ void __launch_bounds__(kRowWarps * 32, 2) paged_rows_kernel(const __g
     __shared__ StepNote notes[kRowWarps][S];
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (!p.beside) pdl_wait();
     pdl_trigger();
     const PagedSched<M, kStep> sched(p);
     // workers next to each other in the list sit on different SMs: a CTA's
@@ -334,6 +335,7 @@ __global__ void __launch_bounds__(256) paged_join_kernel(const __grid_constant__
     const int n = s.q_rows(b), len = s.own_keys(b);
     const bool live = hq < p.H && i < n;
     const int h = fast_div(hq, p.by_G), r = i * p.G + (hq - h * p.G), rt = r / M;
+    pdl_trigger();
     pdl_wait();                                            // the parts are written
     float acc[V], m = -INFINITY, l = 0.f;
 #pragma unroll
@@ -546,26 +548,18 @@ int sm_count() {
 template <int D, int NR>
 cudaError_t launch_rows(const PagedParams& p, cudaStream_t s) {
     using Sh = RowsShape<D>;
-    static bool attr_set[64] = {};
-    int dev = 0;
-    cudaError_t e = cudaGetDevice(&dev);
-    if (e != cudaSuccess || dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
-    if (!attr_set[dev]) {
-        e = cudaFuncSetAttribute(paged_rows_kernel<D, NR>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Sh::kSmem);
-        if (e != cudaSuccess) return e;
-        attr_set[dev] = true;
-    }
-    // beside the prefix's kernel, which it does not depend on
-    e = launch_after(paged_rows_kernel<D, NR>, dim3((unsigned)(p.workers / kRowWarps)), dim3(kRowWarps * 32), Sh::kSmem, s,
-                     p.pre_items_rt > 0 && p.pre_rt == 0, p);
+    static bool ready[64] = {}, join8_ready[64] = {}, join1_ready[64] = {};
+    const cudaError_t e = launch_pdl(paged_rows_kernel<D, NR>, dim3((unsigned)(p.workers / kRowWarps)), dim3(kRowWarps * 32),
+                                     Sh::kSmem, s, ready, p);
     if (e != cudaSuccess) return e;
     // Rows are few: eight warps share the parts of one, else a warp takes a row
     // (8 KV heads x 3 rows of 152 parts each: 4.2 against 13.6 us).
     const int64_t rows = (int64_t)p.H * p.Nq;
     if (rows * p.B <= 1024)
-        return launch_after(paged_join_kernel<D, 8 * NR, kStep, 8>, dim3((unsigned)rows, (unsigned)p.B), dim3(256), 0, s, true, p);
-    return launch_after(paged_join_kernel<D, 8 * NR, kStep, 1>, dim3((unsigned)ceil_div(rows, 8), (unsigned)p.B), dim3(256), 0,
-                        s, true, p);
+        return launch_pdl(paged_join_kernel<D, 8 * NR, kStep, 8>, dim3((unsigned)rows, (unsigned)p.B), dim3(256), 0, s,
+                          join8_ready, p);
+    return launch_pdl(paged_join_kernel<D, 8 * NR, kStep, 1>, dim3((unsigned)ceil_div(rows, 8), (unsigned)p.B), dim3(256), 0, s,
+                      join1_ready, p);
 }
 template <int D>
 cudaError_t launch_rows_d(const PagedParams& p, int nr, cudaStream_t s) {
@@ -686,6 +680,7 @@ int sage_attn_paged(const sage_tensor* q, const sage_tensor* o, const sage_page_
             pp.rt = 0; pp.pre_rt = x.pre_items_rt; pp.workers = p.pre_workers;
             if (launch_paged_tiles(pp, D, x.pre_groups, mq, mk, mv, s) != cudaSuccess) return SAGE_ERR_LAUNCH;
             ++launches;
+            p.beside = 1;
         }
         p.workers = std::min(2 * sms, kMaxRowWorkers / kRowWarps) * kRowWarps;
         e = D == 64 ? launch_rows_d<64>(p, x.nr, s) : launch_rows_d<128>(p, x.nr, s);

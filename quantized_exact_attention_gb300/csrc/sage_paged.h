@@ -53,6 +53,7 @@ struct PagedParams {
     int join;                            // 1: a request's key sequence is the prefix followed by its own keys
     int workers;                         // workers the list is shared among
     int fault_mode;                      // test hook: 0 = none
+    int beside;                          // runs beside the kernel before it, which it does not depend on
     // workspace
     float* part_o;                       // [slot][M][D]
     float2* part_ml;                     // [slot][M] running maximum (log2 domain) and sum
@@ -83,16 +84,33 @@ int take_fault_mode();
 int check_page_cache(const sage_page_cache* c);
 
 #ifdef __CUDACC__
-// Programmatic dependent launch: a kernel launched with `overlap` may start
-// once every CTA of the kernel before it has called pdl_trigger (or ended),
-// which hides its launch and its prologue; pdl_wait returns when that kernel
-// is complete and its writes are visible.
+// Programmatic dependent launch: a kernel may start once every CTA of the
+// kernel before it in the stream has called pdl_trigger (or ended), which hides
+// its launch and its prologue; pdl_wait returns when that kernel is complete
+// and its writes are visible.  Every CTA of every kernel here calls pdl_wait
+// before it ends, so a kernel that is complete has nothing unfinished before
+// it.  The first kernel of an attention call waits before it triggers: what
+// follows it within the call may read the caller's tensors at once.
 __device__ __forceinline__ void pdl_trigger() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
+// Launch a kernel this way.  All of them ask for the same split of an SM's
+// memory, once per device: an SM drains before it changes the split (a short
+// decode call: 10.4 us, with the same split 9.0 us).
 template <class... P, class... A>
-cudaError_t launch_after(void (*kernel)(P...), dim3 grid, dim3 block, size_t smem, cudaStream_t s, bool overlap,
-                         const A&... args) {
+cudaError_t launch_pdl(void (*kernel)(P...), dim3 grid, dim3 block, size_t smem, cudaStream_t s, bool (&ready)[64],
+                       const A&... args) {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess || dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+    if (!ready[dev]) {
+        if ((e = cudaFuncSetAttribute(kernel, cudaFuncAttributePreferredSharedMemoryCarveout,
+                                      (int)cudaSharedmemCarveoutMaxShared)) != cudaSuccess)
+            return e;
+        if (smem > 0 && (e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem)) != cudaSuccess)
+            return e;
+        ready[dev] = true;
+    }
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = grid;
     cfg.blockDim = block;
@@ -102,8 +120,8 @@ cudaError_t launch_after(void (*kernel)(P...), dim3 grid, dim3 block, size_t sme
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = overlap ? 1 : 0;
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, args...);
+    cfg.numAttrs = 1;
+    e = cudaLaunchKernelEx(&cfg, kernel, args...);
     return e != cudaSuccess ? e : cudaGetLastError();
 }
 #endif

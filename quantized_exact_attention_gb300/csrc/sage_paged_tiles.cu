@@ -184,7 +184,6 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
     uint8_t* sgen = smem_raw + (sbase - raw_base);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
-    pdl_trigger();
     auto bar = [&](int i) -> uint32_t { return sbase + L::OFF_BAR + 8u * (uint32_t)i; };
     ItemNote* notes = reinterpret_cast<ItemNote*>(sgen + L::OFF_ITEM);
     volatile uint32_t* tmem_slot = reinterpret_cast<volatile uint32_t*>(sgen + L::OFF_TMEM);
@@ -223,6 +222,8 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
         tma_prefetch_desc(&tm_v);
     }
     tc_fence_before();
+    pdl_wait();
+    pdl_trigger();
     const PagedSched<M, 128> sched(p);
     int* red = reinterpret_cast<int*>(sgen + L::OFF_SCAN);
     int2* found = reinterpret_cast<int2*>(sgen + L::OFF_SCAN + 80);
@@ -628,6 +629,7 @@ __global__ void __launch_bounds__(256) paged_cuts_kernel(const __grid_constant__
     constexpr int V = D / 32;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int w = blockIdx.x + 1;
+    pdl_trigger();
     pdl_wait();
     const int4 cut = __ldcg(p.cuts + w);
     if (cut.x < 0) return;
@@ -686,19 +688,14 @@ template <int D, int kGroups>
 cudaError_t launch_one(const PagedParams& p, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
                        cudaStream_t s) {
     using L = TilesShape<D, kGroups>;
-    static bool attr_set[64] = {};
-    int dev = 0;
-    cudaError_t e = cudaGetDevice(&dev);
-    if (e != cudaSuccess || dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
-    if (!attr_set[dev]) {
-        e = cudaFuncSetAttribute(paged_tiles_kernel<D, kGroups>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)L::kSmem);
-        if (e != cudaSuccess) return e;
-        attr_set[dev] = true;
+    static bool ready[64] = {};
+    cudaError_t e = launch_pdl(paged_tiles_kernel<D, kGroups>, dim3((unsigned)p.workers), dim3(L::kThreads), L::kSmem, s, ready,
+                               tq, tk, tv, p);
+    if (e != cudaSuccess) return e;
+    if (p.pre_rt == 0 && p.workers > 1) {
+        static bool cuts_ready[64] = {};
+        e = launch_pdl(paged_cuts_kernel<D, L::M>, dim3((unsigned)p.workers - 1, L::M / 32), dim3(256), 0, s, cuts_ready, p);
     }
-    paged_tiles_kernel<D, kGroups><<<p.workers, L::kThreads, L::kSmem, s>>>(tq, tk, tv, p);
-    if ((e = cudaGetLastError()) != cudaSuccess) return e;
-    if (p.pre_rt == 0 && p.workers > 1)
-        e = launch_after(paged_cuts_kernel<D, L::M>, dim3((unsigned)p.workers - 1, L::M / 32), dim3(256), 0, s, true, p);
     return e;
 }
 

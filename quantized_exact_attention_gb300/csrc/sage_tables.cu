@@ -49,6 +49,8 @@ constexpr int kTableThreads = 256;
 
 __global__ void __launch_bounds__(kTableThreads, 8) page_tables_kernel(const __grid_constant__ TableParams p) {
     __shared__ int red[kTableThreads / 32];
+    pdl_trigger();
+    pdl_wait();
     const int per = (p.B + gridDim.x - 1) / gridDim.x;
     const int b0 = min((int)blockIdx.x * per, p.B), b1 = min(b0 + per, p.B);
     if (b0 == b1) return;
@@ -129,7 +131,9 @@ struct AppendParams {
 
 constexpr int kAppendThreads = 256;
 
-__global__ void __launch_bounds__(kAppendThreads) cache_append_kernel(const AppendParams p) {
+__global__ void __launch_bounds__(kAppendThreads) cache_append_kernel(const __grid_constant__ AppendParams p) {
+    pdl_trigger();
+    pdl_wait();
     const int lane = threadIdx.x & 31;
     const int64_t warps = (int64_t)gridDim.x * (kAppendThreads / 32);
     const int chunks = p.heads << p.chunk_shift;
@@ -213,8 +217,10 @@ int sage_page_tables(const int32_t* old_len, const int32_t* new_len, int B, int 
     p.page_shift = 31 - __builtin_clz((unsigned)page_size);
     p.len_quads = aligned16(new_len) && (old_len == nullptr || aligned16(old_len));
     // one wave: eight blocks on each of 152 SMs
-    page_tables_kernel<<<std::min(B, 152 * 8), kTableThreads, 0, static_cast<cudaStream_t>(stream)>>>(p);
-    if (cudaGetLastError() != cudaSuccess) return SAGE_ERR_LAUNCH;
+    static bool ready[64] = {};
+    if (launch_pdl(page_tables_kernel, dim3((unsigned)std::min(B, 152 * 8)), dim3(kTableThreads), 0,
+                   static_cast<cudaStream_t>(stream), ready, p) != cudaSuccess)
+        return SAGE_ERR_LAUNCH;
     set_last_launch_count(1);
     return SAGE_OK;
 }
@@ -245,8 +251,10 @@ int sage_cache_append(const sage_tensor* k, const sage_tensor* v, int B, int N, 
     p.page_shift = 31 - __builtin_clz((unsigned)cache->page_size);
     const int64_t blocks = ceil_div(p.tokens, kAppendThreads / 32);
     const int grid = (int)std::min<int64_t>(blocks, 152 * 8);
-    cache_append_kernel<<<grid, kAppendThreads, 0, static_cast<cudaStream_t>(stream)>>>(p);
-    if (cudaGetLastError() != cudaSuccess) return SAGE_ERR_LAUNCH;
+    static bool ready[64] = {};
+    if (launch_pdl(cache_append_kernel, dim3((unsigned)grid), dim3(kAppendThreads), 0, static_cast<cudaStream_t>(stream), ready,
+                   p) != cudaSuccess)
+        return SAGE_ERR_LAUNCH;
     set_last_launch_count(1);
     return SAGE_OK;
 }
