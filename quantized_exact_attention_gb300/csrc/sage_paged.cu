@@ -550,15 +550,15 @@ cudaError_t launch_rows(const PagedParams& p, cudaStream_t s) {
     using Sh = RowsShape<D>;
     static bool ready[64] = {}, join8_ready[64] = {}, join1_ready[64] = {};
     const cudaError_t e = launch_pdl(paged_rows_kernel<D, NR>, dim3((unsigned)(p.workers / kRowWarps)), dim3(kRowWarps * 32),
-                                     Sh::kSmem, s, ready, p);
+                                     Sh::kSmem, s, true, ready, p);
     if (e != cudaSuccess) return e;
     // Rows are few: eight warps share the parts of one, else a warp takes a row
     // (8 KV heads x 3 rows of 152 parts each: 4.2 against 13.6 us).
     const int64_t rows = (int64_t)p.H * p.Nq;
     if (rows * p.B <= 1024)
-        return launch_pdl(paged_join_kernel<D, 8 * NR, kStep, 8>, dim3((unsigned)rows, (unsigned)p.B), dim3(256), 0, s,
+        return launch_pdl(paged_join_kernel<D, 8 * NR, kStep, 8>, dim3((unsigned)rows, (unsigned)p.B), dim3(256), 0, s, true,
                           join8_ready, p);
-    return launch_pdl(paged_join_kernel<D, 8 * NR, kStep, 1>, dim3((unsigned)ceil_div(rows, 8), (unsigned)p.B), dim3(256), 0, s,
+    return launch_pdl(paged_join_kernel<D, 8 * NR, kStep, 1>, dim3((unsigned)ceil_div(rows, 8), (unsigned)p.B), dim3(256), 0, s, true,
                       join1_ready, p);
 }
 template <int D>

@@ -94,18 +94,20 @@ int check_page_cache(const sage_page_cache* c);
 __device__ __forceinline__ void pdl_trigger() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
-// Launch a kernel this way.  All of them ask for the same split of an SM's
-// memory, once per device: an SM drains before it changes the split (a short
-// decode call: 10.4 us, with the same split 9.0 us).
+// Launch a kernel this way.  The kernels of an attention call ask for the same
+// split of an SM's memory (`max_shared`, set once per device): an SM drains
+// before it changes the split (a short decode call: 10.4 us, with the same
+// split 9.0 us).  The append moves its rows through L1 and keeps the default
+// (2 x 122 MB: 40.9 us; with little L1 51.3).
 template <class... P, class... A>
-cudaError_t launch_pdl(void (*kernel)(P...), dim3 grid, dim3 block, size_t smem, cudaStream_t s, bool (&ready)[64],
-                       const A&... args) {
+cudaError_t launch_pdl(void (*kernel)(P...), dim3 grid, dim3 block, size_t smem, cudaStream_t s, bool max_shared,
+                       bool (&ready)[64], const A&... args) {
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess || dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
     if (!ready[dev]) {
-        if ((e = cudaFuncSetAttribute(kernel, cudaFuncAttributePreferredSharedMemoryCarveout,
-                                      (int)cudaSharedmemCarveoutMaxShared)) != cudaSuccess)
+        if (max_shared && (e = cudaFuncSetAttribute(kernel, cudaFuncAttributePreferredSharedMemoryCarveout,
+                                                    (int)cudaSharedmemCarveoutMaxShared)) != cudaSuccess)
             return e;
         if (smem > 0 && (e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem)) != cudaSuccess)
             return e;

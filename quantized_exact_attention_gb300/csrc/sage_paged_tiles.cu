@@ -23,18 +23,18 @@
 //              it alone walks the list and leaves a note for each item
 //   issuers    kGroups = 2: one thread for S and one for PV (an instruction
 //              takes about 48 cycles of the issuing thread, a wait or commit
-//              45: one thread would need longer than the 1,024 cycles of a
-//              unit's products); kGroups = 1: one thread for both
+//              45: one thread, in the order S(u), PV(u - 2), takes 209 us where
+//              the two take 179); kGroups = 1: one thread for both
 //   kGroups = 2 has one more warp, idle: it completes the four whose registers
 //   go to the softmax (setmaxnreg: 512 x 104 + 128 x 56 <= 640 x 96).
-// Tensor memory, kGroups = 2: D = 128: [S 128 | P0 64 | P1 64 | O0 | O1], one S
-// for both groups: a group loads its scores into registers at once and frees
-// it, so the next scores are computed while the exponentials run, and the two
-// groups fall into turns by themselves.  (Each group's P over its own S, every
-// unit a chain S, softmax, PV: the groups fall into step and leave the tensor
-// core idle meanwhile, 2,250 cycles a unit.)  D = 64: [S0 | S1 | P0 | P1 | O0 |
-// O1].  kGroups = 1: D = 128: [S 128, its first half P | O 128], D = 64:
-// [S 128 | P 64 | O 64].
+// Tensor memory: [S 128 | P 64 a group | O D a group].  Both groups share S: a
+// group loads its scores into registers at once and frees it, so the next
+// scores are computed while the exponentials run, and the two groups fall into
+// turns by themselves.  (Each group's P over its own S, every unit a chain S,
+// softmax, PV: the groups fall into step and leave the tensor core idle
+// meanwhile, 2,250 cycles a unit.  An S for each group, at D = 64: 46.6 us
+// where the shared one takes 44.3.)  One group of D = 128, with 256 columns:
+// [S 128, its first half P | O 128].
 //
 // The reference of the exponentials follows the row maximum lazily: O is
 // rescaled only when the maximum has grown by more than 2^8 since the last
@@ -84,8 +84,7 @@ struct TilesShape {
     static constexpr int kNS = (D == 128 ? 1 : 2) * kGroups;       // K and V stages
     static constexpr uint32_t kCols = 256 * kGroups;      // tensor memory
     static constexpr bool kAlias = D == 128 && kGroups == 1;       // P over its S
-    static constexpr int kSBufs = D == 128 ? 1 : kGroups;          // S of group X at 128 (X % kSBufs)
-    static constexpr uint32_t TM_P = kAlias ? 0 : 128 * kSBufs;    // + 64 X
+    static constexpr uint32_t TM_P = kAlias ? 0 : 128;             // + 64 X
     static constexpr uint32_t TM_O = kAlias ? 128 : TM_P + 64 * kGroups;           // + D X
     // shared memory
     static constexpr uint32_t OFF_Q = 0;
@@ -240,7 +239,7 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
         const int X = warp >> 3, half = (warp >> 2) & 1, quarter = warp & 3;
         const int row = quarter * 32 + lane;
         const uint32_t lane_base = (uint32_t)(quarter * 32) << 16;
-        const uint32_t tS = tmem + lane_base + (L::kSBufs == 2 ? 128u * X : 0u) + 64u * half;
+        const uint32_t tS = tmem + lane_base + 64u * half;
         const uint32_t tP = tmem + lane_base + L::TM_P + 64u * X + 32u * half;
         const uint32_t tO = tmem + lane_base + L::TM_O + (uint32_t)D * X + (uint32_t)half * (D / 2);
         const uint32_t bx = bar(L::B_X + 4 * X + quarter);
@@ -545,8 +544,8 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
             if (!mbar_wait_warp(bar(L::B_KF + st), (t / NS) & 1, abort_flag)) return false;
 #pragma unroll 1
             for (int X = 0; X < kGroups; ++X) {
-                if constexpr (!L::kAlias) {               // the unit that used the buffer last has its scores in registers
-                    const int before = t * kGroups + X - L::kSBufs;
+                if constexpr (!L::kAlias) {               // the unit before has its scores in registers
+                    const int before = t * kGroups + X - 1;
                     if (before >= 0 && !mbar_wait_warp(bar(L::B_SFREE + before % kGroups), (before / kGroups) & 1, abort_flag))
                         return false;
                 }
@@ -556,7 +555,7 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
 #pragma unroll
                 for (int kk = 0; kk < D / 16; ++kk) {
                     const uint32_t o = ((kk >> 2) * kBlk + (kk & 3) * 32) >> 4;
-                    mma_ss_elect(tmem + (L::kSBufs == 2 ? 128u * X : 0u), a + o, b + o, kIdescQK, kk > 0 ? 1u : 0u);
+                    mma_ss_elect(tmem, a + o, b + o, kIdescQK, kk > 0 ? 1u : 0u);
                 }
                 commit_elect(bar(L::B_S + X));
             }
@@ -689,12 +688,12 @@ cudaError_t launch_one(const PagedParams& p, const CUtensorMap& tq, const CUtens
                        cudaStream_t s) {
     using L = TilesShape<D, kGroups>;
     static bool ready[64] = {};
-    cudaError_t e = launch_pdl(paged_tiles_kernel<D, kGroups>, dim3((unsigned)p.workers), dim3(L::kThreads), L::kSmem, s, ready,
+    cudaError_t e = launch_pdl(paged_tiles_kernel<D, kGroups>, dim3((unsigned)p.workers), dim3(L::kThreads), L::kSmem, s, true, ready,
                                tq, tk, tv, p);
     if (e != cudaSuccess) return e;
     if (p.pre_rt == 0 && p.workers > 1) {
         static bool cuts_ready[64] = {};
-        e = launch_pdl(paged_cuts_kernel<D, L::M>, dim3((unsigned)p.workers - 1, L::M / 32), dim3(256), 0, s, cuts_ready, p);
+        e = launch_pdl(paged_cuts_kernel<D, L::M>, dim3((unsigned)p.workers - 1, L::M / 32), dim3(256), 0, s, true, cuts_ready, p);
     }
     return e;
 }
