@@ -515,7 +515,7 @@ Lists make_lists(int B, int Hkv, int G, int Nq, bool prefix) {
 
 size_t slot_bytes(int64_t slots, int M, int D) { return (size_t)slots * M * (D * 4 + 8); }
 size_t lists_bytes(const Lists& x, int B, int D) {
-    const size_t index = x.tiles ? (size_t)2 * kMaxTileWorkers * sizeof(int4) : (((size_t)B * x.rt + 1) * 4 + 15) / 16 * 16;
+    const size_t index = x.tiles ? (size_t)2 * kMaxTileWorkers * sizeof(PagedCut) : (((size_t)B * x.rt + 1) * 4 + 15) / 16 * 16;
     return slot_bytes(x.slots, x.M, D) + slot_bytes(x.pre_slots, x.pre_M, D) + index;
 }
 
@@ -660,7 +660,7 @@ int sage_attn_paged(const sage_tensor* q, const sage_tensor* o, const sage_page_
         p.pre_o = reinterpret_cast<float*>(take((size_t)x.pre_slots * x.pre_M * D * 4));
         p.pre_ml = reinterpret_cast<float2*>(take((size_t)x.pre_slots * x.pre_M * 8));
     }
-    if (x.tiles) p.cuts = reinterpret_cast<int4*>(w);
+    if (x.tiles) p.cuts = reinterpret_cast<PagedCut*>(w);
     else p.start = reinterpret_cast<int32_t*>(w);
     const int ctas = std::min(sms, kMaxTileWorkers);       // one per SM; of one row group: two
     p.pre_items_rt = x.pre_items_rt; p.pre_m = x.pre_M; p.pre_tk = x.pre ? 128 : kStep;

@@ -26,6 +26,13 @@ inline FastDiv make_fast_div(uint32_t d) {
     return FastDiv{(uint32_t)(((((uint64_t(1) << s) - d) << 32) / d) + 1), s};
 }
 
+// An item whose tiles several workers share, named by the second of them.
+struct alignas(16) PagedCut {
+    int b, h, rt, n;                     // request (-1: none), key head, row set, query tokens
+    int parts;                           // workers that share it
+    int pad[3];
+};
+
 struct PagedParams {
     const uint16_t* q;                   // BF16 bit patterns
     uint16_t* o;
@@ -57,7 +64,7 @@ struct PagedParams {
     // workspace
     float* part_o;                       // [slot][M][D]
     float2* part_ml;                     // [slot][M] running maximum (log2 domain) and sum
-    int4* cuts;                          // [workers] items that a worker boundary cuts (null: not wanted)
+    PagedCut* cuts;                      // [workers] items that a worker boundary cuts (null: not wanted)
     int32_t* start;                      // [B rt + 1] list position of each (request, row set); last: the length
     // the list that holds the shared prefix's items, for the join
     float* pre_o;

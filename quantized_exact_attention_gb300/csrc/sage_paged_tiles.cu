@@ -419,13 +419,14 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
         // ===================================================== TMA producer
         // Whether this worker's run opens inside an item and is the first to do
         // so: then the item is joined from its parts afterwards.
-        int4 cut = make_int4(-1, 0, 0, 0);                // request, key head, row set, parts
+        PagedCut cut{};
+        cut.b = -1;
         PagedPlace at{};
         at.pos = t1;
         if (t0 < t1) at = paged_place(sched, found[0], t0);
         if (at.pos < t1 && p.cuts != nullptr && at.tile > 0) {
             const int start = at.pos - at.tile, w0 = start / per;
-            if (w0 == worker - 1) cut = make_int4(at.b, at.h, at.rt, (start + at.ntiles - 1) / per - w0 + 1);
+            if (w0 == worker - 1) cut = PagedCut{at.b, at.h, at.rt, at.n, (start + at.ntiles - 1) / per - w0 + 1, {}};
         }
         if (p.cuts != nullptr && lane == 0) p.cuts[worker] = cut;
         const int per_tile = 128 >> p.page_shift;         // pages of a whole tile
@@ -625,46 +626,45 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
 // ---------------------------------------------------------------------------
 template <int D, int M>
 __global__ void __launch_bounds__(256) paged_cuts_kernel(const __grid_constant__ PagedParams p) {
-    constexpr int V = D / 32;
+    constexpr int V = D / 32, kRows = 4;                   // channels of a lane, rows of a warp
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int w = blockIdx.x + 1;
     pdl_trigger();
     pdl_wait();
-    const int4 cut = __ldcg(p.cuts + w);
-    if (cut.x < 0) return;
+    const PagedCut cut = p.cuts[w];
+    if (cut.b < 0) return;
     const PagedSched<M, 128> s(p);
-    const int n = s.q_rows(cut.x);
-    const int r0 = (int)blockIdx.y * 32 + warp * 4;        // four rows of this warp
-    int64_t at[4];                                         // their outputs, -1: no such row
-    bool any = false;
+    const int r0 = (int)blockIdx.y * 32 + warp * kRows;
+    int64_t at[kRows];                                     // their outputs, -1: no such row
+    float acc[kRows][V], m[kRows], l[kRows];
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
+    for (int k = 0; k < kRows; ++k) {
         int b, i, hq;
-        at[k] = paged_row(s, cut.x, cut.y, cut.z, n, r0 + k, b, i, hq) ? b * p.osb + hq * p.osh + i * p.osn : -1;
-        any |= at[k] >= 0;
-    }
-    if (!any) return;
-    float acc[4][V], m[4], l[4];
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
+        at[k] = paged_row(s, cut.b, cut.h, cut.rt, cut.n, r0 + k, b, i, hq) ? b * p.osb + hq * p.osh + i * p.osn : -1;
         m[k] = -INFINITY;
         l[k] = 0.f;
 #pragma unroll
         for (int v = 0; v < V; ++v) acc[k][v] = 0.f;
     }
 #pragma unroll 1
-    for (int j = 0; j < cut.w; ++j) {                      // part 0: the second slot of worker w - 1
+    for (int j = 0; j < cut.parts; ++j) {                  // part 0: the second slot of worker w - 1
         const int64_t q = (int64_t)(j == 0 ? 2 * (w - 1) + 1 : 2 * (w - 1 + j)) * M + r0;
-        float2 ml[4];
-        float y[4][V];
+        float2 ml[kRows];
+        float y[kRows][V];
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {                      // rows that do not exist hold anything and are not stored
+        for (int k = 0; k < kRows; ++k) {                  // rows that do not exist hold anything and are not stored
             ml[k] = __ldcg(p.part_ml + q + k);
-#pragma unroll
-            for (int v = 0; v < V; ++v) y[k][v] = __ldcg(p.part_o + (q + k) * D + lane + 32 * v);
+            const float* src = p.part_o + (q + k) * D + lane * V;
+            if constexpr (V == 4) {
+                const float4 x = __ldcg(reinterpret_cast<const float4*>(src));
+                y[k][0] = x.x; y[k][1] = x.y; y[k][2] = x.z; y[k][3] = x.w;
+            } else {
+                const float2 x = __ldcg(reinterpret_cast<const float2*>(src));
+                y[k][0] = x.x; y[k][1] = x.y;
+            }
         }
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
+        for (int k = 0; k < kRows; ++k) {
             const float mn = fmaxf(m[k], ml[k].x);
             const float ms = mn == -INFINITY ? 0.f : mn;
             const float fa = ex2_approx(m[k] - ms), fb = ex2_approx(ml[k].x - ms);
@@ -675,11 +675,13 @@ __global__ void __launch_bounds__(256) paged_cuts_kernel(const __grid_constant__
         }
     }
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
+    for (int k = 0; k < kRows; ++k) {
         if (at[k] < 0) continue;
         const float inv = l[k] == 0.f ? 0.f : __fdiv_rn(1.f, l[k]);
-#pragma unroll
-        for (int v = 0; v < V; ++v) p.o[at[k] + lane + 32 * v] = (uint16_t)pack2(acc[k][v] * inv, 0.f);
+        uint16_t* dst = p.o + at[k] + lane * V;
+        const uint32_t lo = pack2(acc[k][0] * inv, acc[k][1] * inv);
+        if constexpr (V == 4) *reinterpret_cast<uint2*>(dst) = make_uint2(lo, pack2(acc[k][2] * inv, acc[k][3] * inv));
+        else *reinterpret_cast<uint32_t*>(dst) = lo;
     }
 }
 
