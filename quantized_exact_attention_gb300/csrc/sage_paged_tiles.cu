@@ -153,7 +153,7 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
 }
 
 // Store 32 bytes of each lane's row (at base + at; at < 0: no row) through 32
-// staged rows, so that a store's lanes share sectors.  All 32 lanes call it.
+// staged rows, so that two lanes share a row's sector.  All 32 lanes call it.
 template <class T>
 __device__ __forceinline__ void stage_out(uint8_t* stage, const uint32_t (&w)[8], int64_t at, T* base, int lane) {
 #pragma unroll
@@ -394,7 +394,12 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
 #pragma unroll
                         for (int i = 0; i < 8; ++i)
                             w[i] = pack2(__uint_as_float(o[2 * i]) * inv, __uint_as_float(o[2 * i + 1]) * inv);
-                        stage_out(stage, w, o_at, p.o + c, lane);
+                        if (o_at >= 0) {                  // a whole sector of its row: no staging needed
+                            uint4* dst = reinterpret_cast<uint4*>(p.o + o_at + c);
+                            dst[0] = make_uint4(w[0], w[1], w[2], w[3]);
+                            dst[1] = make_uint4(w[4], w[5], w[6], w[7]);
+                        }
+                        __syncwarp();
                     }
                 } else {
                     const int64_t part = (int64_t)nt.slot * M + X * 128 + row;
