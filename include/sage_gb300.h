@@ -435,7 +435,8 @@ int sage_prep_qkv_noalloc(const sage_tensor* q, const sage_tensor* k, const sage
 size_t sage_prep_noalloc_capacity(void);
 
 /* Test hook for the failure-detection tests: mode 1 makes the next
- * sage_attn_fwd launch withhold its V tile copies, so the MMA issuer's
+ * sage_attn_fwd launch, or the next sage_attn_paged launch of the many-rows
+ * kernel, withhold its V tile copies, so the MMA issuer's
  * bounded wait runs out, the kernel records SAGE_ERR_TIMEOUT, releases its
  * tensor memory and returns; mode 0 restores normal launches.  Use only on
  * a problem of one or a few query tiles (each CTA waits about one second). */

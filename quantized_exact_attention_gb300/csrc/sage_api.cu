@@ -633,8 +633,8 @@ const char* sage_status_string(int code) {
 
 int sage_last_launch_count(void) { return g_last_launches; }
 
-// Test hook (not part of the public header): the next sage_attn_fwd launch
-// withholds one V tile copy so its consumer's bounded wait runs out.
+// Test hook: the next sage_attn_fwd (or many-rows sage_attn_paged) launch
+// withholds its V tile copies so their consumer's bounded wait runs out.
 int sage_debug_inject_fault(int mode) {
     fault_mode_for_next_launch = mode;
     return SAGE_OK;

@@ -171,7 +171,7 @@ __global__ void __launch_bounds__(kRowWarps * 32, 2) paged_rows_kernel(const __g
     // Leave the item's partial result.
     auto leave = [&]() {
         const int64_t slot = (int64_t)worker + item;
-        const int n = ib >= 0 ? sched.q_rows(ib) : 0;
+        const int n = sched.q_rows(ib);
 #pragma unroll
         for (int nr = 0; nr < NR; ++nr) {
 #pragma unroll
@@ -195,7 +195,7 @@ __global__ void __launch_bounds__(kRowWarps * 32, 2) paged_rows_kernel(const __g
     };
     auto enter = [&](const StepNote& nt) {
         item = nt.item; ib = nt.b; ih = nt.h; irt = nt.rt;
-        const int n = ib >= 0 ? sched.q_rows(ib) : 0, len = ib >= 0 ? sched.own_keys(ib) : 0;
+        const int n = sched.q_rows(ib), len = sched.own_keys(ib);
 #pragma unroll
         for (int nr = 0; nr < NR; ++nr) {
             int b, i, hq;
@@ -213,7 +213,7 @@ __global__ void __launch_bounds__(kRowWarps * 32, 2) paged_rows_kernel(const __g
                 m[nr][e] = -INFINITY;
                 l[nr][e] = 0.f;
                 lim[nr][e] = len;
-                if (ib >= 0 && p.causal) {
+                if (p.causal) {
                     const int rr = irt * M + nr * 8 + (lane & 3) * 2 + e;
                     lim[nr][e] = min(len, len - n + fast_div(rr, p.by_G) + 1);
                 }
@@ -343,30 +343,18 @@ __global__ void __launch_bounds__(256) paged_join_kernel(const __grid_constant__
     if (live) {
         const int per = paged_per_worker(p, __ldcg(p.start + p.B * p.rt));
         const int nt = s.item_tiles(n, len, rt), pair = b * p.rt + rt;
-        const RowParts own = parts_of(__ldcg(p.start + pair) + h * s.places(nt) + s.kItemCost, nt, per,
-                                      (p.pre_rt + pair) * p.Hkv + h);
+        const RowParts own = parts_of(__ldcg(p.start + pair) + h * s.places(nt) + s.kItemCost, nt, per, pair * p.Hkv + h);
         const int64_t own_q = own.slot0 * M + (r - rt * M);
         RowParts pre{0, 0};
         int64_t pre_q = 0;
         if (p.pre_items_rt > 0) {
             // the row set of the prefix's list that holds this row, and its place there
-            const int rest = r, pt = (s.lp + p.pre_tk - 1) / p.pre_tk;
-            int set, place;
-            if (p.pre_tok > 0) {
-                const int group = b / p.pre_tok;
-                set = group * 128 / p.pre_m;
-                place = group * 128 - set * p.pre_m + (b - group * p.pre_tok) * p.Nq * p.G + rest;
-            } else {
-                const int rr = b * p.Nq * p.G + rest;
-                set = rr / p.pre_m;
-                place = rr - set * p.pre_m;
-            }
+            using Tiles = PagedSched<128, 128>;
+            const int pt = (s.lp + 127) / 128, group = b / p.pre_tok;
+            const int set = group * 128 / p.pre_m, place = group * 128 - set * p.pre_m + (b - group * p.pre_tok) * p.Nq * p.G + r;
             const int it = set * p.Hkv + h;
-            // alone in its list, or at the front of this one
-            const int cost = p.pre_rt > 0 ? s.kItemCost : PagedSched<128, 128>::kItemCost;
-            const int pre_per =
-                p.pre_rt > 0 ? per : max(1, (p.Hkv * p.pre_items_rt * (pt + cost) + p.pre_workers - 1) / p.pre_workers);
-            pre = parts_of(it * (pt + cost) + cost, pt, pre_per, it);
+            const int pre_per = max(1, (p.Hkv * p.pre_items_rt * Tiles::places(pt) + p.pre_workers - 1) / p.pre_workers);
+            pre = parts_of(it * Tiles::places(pt) + Tiles::kItemCost, pt, pre_per, it);
             pre_q = pre.slot0 * p.pre_m + place;
         }
         const int parts = own.n + pre.n;
@@ -449,36 +437,40 @@ __global__ void __launch_bounds__(256) paged_join_kernel(const __grid_constant__
 // Host side: which kernel reads which keys for which rows.
 //
 // A request brings rows = Nq * G query rows to a key head.
-//  - rows > 32: the many-rows kernel, each request's keys behind the prefix
+//  - rows > 16: the many-rows kernel, each request's keys behind the prefix
 //    (one list; the prefix is read again for every request, mostly from L2).
-//    More than 128 query heads to a key head leave no whole token in a group:
-//    these, which no model is known to have, stay with the few-rows kernel.
-//  - rows <= 32: the few-rows kernel for the own keys.  The prefix, when
-//    several requests share it, is read once for all their rows: by the
-//    few-rows kernel in the same list when all rows together are 32 or
-//    fewer, else by the many-rows kernel in a list of its own.
+//    Rows that fill a quarter of its 128 waste tensor work that reading the
+//    keys hides: 16 requests of 24 rows and up to 4,000 keys take 37 us, in a
+//    32-row form of the few-rows kernel 62; 8 of 32 rows and up to 16,000, 57
+//    and 94.  (More than 128 query heads to a key head leave no whole token in
+//    a group: these, which no model is known to have, stay with the few-rows
+//    kernel.)
+//  - rows <= 16: the few-rows kernel, each request's keys behind the prefix
+//    while reading the prefix again for every request costs less than a list
+//    of its own, which the many-rows kernel then reads once for all rows: 64
+//    requests, 8 key heads, 512 shared keys (134 MB read again) take 36 us so
+//    and 43 with a list, 2,048 keys (537 MB) 66 and 52.
 // ---------------------------------------------------------------------------
-constexpr int kFewRows = 32;
+constexpr int kFewRows = 16;
+constexpr int64_t kReadAgain = int64_t(256) << 20;        // bytes of prefix read again that cost as much as its list
 
 struct Lists {
     // the list with the own keys
     bool tiles;                          // many-rows kernel
     int groups;                          // ... 128-row groups of an item
+    int tok, unit;                       // ... tokens of a group, rows of a token
     int nr;                              // few-rows kernel: 8-row groups of an item
     int M, rt, join;
-    int tok, unit;                       // many-rows kernel: tokens of a 128-row group, rows of a token
-    int pre_rt;                          // shared prefix items in this list
     int64_t slots;
     // the prefix's own list (many-rows kernel)
     bool pre;
-    int pre_groups;
-    int pre_M, pre_items_rt, pre_tok, pre_unit;
+    int pre_groups, pre_tok, pre_unit, pre_M, pre_items_rt;
     int64_t pre_slots;
 };
 
-Lists make_lists(int B, int Hkv, int G, int Nq, bool prefix) {
+Lists make_lists(int B, int Hkv, int G, int Nq, int D, int64_t pre_keys) {
     Lists x{};
-    const int64_t rows = (int64_t)Nq * G, all = rows * B;
+    const int64_t rows = (int64_t)Nq * G;
     if (rows > kFewRows && G <= 128) {
         x.tiles = true;
         x.unit = G;
@@ -486,23 +478,17 @@ Lists make_lists(int B, int Hkv, int G, int Nq, bool prefix) {
         x.groups = Nq <= x.tok ? 1 : 2;
         x.M = 128 * x.groups;
         x.rt = (int)ceil_div(Nq, x.tok * x.groups);
-        x.join = prefix;
+        x.join = pre_keys > 0;
         x.slots = 2 * kMaxTileWorkers * (3 - x.groups);
         return x;
     }
-    const bool shared = prefix && B > 1 && rows <= kFewRows;
-    const int64_t most = shared && all <= kFewRows ? all : rows;
-    x.nr = most <= 8 ? 1 : (most <= 16 ? 2 : 4);             // more than 32 rows: several sets
+    x.nr = rows <= 8 ? 1 : 2;                             // more than 16 rows: several sets
     x.M = 8 * x.nr;
     x.rt = (int)ceil_div(rows, x.M);
-    x.join = prefix && !shared;
     x.slots = (int64_t)B * Hkv * x.rt + kMaxRowWorkers;
-    if (shared && all <= kFewRows) {
-        x.pre_rt = x.pre_items_rt = (int)ceil_div(all, x.M);
-        x.pre_M = x.M;
-        x.slots += (int64_t)Hkv * x.pre_rt;
-    } else if (shared) {
-        x.pre = true;
+    x.pre = rows <= kFewRows && B > 1 && (double)B * Hkv * pre_keys * D * 4 > (double)kReadAgain;
+    x.join = pre_keys > 0 && !x.pre;
+    if (x.pre) {
         x.pre_unit = (int)rows;
         x.pre_tok = 128 / x.pre_unit;
         x.pre_groups = B <= x.pre_tok ? 1 : 2;
@@ -561,9 +547,9 @@ cudaError_t launch_rows(const PagedParams& p, cudaStream_t s) {
     return launch_pdl(paged_join_kernel<D, 8 * NR, kStep, 1>, dim3((unsigned)ceil_div(rows, 8), (unsigned)p.B), dim3(256), 0, s, true,
                       join1_ready, p);
 }
-template <int D>
-cudaError_t launch_rows_d(const PagedParams& p, int nr, cudaStream_t s) {
-    return nr == 1 ? launch_rows<D, 1>(p, s) : (nr == 2 ? launch_rows<D, 2>(p, s) : launch_rows<D, 4>(p, s));
+cudaError_t launch_rows(const PagedParams& p, int D, int nr, cudaStream_t s) {
+    if (D == 64) return nr == 1 ? launch_rows<64, 1>(p, s) : launch_rows<64, 2>(p, s);
+    return nr == 1 ? launch_rows<128, 1>(p, s) : launch_rows<128, 2>(p, s);
 }
 
 }  // namespace
@@ -577,9 +563,10 @@ int sage_paged_workspace(int B, int H, int Hkv, int Nq, int D, size_t* bytes) {
     if (bytes == nullptr) return SAGE_ERR_ARG;
     const int rc = check_batch(B, H, Hkv, Nq, D);
     if (rc != SAGE_OK) return rc;
-    const size_t a = lists_bytes(make_lists(B, Hkv, H / Hkv, Nq, false), B, D);
-    const size_t b = lists_bytes(make_lists(B, Hkv, H / Hkv, Nq, true), B, D);
-    *bytes = a > b ? a : b;
+    // a prefix of any length may come: the form with a list of its own needs the most
+    *bytes = lists_bytes(make_lists(B, Hkv, H / Hkv, Nq, D, INT32_MAX), B, D);
+    const size_t alone = lists_bytes(make_lists(B, Hkv, H / Hkv, Nq, D, 0), B, D);
+    if (alone > *bytes) *bytes = alone;
     return SAGE_OK;
 }
 
@@ -605,7 +592,7 @@ int sage_attn_paged(const sage_tensor* q, const sage_tensor* o, const sage_page_
     const int64_t own_keys = (int64_t)table_width * cache->page_size;
     const int64_t pre_keys = (int64_t)prefix_width * cache->page_size;
     if (own_keys > INT32_MAX - 256 || pre_keys > INT32_MAX - 256) return SAGE_ERR_UNSUPPORTED;
-    const Lists x = make_lists(B, cache->heads, H / cache->heads, Nq, prefix_width > 0);
+    const Lists x = make_lists(B, cache->heads, H / cache->heads, Nq, D, pre_keys);
     if (workspace == nullptr || !aligned16(workspace) || workspace_bytes < lists_bytes(x, B, D)) return SAGE_ERR_ARG;
     // list positions and slot numbers stay in int
     const int tk = x.tiles ? 128 : kStep;
@@ -644,18 +631,15 @@ int sage_attn_paged(const sage_tensor* q, const sage_tensor* o, const sage_page_
     p.causal = causal != 0;
     const double scale = sm_scale > 0.f ? (double)sm_scale : 1.0 / std::sqrt((double)D);
     p.sc = (float)(scale * (1.0 / std::log(2.0)));
-    p.rt = x.rt; p.pre_rt = x.pre_rt; p.join = x.join;
+    p.rt = x.rt; p.join = x.join;
     p.tok = x.tok; p.unit = x.unit;
     p.by_G = make_fast_div(p.G);
-    p.by_rows = make_fast_div(Nq * p.G);
     p.by_rt = make_fast_div(x.rt);
     p.by_unit = make_fast_div(x.unit > 0 ? x.unit : 1);
     char* w = static_cast<char*>(workspace);
     auto take = [&](size_t n) { char* at = w; w += n; return at; };
     p.part_o = reinterpret_cast<float*>(take((size_t)x.slots * x.M * D * 4));
     p.part_ml = reinterpret_cast<float2*>(take((size_t)x.slots * x.M * 8));
-    p.pre_o = p.part_o;
-    p.pre_ml = p.part_ml;
     if (x.pre) {
         p.pre_o = reinterpret_cast<float*>(take((size_t)x.pre_slots * x.pre_M * D * 4));
         p.pre_ml = reinterpret_cast<float2*>(take((size_t)x.pre_slots * x.pre_M * 8));
@@ -663,8 +647,8 @@ int sage_attn_paged(const sage_tensor* q, const sage_tensor* o, const sage_page_
     if (x.tiles) p.cuts = reinterpret_cast<PagedCut*>(w);
     else p.start = reinterpret_cast<int32_t*>(w);
     const int ctas = std::min(sms, kMaxTileWorkers);       // one per SM; of one row group: two
-    p.pre_items_rt = x.pre_items_rt; p.pre_m = x.pre_M; p.pre_tk = x.pre ? 128 : kStep;
-    p.pre_workers = ctas * (3 - x.pre_groups); p.pre_tok = x.pre_tok;
+    p.pre_items_rt = x.pre_items_rt; p.pre_m = x.pre_M; p.pre_tok = x.pre_tok;
+    p.pre_workers = ctas * (3 - x.pre_groups);
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
     cudaError_t e;
     int launches = 0;
@@ -683,7 +667,7 @@ int sage_attn_paged(const sage_tensor* q, const sage_tensor* o, const sage_page_
             p.beside = 1;
         }
         p.workers = std::min(2 * sms, kMaxRowWorkers / kRowWarps) * kRowWarps;
-        e = D == 64 ? launch_rows_d<64>(p, x.nr, s) : launch_rows_d<128>(p, x.nr, s);
+        e = launch_rows(p, D, x.nr, s);
         launches += 2;
     }
     if (e != cudaSuccess) return SAGE_ERR_LAUNCH;

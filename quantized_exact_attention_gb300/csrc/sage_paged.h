@@ -54,9 +54,9 @@ struct PagedParams {
     int* status;
     // schedule (see sage_paged_sched.cuh)
     int rt;                              // row sets of a request
-    int pre_rt;                          // row sets of all requests against the prefix (0: not in this list)
+    int pre_rt;                          // row sets of all requests against the prefix (0: a list of own keys)
     int tok, unit;                       // tiles kernel: tokens (prefix items: requests) of a group, rows of one
-    FastDiv by_G, by_rows, by_rt, by_unit;           // G, Nq * G, rt, unit
+    FastDiv by_G, by_rt, by_unit;        // G, rt, unit
     int join;                            // 1: a request's key sequence is the prefix followed by its own keys
     int workers;                         // workers the list is shared among
     int fault_mode;                      // test hook: 0 = none
@@ -66,11 +66,11 @@ struct PagedParams {
     float2* part_ml;                     // [slot][M] running maximum (log2 domain) and sum
     PagedCut* cuts;                      // [workers] items that a worker boundary cuts (null: not wanted)
     int32_t* start;                      // [B rt + 1] list position of each (request, row set); last: the length
-    // the list that holds the shared prefix's items, for the join
+    // the shared prefix's list, for the join
     float* pre_o;
     float2* pre_ml;
-    int pre_items_rt, pre_m, pre_tk, pre_workers;    // row sets (0: none), rows of an item, keys of a tile, workers
-    int pre_tok;                         // requests of a 128-row group (0: rows after one another)
+    int pre_items_rt, pre_m, pre_workers;            // row sets (0: no such list), rows of an item, workers
+    int pre_tok;                         // requests of a 128-row group
 };
 
 // The many-rows kernel (sage_paged_tiles.cu): workers = CTAs, groups: row groups

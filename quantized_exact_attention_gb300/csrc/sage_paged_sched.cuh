@@ -1,12 +1,13 @@
 // sage_paged_sched.cuh - how the paged attention kernels share their work.
 //
 // The work is a list of items.  An item is a set of query rows of one key head
-// and the key sequence they read, cut into tiles of TK keys.  The list holds,
-// in this order,
-//   (1) for each set of rows out of ALL requests' rows, and each key head: the
-//       shared prefix (only when the prefix is computed once for all);
-//   (2) for each request, each set of its rows, and each key head: its own
-//       keys, preceded by the prefix when join = 1.
+// and the key sequence they read, cut into tiles of TK keys.  The list holds
+// either, for a prefix computed once for all (pre_rt > 0; tiles kernel only),
+//   for each set of rows out of ALL requests' rows, and each key head: the
+//   shared prefix;
+// or
+//   for each request, each set of its rows, and each key head: its own keys,
+//   preceded by the prefix when join = 1.
 // Each item takes as many places in the list as it has tiles, and kItemCost in
 // front of them, which stand for what an item costs a worker besides its tiles
 // (fetching its rows, writing its output).  The places are cut into equal
@@ -18,10 +19,10 @@
 // the worker or the item advances by one, so the slots are distinct.
 //
 // Sets of rows, in the order of query token, then query head of the key head:
-//   rows kernel (TK = 16): M rows after one another;
-//   tiles kernel (TK = 128): groups of 128 rows that hold whole tokens (of the
-//   shared prefix's items: whole requests), `tok` of them, so that a group is
-//   one box of a tensor map; the rows left over stay empty.
+//   few-rows kernel (TK = 16): M rows after one another;
+//   many-rows kernel (TK = 128): groups of 128 rows that hold whole tokens (of
+//   the shared prefix's items: whole requests), `tok` of them, so that a group
+//   is one box of a tensor map; the rows left over stay empty.
 #pragma once
 
 #include "sage_paged.h"
@@ -76,8 +77,8 @@ struct PagedSched {
 // The length of the list, and where the CTA's workers begin.  A block of
 // THREADS threads sums the places of the (request, row set) pairs; the thread
 // whose pairs hold the first place of worker first_worker + w*worker_step
-// (w < NW) leaves {pair, the pair's first place} in found[w] ({-1, 0}: among
-// the prefix items).  With `publish` the positions of all
+// (w < NW) leaves {pair, the pair's first place} in found[w] ({-1, 0}: a
+// list of prefix items).  With `publish` the positions of all
 // pairs go to p.start as well.  `red` holds THREADS/32 ints.  Ends with a
 // barrier.
 template <int M, int TK, int THREADS, int NW>
@@ -167,7 +168,7 @@ __device__ __forceinline__ PagedPlace paged_place(const PagedSched<M, TK>& s, in
         x.ntiles = s.item_tiles(x.n, x.len, x.rt);
         x.h = (t - found.y) / s.places(x.ntiles);
         o = t - found.y - x.h * s.places(x.ntiles);
-        x.item = (p.pre_rt + found.x) * p.Hkv + x.h;
+        x.item = found.x * p.Hkv + x.h;
     }
     x.tile = max(0, o - s.kItemCost);
     x.pos = t - o + s.kItemCost + x.tile;
@@ -188,9 +189,12 @@ __device__ __forceinline__ void paged_next(const PagedSched<M, TK>& s, PagedPlac
     x.item -= p.Hkv;
     do {                                 // the next row set that has tiles
         x.item += p.Hkv;
-        if (x.b < 0 && ++x.rt < p.pre_rt) return;
-        if (x.b < 0 && p.rt == 0) { x.pos = INT32_MAX; return; }      // a list of prefix items only
-        if (x.b < 0 || ++x.rt == p.rt) {
+        ++x.rt;
+        if (x.b < 0) {
+            if (x.rt == p.pre_rt) x.pos = INT32_MAX;
+            return;
+        }
+        if (x.rt == p.rt) {
             x.rt = 0;
             if (++x.b >= p.B) { x.ntiles = 0; x.pos = INT32_MAX; return; }
             x.n = s.q_rows(x.b);
@@ -237,16 +241,11 @@ __device__ __forceinline__ bool paged_row(const PagedSched<M, TK>& s, int ib, in
         hq = ih * p.G + rest;
         return u < p.tok && i < n;
     } else {
-        int row = irt * M + r;
+        const int row = irt * M + r;
         b = ib;
-        if (ib < 0) {
-            b = fast_div(row, p.by_rows);
-            row -= b * p.Nq * p.G;
-            if (b >= p.B) return false;
-        }
         i = fast_div(row, p.by_G);
         hq = ih * p.G + row - i * p.G;
-        return i < (ib < 0 ? s.q_rows(b) : n);
+        return i < n;
     }
 }
 

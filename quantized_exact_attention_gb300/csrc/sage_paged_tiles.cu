@@ -627,11 +627,11 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
 // ---------------------------------------------------------------------------
 // Join the items that a worker boundary cuts (list without shared prefix
 // items; whole items were written by the kernel above).  blockIdx.x + 1 is
-// the worker behind the boundary, blockIdx.y a group of 32 rows.
+// the worker behind the boundary, blockIdx.y a group of 16 rows.
 // ---------------------------------------------------------------------------
 template <int D, int M>
 __global__ void __launch_bounds__(256) paged_cuts_kernel(const __grid_constant__ PagedParams p) {
-    constexpr int V = D / 32, kRows = 4;                   // channels of a lane, rows of a warp
+    constexpr int V = D / 32, kRows = 2, kFlight = 4;      // channels of a lane, rows of a warp, parts in flight
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int w = blockIdx.x + 1;
     pdl_trigger();
@@ -639,53 +639,58 @@ __global__ void __launch_bounds__(256) paged_cuts_kernel(const __grid_constant__
     const PagedCut cut = p.cuts[w];
     if (cut.b < 0) return;
     const PagedSched<M, 128> s(p);
-    const int r0 = (int)blockIdx.y * 32 + warp * kRows;
-    int64_t at[kRows];                                     // their outputs, -1: no such row
-    float acc[kRows][V], m[kRows], l[kRows];
+    const int r0 = ((int)blockIdx.y * 8 + warp) * kRows;
 #pragma unroll
     for (int k = 0; k < kRows; ++k) {
         int b, i, hq;
-        at[k] = paged_row(s, cut.b, cut.h, cut.rt, cut.n, r0 + k, b, i, hq) ? b * p.osb + hq * p.osh + i * p.osn : -1;
-        m[k] = -INFINITY;
-        l[k] = 0.f;
+        if (!paged_row(s, cut.b, cut.h, cut.rt, cut.n, r0 + k, b, i, hq)) continue;
+        float acc[V], m = -INFINITY, l = 0.f;
 #pragma unroll
-        for (int v = 0; v < V; ++v) acc[k][v] = 0.f;
-    }
+        for (int v = 0; v < V; ++v) acc[v] = 0.f;
 #pragma unroll 1
-    for (int j = 0; j < cut.parts; ++j) {                  // part 0: the second slot of worker w - 1
-        const int64_t q = (int64_t)(j == 0 ? 2 * (w - 1) + 1 : 2 * (w - 1 + j)) * M + r0;
-        float2 ml[kRows];
-        float y[kRows][V];
+        for (int j0 = 0; j0 < cut.parts; j0 += kFlight) {
+            float2 ml[kFlight];
+            float y[kFlight][V];
 #pragma unroll
-        for (int k = 0; k < kRows; ++k) {                  // rows that do not exist hold anything and are not stored
-            ml[k] = __ldcg(p.part_ml + q + k);
-            const float* src = p.part_o + (q + k) * D + lane * V;
-            if constexpr (V == 4) {
-                const float4 x = __ldcg(reinterpret_cast<const float4*>(src));
-                y[k][0] = x.x; y[k][1] = x.y; y[k][2] = x.z; y[k][3] = x.w;
-            } else {
-                const float2 x = __ldcg(reinterpret_cast<const float2*>(src));
-                y[k][0] = x.x; y[k][1] = x.y;
+            for (int f = 0; f < kFlight; ++f) {            // part 0: the second slot of worker w - 1
+                const int j = j0 + f;
+                const int64_t q = (int64_t)(j == 0 ? 2 * (w - 1) + 1 : 2 * (w - 1 + j)) * M + r0 + k;
+                ml[f] = make_float2(-INFINITY, 0.f);
+#pragma unroll
+                for (int v = 0; v < V; ++v) y[f][v] = 0.f;
+                if (j < cut.parts) {
+                    ml[f] = __ldcg(p.part_ml + q);
+                    const float* src = p.part_o + q * D + lane * V;
+                    if constexpr (V == 4) {
+                        const float4 x = __ldcg(reinterpret_cast<const float4*>(src));
+                        y[f][0] = x.x; y[f][1] = x.y; y[f][2] = x.z; y[f][3] = x.w;
+                    } else {
+                        const float2 x = __ldcg(reinterpret_cast<const float2*>(src));
+                        y[f][0] = x.x; y[f][1] = x.y;
+                    }
+                }
             }
-        }
+            float mn = m;
 #pragma unroll
-        for (int k = 0; k < kRows; ++k) {
-            const float mn = fmaxf(m[k], ml[k].x);
+            for (int f = 0; f < kFlight; ++f) mn = fmaxf(mn, ml[f].x);
             const float ms = mn == -INFINITY ? 0.f : mn;
-            const float fa = ex2_approx(m[k] - ms), fb = ex2_approx(ml[k].x - ms);
-            l[k] = l[k] * fa + ml[k].y * fb;
+            const float fa = ex2_approx(m - ms);
+            l *= fa;
 #pragma unroll
-            for (int v = 0; v < V; ++v) acc[k][v] = acc[k][v] * fa + y[k][v] * fb;
-            m[k] = mn;
+            for (int v = 0; v < V; ++v) acc[v] *= fa;
+#pragma unroll
+            for (int f = 0; f < kFlight; ++f) {
+                const float fb = ex2_approx(ml[f].x - ms);
+                l += ml[f].y * fb;
+#pragma unroll
+                for (int v = 0; v < V; ++v) acc[v] += y[f][v] * fb;
+            }
+            m = mn;
         }
-    }
-#pragma unroll
-    for (int k = 0; k < kRows; ++k) {
-        if (at[k] < 0) continue;
-        const float inv = l[k] == 0.f ? 0.f : __fdiv_rn(1.f, l[k]);
-        uint16_t* dst = p.o + at[k] + lane * V;
-        const uint32_t lo = pack2(acc[k][0] * inv, acc[k][1] * inv);
-        if constexpr (V == 4) *reinterpret_cast<uint2*>(dst) = make_uint2(lo, pack2(acc[k][2] * inv, acc[k][3] * inv));
+        const float inv = l == 0.f ? 0.f : __fdiv_rn(1.f, l);
+        uint16_t* dst = p.o + b * p.osb + hq * p.osh + i * p.osn + lane * V;
+        const uint32_t lo = pack2(acc[0] * inv, acc[1] * inv);
+        if constexpr (V == 4) *reinterpret_cast<uint2*>(dst) = make_uint2(lo, pack2(acc[V - 2] * inv, acc[V - 1] * inv));
         else *reinterpret_cast<uint32_t*>(dst) = lo;
     }
 }
@@ -700,7 +705,7 @@ cudaError_t launch_one(const PagedParams& p, const CUtensorMap& tq, const CUtens
     if (e != cudaSuccess) return e;
     if (p.pre_rt == 0 && p.workers > 1) {
         static bool cuts_ready[64] = {};
-        e = launch_pdl(paged_cuts_kernel<D, L::M>, dim3((unsigned)p.workers - 1, L::M / 32), dim3(256), 0, s, true, cuts_ready, p);
+        e = launch_pdl(paged_cuts_kernel<D, L::M>, dim3((unsigned)p.workers - 1, L::M / 16), dim3(256), 0, s, true, cuts_ready, p);
     }
     return e;
 }

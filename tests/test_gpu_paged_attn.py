@@ -48,6 +48,17 @@ def test_shared_prefix(prefix, B, Nq, G, D):
     go(B=B, H=2 * G, Hkv=2, D=D, Nq=Nq, page=16, kv_len=kv, prefix=prefix, seed=prefix + B)
 
 
+# A prefix whose repeated reading would cost over 256 MB is read once for all
+# rows: few rows, one and two groups of 128 rows, a last group that is not full.
+@pytest.mark.parametrize("B,Hkv,G,Nq,D,prefix", [
+    (40, 8, 1, 1, 128, 1700), (70, 4, 8, 1, 64, 4001), (33, 8, 2, 3, 128, 2100), (300, 2, 4, 2, 64, 2000),
+    (8, 16, 16, 1, 64, 8200), (2, 8, 3, 5, 128, 33000), (129, 8, 1, 1, 64, 1025), (17, 4, 5, 3, 128, 8000)])
+def test_long_shared_prefix(B, Hkv, G, Nq, D, prefix):
+    kv = [(37 * b) % 90 for b in range(B)]
+    q = [min(Nq, 1 + b % Nq) if b % 7 else 0 for b in range(B)]
+    go(B=B, H=Hkv * G, Hkv=Hkv, D=D, Nq=Nq, page=32, kv_len=kv, q_len=q, prefix=prefix, seed=prefix + B)
+
+
 @pytest.mark.parametrize("prefix", [0, 50])
 @pytest.mark.parametrize("Nq", [1, 4, 40])
 @pytest.mark.parametrize("causal", [True, False])
@@ -94,10 +105,10 @@ def test_lengths_left_out_and_out_of_range(causal):
     assert int(o3.count_nonzero()) == 0
 
 
-@pytest.mark.parametrize("Nq,H", [(1, 8), (1, 128), (60, 8)])
-def test_prefix_without_own_table(Nq, H):
+@pytest.mark.parametrize("B,Nq,H,prefix", [(6, 1, 8, 300), (6, 1, 128, 300), (6, 60, 8, 300), (50, 1, 8, 2700)])
+def test_prefix_without_own_table(B, Nq, H, prefix):
     G.ensure_built()
-    p = P.make(B=6, H=H, Hkv=4, D=128, Nq=Nq, page=32, kv_len=[0] * 6, prefix=300, seed=5)
+    p = P.make(B=B, H=H, Hkv=4, D=128, Nq=Nq, page=32, kv_len=[0] * B, prefix=prefix, seed=5)
     p.table = None
     P.check(p, P.run(p))
 
@@ -123,12 +134,13 @@ def test_long_and_many(B, H, Hkv, D, Nq, n, prefix):
     go(B=B, H=H, Hkv=Hkv, D=D, Nq=Nq, page=64, kv_len=kv, prefix=prefix, seed=n)
 
 
-@pytest.mark.parametrize("Nq,prefix", [(1, 0), (1, 500), (100, 500)])
-def test_strided_views(Nq, prefix):
+@pytest.mark.parametrize("B,Nq,prefix", [(4, 1, 0), (4, 1, 500), (4, 100, 500), (64, 1, 8300)])
+def test_strided_views(B, Nq, prefix):
     """q inside a fused projection, o inside a wider buffer, table rows apart."""
     G.ensure_built()
-    B, H, Hkv, D = 4, 8, 2, 64
-    p = P.make(B=B, H=H, Hkv=Hkv, D=D, Nq=Nq, page=16, kv_len=[Nq + 9, Nq, Nq + 200, Nq + 31], prefix=prefix, seed=21)
+    H, Hkv, D = 8, 2, 64
+    kv = [Nq + (9, 0, 200, 31)[b % 4] for b in range(B)]
+    p = P.make(B=B, H=H, Hkv=Hkv, D=D, Nq=Nq, page=16, kv_len=kv, prefix=prefix, seed=21)
     fused = torch.zeros((B, Nq, H + 2 * Hkv, D), dtype=torch.bfloat16, device="cuda")
     fused[:, :, :H] = p.q.permute(0, 2, 1, 3)
     p.q = fused[:, :, :H].permute(0, 2, 1, 3)
@@ -140,10 +152,11 @@ def test_strided_views(Nq, prefix):
     assert bool((buf[:, :, 0] == 7).all()) and bool((buf[:, :, -1] == 7).all()) and bool((buf[..., D:] == 7).all())
 
 
-@pytest.mark.parametrize("Nq,H,prefix", [(1, 4, 0), (1, 4, 100), (90, 4, 0), (1, 128, 100)])
-def test_a_page_outside_the_cache_reads_as_zeros_and_is_reported(Nq, H, prefix):
+@pytest.mark.parametrize("B,Nq,H,prefix", [(2, 1, 4, 0), (2, 1, 4, 100), (2, 90, 4, 0), (2, 1, 128, 100), (64, 1, 4, 4200)])
+def test_a_page_outside_the_cache_reads_as_zeros_and_is_reported(B, Nq, H, prefix):
     G.ensure_built()
-    p = P.make(B=2, H=H, Hkv=2, D=128, Nq=Nq, page=16, kv_len=[Nq + 100, Nq + 60], prefix=prefix, poison=0.0, seed=31)
+    p = P.make(B=B, H=H, Hkv=2, D=128, Nq=Nq, page=16, kv_len=[Nq + 100, Nq + 60] * (B // 2), prefix=prefix, poison=0.0,
+               seed=31)
     zero = p.cache_k.shape[0]                              # a page of zeros, added to the definition's cache only
     good = P.Paged(**{**p.__dict__})
     good.cache_k = torch.cat((p.cache_k, torch.zeros_like(p.cache_k[:1])))
@@ -162,7 +175,7 @@ def test_a_page_outside_the_cache_reads_as_zeros_and_is_reported(Nq, H, prefix):
         P.check(good, o)
 
 
-@pytest.mark.parametrize("B,H,Hkv,Nq,n,prefix", [(8, 8, 2, 1, 3000, 0), (40, 8, 2, 1, 500, 3000), (2, 4, 2, 200, 2000, 700)])
+@pytest.mark.parametrize("B,H,Hkv,Nq,n,prefix", [(8, 8, 2, 1, 3000, 0), (40, 8, 2, 1, 500, 3000), (70, 8, 2, 1, 500, 4000), (2, 4, 2, 200, 2000, 700)])
 def test_equal_inputs_give_equal_bits(B, H, Hkv, Nq, n, prefix):
     G.ensure_built()
     p = P.make(B=B, H=H, Hkv=Hkv, D=128, Nq=Nq, page=32, kv_len=[Nq + max(0, n - 71 * b) for b in range(B)], prefix=prefix,
@@ -174,12 +187,12 @@ def test_equal_inputs_give_equal_bits(B, H, Hkv, Nq, n, prefix):
         assert torch.equal(P.run(p, workspace=ws), first)
 
 
-@pytest.mark.parametrize("Nq,prefix", [(1, 0), (1, 700), (130, 700)])
-def test_captured_and_replayed_with_growing_lengths(Nq, prefix):
+@pytest.mark.parametrize("B,Nq,prefix", [(3, 1, 0), (3, 1, 700), (3, 130, 700), (60, 1, 4700)])
+def test_captured_and_replayed_with_growing_lengths(B, Nq, prefix):
     """One graph, captured once, serves every later length: the lengths are read on the device."""
     G.ensure_built()
-    B, H, Hkv, D = 3, 8, 2, 128
-    long = [Nq + 400, Nq + 17, Nq + 250]
+    H, Hkv, D = 8, 2, 128
+    long = [Nq + 400, Nq + 17, Nq + 250] * (B // 3)
     p = P.make(B=B, H=H, Hkv=Hkv, D=D, Nq=Nq, page=16, kv_len=long, prefix=prefix, seed=51)
     cache = S.PageCache(p.cache_k, p.cache_v)
     ws = S.alloc_paged_workspace(B, H, Hkv, Nq, D)
@@ -201,7 +214,7 @@ def test_captured_and_replayed_with_growing_lengths(Nq, prefix):
     for g in graphs:
         with torch.cuda.graph(g):
             call()
-    for k, lens in enumerate(([Nq, Nq, Nq], [Nq + 400, Nq + 3, Nq + 99], long)):
+    for k, lens in enumerate(([Nq] * B, [Nq + 400, Nq + 3, Nq + 99] * (B // 3), long)):
         kv_len.copy_(torch.tensor(lens, dtype=torch.int32))
         o.fill_(7.0)
         graphs[k % 2].replay()
@@ -229,6 +242,62 @@ def test_two_streams_with_their_own_workspaces():
                               prefix_len=pl if p.prefix_table is not None else None, stream=s)
     for p, o in zip(ps, outs):
         P.check(p, o)
+
+
+def test_padding_rows_of_q_and_stale_outputs_do_not_matter():
+    """NaN in the query rows behind q_len, and in the output before the call."""
+    G.ensure_built()
+    for Nq, H in ((3, 4), (50, 4), (200, 2)):
+        p = P.make(B=3, H=H, Hkv=2, D=64, Nq=Nq, page=32, q_len=[Nq, 1, Nq // 2], kv_len=[Nq + 70, 40, Nq], prefix=45, seed=Nq)
+        for b, n in enumerate(p.q_len):
+            p.q[b, :, n:] = float("nan")
+        o = torch.full((3, Nq, H, 64), float("nan"), dtype=torch.bfloat16, device="cuda").permute(0, 2, 1, 3)
+        P.run(p, o=o)
+        for b, n in enumerate(p.q_len):
+            assert bool(o[b, :, n:].isnan().all())
+            o[b, :, n:] = 7.0
+        P.check(p, o)
+
+
+def test_waits_for_what_the_stream_waits_for():
+    """Lengths, tables, keys and q written just before, by kernels of this stream and by another stream's."""
+    G.ensure_built()
+    for B, Nq, prefix in ((4, 1, 0), (3, 60, 100), (64, 1, 4300)):
+        p = P.make(B=B, H=8, Hkv=2, D=128, Nq=Nq, page=16, kv_len=[Nq + 300 - 2 * b for b in range(B)], prefix=prefix, seed=B)
+        want = P.run(p).clone()
+        torch.cuda.synchronize()
+        keep = [t.clone() for t in (p.q, p.cache_k, p.cache_v, p.table)]
+        other, big = torch.cuda.Stream(), torch.randn((4096, 4096), device="cuda")
+        for _ in range(3):
+            for t in (p.q, p.cache_k, p.cache_v):
+                t.fill_(float("nan"))
+            p.table.fill_(0)
+            torch.cuda.synchronize()
+            with torch.cuda.stream(other):
+                for _ in range(4):
+                    big = big @ big * 1e-3
+                for t, k in zip((p.q, p.cache_k, p.cache_v, p.table), keep):
+                    t.copy_(k)
+                done = other.record_event()
+            torch.cuda.current_stream().wait_event(done)
+            assert torch.equal(P.run(p), want)
+            p.q.copy_(keep[0] * 0)
+            P.run(p)
+            p.q.copy_(keep[0])
+            assert torch.equal(P.run(p), want)
+    assert S.sage_get_device_status() == S.SAGE_OK
+
+
+def test_a_withheld_copy_times_out_and_the_context_survives():
+    """The many-rows kernel's bounded waits, on a few CTAs (about a second each)."""
+    G.ensure_built()
+    for D, Nq in ((128, 40), (64, 40), (128, 300), (64, 300)):
+        p = P.make(B=1, H=2, Hkv=1, D=D, Nq=Nq, page=64, kv_len=[Nq + 100], seed=D)
+        S.sage_debug_inject_fault(1)
+        P.run(p)
+        torch.cuda.synchronize()
+        assert S.sage_get_device_status() == S.SAGE_ERR_TIMEOUT
+        P.check(p, P.run(p))
 
 
 def test_cache_offsets_behind_two_to_the_32_elements():
