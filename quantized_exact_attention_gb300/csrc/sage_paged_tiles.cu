@@ -211,18 +211,20 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
         for (int i = L::B_KF; i < L::kBars; ++i) mbar_init(bar(i), 1);
         fence_mbar_init();
     }
-    if (warp == L::kWarpIssue) {
-        tmem_alloc(sbase + L::OFF_TMEM, L::kCols);
-        tmem_relinquish();
-    }
     if (warp == L::kWarpLoad && lane == 0) {
         tma_prefetch_desc(&tm_q);
         tma_prefetch_desc(&tm_k);
         tma_prefetch_desc(&tm_v);
     }
-    tc_fence_before();
     pdl_wait();
     pdl_trigger();
+    // Not before the wait: a kernel of another library that has let this one
+    // start may still have to allocate its own.
+    if (warp == L::kWarpIssue) {
+        tmem_alloc(sbase + L::OFF_TMEM, L::kCols);
+        tmem_relinquish();
+    }
+    tc_fence_before();
     const PagedSched<M, 128> sched(p);
     int* red = reinterpret_cast<int*>(sgen + L::OFF_SCAN);
     int2* found = reinterpret_cast<int2*>(sgen + L::OFF_SCAN + 80);
@@ -627,7 +629,8 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
 // ---------------------------------------------------------------------------
 // Join the items that a worker boundary cuts (list without shared prefix
 // items; whole items were written by the kernel above).  blockIdx.x + 1 is
-// the worker behind the boundary, blockIdx.y a group of 16 rows.
+// the worker behind the boundary, blockIdx.y a group of 16 rows.  Bound by
+// latency, so kFlight parts of a row are loaded together.
 // ---------------------------------------------------------------------------
 template <int D, int M>
 __global__ void __launch_bounds__(256) paged_cuts_kernel(const __grid_constant__ PagedParams p) {
