@@ -42,8 +42,6 @@ EncodeTiledFn encode_fn() {
     return fn;
 }
 
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-
 // 3-D tiled map over a [z][y][x] array with a 128-byte swizzled box.
 bool encode_3d(CUtensorMap* m, CUtensorMapDataType dt, void* base, uint64_t x, uint64_t y, uint64_t z,
                uint64_t stride_y_bytes, uint64_t stride_z_bytes, uint32_t box_x, uint32_t box_y) {

@@ -87,7 +87,9 @@ int encode_rows(CUtensorMap* m, const sage_tensor& t, int D, int H, int Nq, int 
 // The fault the next launch has to make (test hook), taken once (sage_api.cu).
 int take_fault_mode();
 
-// Checks of a page cache's description that need no GPU (sage_tables.cu).
+inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+// Checks of a tensor's and of a page cache's description that need no GPU (sage_tables.cu).
+int check_view(const sage_tensor* t);
 int check_page_cache(const sage_page_cache* c);
 
 #ifdef __CUDACC__

@@ -45,11 +45,17 @@ CASES = [
     (2000, 16, 4, 2, 62, 2, 13),                           # ... and too few free pages
     (6, 16, 8, 20, 100, 28, 4),
     (4, 16, 300, 4000, 0, 4800, 0),                        # several passes of a block over a row
+    (9, 16, 12, 24, 130, 60, 0),
+    (1300, 32, 8, 8, 220, 30, 6),
+    (3, 128, 2000, 4, 250000, 5, 0),
+    (5, 64, 8, 0, 100, 300, 0),                            # no slots
 ]
 
 
+# pad: with rows a multiple of 4 long and apart, entries are written in fours
+@pytest.mark.parametrize("pad", [3, 4])
 @pytest.mark.parametrize("B,page,W,N,old_max,new_max,short", CASES)
-def test_tables_from_lengths(B, page, W, N, old_max, new_max, short):
+def test_tables_from_lengths(B, page, W, N, old_max, new_max, short, pad):
     r = random.Random(B * 1000 + W)
     old = [r.randint(0, old_max) for _ in range(B)]
     new = [o + r.randint(0, new_max) for o in old]
@@ -62,13 +68,13 @@ def test_tables_from_lengths(B, page, W, N, old_max, new_max, short):
         for j in range(-(-o // page)):
             table[b][j] = pages.pop()
     free = pages[:max(0, len(pages) - short)]
-    got = call_tables(old, new, page, free, W, N, table, pad=3)
+    got = call_tables(old, new, page, free, W, N, table, pad)
     want = P.tables_reference(old, new, page, free, table, N)
     assert got[0] == want[0]
     assert got[1] == want[1]
     assert got[2] == [want[2]] == [need]
     # the same call on its own output changes nothing
-    again = call_tables(old, new, page, free, W, N, got[0], pad=3)
+    again = call_tables(old, new, page, free, W, N, got[0], pad)
     assert again == got
 
 
