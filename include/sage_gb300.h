@@ -311,7 +311,8 @@ int sage_attention_host_overlapped(const sage_tensor* q_host, const sage_tensor*
 /* A pool of pages.  k, v : BF16 [num_pages, heads, page_size, D] views by
  * element strides (stride_b is the page stride, stride_n the token stride;
  * pages may hold their heads token by token or one after another); pointer
- * and strides as for every sage_tensor.  page_size is 16, 32, 64 or 128, D is
+ * and strides as for every sage_tensor, below 2^38, without a broadcast axis
+ * (every stride at least D, but for an axis of one).  page_size is 16, 32, 64 or 128, D is
  * 64 or 128, and num_pages * page_size is below 2^31. */
 typedef struct {
     sage_tensor k;
@@ -352,7 +353,8 @@ int sage_page_tables(const int32_t* old_len, const int32_t* new_len, int B, int 
  *            slot skips its token; a slot outside the cache is skipped too and
  *            recorded as SAGE_ERR_PAGE in the device status.  A slot that
  *            occurs twice holds either token's rows, or parts of both.
- * Rows of the cache that no slot names are left as they are.  One launch. */
+ * Rows of the cache that no slot names are left as they are.  B * N is below
+ * 2^31 (else SAGE_ERR_UNSUPPORTED).  One launch. */
 int sage_cache_append(const sage_tensor* k, const sage_tensor* v, int B, int N, const int32_t* slots,
                       int64_t slots_stride, const sage_page_cache* cache, void* stream);
 
@@ -369,6 +371,7 @@ int sage_paged_workspace(int B, int H, int Hkv, int Nq, int D, size_t* bytes);
  * over both together; a row that sees no key is written as zero.
  *  q, o    : BF16 [B, H, Nq, D] views (device); rows >= q_len[b] of o are not
  *            written.  H is a multiple of cache->heads; D is cache->D.
+ *            Strides are below 2^38 and at least D, but for an axis of one.
  *  q_len   : device int32 [B], or NULL for Nq; kv_len : device int32 [B], or
  *            NULL for table_width * page_size; prefix_len : device int32 [1],
  *            or NULL for prefix_width * page_size.  Out-of-range lengths are
@@ -383,10 +386,12 @@ int sage_paged_workspace(int B, int H, int Hkv, int Nq, int D, size_t* bytes);
  *  workspace : device scratch of at least sage_paged_workspace bytes, 16-byte
  *            aligned, whose contents do not matter before or after.  Calls on
  *            the same workspace must be ordered.
+ * Lengths, tables and prefix are read on the device, so a captured call
+ * serves later lengths; make the first call on a device before any capture.
  * Cache rows behind a length are never used, whatever they hold; the rows
  * within the lengths must be finite, hidden ones included.  Scores, maxima,
- * sums and outputs are FP32, the weights are rounded to BF16 for the product
- * with the values.  Results do not depend on the workspace or on earlier
+ * sums and the output up to its last rounding are FP32, the weights are
+ * rounded to BF16 for the product with the values.  Results do not depend on the workspace or on earlier
  * calls: equal inputs give equal bits on the same device. */
 int sage_attn_paged(const sage_tensor* q, const sage_tensor* o, const sage_page_cache* cache, int B, int H, int Nq,
                     const int32_t* q_len, const int32_t* table, int64_t table_stride, int table_width,

@@ -118,6 +118,7 @@ PyObject* page_tables(PyObject*, PyObject* const* a, Py_ssize_t n) {
                          *old_len = tensor_or_none(a[6], "old_len: expected a tensor");
         const long page = PyLong_AsLong(a[1]);
         if (page == -1 && PyErr_Occurred()) throw Refused{nullptr};
+        if (page < 0 || page > INT32_MAX) throw Refused{"page_size: expected 16, 32, 64 or 128"};
         OneDevice d;
         for (const at::Tensor* t : {&table, &new_len, &free_pages, &taken, slots, old_len}) d.add(t);
         d.check();

@@ -40,6 +40,17 @@ def test_several_tokens(layout, causal, Nq, G):
        seed=Nq)
 
 
+# A key head with so many query heads that a group of 128 rows holds one token,
+# or (over 128) not a whole one.
+@pytest.mark.parametrize("G,Hkv", [(65, 2), (100, 1), (128, 2), (129, 1), (150, 2), (300, 1)])
+@pytest.mark.parametrize("Nq,causal", [(1, True), (3, True), (3, False), (9, True)])
+@pytest.mark.parametrize("prefix", [0, 130])
+def test_many_heads_to_a_key_head(G, Hkv, Nq, causal, prefix):
+    kv = [0, Nq, 1, 300, 77]
+    go(B=5, H=G * Hkv, Hkv=Hkv, D=64, Nq=Nq, page=16, kv_len=kv, q_len=[Nq, Nq, Nq, 0, max(1, Nq - 1)], prefix=prefix,
+       causal=causal, seed=G + Nq)
+
+
 @pytest.mark.parametrize("prefix", [1, 16, 100, 128, 777])
 @pytest.mark.parametrize("B,Nq,G", [(1, 1, 1), (3, 1, 2), (5, 1, 8), (20, 1, 4), (4, 3, 2), (2, 30, 2), (70, 1, 8)])
 @pytest.mark.parametrize("D", [64, 128])

@@ -72,3 +72,71 @@ def test_serving_loop(B, H, Hkv, D, page, prefix):
             tol = P.U_BF16 * want.abs() + (P.U_BF16 * 1.01 + 2.0 ** -11) * size
             assert bool(((o[b, :, :n].double() - want).abs() <= tol).all())
     assert used <= n_pages
+
+
+def test_a_decode_step_captured_whole():
+    """Tables, append and attention in one graph: replayed with the lengths, the
+    free list and the tokens of each step, it leaves what the eager calls leave."""
+    G.ensure_built()
+    B, H, Hkv, D, page, W, steps = 6, 8, 2, 128, 16, 4, 24
+    n_pages = B * W
+    g = torch.Generator(device="cuda").manual_seed(7)
+    order = torch.randperm(n_pages, generator=torch.Generator().manual_seed(2)).to(torch.int32).cuda()
+    i32 = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")  # noqa: E731
+    starts = [0, 5, 15, 16, 31, 38]
+
+    class Side:
+        """One cache with its step's buffers."""
+        def __init__(self):
+            self.cache = S.alloc_page_cache(n_pages, page, Hkv, D)
+            self.cache.k.zero_()
+            self.cache.v.zero_()
+            self.table = torch.empty((B, W), dtype=torch.int32, device="cuda")
+            self.slots = torch.empty((B, 1), dtype=torch.int32, device="cuda")
+            self.taken = torch.empty(1, dtype=torch.int32, device="cuda")
+            self.q = torch.zeros((B, H, 1, D), dtype=torch.bfloat16, device="cuda")
+            self.k = torch.zeros((B, Hkv, 1, D), dtype=torch.bfloat16, device="cuda")
+            self.v = torch.zeros_like(self.k)
+            self.o = torch.zeros_like(self.q)
+            self.old, self.new, self.free = i32([0] * B), i32([0] * B), order.clone()
+            self.ws = S.alloc_paged_workspace(B, H, Hkv, 1, D)
+
+        def step(self, stream=None):
+            S.sage_page_tables(self.new, page, self.free, self.table, self.slots, self.taken, old_len=self.old,
+                               stream=stream)
+            S.sage_cache_append(self.k, self.v, self.slots, self.cache, stream=stream)
+            S.sage_attn_paged(self.q, self.o, self.cache, self.table, self.ws, kv_len=self.new, stream=stream)
+
+        def begin(self):
+            """Pages of the tokens before the first step (whose keys are zero)."""
+            S.sage_page_tables(i32(starts), page, order, self.table, None, self.taken)
+            torch.cuda.synchronize()
+            return int(self.taken)
+
+    eager, whole = Side(), Side()
+    whole.step()                                           # the first call, before the capture: no token yet
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        whole.step()
+    used = eager.begin()
+    assert whole.begin() == used
+    have = list(starts)
+    for n in range(steps):
+        old, have = have, [a + (n + b) % 2 for b, a in enumerate(have)]
+        q, k, v = (torch.randn((B, h, 1, D), device="cuda", generator=g).to(torch.bfloat16) for h in (H, Hkv, Hkv))
+        for x in (eager, whole):
+            for dst, src in ((x.q, q), (x.k, k), (x.v, v), (x.old, i32(old)), (x.new, i32(have)),
+                             (x.free, torch.cat((order[used:], order[:used])))):
+                dst.copy_(src)
+        eager.step()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert S.sage_get_device_status() == S.SAGE_OK
+        used += int(eager.taken)
+        assert used <= n_pages
+        for a, b in ((eager.taken, whole.taken), (eager.table, whole.table), (eager.slots, whole.slots),
+                     (eager.o, whole.o), (eager.cache.k, whole.cache.k), (eager.cache.v, whole.cache.v)):
+            assert torch.equal(a, b)
+    assert int(eager.o.count_nonzero()) > 0

@@ -55,6 +55,11 @@ def test_attn_paged_refuses(lib):
     assert lib.sage_paged_workspace(1, 1, 1, 1, 128, None) == S.SAGE_ERR_ARG
     assert lib.sage_paged_workspace(1, 3, 2, 1, 128, ctypes.byref(n)) == S.SAGE_ERR_ARG
     assert lib.sage_paged_workspace(1, 2, 2, 1, 96, ctypes.byref(n)) == S.SAGE_ERR_UNSUPPORTED
+    assert lib.sage_paged_workspace(1, 1024, 1024, 1 << 21, 64, ctypes.byref(n)) == S.SAGE_ERR_UNSUPPORTED
+    assert attn(lib, q=tensor(sh=0)) == S.SAGE_ERR_UNSUPPORTED     # a broadcast axis
+    assert attn(lib, o=tensor(sb=64)) == S.SAGE_ERR_UNSUPPORTED
+    assert attn(lib, c=cache(k=tensor(sn=0))) == S.SAGE_ERR_UNSUPPORTED
+    assert attn(lib, c=cache(v=tensor(sb=1 << 40))) == S.SAGE_ERR_UNSUPPORTED
 
 
 @pytest.mark.parametrize("bad,code", [(dict(pages=0), S.SAGE_ERR_ARG), (dict(heads=0), S.SAGE_ERR_ARG),
@@ -113,6 +118,9 @@ def test_python_checks_name_the_argument():
     q = torch.zeros((1, 2, 1, 64), dtype=torch.bfloat16)
     with pytest.raises(ValueError):                        # tensors of the CPU
         S.sage_attn_paged(q, q.clone(), cache_, torch.zeros((1, 1), dtype=torch.int32), torch.zeros(16))
+    n = torch.zeros(1, dtype=torch.int32)
+    with pytest.raises(ValueError, match="page_size"):     # not taken modulo 2^32
+        S.sage_page_tables(n, (1 << 32) + 16, n, torch.zeros((1, 1), dtype=torch.int32), taken=n)
     with pytest.raises(ValueError):                        # another head dimension than the cache's
         S.sage_attn_paged(q[..., :32], q[..., :32], cache_, None, torch.zeros(16))
     with pytest.raises(ValueError):                        # heads other than the cache's
