@@ -105,11 +105,11 @@ __global__ void __launch_bounds__(kRowWarps * 32, 2) paged_rows_kernel(const __g
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (!p.beside) pdl_wait();
     pdl_trigger();
-    const PagedSched<M, kStep> sched(p);
+    const PagedSched<M, kStep, false> sched(p);
     // workers next to each other in the list sit on different SMs: a CTA's
     // warps are a grid apart, so a short list still uses every SM
     const int worker = warp * gridDim.x + blockIdx.x;
-    const int total = paged_scan<M, kStep, kRowWarps * 32, kRowWarps>(sched, blockIdx.x, gridDim.x, found, warp_sums,
+    const int total = paged_scan<M, kStep, false, kRowWarps * 32, kRowWarps>(sched, blockIdx.x, gridDim.x, found, warp_sums,
                                                                       blockIdx.x == 0);
     const int per = paged_per_worker(p, total);
     const int t0 = min(worker * per, total), t1 = min(t0 + per, total);   // this worker's run of the list
@@ -335,11 +335,13 @@ __global__ void __launch_bounds__(256) paged_join_kernel(const __grid_constant__
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int row = (int)blockIdx.x * (8 / WPR) + warp / WPR, sub = warp % WPR;
     const int b = blockIdx.y;
-    const PagedSched<M, TK> s(p);
+    constexpr bool kTiles = TK == 128;                     // a list of the many-rows kernel, the prefix's items in it
+    const PagedSched<M, TK, kTiles> s(p);
     const int hq = row / p.Nq, i = row - hq * p.Nq;
     const int n = s.q_rows(b), len = s.own_keys(b);
     const bool live = hq < p.H && i < n;
-    const int h = fast_div(hq, p.by_G), r = i * p.G + (hq - h * p.G), rt = r / M;
+    const int h = fast_div(hq, p.by_G), r = i * p.G + (hq - h * p.G);
+    const int rt = kTiles ? 0 : r / M;  // tiles: one group holds a request's rows
     pdl_trigger();
     pdl_wait();                                            // the parts are written
     float acc[V], m = -INFINITY, l = 0.f;
@@ -349,16 +351,18 @@ __global__ void __launch_bounds__(256) paged_join_kernel(const __grid_constant__
         const int per = paged_per_worker(p, __ldcg(p.start + p.B * p.rt));
         const int nt = s.item_tiles(n, len, rt), pair = b * p.rt + rt;
         const RowParts own = parts_of(__ldcg(p.start + pair) + h * s.places(nt) + s.kItemCost, nt, per, pair * p.Hkv + h);
-        const int64_t own_q = own.slot0 * M + (r - rt * M);
+        const int64_t own_q = own.slot0 * p.part_m + (r - rt * M);
         RowParts pre{0, 0};
         int64_t pre_q = 0;
         if (p.pre_items_rt > 0) {
-            // the row set of the prefix's list that holds this row, and its place there
-            using Tiles = PagedSched<128, 128>;
+            // the row set of the prefix that holds this row, and its place there
+            using Tiles = PagedSched<128, 128, true>;
             const int pt = (s.lp + 127) / 128, group = b / p.pre_tok;
             const int set = group * 128 / p.pre_m, place = group * 128 - set * p.pre_m + (b - group * p.pre_tok) * p.Nq * p.G + r;
             const int it = set * p.Hkv + h;
-            const int pre_per = max(1, (p.Hkv * p.pre_items_rt * Tiles::places(pt) + p.pre_workers - 1) / p.pre_workers);
+            // ... in the same list, or in one of its own
+            const int pre_per = kTiles ? per
+                                : max(1, (p.Hkv * p.pre_items_rt * Tiles::places(pt) + p.pre_workers - 1) / p.pre_workers);
             pre = parts_of(it * Tiles::places(pt) + Tiles::kItemCost, pt, pre_per, it);
             pre_q = pre.slot0 * p.pre_m + place;
         }
@@ -375,7 +379,7 @@ __global__ void __launch_bounds__(256) paged_join_kernel(const __grid_constant__
                 for (int v = 0; v < V; ++v) w[k][v] = 0.f;
                 if (x < parts) {
                     const bool from_pre = x < pre.n;
-                    const int64_t q = from_pre ? pre_q + (int64_t)x * p.pre_m : own_q + (int64_t)(x - pre.n) * M;
+                    const int64_t q = from_pre ? pre_q + (int64_t)x * p.pre_m : own_q + (int64_t)(x - pre.n) * p.part_m;
                     ml[k] = __ldcg((from_pre ? p.pre_ml : p.part_ml) + q);
                     const float* po = (from_pre ? p.pre_o : p.part_o) + q * D + lane * V;
                     if (V == 4) {
@@ -450,6 +454,14 @@ __global__ void __launch_bounds__(256) paged_join_kernel(const __grid_constant__
 //    and 94.  (More than 128 query heads to a key head leave no whole token in
 //    a group: these, which no model is known to have, stay with the few-rows
 //    kernel.)
+//    Up to 64 rows, of which two requests or more fill a group, the prefix may
+//    have items of its own in front of the requests', each for the rows of
+//    several requests.  That saves tiles and costs a join of all rows, about
+//    as much as 12 MB of tiles and 6 KB for each row (32 requests of 20 rows, 8
+//    key heads of 128 channels, 8,192 shared keys: 51 us against 125; 4 key
+//    heads of 64, 4,099 keys: 22 against 30; on the other side 200 requests of
+//    21 rows, 512 shared keys: 34 against 32.5; 16 of 64 rows, 2 key heads,
+//    4,096: 20.5 against 17.5).
 //  - rows <= 16: the few-rows kernel, each request's keys behind the prefix
 //    while reading the prefix again for every request costs less than a list
 //    of its own, which the many-rows kernel then reads once for all rows: 64
@@ -458,16 +470,17 @@ __global__ void __launch_bounds__(256) paged_join_kernel(const __grid_constant__
 // ---------------------------------------------------------------------------
 constexpr int kFewRows = 16;
 constexpr int64_t kReadAgain = int64_t(256) << 20;        // bytes of prefix read again that cost as much as its list
+constexpr double kOwnList = 12e6, kRowJoin = 6e3;         // many-rows kernel: ... as much as joining all rows, and one row
 
 struct Lists {
-    // the list with the own keys
+    // items of the own keys
     bool tiles;                          // many-rows kernel
     int groups;                          // ... 128-row groups of an item
-    int tok, unit;                       // ... tokens of a group, rows of a token
+    int tok;                             // ... tokens of a group
     int nr;                              // few-rows kernel: 8-row groups of an item
-    int M, rt, join;
+    int M, rt, join;                     // M: rows of a partial result
     int64_t slots;
-    // the prefix's own list (many-rows kernel)
+    // items of the prefix for the rows of all requests (many-rows kernel): in the same list when `tiles`
     bool pre;
     int pre_groups, pre_tok, pre_unit, pre_M, pre_items_rt;
     int64_t pre_slots;
@@ -476,10 +489,30 @@ struct Lists {
 Lists make_lists(int B, int Hkv, int G, int Nq, int D, int64_t pre_keys) {
     Lists x{};
     const int64_t rows = (int64_t)Nq * G;
-    if (rows > kFewRows && G <= 128) {
-        x.tiles = true;
-        x.unit = G;
+    x.tiles = rows > kFewRows && G <= 128;
+    if (x.tiles && B > 1 && rows <= 64) {
+        const int64_t tiles = ceil_div(pre_keys, 128), sets = ceil_div(B, 128 / rows);
+        const double saved = (double)Hkv * ((double)B * tiles - (double)sets * (tiles + 3)) * 128 * D * 4;
+        x.pre = saved > kOwnList + kRowJoin * (double)B * Hkv * rows;
+    }
+    if (!x.tiles) x.pre = rows <= kFewRows && B > 1 && (double)B * Hkv * pre_keys * D * 4 > (double)kReadAgain;
+    if (x.pre) {
+        x.pre_unit = (int)rows;
+        x.pre_tok = 128 / x.pre_unit;
+        x.pre_groups = x.tiles || B <= x.pre_tok ? 1 : 2;
+        x.pre_M = 128 * x.pre_groups;
+        x.pre_items_rt = (int)ceil_div(B, x.pre_tok * x.pre_groups);
+        x.pre_slots = (int64_t)Hkv * x.pre_items_rt + kMaxTileWorkers * (3 - x.pre_groups);
+    }
+    if (x.tiles) {
         x.tok = 128 / G;
+        if (x.pre) {
+            x.groups = 1;
+            x.M = (int)rows;
+            x.rt = 1;
+            x.slots = (int64_t)B * Hkv + 2 * kMaxTileWorkers;
+            return x;
+        }
         x.groups = Nq <= x.tok ? 1 : 2;
         x.M = 128 * x.groups;
         x.rt = (int)ceil_div(Nq, x.tok * x.groups);
@@ -491,22 +524,15 @@ Lists make_lists(int B, int Hkv, int G, int Nq, int D, int64_t pre_keys) {
     x.M = 8 * x.nr;
     x.rt = (int)ceil_div(rows, x.M);
     x.slots = (int64_t)B * Hkv * x.rt + kMaxRowWorkers;
-    x.pre = rows <= kFewRows && B > 1 && (double)B * Hkv * pre_keys * D * 4 > (double)kReadAgain;
     x.join = pre_keys > 0 && !x.pre;
-    if (x.pre) {
-        x.pre_unit = (int)rows;
-        x.pre_tok = 128 / x.pre_unit;
-        x.pre_groups = B <= x.pre_tok ? 1 : 2;
-        x.pre_M = 128 * x.pre_groups;
-        x.pre_items_rt = (int)ceil_div(B, x.pre_tok * x.pre_groups);
-        x.pre_slots = (int64_t)Hkv * x.pre_items_rt + kMaxTileWorkers * (3 - x.pre_groups);
-    }
     return x;
 }
 
-size_t slot_bytes(int64_t slots, int M, int D) { return (size_t)slots * M * (D * 4 + 8); }
+// Each array of the workspace begins on 16 bytes.
+size_t padded(size_t n) { return (n + 15) / 16 * 16; }
+size_t slot_bytes(int64_t slots, int M, int D) { return (size_t)slots * M * D * 4 + padded((size_t)slots * M * 8); }
 size_t lists_bytes(const Lists& x, int B, int D) {
-    const size_t index = x.tiles ? (size_t)2 * kMaxTileWorkers * sizeof(PagedCut) : (((size_t)B * x.rt + 1) * 4 + 15) / 16 * 16;
+    const size_t index = x.tiles && !x.pre ? (size_t)2 * kMaxTileWorkers * sizeof(PagedCut) : padded(((size_t)B * x.rt + 1) * 4);
     return slot_bytes(x.slots, x.M, D) + slot_bytes(x.pre_slots, x.pre_M, D) + index;
 }
 
@@ -527,21 +553,25 @@ int sm_count() {
     return n[dev];
 }
 
-template <int D, int NR>
-cudaError_t launch_rows(const PagedParams& p, cudaStream_t s) {
-    using Sh = RowsShape<D>;
-    static bool ready[64] = {}, join8_ready[64] = {}, join1_ready[64] = {};
-    const cudaError_t e = launch_pdl(paged_rows_kernel<D, NR>, dim3((unsigned)(p.workers / kRowWarps)), dim3(kRowWarps * 32),
-                                     Sh::kSmem, s, true, ready, p);
-    if (e != cudaSuccess) return e;
+// Join after a list of items of M rows and TK-key tiles.
+template <int D, int M, int TK>
+cudaError_t launch_join(const PagedParams& p, cudaStream_t s) {
+    static bool ready8[64] = {}, ready1[64] = {};
     // Rows are few: eight warps share the parts of one, else a warp takes a row
     // (8 KV heads x 3 rows of 152 parts each: 4.2 against 13.6 us).
     const int64_t rows = (int64_t)p.H * p.Nq;
     if (rows * p.B <= 1024)
-        return launch_pdl(paged_join_kernel<D, 8 * NR, kStep, 8>, dim3((unsigned)rows, (unsigned)p.B), dim3(256), 0, s, true,
-                          join8_ready, p);
-    return launch_pdl(paged_join_kernel<D, 8 * NR, kStep, 1>, dim3((unsigned)ceil_div(rows, 8), (unsigned)p.B), dim3(256), 0, s, true,
-                      join1_ready, p);
+        return launch_pdl(paged_join_kernel<D, M, TK, 8>, dim3((unsigned)rows, (unsigned)p.B), dim3(256), 0, s, true, ready8, p);
+    return launch_pdl(paged_join_kernel<D, M, TK, 1>, dim3((unsigned)ceil_div(rows, 8), (unsigned)p.B), dim3(256), 0, s, true,
+                      ready1, p);
+}
+
+template <int D, int NR>
+cudaError_t launch_rows(const PagedParams& p, cudaStream_t s) {
+    static bool ready[64] = {};
+    const cudaError_t e = launch_pdl(paged_rows_kernel<D, NR>, dim3((unsigned)(p.workers / kRowWarps)), dim3(kRowWarps * 32),
+                                     RowsShape<D>::kSmem, s, true, ready, p);
+    return e != cudaSuccess ? e : launch_join<D, 8 * NR, kStep>(p, s);
 }
 cudaError_t launch_rows(const PagedParams& p, int D, int nr, cudaStream_t s) {
     if (D == 64) return nr == 1 ? launch_rows<64, 1>(p, s) : launch_rows<64, 2>(p, s);
@@ -600,14 +630,17 @@ int sage_attn_paged(const sage_tensor* q, const sage_tensor* o, const sage_page_
     p.status = device_status_ptr();
     const int sms = sm_count();
     if (p.status == nullptr || sms == 0) return SAGE_ERR_LAUNCH;
-    CUtensorMap mq, mk, mv;
+    CUtensorMap mq, mqp, mk, mv;
     if (x.tiles || x.pre) {
         // q in boxes of whole tokens; for the prefix's items, of whole requests
         const int heads = H / cache->heads;
-        if ((rc = encode_rows(&mq, *q, D, H, Nq, B, heads, x.tiles ? x.tok : Nq, x.tiles ? 1 : x.pre_tok)) != SAGE_OK ||
+        if ((x.tiles && (rc = encode_rows(&mq, *q, D, H, Nq, B, heads, x.tok, 1)) != SAGE_OK) ||
+            (x.pre && (rc = encode_rows(&mqp, *q, D, H, Nq, B, heads, Nq, x.pre_tok)) != SAGE_OK) ||
             (rc = encode_pages(&mk, cache->k, D, cache->page_size, cache->heads, cache->num_pages)) != SAGE_OK ||
             (rc = encode_pages(&mv, cache->v, D, cache->page_size, cache->heads, cache->num_pages)) != SAGE_OK)
             return rc;
+        if (!x.tiles) mq = mqp;
+        if (!x.pre) mqp = mq;
         p.fault_mode = take_fault_mode();
     }
     p.q = static_cast<const uint16_t*>(q->ptr);
@@ -628,19 +661,20 @@ int sage_attn_paged(const sage_tensor* q, const sage_tensor* o, const sage_page_
     const double scale = sm_scale > 0.f ? (double)sm_scale : 1.0 / std::sqrt((double)D);
     p.sc = (float)(scale * (1.0 / std::log(2.0)));
     p.rt = x.rt; p.join = x.join;
-    p.tok = x.tok; p.unit = x.unit;
+    p.tok = x.tok; p.part_m = x.M;
     p.by_G = make_fast_div(p.G);
     p.by_rt = make_fast_div(x.rt);
-    p.by_unit = make_fast_div(x.unit > 0 ? x.unit : 1);
     char* w = static_cast<char*>(workspace);
-    auto take = [&](size_t n) { char* at = w; w += n; return at; };
+    auto take = [&](size_t n) { char* at = w; w += padded(n); return at; };
     p.part_o = reinterpret_cast<float*>(take((size_t)x.slots * x.M * D * 4));
     p.part_ml = reinterpret_cast<float2*>(take((size_t)x.slots * x.M * 8));
     if (x.pre) {
         p.pre_o = reinterpret_cast<float*>(take((size_t)x.pre_slots * x.pre_M * D * 4));
         p.pre_ml = reinterpret_cast<float2*>(take((size_t)x.pre_slots * x.pre_M * 8));
+        p.pre_unit = x.pre_unit;
+        p.by_pre_unit = make_fast_div(x.pre_unit);
     }
-    if (x.tiles) p.cuts = reinterpret_cast<PagedCut*>(w);
+    if (x.tiles && !x.pre) p.cuts = reinterpret_cast<PagedCut*>(w);
     else p.start = reinterpret_cast<int32_t*>(w);
     const int ctas = std::min(sms, kMaxTileWorkers);       // one per SM; of one row group: two
     p.pre_items_rt = x.pre_items_rt; p.pre_m = x.pre_M; p.pre_tok = x.pre_tok;
@@ -650,15 +684,16 @@ int sage_attn_paged(const sage_tensor* q, const sage_tensor* o, const sage_page_
     int launches = 0;
     if (x.tiles) {
         p.workers = ctas * (3 - x.groups);
-        e = launch_paged_tiles(p, D, x.groups, mq, mk, mv, s);
+        if (x.pre) p.pre_rt = x.pre_items_rt;
+        e = launch_paged_tiles(p, D, x.groups, mq, mqp, mk, mv, s);
+        if (e == cudaSuccess && x.pre) e = D == 64 ? launch_join<64, 128, 128>(p, s) : launch_join<128, 128, 128>(p, s);
         launches = 2;
     } else {
         if (x.pre) {
             PagedParams pp = p;
-            pp.part_o = p.pre_o; pp.part_ml = p.pre_ml; pp.start = nullptr; pp.cuts = nullptr;
-            pp.tok = x.pre_tok; pp.unit = x.pre_unit; pp.by_unit = make_fast_div(x.pre_unit);
+            pp.start = nullptr;
             pp.rt = 0; pp.pre_rt = x.pre_items_rt; pp.workers = p.pre_workers;
-            if (launch_paged_tiles(pp, D, x.pre_groups, mq, mk, mv, s) != cudaSuccess) return SAGE_ERR_LAUNCH;
+            if (launch_paged_tiles(pp, D, x.pre_groups, mq, mqp, mk, mv, s) != cudaSuccess) return SAGE_ERR_LAUNCH;
             ++launches;
             p.beside = 1;
         }

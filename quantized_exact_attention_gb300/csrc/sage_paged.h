@@ -55,29 +55,32 @@ struct PagedParams {
     // schedule (see sage_paged_sched.cuh)
     int rt;                              // row sets of a request
     int pre_rt;                          // row sets of all requests against the prefix (0: a list of own keys)
-    int tok, unit;                       // tiles kernel: tokens (prefix items: requests) of a group, rows of one
-    FastDiv by_G, by_rt, by_unit;        // G, rt, unit
+    int tok;                             // tiles kernel: tokens of a 128-row group
+    FastDiv by_G, by_rt;                 // G, rt
     int join;                            // 1: a request's key sequence is the prefix followed by its own keys
     int workers;                         // workers the list is shared among
     int fault_mode;                      // test hook: 0 = none
     int beside;                          // runs beside the kernel before it, which it does not depend on
     // workspace
-    float* part_o;                       // [slot][M][D]
-    float2* part_ml;                     // [slot][M] running maximum (log2 domain) and sum
+    float* part_o;                       // [slot][part_m][D]
+    float2* part_ml;                     // [slot][part_m] running maximum (log2 domain) and sum
+    int part_m;                          // rows of a slot
     PagedCut* cuts;                      // [workers] items that a worker boundary cuts (null: not wanted)
     int32_t* start;                      // [B rt + 1] list position of each (request, row set); last: the length
-    // the shared prefix's list, for the join
-    float* pre_o;
+    // the shared prefix's items, and the list they are in for the join
+    float* pre_o;                        // [slot][pre_m][D]
     float2* pre_ml;
-    int pre_items_rt, pre_m, pre_workers;            // row sets (0: no such list), rows of an item, workers
-    int pre_tok;                         // requests of a 128-row group
+    int pre_items_rt, pre_m, pre_workers;            // row sets (0: no such items), rows of an item, workers
+    int pre_tok, pre_unit;               // requests of a 128-row group, rows of a request
+    FastDiv by_pre_unit;
 };
 
 // The many-rows kernel (sage_paged_tiles.cu): workers = CTAs, groups: row groups
 // of 128 of an item (1 or 2).  Writes whole rows unless the list holds shared
-// prefix items; then every result is partial.
-cudaError_t launch_paged_tiles(const PagedParams& p, int D, int groups, const CUtensorMap& tq, const CUtensorMap& tk,
-                               const CUtensorMap& tv, cudaStream_t s);
+// prefix items; then every result is partial.  tq: q in boxes of `tok` tokens,
+// tqp: of `pre_tok` requests (either may stand for one that no item uses).
+cudaError_t launch_paged_tiles(const PagedParams& p, int D, int groups, const CUtensorMap& tq, const CUtensorMap& tqp,
+                               const CUtensorMap& tk, const CUtensorMap& tv, cudaStream_t s);
 
 // Tensor map over one tensor of a page cache, box: one page of one head, 64 channels (sage_api.cu).
 int encode_pages(CUtensorMap* m, const sage_tensor& t, int D, int page, int heads, int pages);

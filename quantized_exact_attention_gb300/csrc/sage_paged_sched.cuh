@@ -2,12 +2,11 @@
 //
 // The work is a list of items.  An item is a set of query rows of one key head
 // and the key sequence they read, cut into tiles of TK keys.  The list holds
-// either, for a prefix computed once for all (pre_rt > 0; tiles kernel only),
-//   for each set of rows out of ALL requests' rows, and each key head: the
-//   shared prefix;
-// or
-//   for each request, each set of its rows, and each key head: its own keys,
-//   preceded by the prefix when join = 1.
+//   for a prefix computed once for all (pre_rt > 0; tiles kernel only): for
+//   each set of rows out of ALL requests' rows, and each key head, the shared
+//   prefix;
+//   then, for each request, each set of its rows (rt > 0), and each key head:
+//   its own keys, preceded by the prefix when join = 1.
 // Each item takes as many places in the list as it has tiles, and kItemCost in
 // front of them, which stand for what an item costs a worker besides its tiles
 // (fetching its rows, writing its output).  The places are cut into equal
@@ -15,14 +14,15 @@
 // device holds: a long sequence is shared among many workers, several short
 // ones fall to a single worker, and no host value depends on the lengths.
 // A worker leaves a partial result (running maximum, sum and unnormalised
-// output) for an item it shares, in slot worker + item: along the list either
-// the worker or the item advances by one, so the slots are distinct.
+// output) for an item it shares, in slot worker + item (the prefix's items and
+// the others are numbered and kept apart): along the list either the worker or
+// the item advances by one, so the slots are distinct.
 //
 // Sets of rows, in the order of query token, then query head of the key head:
 //   few-rows kernel (TK = 16): M rows after one another;
-//   many-rows kernel (TK = 128): groups of 128 rows that hold whole tokens (of
-//   the shared prefix's items: whole requests), `tok` of them, so that a group
-//   is one box of a tensor map; the rows left over stay empty.
+//   many-rows kernel (TK = 128): groups of 128 rows that hold `tok` whole tokens
+//   (of the shared prefix's items: `pre_tok` whole requests), so that a group is
+//   one box of a tensor map; the rows left over stay empty.
 #pragma once
 
 #include "sage_paged.h"
@@ -40,7 +40,8 @@ __device__ __forceinline__ int fast_div(int n, const FastDiv& f) {
     return (int)((__umulhi((uint32_t)n, f.m) + (uint32_t)n) >> f.s);
 }
 
-template <int M, int TK>
+// kPre: the list holds items of the shared prefix.
+template <int M, int TK, bool kPre>
 struct PagedSched {
     static constexpr bool kTiles = TK == 128;
     static constexpr int kItemCost = kTiles ? 3 : 1;
@@ -54,7 +55,7 @@ struct PagedSched {
     __device__ int pre_tiles() const { return (lp + TK - 1) / TK; }
     // places of an item of nt tiles
     __device__ static int places(int nt) { return nt > 0 ? nt + kItemCost : 0; }
-    __device__ int pre_total() const { return p.pre_rt * p.Hkv * places(pre_tiles()); }
+    __device__ int pre_total() const { return kPre ? p.pre_rt * p.Hkv * places(pre_tiles()) : 0; }
     // Tiles of row set rt of a request with n query tokens and len own keys.
     __device__ int item_tiles(int n, int len, int rt) const {
         int last;                        // last token of the set that exists
@@ -68,9 +69,10 @@ struct PagedSched {
         }
         const int end = p.causal ? max(0, min(len, len - n + last + 1)) : len;      // own keys that some row sees
         const int nt = (end + TK - 1) / TK + (p.join ? pre_tiles() : 0);
-        // the tiles kernel writes whole rows itself, so rows that see no key
-        // have a tile too (with no visible key: zeros)
-        return kTiles ? max(nt, 1) : nt;
+        // the tiles kernel writes whole rows itself unless the prefix's parts
+        // are still to come, so rows that see no key have a tile too (with no
+        // visible key: zeros)
+        return kTiles && !kPre ? max(nt, 1) : nt;
     }
 };
 
@@ -81,8 +83,8 @@ struct PagedSched {
 // list of prefix items).  With `publish` the positions of all
 // pairs go to p.start as well.  `red` holds THREADS/32 ints.  Ends with a
 // barrier.
-template <int M, int TK, int THREADS, int NW>
-__device__ __forceinline__ int paged_scan(const PagedSched<M, TK>& s, int first_worker, int worker_step, int2* found,
+template <int M, int TK, bool kPre, int THREADS, int NW>
+__device__ __forceinline__ int paged_scan(const PagedSched<M, TK, kPre>& s, int first_worker, int worker_step, int2* found,
                                           int* red, bool publish) {
     const PagedParams& p = s.p;
     const int t = threadIdx.x, lane = t & 31, w = t >> 5;
@@ -148,12 +150,12 @@ struct PagedPlace {
 };
 
 // The first tile at or behind place t (t < total), with paged_scan's finding.
-template <int M, int TK>
-__device__ __forceinline__ PagedPlace paged_place(const PagedSched<M, TK>& s, int2 found, int t) {
+template <int M, int TK, bool kPre>
+__device__ __forceinline__ PagedPlace paged_place(const PagedSched<M, TK, kPre>& s, int2 found, int t) {
     const PagedParams& p = s.p;
     PagedPlace x{};
     int o;                               // place within the item
-    if (found.x < 0) {
+    if (kPre && found.x < 0) {
         x.b = -1;
         x.ntiles = s.pre_tiles();
         x.item = t / s.places(x.ntiles);
@@ -176,8 +178,8 @@ __device__ __forceinline__ PagedPlace paged_place(const PagedSched<M, TK>& s, in
 }
 
 // The next tile of the list (its place is behind the list when there is none).
-template <int M, int TK>
-__device__ __forceinline__ void paged_next(const PagedSched<M, TK>& s, PagedPlace& x) {
+template <int M, int TK, bool kPre>
+__device__ __forceinline__ void paged_next(const PagedSched<M, TK, kPre>& s, PagedPlace& x) {
     const PagedParams& p = s.p;
     ++x.pos;
     if (++x.tile < x.ntiles) return;
@@ -186,22 +188,22 @@ __device__ __forceinline__ void paged_next(const PagedSched<M, TK>& s, PagedPlac
     ++x.item;
     if (++x.h < p.Hkv) return;
     x.h = 0;
-    x.item -= p.Hkv;
-    do {                                 // the next row set that has tiles
-        x.item += p.Hkv;
-        ++x.rt;
-        if (x.b < 0) {
-            if (x.rt == p.pre_rt) x.pos = INT32_MAX;
-            return;
-        }
+    ++x.rt;
+    if (kPre && x.b < 0) {
+        if (x.rt < p.pre_rt) return;
+        x.item = 0;
+        x.rt = p.rt;                     // behind request -1
+    }
+    for (;; ++x.rt, x.item += p.Hkv) {   // the next row set that has tiles
         if (x.rt == p.rt) {
             x.rt = 0;
-            if (++x.b >= p.B) { x.ntiles = 0; x.pos = INT32_MAX; return; }
+            if (++x.b >= p.B || (kPre && p.rt == 0)) { x.ntiles = 0; x.pos = INT32_MAX; return; }
             x.n = s.q_rows(x.b);
             x.len = s.own_keys(x.b);
         }
         x.ntiles = s.item_tiles(x.n, x.len, x.rt);
-    } while (x.ntiles == 0);
+        if (x.ntiles > 0) return;
+    }
 }
 
 // What a tile's keys are.
@@ -210,11 +212,12 @@ struct PagedSpan {
     int key0;                            // first key, in its sequence
     int nkeys;                           // keys of the tile that exist (<= TK; 0 in an item without keys)
 };
-template <int M, int TK>
-__device__ __forceinline__ PagedSpan paged_span(const PagedSched<M, TK>& s, int b, int len, int tile) {
+template <int M, int TK, bool kPre>
+__device__ __forceinline__ PagedSpan paged_span(const PagedSched<M, TK, kPre>& s, int b, int len, int tile) {
     PagedSpan r;
-    const int np = b < 0 || s.p.join ? s.pre_tiles() : 0;
-    r.own = b >= 0 && tile >= np;
+    const bool pre = kPre && b < 0;
+    const int np = pre || s.p.join ? s.pre_tiles() : 0;
+    r.own = !pre && tile >= np;
     r.key0 = (r.own ? tile - np : tile) * TK;
     r.nkeys = min(TK, (r.own ? len : s.lp) - r.key0);
     return r;
@@ -222,23 +225,25 @@ __device__ __forceinline__ PagedSpan paged_span(const PagedSched<M, TK>& s, int 
 
 // Row r of an item: its request, query token and query head (false: no such
 // row).  n: query tokens of the item's request.
-template <int M, int TK>
-__device__ __forceinline__ bool paged_row(const PagedSched<M, TK>& s, int ib, int ih, int irt, int n, int r, int& b, int& i,
+template <int M, int TK, bool kPre>
+__device__ __forceinline__ bool paged_row(const PagedSched<M, TK, kPre>& s, int ib, int ih, int irt, int n, int r, int& b, int& i,
                                           int& hq) {
     const PagedParams& p = s.p;
-    if constexpr (PagedSched<M, TK>::kTiles) {
-        const int group = irt * (M / 128) + (r >> 7);      // of `tok` tokens (requests)
-        const int rr = r & 127, u = fast_div(rr, p.by_unit);
-        const int at = group * p.tok + u, rest = rr - u * p.unit;
-        if (ib < 0) {
-            b = at;
-            i = fast_div(rest, p.by_G);
-            hq = ih * p.G + rest - i * p.G;
-            return u < p.tok && b < p.B && i < s.q_rows(b);
+    if constexpr (PagedSched<M, TK, kPre>::kTiles) {
+        const int group = irt * (M / 128) + (r >> 7);
+        int rr = r & 127;
+        if (kPre && ib < 0) {
+            const int u = fast_div(rr, p.by_pre_unit);
+            rr -= u * p.pre_unit;
+            b = group * p.pre_tok + u;
+            i = fast_div(rr, p.by_G);
+            hq = ih * p.G + rr - i * p.G;
+            return u < p.pre_tok && b < p.B && i < s.q_rows(b);
         }
+        const int u = fast_div(rr, p.by_G);
         b = ib;
-        i = at;
-        hq = ih * p.G + rest;
+        i = group * p.tok + u;
+        hq = ih * p.G + rr - u * p.G;
         return u < p.tok && i < n;
     } else {
         const int row = irt * M + r;

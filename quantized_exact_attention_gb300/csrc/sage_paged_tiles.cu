@@ -68,7 +68,7 @@ struct ItemNote {
     int b, h, rt;
     int n, len;                                           // the request's query tokens and own keys
     int tile, run;                                        // its first tile in this worker, and how many (0: no item)
-    int slot;                                             // of a partial result
+    int slot;                                             // of a partial result (of the prefix's, or the others')
     int whole;                                            // no other worker shares it: the output is final
     int pad[3];
 };
@@ -171,10 +171,11 @@ __device__ __forceinline__ void stage_out(uint8_t* stage, const uint32_t (&w)[8]
     __syncwarp();
 }
 
-template <int D, int kGroups>
+template <int D, int kGroups, bool kPre>
 __global__ void __launch_bounds__(TilesShape<D, kGroups>::kThreads, TilesShape<D, kGroups>::kCtasPerSm)
-paged_tiles_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
-                   const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ PagedParams p) {
+paged_tiles_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_qp,
+                   const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
+                   const __grid_constant__ PagedParams p) {
     using L = TilesShape<D, kGroups>;
     constexpr int M = L::M, NS = L::kNS;
     extern __shared__ uint8_t smem_raw[];
@@ -212,7 +213,7 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
         fence_mbar_init();
     }
     if (warp == L::kWarpLoad && lane == 0) {
-        tma_prefetch_desc(&tm_q);
+        tma_prefetch_desc(kPre ? &tm_qp : &tm_q);
         tma_prefetch_desc(&tm_k);
         tma_prefetch_desc(&tm_v);
     }
@@ -225,11 +226,12 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
         tmem_relinquish();
     }
     tc_fence_before();
-    const PagedSched<M, 128> sched(p);
+    const PagedSched<M, 128, kPre> sched(p);
     int* red = reinterpret_cast<int*>(sgen + L::OFF_SCAN);
     int2* found = reinterpret_cast<int2*>(sgen + L::OFF_SCAN + 80);
     const int worker = blockIdx.x;
-    const int total = paged_scan<M, 128, L::kThreads, 1>(sched, worker, 0, found, red, false);   // ends with a barrier
+    const int total = paged_scan<M, 128, kPre, L::kThreads, 1>(sched, worker, 0, found, red,      // ends with a barrier
+                                                               kPre && worker == 0 && p.start != nullptr);
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
     const int per = paged_per_worker(p, total);
@@ -263,7 +265,7 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
             int lim_own, rb, ri, rh;
             const bool valid = paged_row(sched, ib, nt.h, nt.rt, nt.n, X * 128 + row, rb, ri, rh);
             const bool active = __any_sync(0xffffffffu, valid);        // some row of this warp exists
-            lim_own = p.causal && ib >= 0 ? min(len, len - nt.n + ri + 1) : len;   // own keys this row sees
+            lim_own = p.causal && !(kPre && ib < 0) ? min(len, len - nt.n + ri + 1) : len;   // own keys this row sees
             float m = -INFINITY, l = 0.f;                 // reference of the exponentials (log2 domain), sum of this half
             bool fresh = true;                            // no tile of this item yet: O holds nothing
             int tile = nt.tile;
@@ -385,7 +387,7 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                 ++turn;
                 l += at[other];
                 uint8_t* stage = sgen + L::OFF_STAGE + warp * 1024;
-                if (nt.whole) {
+                if (!kPre && nt.whole) {
                     const int64_t o_at = valid ? rb * p.osb + rh * p.osh + ri * p.osn + half * (D / 2) : -1;
                     const float inv = l == 0.f ? 0.f : __fdiv_rn(1.f, l);
 #pragma unroll 1
@@ -404,15 +406,17 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                         __syncwarp();
                     }
                 } else {
-                    const int64_t part = (int64_t)nt.slot * M + X * 128 + row;
-                    if (valid && half == 0) p.part_ml[part] = make_float2(m, l);
+                    const bool pre = kPre && ib < 0;
+                    const int64_t part = (int64_t)nt.slot * (pre ? M : p.part_m) + X * 128 + row;
+                    if (valid && half == 0) (pre ? p.pre_ml : p.part_ml)[part] = make_float2(m, l);
+                    float* po = pre ? p.pre_o : p.part_o;
                     const int64_t part_at = valid ? part * D + half * (D / 2) : -1;
 #pragma unroll 1
                     for (int c = 0; c < D / 2; c += 8) {
                         uint32_t o[8];
                         tmem_ld8(tO + c, o);
                         tmem_wait_ld();
-                        stage_out(stage, o, part_at, p.part_o + c, lane);
+                        stage_out(stage, o, part_at, po + c, lane);
                     }
                 }
             }
@@ -431,11 +435,11 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
         PagedPlace at{};
         at.pos = t1;
         if (t0 < t1) at = paged_place(sched, found[0], t0);
-        if (at.pos < t1 && p.cuts != nullptr && at.tile > 0) {
+        if (!kPre && at.pos < t1 && at.tile > 0) {
             const int start = at.pos - at.tile, w0 = start / per;
             if (w0 == worker - 1) cut = PagedCut{at.b, at.h, at.rt, at.n, (start + at.ntiles - 1) / per - w0 + 1, {}};
         }
-        if (p.cuts != nullptr && lane == 0) p.cuts[worker] = cut;
+        if (!kPre && lane == 0) p.cuts[worker] = cut;
         const int per_tile = 128 >> p.page_shift;         // pages of a whole tile
         PagedSpan span{};
         int page = 0;
@@ -468,8 +472,8 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                     nt.b = at.b; nt.h = at.h; nt.rt = at.rt;
                     nt.n = at.n; nt.len = at.len;
                     nt.tile = at.tile; nt.run = min(at.ntiles - at.tile, t1 - at.pos);
-                    nt.slot = p.pre_rt > 0 ? worker + at.item : 2 * worker + (at.tile == 0 ? 1 : 0);
-                    nt.whole = p.pre_rt == 0 && nt.run == at.ntiles;
+                    nt.slot = kPre ? worker + at.item : 2 * worker + (at.tile == 0 ? 1 : 0);
+                    nt.whole = nt.run == at.ntiles;
                     mbar_arrive(bar(L::B_ITEM + items % kItemNotes));
                 }
                 mbar_arrive_expect_tx(bar(L::B_KF + st), bytes);
@@ -489,14 +493,16 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                 // before are computed, well before that item's output is written.
                 if (t > 0 && !mbar_wait_warp(bar(L::B_KE + (t - 1) % NS), ((t - 1) / NS) & 1, abort_flag)) { ok = false; break; }
                 if (lane == 0) {
-                    mbar_arrive_expect_tx(bar(L::B_Q), (uint32_t)(kGroups * L::kNB * p.tok * p.unit) * 128u);
+                    const bool pre = kPre && at.b < 0;
+                    const int tok = pre ? p.pre_tok : p.tok;
+                    mbar_arrive_expect_tx(bar(L::B_Q), (uint32_t)(kGroups * L::kNB * tok * (pre ? p.pre_unit : p.G)) * 128u);
 #pragma unroll
                     for (int X = 0; X < kGroups; ++X)
 #pragma unroll
                         for (int hb = 0; hb < L::kNB; ++hb) {
-                            const int g = (at.rt * kGroups + X) * p.tok;
-                            tma_load_4d(sbase + L::OFF_Q + X * L::kTile + hb * kBlk, &tm_q, hb * 64, at.h * p.G,
-                                        at.b < 0 ? 0 : g, at.b < 0 ? g : at.b, bar(L::B_Q));
+                            const int g = (at.rt * kGroups + X) * tok;
+                            tma_load_4d(sbase + L::OFF_Q + X * L::kTile + hb * kBlk, pre ? &tm_qp : &tm_q, hb * 64,
+                                        at.h * p.G, pre ? 0 : g, pre ? g : at.b, bar(L::B_Q));
                         }
                 }
                 ++items;
@@ -511,9 +517,8 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                                 bar(L::B_VF + st));
             }
             loaded_v = t + 1;
-            const int item = at.item;
             paged_next(sched, at);
-            first = at.item != item;
+            first = at.tile == 0;
             if (at.pos < t1) look_up();
         }
         if (!ok && lane == 0) fail(R_LOAD, loaded_v);
@@ -641,7 +646,7 @@ __global__ void __launch_bounds__(256) paged_cuts_kernel(const __grid_constant__
     pdl_wait();
     const PagedCut cut = p.cuts[w];
     if (cut.b < 0) return;
-    const PagedSched<M, 128> s(p);
+    const PagedSched<M, 128, false> s(p);
     const int r0 = ((int)blockIdx.y * 8 + warp) * kRows;
 #pragma unroll
     for (int k = 0; k < kRows; ++k) {
@@ -698,15 +703,15 @@ __global__ void __launch_bounds__(256) paged_cuts_kernel(const __grid_constant__
     }
 }
 
-template <int D, int kGroups>
-cudaError_t launch_one(const PagedParams& p, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
-                       cudaStream_t s) {
+template <int D, int kGroups, bool kPre>
+cudaError_t launch_one(const PagedParams& p, const CUtensorMap& tq, const CUtensorMap& tqp, const CUtensorMap& tk,
+                       const CUtensorMap& tv, cudaStream_t s) {
     using L = TilesShape<D, kGroups>;
     static bool ready[64] = {};
-    cudaError_t e = launch_pdl(paged_tiles_kernel<D, kGroups>, dim3((unsigned)p.workers), dim3(L::kThreads), L::kSmem, s, true, ready,
-                               tq, tk, tv, p);
+    cudaError_t e = launch_pdl(paged_tiles_kernel<D, kGroups, kPre>, dim3((unsigned)p.workers), dim3(L::kThreads), L::kSmem, s, true, ready,
+                               tq, tqp, tk, tv, p);
     if (e != cudaSuccess) return e;
-    if (p.pre_rt == 0 && p.workers > 1) {
+    if (!kPre && p.workers > 1) {
         static bool cuts_ready[64] = {};
         e = launch_pdl(paged_cuts_kernel<D, L::M>, dim3((unsigned)p.workers - 1, L::M / 16), dim3(256), 0, s, true, cuts_ready, p);
     }
@@ -715,10 +720,13 @@ cudaError_t launch_one(const PagedParams& p, const CUtensorMap& tq, const CUtens
 
 }  // namespace
 
-cudaError_t launch_paged_tiles(const PagedParams& p, int D, int groups, const CUtensorMap& tq, const CUtensorMap& tk,
-                               const CUtensorMap& tv, cudaStream_t s) {
-    if (D == 64) return groups == 1 ? launch_one<64, 1>(p, tq, tk, tv, s) : launch_one<64, 2>(p, tq, tk, tv, s);
-    return groups == 1 ? launch_one<128, 1>(p, tq, tk, tv, s) : launch_one<128, 2>(p, tq, tk, tv, s);
+cudaError_t launch_paged_tiles(const PagedParams& p, int D, int groups, const CUtensorMap& tq, const CUtensorMap& tqp,
+                               const CUtensorMap& tk, const CUtensorMap& tv, cudaStream_t s) {
+    const auto launch = p.pre_rt > 0 ? (D == 64 ? (groups == 1 ? launch_one<64, 1, true> : launch_one<64, 2, true>)
+                                                : (groups == 1 ? launch_one<128, 1, true> : launch_one<128, 2, true>))
+                                     : (D == 64 ? (groups == 1 ? launch_one<64, 1, false> : launch_one<64, 2, false>)
+                                                : (groups == 1 ? launch_one<128, 1, false> : launch_one<128, 2, false>));
+    return launch(p, tq, tqp, tk, tv, s);
 }
 
 }  // namespace sage

@@ -70,6 +70,23 @@ def test_long_shared_prefix(B, Hkv, G, Nq, D, prefix):
     go(B=B, H=Hkv * G, Hkv=Hkv, D=D, Nq=Nq, page=32, kv_len=kv, q_len=q, prefix=prefix, seed=prefix + B)
 
 
+# Between 17 and 64 rows to a key head: with enough to save, the prefix's items
+# and the requests' in one list; short and long prefixes, prefixes of which the
+# device says less than its table lists, requests without rows or keys.
+@pytest.mark.parametrize("B,Hkv,G,Nq,D", [
+    (2, 1, 17, 1, 64), (3, 1, 1, 17, 128), (32, 4, 4, 5, 64), (9, 8, 4, 5, 128), (7, 3, 8, 8, 128), (65, 2, 8, 3, 64),
+    (130, 1, 64, 1, 128), (40, 2, 1, 33, 64), (300, 3, 9, 7, 64)])
+@pytest.mark.parametrize("prefix", [1, 130, 1000, 4099])
+@pytest.mark.parametrize("causal", [True, False])
+def test_prefix_for_some_rows(B, Hkv, G, Nq, D, prefix, causal):
+    kv = [(37 * b) % 300 if b % 5 else 0 for b in range(B)]
+    q = [min(Nq, 1 + b % (Nq + 3)) if b % 7 else 0 for b in range(B)]
+    p = go(B=B, H=Hkv * G, Hkv=Hkv, D=D, Nq=Nq, page=32, kv_len=kv, q_len=q, prefix=prefix, causal=causal,
+           seed=prefix + B)
+    for p.prefix_len in (prefix // 3, 0):
+        P.check(p, P.run(p))
+
+
 @pytest.mark.parametrize("prefix", [0, 50])
 @pytest.mark.parametrize("Nq", [1, 4, 40])
 @pytest.mark.parametrize("causal", [True, False])
@@ -116,7 +133,7 @@ def test_lengths_left_out_and_out_of_range(causal):
     assert int(o3.count_nonzero()) == 0
 
 
-@pytest.mark.parametrize("B,Nq,H,prefix", [(6, 1, 8, 300), (6, 1, 128, 300), (6, 60, 8, 300), (50, 1, 8, 2700)])
+@pytest.mark.parametrize("B,Nq,H,prefix", [(6, 1, 8, 300), (6, 1, 128, 300), (6, 60, 8, 300), (50, 1, 8, 2700), (30, 5, 16, 4200)])
 def test_prefix_without_own_table(B, Nq, H, prefix):
     G.ensure_built()
     p = P.make(B=B, H=H, Hkv=4, D=128, Nq=Nq, page=32, kv_len=[0] * B, prefix=prefix, seed=5)
@@ -145,7 +162,7 @@ def test_long_and_many(B, H, Hkv, D, Nq, n, prefix):
     go(B=B, H=H, Hkv=Hkv, D=D, Nq=Nq, page=64, kv_len=kv, prefix=prefix, seed=n)
 
 
-@pytest.mark.parametrize("B,Nq,prefix", [(4, 1, 0), (4, 1, 500), (4, 100, 500), (64, 1, 8300)])
+@pytest.mark.parametrize("B,Nq,prefix", [(4, 1, 0), (4, 1, 500), (4, 100, 500), (64, 1, 8300), (40, 6, 4300)])
 def test_strided_views(B, Nq, prefix):
     """q inside a fused projection, o inside a wider buffer, table rows apart."""
     G.ensure_built()
@@ -163,7 +180,8 @@ def test_strided_views(B, Nq, prefix):
     assert bool((buf[:, :, 0] == 7).all()) and bool((buf[:, :, -1] == 7).all()) and bool((buf[..., D:] == 7).all())
 
 
-@pytest.mark.parametrize("B,Nq,H,prefix", [(2, 1, 4, 0), (2, 1, 4, 100), (2, 90, 4, 0), (2, 1, 128, 100), (64, 1, 4, 4200)])
+@pytest.mark.parametrize("B,Nq,H,prefix", [(2, 1, 4, 0), (2, 1, 4, 100), (2, 90, 4, 0), (2, 1, 128, 100), (64, 1, 4, 4200),
+                                           (24, 5, 8, 4200)])
 def test_a_page_outside_the_cache_reads_as_zeros_and_is_reported(B, Nq, H, prefix):
     G.ensure_built()
     p = P.make(B=B, H=H, Hkv=2, D=128, Nq=Nq, page=16, kv_len=[Nq + 100, Nq + 60] * (B // 2), prefix=prefix, poison=0.0,
@@ -186,7 +204,8 @@ def test_a_page_outside_the_cache_reads_as_zeros_and_is_reported(B, Nq, H, prefi
         P.check(good, o)
 
 
-@pytest.mark.parametrize("B,H,Hkv,Nq,n,prefix", [(8, 8, 2, 1, 3000, 0), (40, 8, 2, 1, 500, 3000), (70, 8, 2, 1, 500, 4000), (2, 4, 2, 200, 2000, 700)])
+@pytest.mark.parametrize("B,H,Hkv,Nq,n,prefix", [(8, 8, 2, 1, 3000, 0), (40, 8, 2, 1, 500, 3000), (70, 8, 2, 1, 500, 4000), (2, 4, 2, 200, 2000, 700),
+                                                  (30, 8, 2, 5, 500, 4000)])
 def test_equal_inputs_give_equal_bits(B, H, Hkv, Nq, n, prefix):
     G.ensure_built()
     p = P.make(B=B, H=H, Hkv=Hkv, D=128, Nq=Nq, page=32, kv_len=[Nq + max(0, n - 71 * b) for b in range(B)], prefix=prefix,
@@ -198,7 +217,7 @@ def test_equal_inputs_give_equal_bits(B, H, Hkv, Nq, n, prefix):
         assert torch.equal(P.run(p, workspace=ws), first)
 
 
-@pytest.mark.parametrize("B,Nq,prefix", [(3, 1, 0), (3, 1, 700), (3, 130, 700), (60, 1, 4700)])
+@pytest.mark.parametrize("B,Nq,prefix", [(3, 1, 0), (3, 1, 700), (3, 130, 700), (60, 1, 4700), (30, 5, 4700)])
 def test_captured_and_replayed_with_growing_lengths(B, Nq, prefix):
     """One graph, captured once, serves every later length: the lengths are read on the device."""
     G.ensure_built()
@@ -273,7 +292,7 @@ def test_padding_rows_of_q_and_stale_outputs_do_not_matter():
 def test_waits_for_what_the_stream_waits_for():
     """Lengths, tables, keys and q written just before, by kernels of this stream and by another stream's."""
     G.ensure_built()
-    for B, Nq, prefix in ((4, 1, 0), (3, 60, 100), (64, 1, 4300)):
+    for B, Nq, prefix in ((4, 1, 0), (3, 60, 100), (64, 1, 4300), (30, 5, 4300)):
         p = P.make(B=B, H=8, Hkv=2, D=128, Nq=Nq, page=16, kv_len=[Nq + 300 - 2 * b for b in range(B)], prefix=prefix, seed=B)
         want = P.run(p).clone()
         torch.cuda.synchronize()
