@@ -40,6 +40,10 @@ namespace {
 // Measured: 64 ragged requests of up to 8,192 keys (1,077 MB read) in 164 us,
 // 0.94 of the copy rate; one of 131,072 keys (537 MB) in 84 us with its join
 // behind it.
+// kWhole: for short sequences, bound by latency, a cluster of `split` CTAs
+// takes an item, shares its steps among its warps and joins them through
+// shared memory, so the call is one kernel (8 key heads, 60 keys: 3.9 us
+// against 6.6 with the join behind it; 777 keys: 6.7 against 7.4).
 // ---------------------------------------------------------------------------
 constexpr int kRowWarps = 4;             // warps of a CTA
 constexpr int kStep = 16;                // keys of a step
@@ -81,6 +85,16 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
     asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
     return r;
 }
+__device__ __forceinline__ float4 ld_cluster4(uint32_t a) {
+    float4 v;
+    asm volatile("ld.shared::cluster.v4.f32 {%0,%1,%2,%3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(a) : "memory");
+    return v;
+}
+__device__ __forceinline__ float2 ld_cluster2(uint32_t a) {
+    float2 v;
+    asm volatile("ld.shared::cluster.v2.f32 {%0,%1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(a) : "memory");
+    return v;
+}
 __device__ __forceinline__ void record_page(const PagedParams& p, int page) {
     if (atomicCAS(p.status, 0, kErrPage) == 0) p.status[3] = page;
 }
@@ -92,7 +106,7 @@ struct StepNote {
     int own, first;                      // own keys; first step of its item in this warp
 };
 
-template <int D, int NR>
+template <int D, int NR, bool kWhole>
 __global__ void __launch_bounds__(kRowWarps * 32, 2) paged_rows_kernel(const __grid_constant__ PagedParams p) {
     using Sh = RowsShape<D>;
     constexpr int M = 8 * NR, S = Sh::kStages;
@@ -101,24 +115,45 @@ __global__ void __launch_bounds__(kRowWarps * 32, 2) paged_rows_kernel(const __g
     __shared__ int2 found[kRowWarps];
     __shared__ int warp_sums[kRowWarps];
     __shared__ StepNote notes[kRowWarps][S];
+    __shared__ float2 part_ml[kRowWarps][M];
+    constexpr int kPartRow = D + 4;                       // floats; rows two apart lie in other banks
+    static_assert(M * kPartRow * 4 <= S * Sh::kStage && (S * Sh::kStage) % 16 == 0);
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (!p.beside) pdl_wait();
     pdl_trigger();
     const PagedSched<M, kStep, false> sched(p);
-    // workers next to each other in the list sit on different SMs: a CTA's
-    // warps are a grid apart, so a short list still uses every SM
-    const int worker = warp * gridDim.x + blockIdx.x;
-    const int total = paged_scan<M, kStep, false, kRowWarps * 32, kRowWarps>(sched, blockIdx.x, gridDim.x, found, warp_sums,
-                                                                      blockIdx.x == 0);
-    const int per = paged_per_worker(p, total);
-    const int t0 = min(worker * per, total), t1 = min(t0 + per, total);   // this worker's run of the list
+    int worker, t1;                                       // this worker, the end of its run of places
+    int parts = 0;                                        // kWhole: workers that share the item
     PagedPlace at{};
-    at.pos = t1;
-    if (t0 < t1) at = paged_place(sched, found[warp], t0);
-    if (at.pos >= t1) {
-        pdl_wait();
-        return;
+    if constexpr (kWhole) {
+        const int all = (int)blockIdx.x / p.split;        // a cluster takes an item
+        worker = ((int)blockIdx.x - all * p.split) * kRowWarps + warp;
+        const int pair = all / p.Hkv;
+        at.h = all - pair * p.Hkv;
+        at.b = pair / p.rt;
+        at.rt = pair - at.b * p.rt;
+        at.n = sched.q_rows(at.b);
+        at.len = sched.own_keys(at.b);
+        at.ntiles = sched.item_tiles(at.n, at.len, at.rt);
+        const int workers = p.split * kRowWarps, per = max(1, (at.ntiles + workers - 1) / workers);
+        parts = (at.ntiles + per - 1) / per;
+        at.tile = at.pos = min(worker * per, at.ntiles);
+        t1 = min(at.pos + per, at.ntiles);
+    } else {
+        // workers next to each other in the list sit on different SMs: a CTA's
+        // warps are a grid apart, so a short list still uses every SM
+        worker = warp * gridDim.x + blockIdx.x;
+        const int total = paged_scan<M, kStep, false, kRowWarps * 32, kRowWarps>(sched, blockIdx.x, gridDim.x, found,
+                                                                                 warp_sums, blockIdx.x == 0);
+        const int per = paged_per_worker(p, total), t0 = min(worker * per, total);
+        t1 = min(t0 + per, total);
+        at.pos = t1;
+        if (t0 < t1) at = paged_place(sched, found[warp], t0);
+        if (at.pos >= t1) {
+            pdl_wait();
+            return;
+        }
     }
     const uint32_t ring = smem_u32(smem) + warp * S * Sh::kStage;
     int issued = 0;                                       // steps whose copies were issued
@@ -157,13 +192,19 @@ __global__ void __launch_bounds__(kRowWarps * 32, 2) paged_rows_kernel(const __g
             nt.own = span.own; nt.first = first;
         }
         ++issued;
-        const int item = at.item;
-        paged_next(sched, at);
-        first = at.item != item;
+        if constexpr (kWhole) {
+            ++at.pos;
+            ++at.tile;
+            first = false;
+        } else {
+            const int item = at.item;
+            paged_next(sched, at);
+            first = at.item != item;
+        }
         if (at.pos < t1) fetch();
     };
 
-    fetch();
+    if (at.pos < t1) fetch();
 
     uint32_t qf[NR][D / 16][2];                           // Q^T fragments
     float o[NR][D / 16][4];                               // O^T: channels x query rows
@@ -185,9 +226,15 @@ __global__ void __launch_bounds__(kRowWarps * 32, 2) paged_rows_kernel(const __g
                 s += __shfl_xor_sync(0xffffffffu, s, 16);
                 const int r = nr * 8 + (lane & 3) * 2 + e;
                 int b, i, hq;
-                if (!paged_row(sched, ib, ih, irt, n, r, b, i, hq)) continue;
-                if (lane < 4) p.part_ml[slot * M + r] = make_float2(m[nr][e], s);
-                float* dst = p.part_o + (slot * M + r) * D + (lane >> 2);
+                float* dst;
+                if constexpr (kWhole) {                   // in place of the ring
+                    if (lane < 4) part_ml[warp][r] = make_float2(m[nr][e], s);
+                    dst = reinterpret_cast<float*>(smem + warp * S * Sh::kStage) + r * kPartRow + (lane >> 2);
+                } else {
+                    if (!paged_row(sched, ib, ih, irt, n, r, b, i, hq)) continue;
+                    if (lane < 4) p.part_ml[slot * M + r] = make_float2(m[nr][e], s);
+                    dst = p.part_o + (slot * M + r) * D + (lane >> 2);
+                }
 #pragma unroll
                 for (int j = 0; j < D / 16; ++j) {
                     dst[j * 16] = o[nr][j][e];
@@ -300,9 +347,46 @@ __global__ void __launch_bounds__(kRowWarps * 32, 2) paged_rows_kernel(const __g
             }
         }
     }
-    leave();
     cp_async_wait<0>();
-    pdl_wait();                          // the prefix's kernel, where one runs beside this one, is through too
+    if constexpr (kWhole) {
+        __syncwarp();
+        if (issued > 0) leave();
+        __syncwarp();
+        cluster_sync_all();
+        // Join the workers' parts: a thread takes four channels of a row at a time.
+        const int rank = (int)blockIdx.x % p.split;
+        for (int v = rank * (int)blockDim.x + (int)threadIdx.x; v < M * D / 4; v += p.split * (int)blockDim.x) {
+            const int r = v / (D / 4), c = (v - r * (D / 4)) * 4;
+            int b, i, hq;
+            if (!paged_row(sched, at.b, at.h, at.rt, at.n, r, b, i, hq)) continue;
+            const uint32_t ml0 = smem_u32(&part_ml[0][r]), o0 = smem_u32(smem) + (uint32_t)(r * kPartRow + c) * 4;
+            float mx = -INFINITY, l = 0.f;
+            float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+            for (int w = 0; w < parts; ++w) {
+                const uint32_t cta = (uint32_t)w / kRowWarps, in = (uint32_t)w % kRowWarps;
+                const float2 ml = ld_cluster2(mapa_rank(ml0 + in * (uint32_t)sizeof(part_ml[0]), cta));
+                const float4 x = ld_cluster4(mapa_rank(o0 + in * S * Sh::kStage, cta));
+                const float mn = fmaxf(mx, ml.x), ms = mn == -INFINITY ? 0.f : mn;
+                const float fa = ex2_approx(mx - ms), fb = ex2_approx(ml.x - ms);
+                l = l * fa + ml.y * fb;
+                acc.x = acc.x * fa + x.x * fb;
+                acc.y = acc.y * fa + x.y * fb;
+                acc.z = acc.z * fa + x.z * fb;
+                acc.w = acc.w * fa + x.w * fb;
+                mx = mn;
+            }
+            // as in the join kernel: l is 0 exactly when the row saw no key
+            const float inv = l == 0.f ? 0.f : __fdiv_rn(1.f, l);
+            uint16_t* dst = p.o + b * p.osb + hq * p.osh + (int64_t)i * p.osn + c;
+            *reinterpret_cast<uint2*>(dst) = make_uint2(pack_bf16(acc.x * inv, acc.y * inv), pack_bf16(acc.z * inv, acc.w * inv));
+        }
+        __syncwarp();
+        cluster_sync_all();                                // the parts stay until all have read them
+    } else {
+        leave();
+        pdl_wait();                      // the prefix's kernel, where one runs beside this one, is through too
+    }
 }
 
 // ---------------------------------------------------------------------------
@@ -467,9 +551,17 @@ __global__ void __launch_bounds__(256) paged_join_kernel(const __grid_constant__
 //    of its own, which the many-rows kernel then reads once for all rows: 64
 //    requests, 8 key heads, 512 shared keys (134 MB read again) take 36 us so
 //    and 43 with a list, 2,048 keys (537 MB) 66 and 52.
+//    Without a list of its own: up to four items an SM take a cluster each when
+//    the table widths bound a warp's share to 12 steps, a cluster of 2, 4 or 8
+//    CTAs counted as 2, 3 or 4 steps more.  A cluster does not even out the
+//    lengths: 38 requests, 8 key heads, one request of n keys and 37 of 30 take
+//    5.9 us for n = 250 and 8.9 for 500 so, 8.3 both from a list; at 1,000 (16
+//    steps) 14.4 and 9.1, though with 1,000 keys each 27.8 and 32.3.  Eight
+//    items an SM of 30 keys: 13.3 us, from a list 9.5; four 7.4 and 8.3.
 // ---------------------------------------------------------------------------
 constexpr int kFewRows = 16;
 constexpr int64_t kReadAgain = int64_t(256) << 20;        // bytes of prefix read again that cost as much as its list
+constexpr int kWholeSteps = 12, kWholeItems = 4;          // few-rows kernel: a cluster takes an item up to these
 constexpr double kOwnList = 12e6, kRowJoin = 6e3;         // many-rows kernel: ... as much as joining all rows, and one row
 
 struct Lists {
@@ -528,6 +620,23 @@ Lists make_lists(int B, int Hkv, int G, int Nq, int D, int64_t pre_keys) {
     return x;
 }
 
+// CTAs of a cluster that takes an item of up to `steps` steps whole; 0: the list.
+int whole_split(int64_t items, int64_t steps, int sms) {
+    int split = 0;
+    if (items > (int64_t)kWholeItems * sms) return 0;
+    int64_t least = kWholeSteps + 1;
+    // Clusters do not fill a GPU to the last SM: 304 CTAs in fours take 9.3 us
+    // where 152 in pairs take 5.8, 288 in fours 6.4.
+    for (int j = 0; j < 4 && (j == 0 || (items << j) * 10 <= 19 * sms); ++j) {
+        const int64_t cost = ceil_div(steps, kRowWarps << j) + (j > 0 ? j + 1 : 0);
+        if (cost < least) {
+            least = cost;
+            split = 1 << j;
+        }
+    }
+    return split;
+}
+
 // Each array of the workspace begins on 16 bytes.
 size_t padded(size_t n) { return (n + 15) / 16 * 16; }
 size_t slot_bytes(int64_t slots, int M, int D) { return (size_t)slots * M * D * 4 + padded((size_t)slots * M * 8); }
@@ -561,16 +670,21 @@ cudaError_t launch_join(const PagedParams& p, cudaStream_t s) {
     // (8 KV heads x 3 rows of 152 parts each: 4.2 against 13.6 us).
     const int64_t rows = (int64_t)p.H * p.Nq;
     if (rows * p.B <= 1024)
-        return launch_pdl(paged_join_kernel<D, M, TK, 8>, dim3((unsigned)rows, (unsigned)p.B), dim3(256), 0, s, true, ready8, p);
-    return launch_pdl(paged_join_kernel<D, M, TK, 1>, dim3((unsigned)ceil_div(rows, 8), (unsigned)p.B), dim3(256), 0, s, true,
+        return launch_pdl(paged_join_kernel<D, M, TK, 8>, dim3((unsigned)rows, (unsigned)p.B), dim3(256), 0, s, 1, true, ready8, p);
+    return launch_pdl(paged_join_kernel<D, M, TK, 1>, dim3((unsigned)ceil_div(rows, 8), (unsigned)p.B), dim3(256), 0, s, 1, true,
                       ready1, p);
 }
 
 template <int D, int NR>
 cudaError_t launch_rows(const PagedParams& p, cudaStream_t s) {
+    if (p.split > 0) {
+        static bool whole_ready[64] = {};
+        return launch_pdl(paged_rows_kernel<D, NR, true>, dim3((unsigned)(p.B * p.rt * p.Hkv * p.split)), dim3(kRowWarps * 32),
+                          RowsShape<D>::kSmem, s, p.split, true, whole_ready, p);
+    }
     static bool ready[64] = {};
-    const cudaError_t e = launch_pdl(paged_rows_kernel<D, NR>, dim3((unsigned)(p.workers / kRowWarps)), dim3(kRowWarps * 32),
-                                     RowsShape<D>::kSmem, s, true, ready, p);
+    const cudaError_t e = launch_pdl(paged_rows_kernel<D, NR, false>, dim3((unsigned)(p.workers / kRowWarps)), dim3(kRowWarps * 32),
+                                     RowsShape<D>::kSmem, s, 1, true, ready, p);
     return e != cudaSuccess ? e : launch_join<D, 8 * NR, kStep>(p, s);
 }
 cudaError_t launch_rows(const PagedParams& p, int D, int nr, cudaStream_t s) {
@@ -698,8 +812,11 @@ int sage_attn_paged(const sage_tensor* q, const sage_tensor* o, const sage_page_
             p.beside = 1;
         }
         p.workers = std::min(2 * sms, kMaxRowWorkers / kRowWarps) * kRowWarps;
+        if (!x.pre)
+            p.split = whole_split((int64_t)B * cache->heads * x.rt,
+                                  ceil_div(own_keys, kStep) + (x.join ? ceil_div(pre_keys, kStep) : 0), sms);
         e = launch_rows(p, D, x.nr, s);
-        launches += 2;
+        launches += p.split > 0 ? 1 : 2;
     }
     if (e != cudaSuccess) return SAGE_ERR_LAUNCH;
     set_last_launch_count(launches);

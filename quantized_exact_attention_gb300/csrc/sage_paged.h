@@ -60,6 +60,7 @@ struct PagedParams {
     int join;                            // 1: a request's key sequence is the prefix followed by its own keys
     int workers;                         // workers the list is shared among
     int fault_mode;                      // test hook: 0 = none
+    int split;                           // few-rows kernel, whole items: CTAs of a cluster
     int beside;                          // runs beside the kernel before it, which it does not depend on
     // workspace
     float* part_o;                       // [slot][part_m][D]
@@ -112,8 +113,8 @@ __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;"
 // split 9.0 us).  The append moves its rows through L1 and keeps the default
 // (2 x 122 MB: 40.9 us; with little L1 51.3).
 template <class... P, class... A>
-cudaError_t launch_pdl(void (*kernel)(P...), dim3 grid, dim3 block, size_t smem, cudaStream_t s, bool max_shared,
-                       bool (&ready)[64], const A&... args) {
+cudaError_t launch_pdl(void (*kernel)(P...), dim3 grid, dim3 block, size_t smem, cudaStream_t s, int cluster,
+                       bool max_shared, bool (&ready)[64], const A&... args) {
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess || dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
@@ -130,11 +131,14 @@ cudaError_t launch_pdl(void (*kernel)(P...), dim3 grid, dim3 block, size_t smem,
     cfg.blockDim = block;
     cfg.dynamicSmemBytes = smem;
     cfg.stream = s;
-    cudaLaunchAttribute attr[1];
+    cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = (unsigned)cluster;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = cluster > 1 ? 2 : 1;
     e = cudaLaunchKernelEx(&cfg, kernel, args...);
     return e != cudaSuccess ? e : cudaGetLastError();
 }

@@ -708,12 +708,12 @@ cudaError_t launch_one(const PagedParams& p, const CUtensorMap& tq, const CUtens
                        const CUtensorMap& tv, cudaStream_t s) {
     using L = TilesShape<D, kGroups>;
     static bool ready[64] = {};
-    cudaError_t e = launch_pdl(paged_tiles_kernel<D, kGroups, kPre>, dim3((unsigned)p.workers), dim3(L::kThreads), L::kSmem, s, true, ready,
+    cudaError_t e = launch_pdl(paged_tiles_kernel<D, kGroups, kPre>, dim3((unsigned)p.workers), dim3(L::kThreads), L::kSmem, s, 1, true, ready,
                                tq, tqp, tk, tv, p);
     if (e != cudaSuccess) return e;
     if (!kPre && p.workers > 1) {
         static bool cuts_ready[64] = {};
-        e = launch_pdl(paged_cuts_kernel<D, L::M>, dim3((unsigned)p.workers - 1, L::M / 16), dim3(256), 0, s, true, cuts_ready, p);
+        e = launch_pdl(paged_cuts_kernel<D, L::M>, dim3((unsigned)p.workers - 1, L::M / 16), dim3(256), 0, s, 1, true, cuts_ready, p);
     }
     return e;
 }

@@ -251,8 +251,8 @@ int sage_page_tables(const int32_t* old_len, const int32_t* new_len, int B, int 
     static bool ready[2][64] = {};
     const dim3 grid((unsigned)std::min(B, 152 * 8)), block(kTableThreads);     // one wave: eight blocks an SM
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
-    if ((quads ? launch_pdl(page_tables_kernel<true>, grid, block, 0, s, false, ready[1], p)
-               : launch_pdl(page_tables_kernel<false>, grid, block, 0, s, false, ready[0], p)) != cudaSuccess)
+    if ((quads ? launch_pdl(page_tables_kernel<true>, grid, block, 0, s, 1, false, ready[1], p)
+               : launch_pdl(page_tables_kernel<false>, grid, block, 0, s, 1, false, ready[0], p)) != cudaSuccess)
         return SAGE_ERR_LAUNCH;
     set_last_launch_count(1);
     return SAGE_OK;
@@ -284,7 +284,7 @@ int sage_cache_append(const sage_tensor* k, const sage_tensor* v, int B, int N, 
     p.page_shift = 31 - __builtin_clz((unsigned)cache->page_size);
     const int64_t grid = ceil_div(p.tokens, kAppendThreads / 32);
     static bool ready[64] = {};
-    if (launch_pdl(cache_append_kernel, dim3((unsigned)grid), dim3(kAppendThreads), 0, static_cast<cudaStream_t>(stream), false,
+    if (launch_pdl(cache_append_kernel, dim3((unsigned)grid), dim3(kAppendThreads), 0, static_cast<cudaStream_t>(stream), 1, false,
                    ready, p) != cudaSuccess)
         return SAGE_ERR_LAUNCH;
     set_last_launch_count(1);

@@ -18,45 +18,68 @@ def go(**kw):
     return p
 
 
+# Few rows: a wide table (its entries behind the lengths unused) takes the list,
+# a narrow one clusters that each take an item whole.
+wide = pytest.mark.parametrize("wide", [0, 1])
+
+
+def pad(wide):
+    return {"table_pad": 1200 if wide else 2}
+
+
+@wide
 @pytest.mark.parametrize("D", [64, 128])
 @pytest.mark.parametrize("page", [16, 32, 64, 128])
 @pytest.mark.parametrize("n", [1, 15, 16, 17, 63, 64, 65, 127, 128, 129, 500])
-def test_one_token_one_request(D, page, n):
-    go(B=1, H=2, Hkv=2, D=D, Nq=1, page=page, kv_len=[n], seed=n)
+def test_one_token_one_request(D, page, n, wide):
+    go(B=1, H=2, Hkv=2, D=D, Nq=1, page=page, kv_len=[n], seed=n, **pad(wide))
 
 
+@pytest.mark.parametrize("G", [1, 4, 16])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("B,n", [(1, 180), (1, 300), (1, 1000), (3, 2000), (9, 700), (36, 700), (37, 350), (75, 190), (77, 190)])
+def test_sequences_of_one_cluster(B, n, G, D):
+    """From one CTA to clusters of eight, up to the shares where the list takes over."""
+    go(B=B, H=8 * G, Hkv=8, D=D, Nq=1, page=16, kv_len=[max(0, n - 37 * b % (n + 1)) for b in range(B)], table_pad=0, seed=n)
+
+
+@wide
 @pytest.mark.parametrize("H,Hkv", [(1, 1), (4, 4), (6, 2), (8, 1), (24, 8), (16, 1), (9, 3), (20, 1), (33, 1)])
 @pytest.mark.parametrize("D", [64, 128])
-def test_heads(H, Hkv, D):
-    go(B=3, H=H, Hkv=Hkv, D=D, Nq=1, page=16, kv_len=[70, 1, 333], seed=H)
+def test_heads(H, Hkv, D, wide):
+    go(B=3, H=H, Hkv=Hkv, D=D, Nq=1, page=16, kv_len=[70, 1, 333], seed=H, **pad(wide))
 
 
+@wide
 @pytest.mark.parametrize("layout", ["nhd", "hnd"])
 @pytest.mark.parametrize("causal", [True, False])
 @pytest.mark.parametrize("Nq,G", [(2, 1), (5, 2), (3, 8), (17, 3), (40, 1), (129, 2)])
-def test_several_tokens(layout, causal, Nq, G):
+def test_several_tokens(layout, causal, Nq, G, wide):
     kv = [Nq, Nq + 100, Nq + 1, Nq + 37]
     go(B=4, H=2 * G, Hkv=2, D=128, Nq=Nq, page=32, kv_len=kv, q_len=[Nq, 1, Nq - 1, Nq], causal=causal, layout=layout,
-       seed=Nq)
+       seed=Nq, **pad(wide))
 
 
 # A key head with so many query heads that a group of 128 rows holds one token,
 # or (over 128) not a whole one.
+@wide
 @pytest.mark.parametrize("G,Hkv", [(65, 2), (100, 1), (128, 2), (129, 1), (150, 2), (300, 1)])
 @pytest.mark.parametrize("Nq,causal", [(1, True), (3, True), (3, False), (9, True)])
 @pytest.mark.parametrize("prefix", [0, 130])
-def test_many_heads_to_a_key_head(G, Hkv, Nq, causal, prefix):
+def test_many_heads_to_a_key_head(G, Hkv, Nq, causal, prefix, wide):
     kv = [0, Nq, 1, 300, 77]
     go(B=5, H=G * Hkv, Hkv=Hkv, D=64, Nq=Nq, page=16, kv_len=kv, q_len=[Nq, Nq, Nq, 0, max(1, Nq - 1)], prefix=prefix,
-       causal=causal, seed=G + Nq)
+       causal=causal, seed=G + Nq, **pad(wide))
 
 
+@wide
 @pytest.mark.parametrize("prefix", [1, 16, 100, 128, 777])
 @pytest.mark.parametrize("B,Nq,G", [(1, 1, 1), (3, 1, 2), (5, 1, 8), (20, 1, 4), (4, 3, 2), (2, 30, 2), (70, 1, 8)])
 @pytest.mark.parametrize("D", [64, 128])
-def test_shared_prefix(prefix, B, Nq, G, D):
+def test_shared_prefix(prefix, B, Nq, G, D, wide):
     kv = [Nq + (37 * b) % 90 for b in range(B)]
-    go(B=B, H=2 * G, Hkv=2, D=D, Nq=Nq, page=16, kv_len=kv, prefix=prefix, seed=prefix + B)
+    go(B=B, H=2 * G, Hkv=2, D=D, Nq=Nq, page=16, kv_len=kv, prefix=prefix, seed=prefix + B,
+       **pad(wide))
 
 
 # A prefix whose repeated reading would cost over 256 MB is read once for all
@@ -87,13 +110,14 @@ def test_prefix_for_some_rows(B, Hkv, G, Nq, D, prefix, causal):
         P.check(p, P.run(p))
 
 
+@wide
 @pytest.mark.parametrize("prefix", [0, 50])
 @pytest.mark.parametrize("Nq", [1, 4, 40])
 @pytest.mark.parametrize("causal", [True, False])
-def test_rows_without_keys(prefix, Nq, causal):
+def test_rows_without_keys(prefix, Nq, causal, wide):
     """No own keys, no query rows, and (causal) fewer keys than query rows: rows that see nothing are zero."""
     p = go(B=5, H=4, Hkv=2, D=64, Nq=Nq, page=16, q_len=[Nq, 0, Nq, Nq, 0], kv_len=[0, 5, max(Nq - 2, 0), Nq + 3, 0],
-           prefix=prefix, causal=causal, seed=Nq)
+           prefix=prefix, causal=causal, seed=Nq, **pad(wide))
     if prefix == 0:
         o = P.run(p)
         torch.cuda.synchronize()
