@@ -144,8 +144,9 @@ __global__ void __launch_bounds__(kTableThreads, 8) page_tables_kernel(const __g
 // ---------------------------------------------------------------------------
 // Append: one warp copies the K and V rows of one token, 16 bytes a lane.
 // Reads and writes each row once; HBM bounds it (16 prompts of up to 2,048
-// tokens, 16 heads of 128 channels: 38 us, the copy's rate 36).  With eight
-// blocks an SM that loop over the tokens it takes 41 us.
+// tokens, 16 heads of 128 channels: 38 us, the copy's rate 36).  Four blocks an
+// SM, whose registers hold a warp's loads before its stores; with six it takes
+// 39.8 us, with eight 40.9, with eight that loop over the tokens 41.
 // ---------------------------------------------------------------------------
 struct AppendParams {
     const uint16_t* k;
@@ -164,7 +165,7 @@ struct AppendParams {
 
 constexpr int kAppendThreads = 256;
 
-__global__ void __launch_bounds__(kAppendThreads) cache_append_kernel(const __grid_constant__ AppendParams p) {
+__global__ void __launch_bounds__(kAppendThreads, 4) cache_append_kernel(const __grid_constant__ AppendParams p) {
     pdl_trigger();
     pdl_wait();
     const int lane = threadIdx.x & 31;
