@@ -538,6 +538,16 @@ __global__ void __launch_bounds__(256) paged_join_kernel(const __grid_constant__
 //    and 94.  (More than 128 query heads to a key head leave no whole token in
 //    a group: these, which no model is known to have, stay with the few-rows
 //    kernel.)
+//    A CTA takes an item whole, with no list and no join behind it, while that
+//    leaves few of them idle: items of up to T tiles times groups (by the table
+//    widths), half of that on average, for r items a CTA, waste T (1 - r / 2) of
+//    a CTA's time, which may be 12; later items start as CTAs end, the longest
+//    (of a causal mask) first.  4 requests of 32 tokens, 8 key heads, 500 keys:
+//    14.0 us from the list, 9.8 so; 16 heads of 2,048 tokens, two prompts, D =
+//    64, T = 32, r = 1.7: 42.6 and 33.4; on the other side 8 heads of 4,096
+//    tokens, T = 64, r = 0.8: 50.5 and 63.3; 128 items of 24 rows and up to
+//    4,000 keys, T = 32: 36.5 and 53.5; 16 x 16 heads of 1,024 tokens, r = 6.7:
+//    112 and 124, the start of every CTA.
 //    Up to 64 rows, of which two requests or more fill a group, the prefix may
 //    have items of its own in front of the requests', each for the rows of
 //    several requests.  That saves tiles and costs a join of all rows, about
@@ -618,6 +628,12 @@ Lists make_lists(int B, int Hkv, int G, int Nq, int D, int64_t pre_keys) {
     x.slots = (int64_t)B * Hkv * x.rt + kMaxRowWorkers;
     x.join = pre_keys > 0 && !x.pre;
     return x;
+}
+
+// Whether the many-rows kernel gives each CTA an item of up to `tiles` tiles.
+bool whole_items(int64_t items, int64_t tiles, int groups, int workers) {
+    return 5 * items <= 13 * (int64_t)workers && tiles <= 16 * groups &&
+           tiles * groups * (2 * (int64_t)workers - items) <= 24 * (int64_t)workers;
 }
 
 // CTAs of a cluster that takes an item of up to `steps` steps whole; 0: the list.
@@ -799,9 +815,14 @@ int sage_attn_paged(const sage_tensor* q, const sage_tensor* o, const sage_page_
     if (x.tiles) {
         p.workers = ctas * (3 - x.groups);
         if (x.pre) p.pre_rt = x.pre_items_rt;
+        const int64_t items = (int64_t)B * cache->heads * x.rt;
+        if (!x.pre && whole_items(items, ceil_div(own_keys, 128) + (x.join ? ceil_div(pre_keys, 128) : 0), x.groups, p.workers)) {
+            p.whole = 1;
+            p.workers = (int)items;
+        }
         e = launch_paged_tiles(p, D, x.groups, mq, mqp, mk, mv, s);
         if (e == cudaSuccess && x.pre) e = D == 64 ? launch_join<64, 128, 128>(p, s) : launch_join<128, 128, 128>(p, s);
-        launches = 2;
+        launches = p.whole ? 1 : 2;
     } else {
         if (x.pre) {
             PagedParams pp = p;

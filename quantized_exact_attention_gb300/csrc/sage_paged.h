@@ -61,6 +61,7 @@ struct PagedParams {
     int workers;                         // workers the list is shared among
     int fault_mode;                      // test hook: 0 = none
     int split;                           // few-rows kernel, whole items: CTAs of a cluster
+    int whole;                           // many-rows kernel: a CTA takes an item
     int beside;                          // runs beside the kernel before it, which it does not depend on
     // workspace
     float* part_o;                       // [slot][part_m][D]

@@ -2,7 +2,7 @@
 // the tcgen05 tensor cores.
 //
 // A persistent CTA is one worker of the list of sage_paged_sched.cuh with
-// 128-key tiles.  Its query rows form groups of 128; a "unit" is one group's
+// 128-key tiles, or it takes one item of that list whole.  Its query rows form groups of 128; a "unit" is one group's
 // S = Q K^T and O += P V of one tile.
 //   kGroups = 2 (one CTA per SM): both groups see every tile and take turns at
 //     the tensor core, so that one group's softmax runs beside the other's
@@ -171,13 +171,18 @@ __device__ __forceinline__ void stage_out(uint8_t* stage, const uint32_t (&w)[8]
     __syncwarp();
 }
 
-template <int D, int kGroups, bool kPre>
+// What the kernel's work is: the list of the requests' own items, the list with
+// the prefix's items in front, or an item for each CTA.
+enum TileForm { F_LIST, F_PREFIX, F_ITEM };
+
+template <int D, int kGroups, int kForm>
 __global__ void __launch_bounds__(TilesShape<D, kGroups>::kThreads, TilesShape<D, kGroups>::kCtasPerSm)
 paged_tiles_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_qp,
                    const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                    const __grid_constant__ PagedParams p) {
     using L = TilesShape<D, kGroups>;
     constexpr int M = L::M, NS = L::kNS;
+    constexpr bool kPre = kForm == F_PREFIX, kItem = kForm == F_ITEM;
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw_base = smem_u32(smem_raw);
     const uint32_t sbase = (raw_base + 1023u) & ~1023u;
@@ -230,12 +235,18 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
     int* red = reinterpret_cast<int*>(sgen + L::OFF_SCAN);
     int2* found = reinterpret_cast<int2*>(sgen + L::OFF_SCAN + 80);
     const int worker = blockIdx.x;
-    const int total = paged_scan<M, 128, kPre, L::kThreads, 1>(sched, worker, 0, found, red,      // ends with a barrier
-                                                               kPre && worker == 0 && p.start != nullptr);
+    int t0 = 0, t1 = 0, per = 1;                          // this worker's run of the list
+    if constexpr (kItem) {
+        __syncthreads();                                  // a CTA takes an item
+    } else {
+        const int total = paged_scan<M, 128, kPre, L::kThreads, 1>(sched, worker, 0, found, red,      // ends with a barrier
+                                                                   kPre && worker == 0 && p.start != nullptr);
+        per = paged_per_worker(p, total);
+        t0 = min(worker * per, total);
+        t1 = min(t0 + per, total);
+    }
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
-    const int per = paged_per_worker(p, total);
-    const int t0 = min(worker * per, total), t1 = min(t0 + per, total);   // this worker's run of the list
 
     if (warp < 8 * kGroups) {
         // ===================================================== softmax
@@ -387,7 +398,7 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                 ++turn;
                 l += at[other];
                 uint8_t* stage = sgen + L::OFF_STAGE + warp * 1024;
-                if (!kPre && nt.whole) {
+                if (kItem || (!kPre && nt.whole)) {
                     const int64_t o_at = valid ? rb * p.osb + rh * p.osh + ri * p.osn + half * (D / 2) : -1;
                     const float inv = l == 0.f ? 0.f : __fdiv_rn(1.f, l);
 #pragma unroll 1
@@ -434,12 +445,22 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
         cut.b = -1;
         PagedPlace at{};
         at.pos = t1;
-        if (t0 < t1) at = paged_place(sched, found[0], t0);
-        if (!kPre && at.pos < t1 && at.tile > 0) {
+        if constexpr (kItem) {
+            // last row sets first: with a causal mask they are the longest
+            const int each = p.B * p.Hkv, set = worker / each, rest = worker - set * each;
+            at.rt = p.rt - 1 - set;
+            at.b = rest / p.Hkv;
+            at.h = rest - at.b * p.Hkv;
+            at.n = sched.q_rows(at.b);
+            at.len = sched.own_keys(at.b);
+            t1 = at.ntiles = sched.item_tiles(at.n, at.len, at.rt);
+        }
+        else if (t0 < t1) at = paged_place(sched, found[0], t0);
+        if (kForm == F_LIST && at.pos < t1 && at.tile > 0) {
             const int start = at.pos - at.tile, w0 = start / per;
             if (w0 == worker - 1) cut = PagedCut{at.b, at.h, at.rt, at.n, (start + at.ntiles - 1) / per - w0 + 1, {}};
         }
-        if (!kPre && lane == 0) p.cuts[worker] = cut;
+        if (kForm == F_LIST && lane == 0) p.cuts[worker] = cut;
         const int per_tile = 128 >> p.page_shift;         // pages of a whole tile
         PagedSpan span{};
         int page = 0;
@@ -517,7 +538,8 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                                 bar(L::B_VF + st));
             }
             loaded_v = t + 1;
-            paged_next(sched, at);
+            if constexpr (kItem) ++at.pos, ++at.tile;
+            else paged_next(sched, at);
             first = at.tile == 0;
             if (at.pos < t1) look_up();
         }
@@ -703,30 +725,37 @@ __global__ void __launch_bounds__(256) paged_cuts_kernel(const __grid_constant__
     }
 }
 
-template <int D, int kGroups, bool kPre>
+template <int D, int kGroups, int kForm>
 cudaError_t launch_one(const PagedParams& p, const CUtensorMap& tq, const CUtensorMap& tqp, const CUtensorMap& tk,
                        const CUtensorMap& tv, cudaStream_t s) {
     using L = TilesShape<D, kGroups>;
     static bool ready[64] = {};
-    cudaError_t e = launch_pdl(paged_tiles_kernel<D, kGroups, kPre>, dim3((unsigned)p.workers), dim3(L::kThreads), L::kSmem, s, 1, true, ready,
+    cudaError_t e = launch_pdl(paged_tiles_kernel<D, kGroups, kForm>, dim3((unsigned)p.workers), dim3(L::kThreads), L::kSmem, s, 1, true, ready,
                                tq, tqp, tk, tv, p);
     if (e != cudaSuccess) return e;
-    if (!kPre && p.workers > 1) {
+    if (kForm == F_LIST && p.workers > 1) {
         static bool cuts_ready[64] = {};
         e = launch_pdl(paged_cuts_kernel<D, L::M>, dim3((unsigned)p.workers - 1, L::M / 16), dim3(256), 0, s, 1, true, cuts_ready, p);
     }
     return e;
 }
 
+template <int D, int kGroups>
+cudaError_t launch_form(int form, const PagedParams& p, const CUtensorMap& tq, const CUtensorMap& tqp, const CUtensorMap& tk,
+                        const CUtensorMap& tv, cudaStream_t s) {
+    if (form == F_ITEM) return launch_one<D, kGroups, F_ITEM>(p, tq, tqp, tk, tv, s);
+    if (form == F_PREFIX) return launch_one<D, kGroups, F_PREFIX>(p, tq, tqp, tk, tv, s);
+    return launch_one<D, kGroups, F_LIST>(p, tq, tqp, tk, tv, s);
+}
+
 }  // namespace
 
 cudaError_t launch_paged_tiles(const PagedParams& p, int D, int groups, const CUtensorMap& tq, const CUtensorMap& tqp,
                                const CUtensorMap& tk, const CUtensorMap& tv, cudaStream_t s) {
-    const auto launch = p.pre_rt > 0 ? (D == 64 ? (groups == 1 ? launch_one<64, 1, true> : launch_one<64, 2, true>)
-                                                : (groups == 1 ? launch_one<128, 1, true> : launch_one<128, 2, true>))
-                                     : (D == 64 ? (groups == 1 ? launch_one<64, 1, false> : launch_one<64, 2, false>)
-                                                : (groups == 1 ? launch_one<128, 1, false> : launch_one<128, 2, false>));
-    return launch(p, tq, tqp, tk, tv, s);
+    const int form = p.whole ? F_ITEM : p.pre_rt > 0 ? F_PREFIX : F_LIST;
+    if (D == 64)
+        return groups == 1 ? launch_form<64, 1>(form, p, tq, tqp, tk, tv, s) : launch_form<64, 2>(form, p, tq, tqp, tk, tv, s);
+    return groups == 1 ? launch_form<128, 1>(form, p, tq, tqp, tk, tv, s) : launch_form<128, 2>(form, p, tq, tqp, tk, tv, s);
 }
 
 }  // namespace sage

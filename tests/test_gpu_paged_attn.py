@@ -60,6 +60,17 @@ def test_several_tokens(layout, causal, Nq, G, wide):
        seed=Nq, **pad(wide))
 
 
+@pytest.mark.parametrize("B,H,Hkv,Nq,n,D", [
+    (25, 8, 8, 300, 300, 128), (40, 8, 8, 150, 700, 64), (50, 32, 8, 32, 500, 128), (90, 24, 8, 20, 1500, 64),
+    (3, 6, 3, 700, 1100, 128), (38, 8, 8, 100, 130, 64)])
+@pytest.mark.parametrize("causal", [True, False])
+def test_items_taken_whole(B, H, Hkv, Nq, n, D, causal):
+    """More items than CTAs at a time, and fewer; requests of very different lengths."""
+    kv = [max(Nq if b % 3 else 0, n - 211 * b % n) for b in range(B)]
+    q = [Nq - 17 * b % (Nq + 1) for b in range(B)]
+    go(B=B, H=H, Hkv=Hkv, D=D, Nq=Nq, page=64, q_len=q, kv_len=kv, causal=causal, table_pad=0, seed=n)
+
+
 # A key head with so many query heads that a group of 128 rows holds one token,
 # or (over 128) not a whole one.
 @wide
