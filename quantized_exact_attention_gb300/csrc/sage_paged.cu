@@ -548,6 +548,10 @@ __global__ void __launch_bounds__(256) paged_join_kernel(const __grid_constant__
 //    tokens, T = 64, r = 0.8: 50.5 and 63.3; 128 items of 24 rows and up to
 //    4,000 keys, T = 32: 36.5 and 53.5; 16 x 16 heads of 1,024 tokens, r = 6.7:
 //    112 and 124, the start of every CTA.
+//    Requests of more than one group take two to an item, but one where whole
+//    items then run all at a time or have up to four tiles: 8 heads of 256 tokens
+//    11.6 and 9.3 us, 20 x 16 of 200 25.0 and 19.9; 32 of 2,048 tokens, which do
+//    not, 45.3 and 48.5.
 //    Up to 64 rows, of which two requests or more fill a group, the prefix may
 //    have items of its own in front of the requests', each for the rows of
 //    several requests.  That saves tiles and costs a join of all rows, about
@@ -580,6 +584,8 @@ struct Lists {
     int groups;                          // ... 128-row groups of an item
     int tok;                             // ... tokens of a group
     int nr;                              // few-rows kernel: 8-row groups of an item
+    bool whole;                          // ... a CTA takes an item
+    int split;                           // few-rows kernel: CTAs of the cluster that takes an item (0: a list)
     int M, rt, join;                     // M: rows of a partial result
     int64_t slots;
     // items of the prefix for the rows of all requests (many-rows kernel): in the same list when `tiles`
@@ -588,7 +594,35 @@ struct Lists {
     int64_t pre_slots;
 };
 
-Lists make_lists(int B, int Hkv, int G, int Nq, int D, int64_t pre_keys) {
+// CTAs of the many-rows kernel at a time: one per SM, of one row group two.
+int tile_workers(int sms, int groups) { return std::min(sms, kMaxTileWorkers) * (3 - groups); }
+
+// Whether the many-rows kernel gives each CTA an item of up to `tiles` tiles.
+bool whole_items(int64_t items, int64_t tiles, int groups, int workers) {
+    return 5 * items <= 13 * (int64_t)workers && tiles <= 16 * groups &&
+           tiles * groups * (2 * (int64_t)workers - items) <= 24 * (int64_t)workers;
+}
+
+// CTAs of a cluster that takes an item of up to `steps` steps whole; 0: the list.
+int whole_split(int64_t items, int64_t steps, int sms) {
+    int split = 0;
+    if (items > (int64_t)kWholeItems * sms) return 0;
+    int64_t least = kWholeSteps + 1;
+    // Clusters do not fill a GPU to the last SM: 304 CTAs in fours take 9.3 us
+    // where 152 in pairs take 5.8, 288 in fours 6.4.
+    for (int j = 0; j < 4 && (j == 0 || (items << j) * 10 <= 19 * sms); ++j) {
+        const int64_t cost = ceil_div(steps, kRowWarps << j) + (j > 0 ? j + 1 : 0);
+        if (cost < least) {
+            least = cost;
+            split = 1 << j;
+        }
+    }
+    return split;
+}
+
+// own_keys, pre_keys: by the table widths.  What a workspace has to hold does not
+// depend on own_keys or sms.
+Lists make_lists(int B, int Hkv, int G, int Nq, int D, int64_t own_keys, int64_t pre_keys, int sms) {
     Lists x{};
     const int64_t rows = (int64_t)Nq * G;
     x.tiles = rows > kFewRows && G <= 128;
@@ -615,10 +649,14 @@ Lists make_lists(int B, int Hkv, int G, int Nq, int D, int64_t pre_keys) {
             x.slots = (int64_t)B * Hkv + 2 * kMaxTileWorkers;
             return x;
         }
-        x.groups = Nq <= x.tok ? 1 : 2;
+        const int64_t tiles = ceil_div(own_keys, 128) + ceil_div(pre_keys, 128);
+        const int workers = tile_workers(sms, 1);
+        const int64_t items = (int64_t)B * Hkv * ceil_div(Nq, x.tok);      // of one group
+        x.groups = Nq <= x.tok || ((items <= workers || tiles <= 4) && whole_items(items, tiles, 1, workers)) ? 1 : 2;
         x.M = 128 * x.groups;
         x.rt = (int)ceil_div(Nq, x.tok * x.groups);
         x.join = pre_keys > 0;
+        x.whole = whole_items((int64_t)B * Hkv * x.rt, tiles, x.groups, tile_workers(sms, x.groups));
         x.slots = 2 * kMaxTileWorkers * (3 - x.groups);
         return x;
     }
@@ -627,30 +665,8 @@ Lists make_lists(int B, int Hkv, int G, int Nq, int D, int64_t pre_keys) {
     x.rt = (int)ceil_div(rows, x.M);
     x.slots = (int64_t)B * Hkv * x.rt + kMaxRowWorkers;
     x.join = pre_keys > 0 && !x.pre;
+    if (!x.pre) x.split = whole_split((int64_t)B * Hkv * x.rt, ceil_div(own_keys, kStep) + ceil_div(pre_keys, kStep), sms);
     return x;
-}
-
-// Whether the many-rows kernel gives each CTA an item of up to `tiles` tiles.
-bool whole_items(int64_t items, int64_t tiles, int groups, int workers) {
-    return 5 * items <= 13 * (int64_t)workers && tiles <= 16 * groups &&
-           tiles * groups * (2 * (int64_t)workers - items) <= 24 * (int64_t)workers;
-}
-
-// CTAs of a cluster that takes an item of up to `steps` steps whole; 0: the list.
-int whole_split(int64_t items, int64_t steps, int sms) {
-    int split = 0;
-    if (items > (int64_t)kWholeItems * sms) return 0;
-    int64_t least = kWholeSteps + 1;
-    // Clusters do not fill a GPU to the last SM: 304 CTAs in fours take 9.3 us
-    // where 152 in pairs take 5.8, 288 in fours 6.4.
-    for (int j = 0; j < 4 && (j == 0 || (items << j) * 10 <= 19 * sms); ++j) {
-        const int64_t cost = ceil_div(steps, kRowWarps << j) + (j > 0 ? j + 1 : 0);
-        if (cost < least) {
-            least = cost;
-            split = 1 << j;
-        }
-    }
-    return split;
 }
 
 // Each array of the workspace begins on 16 bytes.
@@ -720,8 +736,8 @@ int sage_paged_workspace(int B, int H, int Hkv, int Nq, int D, size_t* bytes) {
     const int rc = check_batch(B, H, Hkv, Nq, D);
     if (rc != SAGE_OK) return rc;
     // a prefix of any length may come: the form with a list of its own needs the most
-    *bytes = lists_bytes(make_lists(B, Hkv, H / Hkv, Nq, D, INT32_MAX), B, D);
-    const size_t alone = lists_bytes(make_lists(B, Hkv, H / Hkv, Nq, D, 0), B, D);
+    *bytes = lists_bytes(make_lists(B, Hkv, H / Hkv, Nq, D, 0, INT32_MAX, 0), B, D);
+    const size_t alone = lists_bytes(make_lists(B, Hkv, H / Hkv, Nq, D, 0, 0, 0), B, D);
     if (alone > *bytes) *bytes = alone;
     return SAGE_OK;
 }
@@ -748,7 +764,8 @@ int sage_attn_paged(const sage_tensor* q, const sage_tensor* o, const sage_page_
     const int64_t own_keys = (int64_t)table_width * cache->page_size;
     const int64_t pre_keys = (int64_t)prefix_width * cache->page_size;
     if (own_keys > INT32_MAX - 256 || pre_keys > INT32_MAX - 256) return SAGE_ERR_UNSUPPORTED;
-    const Lists x = make_lists(B, cache->heads, H / cache->heads, Nq, D, pre_keys);
+    const int sms = sm_count();
+    const Lists x = make_lists(B, cache->heads, H / cache->heads, Nq, D, own_keys, pre_keys, sms);
     if (workspace == nullptr || !aligned16(workspace) || workspace_bytes < lists_bytes(x, B, D)) return SAGE_ERR_ARG;
     // list positions and slot numbers stay in int
     const int tk = x.tiles ? 128 : kStep;
@@ -758,7 +775,6 @@ int sage_attn_paged(const sage_tensor* q, const sage_tensor* o, const sage_page_
 
     PagedParams p{};
     p.status = device_status_ptr();
-    const int sms = sm_count();
     if (p.status == nullptr || sms == 0) return SAGE_ERR_LAUNCH;
     CUtensorMap mq, mqp, mk, mv;
     if (x.tiles || x.pre) {
@@ -806,20 +822,15 @@ int sage_attn_paged(const sage_tensor* q, const sage_tensor* o, const sage_page_
     }
     if (x.tiles && !x.pre) p.cuts = reinterpret_cast<PagedCut*>(w);
     else p.start = reinterpret_cast<int32_t*>(w);
-    const int ctas = std::min(sms, kMaxTileWorkers);       // one per SM; of one row group: two
     p.pre_items_rt = x.pre_items_rt; p.pre_m = x.pre_M; p.pre_tok = x.pre_tok;
-    p.pre_workers = ctas * (3 - x.pre_groups);
+    p.pre_workers = tile_workers(sms, x.pre_groups);
+    p.whole = x.whole; p.split = x.split;
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
     cudaError_t e;
     int launches = 0;
     if (x.tiles) {
-        p.workers = ctas * (3 - x.groups);
+        p.workers = x.whole ? B * cache->heads * x.rt : tile_workers(sms, x.groups);
         if (x.pre) p.pre_rt = x.pre_items_rt;
-        const int64_t items = (int64_t)B * cache->heads * x.rt;
-        if (!x.pre && whole_items(items, ceil_div(own_keys, 128) + (x.join ? ceil_div(pre_keys, 128) : 0), x.groups, p.workers)) {
-            p.whole = 1;
-            p.workers = (int)items;
-        }
         e = launch_paged_tiles(p, D, x.groups, mq, mqp, mk, mv, s);
         if (e == cudaSuccess && x.pre) e = D == 64 ? launch_join<64, 128, 128>(p, s) : launch_join<128, 128, 128>(p, s);
         launches = p.whole ? 1 : 2;
@@ -833,9 +844,6 @@ int sage_attn_paged(const sage_tensor* q, const sage_tensor* o, const sage_page_
             p.beside = 1;
         }
         p.workers = std::min(2 * sms, kMaxRowWorkers / kRowWarps) * kRowWarps;
-        if (!x.pre)
-            p.split = whole_split((int64_t)B * cache->heads * x.rt,
-                                  ceil_div(own_keys, kStep) + (x.join ? ceil_div(pre_keys, kStep) : 0), sms);
         e = launch_rows(p, D, x.nr, s);
         launches += p.split > 0 ? 1 : 2;
     }
