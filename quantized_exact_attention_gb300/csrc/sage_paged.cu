@@ -563,8 +563,9 @@ __global__ void __launch_bounds__(256) paged_join_kernel(const __grid_constant__
 //  - rows <= 16: the few-rows kernel, each request's keys behind the prefix
 //    while reading the prefix again for every request costs less than a list
 //    of its own, which the many-rows kernel then reads once for all rows: 64
-//    requests, 8 key heads, 512 shared keys (134 MB read again) take 36 us so
-//    and 43 with a list, 2,048 keys (537 MB) 66 and 52.
+//    requests, 8 key heads, 512 shared keys (134 MB read again) take 35 us so
+//    and 43 with a list, 1,024 keys (268 MB) 44 and 43, 2,048 keys 64 and 44; 16
+//    requests, 4,096 keys (268 MB) 32 and 23.
 //    Without a list of its own: up to four items an SM take a cluster each when
 //    the table widths bound a warp's share to 12 steps, a cluster of 2, 4 or 8
 //    CTAs counted as 2, 3 or 4 steps more.  A cluster does not even out the
@@ -574,7 +575,7 @@ __global__ void __launch_bounds__(256) paged_join_kernel(const __grid_constant__
 //    items an SM of 30 keys: 13.3 us, from a list 9.5; four 7.4 and 8.3.
 // ---------------------------------------------------------------------------
 constexpr int kFewRows = 16;
-constexpr int64_t kReadAgain = int64_t(256) << 20;        // bytes of prefix read again that cost as much as its list
+constexpr int64_t kReadAgain = int64_t(128) << 20;        // bytes of prefix read again that cost as much as its list
 constexpr int kWholeSteps = 12, kWholeItems = 4;          // few-rows kernel: a cluster takes an item up to these
 constexpr double kOwnList = 12e6, kRowJoin = 6e3;         // many-rows kernel: ... as much as joining all rows, and one row
 

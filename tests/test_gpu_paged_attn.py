@@ -93,7 +93,7 @@ def test_shared_prefix(prefix, B, Nq, G, D, wide):
        **pad(wide))
 
 
-# A prefix whose repeated reading would cost over 256 MB is read once for all
+# A prefix whose repeated reading would cost over 134 MB is read once for all
 # rows: few rows, one and two groups of 128 rows, a last group that is not full.
 @pytest.mark.parametrize("B,Hkv,G,Nq,D,prefix", [
     (40, 8, 1, 1, 128, 1700), (70, 4, 8, 1, 64, 4001), (33, 8, 2, 3, 128, 2100), (300, 2, 4, 2, 64, 2000),
