@@ -146,7 +146,7 @@ __global__ void __launch_bounds__(kRowWarps * 32, 2) paged_rows_kernel(const __g
         worker = warp * gridDim.x + blockIdx.x;
         const int total = paged_scan<M, kStep, false, kRowWarps * 32, kRowWarps>(sched, blockIdx.x, gridDim.x, found,
                                                                                  warp_sums, blockIdx.x == 0);
-        const int per = sched.share(total, p.workers), t0 = min(worker * per, total);
+        const int per = sched.share(total, p.workers, p.B * p.rt * p.Hkv), t0 = min(worker * per, total);
         t1 = min(t0 + per, total);
         at.pos = t1;
         if (t0 < t1) at = paged_place(sched, found[warp], t0);
@@ -432,7 +432,7 @@ __global__ void __launch_bounds__(256) paged_join_kernel(const __grid_constant__
 #pragma unroll
     for (int v = 0; v < V; ++v) acc[v] = 0.f;
     if (live) {
-        const int per = s.share(__ldcg(p.start + p.B * p.rt), p.workers);
+        const int per = s.share(__ldcg(p.start + p.B * p.rt), p.workers, p.B * p.rt * p.Hkv);
         const int nt = s.item_tiles(n, len, rt), pair = b * p.rt + rt;
         const RowParts own = parts_of(__ldcg(p.start + pair) + h * s.places(nt) + s.kItemCost, nt, per, pair * p.Hkv + h);
         const int64_t own_q = own.slot0 * p.part_m + (r - rt * M);
@@ -446,7 +446,7 @@ __global__ void __launch_bounds__(256) paged_join_kernel(const __grid_constant__
             const int it = set * p.Hkv + h;
             // ... in the same list, or in one of its own
             const int pre_per = kTiles ? per
-                                : Tiles::share(p.Hkv * p.pre_items_rt * Tiles::places(pt), p.pre_workers);
+                                : Tiles::share(p.Hkv * p.pre_items_rt * Tiles::places(pt), p.pre_workers, 0);
             pre = parts_of(it * Tiles::places(pt) + Tiles::kItemCost, pt, pre_per, it);
             pre_q = pre.slot0 * p.pre_m + place;
         }

@@ -10,11 +10,15 @@
 // Each item takes as many places in the list as it has tiles, and kItemCost in
 // front of them, which stand for what an item costs a worker besides its tiles
 // (fetching its rows, writing its output).  The places are cut into equal
-// runs, one for each worker (a warp or a CTA), of kItemCost places at least: a
-// shorter run costs more at its ends than it saves (64 requests behind 2,048
-// shared keys, runs of 1 place: 51 us, 3: 43.7, 6: 46.4).  So the split follows the lengths that the
-// device holds: a long sequence is shared among many workers, several short
-// ones fall to a single worker, and no host value depends on the lengths.
+// runs, one for each worker (a warp or a CTA).  So the split follows the lengths
+// that the device holds: a long sequence is shared among many workers, several
+// short ones fall to a single worker, and no host value depends on the lengths.
+// Runs have a least length.  Tiles: kItemCost, as a shorter run costs more at
+// its ends than it saves (64 requests behind 2,048 shared keys, runs of 1 place:
+// 51 us, 3: 43.7, 6: 46.4).  Few rows: a run of r places of an item of T takes r
+// steps and leaves T / r parts to join, which is least at r = sqrt(kPartCost T)
+// (one key head, 12,000 keys, 1 place: 21.3 us, 6: 12.0; 40,000 keys, 3: 24.4,
+// 8: 17.7; but items of 2 steps, 1: 9.6, 6: 11.4).
 // A worker leaves a partial result (running maximum, sum and unnormalised
 // output) for an item it shares, in slot worker + item (the prefix's items and
 // the others are numbered and kept apart): along the list either the worker or
@@ -47,6 +51,7 @@ template <int M, int TK, bool kPre>
 struct PagedSched {
     static constexpr bool kTiles = TK == 128;
     static constexpr int kItemCost = kTiles ? 3 : 1;
+    static constexpr float kPartCost = 0.04f;             // joining a part, in places
     const PagedParams& p;
     int lp;                              // prefix length
     __device__ explicit PagedSched(const PagedParams& pp) : p(pp) {
@@ -57,8 +62,11 @@ struct PagedSched {
     __device__ int pre_tiles() const { return (lp + TK - 1) / TK; }
     // places of an item of nt tiles
     __device__ static int places(int nt) { return nt > 0 ? nt + kItemCost : 0; }
-    // places of each of `workers` runs of a list of `total`
-    __device__ static int share(int total, int workers) { return max(kItemCost, (total + workers - 1) / workers); }
+    // Places of each of `workers` runs of a list of `total` places, `items` items.
+    __device__ static int share(int total, int workers, int items) {
+        const int least = kTiles ? kItemCost : 1 + (int)sqrtf(kPartCost * (float)total / (float)items);
+        return max(least, (total + workers - 1) / workers);
+    }
     __device__ int pre_total() const { return kPre ? p.pre_rt * p.Hkv * places(pre_tiles()) : 0; }
     // Tiles of row set rt of a request with n query tokens and len own keys.
     __device__ int item_tiles(int n, int len, int rt) const {
@@ -120,7 +128,7 @@ __device__ __forceinline__ int paged_scan(const PagedSched<M, TK, kPre>& s, int 
         total += red[i];
     }
     base += inc - mine;
-    const int per = s.share(total, p.workers);
+    const int per = s.share(total, p.workers, pairs * p.Hkv);
     int b = b0, rt = u0 - b0 * p.rt;
 #pragma unroll 1
     for (int u = u0; u < u1; ++u) {

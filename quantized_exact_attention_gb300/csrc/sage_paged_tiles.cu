@@ -241,7 +241,7 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
     } else {
         const int total = paged_scan<M, 128, kPre, L::kThreads, 1>(sched, worker, 0, found, red,      // ends with a barrier
                                                                    kPre && worker == 0 && p.start != nullptr);
-        per = sched.share(total, p.workers);
+        per = sched.share(total, p.workers, 0);
         t0 = min(worker * per, total);
         t1 = min(t0 + per, total);
     }
