@@ -388,11 +388,13 @@ int sage_paged_workspace(int B, int H, int Hkv, int Nq, int D, size_t* bytes);
  *            the same workspace must be ordered.
  * Lengths, tables and prefix are read on the device, so a captured call
  * serves later lengths; make the first call on a device before any capture.
+ * The widths bound the lengths on the host and choose between kernels: rows no
+ * wider than the requests may grow are served faster.
  * Cache rows behind a length are never used, whatever they hold; the rows
  * within the lengths must be finite, hidden ones included.  Scores, maxima,
  * sums and the output up to its last rounding are FP32, the weights are
  * rounded to BF16 for the product with the values.  Results do not depend on the workspace or on earlier
- * calls: equal inputs give equal bits on the same device. */
+ * calls: equal inputs and widths give equal bits on the same device. */
 int sage_attn_paged(const sage_tensor* q, const sage_tensor* o, const sage_page_cache* cache, int B, int H, int Nq,
                     const int32_t* q_len, const int32_t* table, int64_t table_stride, int table_width,
                     const int32_t* kv_len, const int32_t* prefix_table, int prefix_width, const int32_t* prefix_len,

@@ -356,8 +356,8 @@ def test_waits_for_what_the_stream_waits_for():
 def test_a_withheld_copy_times_out_and_the_context_survives():
     """The many-rows kernel's bounded waits, on a few CTAs (about a second each)."""
     G.ensure_built()
-    for D, Nq in ((128, 40), (64, 40), (128, 300), (64, 300)):
-        p = P.make(B=1, H=2, Hkv=1, D=D, Nq=Nq, page=64, kv_len=[Nq + 100], seed=D)
+    for D, Nq, list_ in ((128, 40, 0), (64, 40, 1), (128, 300, 1), (64, 300, 0)):
+        p = P.make(B=1, H=2, Hkv=1, D=D, Nq=Nq, page=64, kv_len=[Nq + 100], seed=D, **pad(list_))
         S.sage_debug_inject_fault(1)
         P.run(p)
         torch.cuda.synchronize()
