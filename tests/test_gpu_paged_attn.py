@@ -309,6 +309,33 @@ def test_two_streams_with_their_own_workspaces():
         P.check(p, o)
 
 
+def test_every_form_at_once():
+    """Calls of all forms in flight together, each on its own stream, over and over."""
+    G.ensure_built()
+    shapes = [dict(B=3, Nq=300, kv=700, prefix=0, pad=2), dict(B=3, Nq=300, kv=700, prefix=130, pad=1200),
+              dict(B=4, Nq=40, kv=500, prefix=0, pad=2), dict(B=30, Nq=5, kv=90, prefix=4700, pad=2),
+              dict(B=6, Nq=1, kv=900, prefix=0, pad=2), dict(B=6, Nq=1, kv=900, prefix=50, pad=1200),
+              dict(B=60, Nq=1, kv=90, prefix=4700, pad=2)]
+    H, Hkv, D = 8, 2, 128
+    calls = []
+    for x in shapes:
+        p = P.make(B=x["B"], H=H, Hkv=Hkv, D=D, Nq=x["Nq"], page=16, prefix=x["prefix"], table_pad=x["pad"],
+                   kv_len=[x["Nq"] + (x["kv"] - 31 * b) % x["kv"] for b in range(x["B"])], seed=x["kv"])
+        want = P.run(p).clone()
+        calls.append((p, want, S.alloc_paged_workspace(x["B"], H, Hkv, x["Nq"], D), torch.zeros_like(want),
+                      torch.tensor(p.kv_len, dtype=torch.int32, device="cuda"),
+                      torch.tensor([x["prefix"]], dtype=torch.int32, device="cuda"), torch.cuda.Stream()))
+    torch.cuda.synchronize()
+    for _ in range(15):
+        for p, _, ws, o, n, pre, s in calls:
+            S.sage_attn_paged(p.q, o, S.PageCache(p.cache_k, p.cache_v), p.table, ws, kv_len=n,
+                              prefix_table=p.prefix_table, prefix_len=pre if p.prefix_table is not None else None, stream=s)
+    torch.cuda.synchronize()
+    assert S.sage_get_device_status() == S.SAGE_OK
+    for _, want, _, o, _, _, _ in calls:
+        assert torch.equal(o, want)
+
+
 def test_padding_rows_of_q_and_stale_outputs_do_not_matter():
     """NaN in the query rows behind q_len, and in the output before the call."""
     G.ensure_built()
