@@ -102,6 +102,7 @@ __device__ __forceinline__ void record_page(const PagedParams& p, int page) {
 // A step as the loading side leaves it for the computing side.
 struct StepNote {
     int b, h, rt, item;                  // of its item
+    int n, len;                          // the request's query tokens and own keys
     int key0, nkeys;
     int own, first;                      // own keys; first step of its item in this warp
 };
@@ -120,7 +121,8 @@ __global__ void __launch_bounds__(kRowWarps * 32, 2) paged_rows_kernel(const __g
     static_assert(M * kPartRow * 4 <= S * Sh::kStage && (S * Sh::kStage) % 16 == 0);
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    if (!p.beside) pdl_wait();
+    if (!kWhole && p.beside) fence_before_early_loads();
+    else pdl_wait();
     pdl_trigger();
     const PagedSched<M, kStep, false> sched(p);
     int worker, t1;                                       // this worker, the end of its run of places
@@ -165,7 +167,7 @@ __global__ void __launch_bounds__(kRowWarps * 32, 2) paged_rows_kernel(const __g
     auto fetch = [&]() {
         span = paged_span(sched, at.b, at.len, at.tile);
         const int j = span.key0 >> p.page_shift;
-        page = span.own ? __ldg(p.table + (int64_t)at.b * p.table_stride + j) : __ldg(p.ptable + j);
+        page = span.own ? p.table[(int64_t)at.b * p.table_stride + j] : p.ptable[j];
     };
     auto issue = [&](int stage) {
         const bool ok = (unsigned)page < (unsigned)p.num_pages;
@@ -188,6 +190,7 @@ __global__ void __launch_bounds__(kRowWarps * 32, 2) paged_rows_kernel(const __g
         if (lane == 0) {
             StepNote& nt = notes[warp][stage];
             nt.b = at.b; nt.h = at.h; nt.rt = at.rt; nt.item = at.item;
+            nt.n = at.n; nt.len = at.len;
             nt.key0 = span.key0; nt.nkeys = span.nkeys;
             nt.own = span.own; nt.first = first;
         }
@@ -210,12 +213,11 @@ __global__ void __launch_bounds__(kRowWarps * 32, 2) paged_rows_kernel(const __g
     float o[NR][D / 16][4];                               // O^T: channels x query rows
     float m[NR][2], l[NR][2];                             // of the two query rows this lane's columns are
     int lim[NR][2];                                       // own keys each of them sees
-    int item = -1, ib = 0, ih = 0, irt = 0;               // the item these belong to
+    int item = -1, ib = 0, ih = 0, irt = 0, tokens = 0;   // the item these belong to, its request's query tokens
 
     // Leave the item's partial result.
     auto leave = [&]() {
         const int64_t slot = (int64_t)worker + item;
-        const int n = sched.q_rows(ib);
 #pragma unroll
         for (int nr = 0; nr < NR; ++nr) {
 #pragma unroll
@@ -231,7 +233,7 @@ __global__ void __launch_bounds__(kRowWarps * 32, 2) paged_rows_kernel(const __g
                     if (lane < 4) part_ml[warp][r] = make_float2(m[nr][e], s);
                     dst = reinterpret_cast<float*>(smem + warp * S * Sh::kStage) + r * kPartRow + (lane >> 2);
                 } else {
-                    if (!paged_row(sched, ib, ih, irt, n, r, b, i, hq)) continue;
+                    if (!paged_row(sched, ib, ih, irt, tokens, r, b, i, hq)) continue;
                     if (lane < 4) p.part_ml[slot * M + r] = make_float2(m[nr][e], s);
                     dst = p.part_o + (slot * M + r) * D + (lane >> 2);
                 }
@@ -245,7 +247,8 @@ __global__ void __launch_bounds__(kRowWarps * 32, 2) paged_rows_kernel(const __g
     };
     auto enter = [&](const StepNote& nt) {
         item = nt.item; ib = nt.b; ih = nt.h; irt = nt.rt;
-        const int n = sched.q_rows(ib), len = sched.own_keys(ib);
+        const int n = nt.n, len = nt.len;
+        tokens = n;
 #pragma unroll
         for (int nr = 0; nr < NR; ++nr) {
             int b, i, hq;
@@ -253,8 +256,8 @@ __global__ void __launch_bounds__(kRowWarps * 32, 2) paged_rows_kernel(const __g
             const uint16_t* qp = p.q + (in ? b * p.qsb + hq * p.qsh + i * p.qsn : 0) + (lane & 3) * 2;
 #pragma unroll
             for (int j = 0; j < D / 16; ++j) {
-                qf[nr][j][0] = in ? __ldg(reinterpret_cast<const uint32_t*>(qp + j * 16)) : 0u;
-                qf[nr][j][1] = in ? __ldg(reinterpret_cast<const uint32_t*>(qp + j * 16 + 8)) : 0u;
+                qf[nr][j][0] = in ? *reinterpret_cast<const uint32_t*>(qp + j * 16) : 0u;
+                qf[nr][j][1] = in ? *reinterpret_cast<const uint32_t*>(qp + j * 16 + 8) : 0u;
 #pragma unroll
                 for (int e = 0; e < 4; ++e) o[nr][j][e] = 0.f;
             }
@@ -420,7 +423,7 @@ __global__ void __launch_bounds__(256) paged_join_kernel(const __grid_constant__
     const int row = (int)blockIdx.x * (8 / WPR) + warp / WPR, sub = warp % WPR;
     const int b = blockIdx.y;
     constexpr bool kTiles = TK == 128;                     // a list of the many-rows kernel, the prefix's items in it
-    const PagedSched<M, TK, kTiles> s(p);
+    const PagedSched<M, TK, kTiles> s(p, true);
     const int hq = row / p.Nq, i = row - hq * p.Nq;
     const int n = s.q_rows(b), len = s.own_keys(b);
     const bool live = hq < p.H && i < n;
@@ -432,9 +435,9 @@ __global__ void __launch_bounds__(256) paged_join_kernel(const __grid_constant__
 #pragma unroll
     for (int v = 0; v < V; ++v) acc[v] = 0.f;
     if (live) {
-        const int per = s.share(__ldcg(p.start + p.B * p.rt), p.workers, p.B * p.rt * p.Hkv);
+        const int per = s.share(p.start[p.B * p.rt], p.workers, p.B * p.rt * p.Hkv);
         const int nt = s.item_tiles(n, len, rt), pair = b * p.rt + rt;
-        const RowParts own = parts_of(__ldcg(p.start + pair) + h * s.places(nt) + s.kItemCost, nt, per, pair * p.Hkv + h);
+        const RowParts own = parts_of(p.start[pair] + h * s.places(nt) + s.kItemCost, nt, per, pair * p.Hkv + h);
         const int64_t own_q = own.slot0 * p.part_m + (r - rt * M);
         RowParts pre{0, 0};
         int64_t pre_q = 0;
@@ -464,13 +467,13 @@ __global__ void __launch_bounds__(256) paged_join_kernel(const __grid_constant__
                 if (x < parts) {
                     const bool from_pre = x < pre.n;
                     const int64_t q = from_pre ? pre_q + (int64_t)x * p.pre_m : own_q + (int64_t)(x - pre.n) * p.part_m;
-                    ml[k] = __ldcg((from_pre ? p.pre_ml : p.part_ml) + q);
+                    ml[k] = (from_pre ? p.pre_ml : p.part_ml)[q];
                     const float* po = (from_pre ? p.pre_o : p.part_o) + q * D + lane * V;
                     if (V == 4) {
-                        const float4 y = __ldcg(reinterpret_cast<const float4*>(po));
+                        const float4 y = *reinterpret_cast<const float4*>(po);
                         w[k][0] = y.x; w[k][1] = y.y; w[k][V - 2] = y.z; w[k][V - 1] = y.w;
                     } else {
-                        const float2 y = __ldcg(reinterpret_cast<const float2*>(po));
+                        const float2 y = *reinterpret_cast<const float2*>(po);
                         w[k][0] = y.x; w[k][1] = y.y;
                     }
                 }

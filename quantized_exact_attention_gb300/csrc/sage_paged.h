@@ -108,6 +108,21 @@ int check_page_cache(const sage_page_cache* c);
 __device__ __forceinline__ void pdl_trigger() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
+// Loads of what an earlier kernel of the stream may have written (lengths,
+// tables, slots, new rows, partial results).  This kernel's life begins before
+// that one ends, so they are not __ldg's, which is for data that nothing writes
+// while the kernel lives; and the compiler may move __ldg and __ldcg above
+// pdl_wait.  A plain load stays behind it, and sees all that was waited for.
+// A kernel may read before its own pdl_wait what was complete when the kernel
+// before it, which waited, let it start.  Such values are in L2, but nothing has
+// emptied this SM's L1 since: either a fence does first, or the load goes past it.
+__device__ __forceinline__ void fence_before_early_loads() { asm volatile("fence.acq_rel.gpu;" ::: "memory"); }
+__device__ __forceinline__ int ld_gpu(const int32_t* a) {
+    int v;
+    asm volatile("ld.relaxed.gpu.global.s32 %0, [%1];" : "=r"(v) : "l"(a) : "memory");
+    return v;
+}
+
 // Launch a kernel this way.  The kernels of an attention call ask for the same
 // split of an SM's memory (`max_shared`, set once per device): an SM drains
 // before it changes the split (a short decode call: 10.4 us, with the same

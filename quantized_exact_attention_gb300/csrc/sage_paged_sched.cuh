@@ -35,9 +35,9 @@
 
 namespace sage {
 
-__device__ __forceinline__ int paged_clamp(const int32_t* lens, int b, int n) {
+__device__ __forceinline__ int paged_clamp(const int32_t* lens, int b, int n, bool early) {
     if (lens == nullptr) return n;
-    const int v = __ldg(lens + b);
+    const int v = early ? ld_gpu(lens + b) : lens[b];
     return v < 0 ? 0 : (v > n ? n : v);
 }
 
@@ -53,12 +53,13 @@ struct PagedSched {
     static constexpr int kItemCost = kTiles ? 3 : 1;
     static constexpr float kPartCost = 0.04f;             // joining a part, in places
     const PagedParams& p;
+    bool early;                          // the lengths are read before the kernel's own pdl_wait, without a fence
     int lp;                              // prefix length
-    __device__ explicit PagedSched(const PagedParams& pp) : p(pp) {
-        lp = p.Wp > 0 ? paged_clamp(p.prefix_len, 0, p.Wp * p.page) : 0;
+    __device__ explicit PagedSched(const PagedParams& pp, bool before_wait = false) : p(pp), early(before_wait) {
+        lp = p.Wp > 0 ? paged_clamp(p.prefix_len, 0, p.Wp * p.page, early) : 0;
     }
-    __device__ int q_rows(int b) const { return paged_clamp(p.q_len, b, p.Nq); }
-    __device__ int own_keys(int b) const { return paged_clamp(p.kv_len, b, p.W * p.page); }
+    __device__ int q_rows(int b) const { return paged_clamp(p.q_len, b, p.Nq, early); }
+    __device__ int own_keys(int b) const { return paged_clamp(p.kv_len, b, p.W * p.page, early); }
     __device__ int pre_tiles() const { return (lp + TK - 1) / TK; }
     // places of an item of nt tiles
     __device__ static int places(int nt) { return nt > 0 ? nt + kItemCost : 0; }

@@ -470,7 +470,7 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
             page = 0;
             if (lane < per_tile && (lane << p.page_shift) < span.nkeys) {
                 const int j = (span.key0 >> p.page_shift) + lane;
-                page = span.own ? __ldg(p.table + (int64_t)at.b * p.table_stride + j) : __ldg(p.ptable + j);
+                page = span.own ? p.table[(int64_t)at.b * p.table_stride + j] : p.ptable[j];
             }
         };
         if (at.pos < t1) look_up();
@@ -689,13 +689,13 @@ __global__ void __launch_bounds__(256) paged_cuts_kernel(const __grid_constant__
 #pragma unroll
                 for (int v = 0; v < V; ++v) y[f][v] = 0.f;
                 if (j < cut.parts) {
-                    ml[f] = __ldcg(p.part_ml + q);
+                    ml[f] = p.part_ml[q];
                     const float* src = p.part_o + q * D + lane * V;
                     if constexpr (V == 4) {
-                        const float4 x = __ldcg(reinterpret_cast<const float4*>(src));
+                        const float4 x = *reinterpret_cast<const float4*>(src);
                         y[f][0] = x.x; y[f][1] = x.y; y[f][2] = x.z; y[f][3] = x.w;
                     } else {
-                        const float2 x = __ldcg(reinterpret_cast<const float2*>(src));
+                        const float2 x = *reinterpret_cast<const float2*>(src);
                         y[f][0] = x.x; y[f][1] = x.y;
                     }
                 }

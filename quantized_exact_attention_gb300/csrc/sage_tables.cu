@@ -42,7 +42,7 @@ __device__ __forceinline__ Held held(const TableParams& p, int o, int n) {
     return x;
 }
 __device__ __forceinline__ Held held(const TableParams& p, int b) {
-    return held(p, p.old_len == nullptr ? 0 : __ldg(p.old_len + b), __ldg(p.new_len + b));
+    return held(p, p.old_len == nullptr ? 0 : p.old_len[b], p.new_len[b]);
 }
 
 constexpr int kTableThreads = 256;
@@ -66,8 +66,8 @@ __global__ void __launch_bounds__(kTableThreads, 8) page_tables_kernel(const __g
         quads = b0 & ~3;
 #pragma unroll 2
         for (int b = 4 * (int)threadIdx.x; b < quads; b += 4 * kTableThreads) {
-            const int4 n = __ldg(reinterpret_cast<const int4*>(p.new_len + b));
-            const int4 o = p.old_len == nullptr ? make_int4(0, 0, 0, 0) : __ldg(reinterpret_cast<const int4*>(p.old_len + b));
+            const int4 n = *reinterpret_cast<const int4*>(p.new_len + b);
+            const int4 o = p.old_len == nullptr ? make_int4(0, 0, 0, 0) : *reinterpret_cast<const int4*>(p.old_len + b);
             const int nn[4] = {n.x, n.y, n.z, n.w}, oo[4] = {o.x, o.y, o.z, o.w};
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
@@ -95,7 +95,7 @@ __global__ void __launch_bounds__(kTableThreads, 8) page_tables_kernel(const __g
         auto entry = [&](int j) -> int {
             if (j < x.old_pages) return row[j];
             const int f = first + (j - x.old_pages);
-            return j < x.new_pages && f < p.n_free ? __ldg(p.free_pages + f) : -1;
+            return j < x.new_pages && f < p.n_free ? p.free_pages[f] : -1;
         };
         // first slot of a page; -1 for none, or when its slots pass 2^31 - 1
         auto slots_of = [&](int pg) -> int {
@@ -173,7 +173,7 @@ __global__ void __launch_bounds__(kAppendThreads, 4) cache_append_kernel(const _
     const int64_t t = (int64_t)blockIdx.x * (kAppendThreads / 32) + (threadIdx.x >> 5);
     if (t >= p.tokens) return;
     const int b = (int)((uint32_t)t / (uint32_t)p.N), i = (int)t - b * p.N;
-    const int slot = __ldg(p.slots + b * p.slots_stride + i);
+    const int slot = p.slots[b * p.slots_stride + i];
     if (slot < 0) return;
     if (slot >= p.capacity) {
         if (lane == 0 && atomicCAS(p.status, 0, kErrPage) == 0) p.status[3] = slot >> p.page_shift;
@@ -185,13 +185,26 @@ __global__ void __launch_bounds__(kAppendThreads, 4) cache_append_kernel(const _
     const uint16_t* v = p.v + b * p.vsb + i * p.vsn;
     uint16_t* ck = p.ck + pg * p.ckp + off * p.ckt;
     uint16_t* cv = p.cv + pg * p.cvp + off * p.cvt;
-#pragma unroll 4
-    for (int c = lane; c < chunks; c += 32) {
-        const int h = c >> p.chunk_shift, x = (c - (h << p.chunk_shift)) * 8;
-        const uint4 a = __ldg(reinterpret_cast<const uint4*>(k + h * p.ksh + x));
-        const uint4 d = __ldg(reinterpret_cast<const uint4*>(v + h * p.vsh + x));
-        *reinterpret_cast<uint4*>(ck + h * p.ckh + x) = a;
-        *reinterpret_cast<uint4*>(cv + h * p.cvh + x) = d;
+    constexpr int kFlight = 4;                             // chunks of a lane whose loads precede their stores
+#pragma unroll 1
+    for (int c0 = lane; c0 < chunks; c0 += 32 * kFlight) {
+        uint4 a[kFlight], d[kFlight];
+#pragma unroll
+        for (int u = 0; u < kFlight; ++u) {
+            const int c = c0 + 32 * u, h = c >> p.chunk_shift, x = (c - (h << p.chunk_shift)) * 8;
+            if (c < chunks) {
+                a[u] = *reinterpret_cast<const uint4*>(k + h * p.ksh + x);
+                d[u] = *reinterpret_cast<const uint4*>(v + h * p.vsh + x);
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < kFlight; ++u) {
+            const int c = c0 + 32 * u, h = c >> p.chunk_shift, x = (c - (h << p.chunk_shift)) * 8;
+            if (c < chunks) {
+                *reinterpret_cast<uint4*>(ck + h * p.ckh + x) = a[u];
+                *reinterpret_cast<uint4*>(cv + h * p.cvh + x) = d[u];
+            }
+        }
     }
 }
 

@@ -140,3 +140,80 @@ def test_a_decode_step_captured_whole():
                      (eager.o, whole.o), (eager.cache.k, whole.cache.k), (eager.cache.v, whole.cache.v)):
             assert torch.equal(a, b)
     assert int(eager.o.count_nonzero()) > 0
+
+
+@pytest.mark.parametrize("B,H,Hkv,D,Nq,keys,prefix,pad", [
+    (4, 8, 2, 128, 1, 300, 0, 0),                          # clusters
+    (4, 8, 2, 128, 1, 300, 60, 1200),                      # few rows from a list
+    (40, 16, 8, 128, 1, 60, 1000, 2),                      # ... beside the prefix's list
+    (30, 8, 2, 128, 5, 90, 4300, 2),                       # the prefix's items and the requests' in one list
+    (3, 4, 2, 64, 40, 500, 0, 2),                          # many rows, whole items
+    (3, 4, 2, 128, 300, 700, 130, 1200)])                  # ... from a list
+def test_steps_in_flight(B, H, Hkv, D, Nq, keys, prefix, pad):
+    """Steps that rebuild the tables from another order of the pages and write
+    every key again, one table, slot map, cache and workspace for all of them:
+    enqueued without a wait between them, and as one graph replayed at once, they
+    leave what they leave one by one."""
+    G.ensure_built()
+    page, steps = 16, 10
+    r, g = random.Random(B), torch.Generator(device="cuda").manual_seed(B)
+    i32 = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")  # noqa: E731
+    randn = lambda *s: torch.randn(s, device="cuda", generator=g).to(torch.bfloat16)  # noqa: E731
+    N, wp = Nq + keys, -(-prefix // page)
+    W = -(-N // page) + pad
+    n_pages = wp + B * -(-N // page) + 3
+    lens = [[Nq + r.randrange(keys + 1) for _ in range(B)] for _ in range(steps)]
+    new = [i32(x) for x in lens]
+    order = [torch.randperm(n_pages, device="cuda", generator=g).to(torch.int32) for _ in range(steps)]
+    q, k, v = ([randn(B, h, n, D) for _ in range(steps)] for h, n in ((H, Nq), (Hkv, N), (Hkv, N)))
+    pk, pv = ([randn(1, Hkv, max(prefix, 1), D) for _ in range(steps)] for _ in range(2))
+    plen = i32([prefix])
+    cache = S.alloc_page_cache(n_pages, page, Hkv, D)
+    ws = S.alloc_paged_workspace(B, H, Hkv, Nq, D)
+    table, slots = (torch.empty((B, n), dtype=torch.int32, device="cuda") for n in (W, N))
+    ptable, pslots = (torch.empty((1, max(n, 1)), dtype=torch.int32, device="cuda") for n in (wp, prefix))
+    taken, ptaken = (torch.empty(1, dtype=torch.int32, device="cuda") for _ in range(2))
+    o = [torch.empty((B, Nq, H, D), dtype=torch.bfloat16, device="cuda").permute(0, 2, 1, 3) for _ in range(steps)]
+
+    def step(n):
+        if prefix:
+            S.sage_page_tables(plen, page, order[n][:wp], ptable, pslots, ptaken)
+            S.sage_cache_append(pk[n], pv[n], pslots, cache)
+        S.sage_page_tables(new[n], page, order[n][wp:], table, slots, taken)
+        S.sage_cache_append(k[n], v[n], slots, cache)
+        S.sage_attn_paged(q[n], o[n], cache, table, ws, kv_len=new[n], prefix_table=ptable[0] if prefix else None,
+                          prefix_len=plen if prefix else None)
+
+    def reset():
+        for t in (table, slots, ptable, pslots, taken, *o):
+            t.fill_(0)
+        for t in (cache.k, cache.v):
+            t.fill_(float("nan"))
+        torch.cuda.synchronize()
+
+    def left():
+        torch.cuda.synchronize()
+        assert S.sage_get_device_status() == S.SAGE_OK
+        return [t.clone().view(torch.int16) for t in (*o, cache.k.contiguous(), cache.v.contiguous())] + [
+            t.clone() for t in (table, slots, taken)]
+
+    reset()
+    for n in range(steps):
+        step(n)
+        P.check(P.Paged(q[n], cache.k, cache.v, table, [Nq] * B, lens[n], ptable[0] if prefix else None, prefix, True), o[n])
+    want = left()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        for n in range(steps):
+            step(n)
+    for _ in range(3):
+        reset()
+        for n in range(steps):
+            step(n)
+        assert all(torch.equal(a, b) for a, b in zip(left(), want))
+        reset()
+        graph.replay()
+        assert all(torch.equal(a, b) for a, b in zip(left(), want))
+    for _ in range(4):                                     # replays behind one another
+        graph.replay()
+    assert all(torch.equal(a, b) for a, b in zip(left()[:steps], want))
