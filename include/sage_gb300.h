@@ -383,6 +383,14 @@ int sage_paged_workspace(int B, int H, int Hkv, int Nq, int D, size_t* bytes);
  *            listed page outside the cache reads as zeros and is recorded as
  *            SAGE_ERR_PAGE in the device status.
  *  sm_scale <= 0 selects 1/sqrt(D).
+ *  Widths: a table's tokens stay below 2^31 - 256, and a call's work, by the
+ *            widths, below 2^30 tiles: B * heads * sets * (tokens / t + 6), with
+ *            heads = cache->heads, tokens = (table_width + prefix_width) *
+ *            page_size, and for up to 16 query rows to a key head (Nq * H /
+ *            heads) t = 16 and one set, for more t = 128 and a set for each 128
+ *            or 256 rows.  SAGE_ERR_UNSUPPORTED beyond, whatever the lengths on
+ *            the device are: 511 requests of one token, 32 key heads, tables of
+ *            2^20 tokens are served, 512 are not.
  *  workspace : device scratch of at least sage_paged_workspace bytes, 16-byte
  *            aligned, whose contents do not matter before or after.  Calls on
  *            the same workspace must be ordered.

@@ -420,3 +420,20 @@ def test_convenience_call_and_launch_count():
     s.synchronize()
     assert 1 <= S.sage_last_launch_count() <= 3
     P.check(p, o)
+
+
+@pytest.mark.parametrize("D", [64, 128])
+def test_the_widest_tables(D):
+    """9 (B * heads) * (tokens / 16 + 6) tiles just below 2^30 are served, one page more is refused."""
+    G.ensure_built()
+    B, page, W = 3, 128, (((2 ** 30 - 1) // 9 - 6) * 16) // 128
+    p = P.make(B=B, H=6, Hkv=3, D=D, Nq=1, page=page, kv_len=[40000, 0, 77], seed=9)
+    row = torch.full((1, W + 1), 1 << 30, dtype=torch.int32, device="cuda")
+    own = p.table[0, :-(-40000 // page)]
+    row[0, :own.numel()] = own
+    p.table, p.kv_len = row[:, :W].expand(B, W), [40000, 0, 39999]     # one list of pages for all
+    P.check(p, P.run(p))
+    p.table = row.expand(B, W + 1)
+    with pytest.raises(S.SageError) as e:
+        P.run(p)
+    assert e.value.code == S.SAGE_ERR_UNSUPPORTED

@@ -125,3 +125,14 @@ def test_python_checks_name_the_argument():
         S.sage_attn_paged(q[..., :32], q[..., :32], cache_, None, torch.zeros(16))
     with pytest.raises(ValueError):                        # heads other than the cache's
         S.sage_cache_append(q[:, :1], q[:, :1], torch.zeros((1, 1), dtype=torch.int32), cache_)
+
+
+def test_widths_whose_tiles_pass_int_are_refused(lib):
+    """The bound counts tiles by the table widths, for few rows (16 keys) and for many (128)."""
+    c = cache(heads=32)
+    assert attn(lib, B=512, H=32, Hkv=32, c=c, width=65536, stride=65536) == S.SAGE_ERR_UNSUPPORTED
+    # the same with half of the width in a shared prefix that is read with each request's keys
+    assert attn(lib, B=1, H=65535, Hkv=65535, c=cache(heads=65535), width=65536, ptable=0x30000,
+                pwidth=200000) == S.SAGE_ERR_UNSUPPORTED
+    assert attn(lib, B=512, H=32, Hkv=32, Nq=4096, c=c, width=65536, q=tensor(sb=1 << 30, sn=4096),
+                o=tensor(sb=1 << 30, sn=4096)) == S.SAGE_ERR_UNSUPPORTED
