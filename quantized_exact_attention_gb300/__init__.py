@@ -10,6 +10,7 @@ from __future__ import annotations
 
 import ctypes
 import functools
+import importlib.util
 import os
 from dataclasses import dataclass
 
@@ -481,7 +482,14 @@ def _paged_binding():
     global _paged
     if _paged is None:
         lib = load_library()
-        from . import _sage_binding
+        from . import build
+        path = build.binding_path()
+        if not os.path.exists(path):
+            raise RuntimeError(f"{os.path.basename(path)} was not built for this torch and Python; "
+                               "run quantized_exact_attention_gb300.build.build()")
+        spec = importlib.util.spec_from_file_location(__name__ + "._sage_binding", path)
+        _sage_binding = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(_sage_binding)
         _sage_binding.bind(*[ctypes.cast(f, ctypes.c_void_p).value
                              for f in (lib.sage_page_tables, lib.sage_cache_append, lib.sage_attn_paged)])
         _paged = _sage_binding

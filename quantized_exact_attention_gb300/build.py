@@ -2,8 +2,8 @@
 
 Each CUDA translation unit is compiled in parallel, then linked into one
 shared library next to this file.  Beside it the host compiler makes
-_sage_binding.so, the CPython module that hands torch tensors to the page-cache
-entries.  No cmake, no torch extension machinery.
+_sage_binding-torch<version><suffix>.so, the CPython module that hands torch
+tensors to the page-cache entries.  No cmake, no torch extension machinery.
 """
 from __future__ import annotations
 
@@ -22,11 +22,19 @@ BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libsage_gb300.so")
 SOURCES = ["sage_api.cu", "sage_prep.cu", "sage_attn.cu", "sage_noalloc.cu", "sage_tables.cu", "sage_paged.cu",
            "sage_paged_tiles.cu"]
-BINDING = os.path.join(PKG, "_sage_binding.so")
 BINDING_SOURCE = os.path.join(CSRC, "sage_binding.cpp")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-O2",
          "--expt-relaxed-constexpr", "-I", INCLUDE, "-I", CSRC]
+
+
+def binding_path() -> str:
+    """The tensor-marshalling module of the torch and Python that run this.  It
+    reads tensors by the layout of one torch and links against one Python, so
+    its name holds both versions (and, in Python's suffix, the machine): after
+    a change of either, what was built before is not loaded."""
+    import torch
+    return os.path.join(PKG, f"_sage_binding-torch{torch.__version__}{sysconfig.get_config_var('EXT_SUFFIX')}")
 
 
 def nvcc() -> str:
@@ -57,7 +65,8 @@ def _compile_binding() -> None:
     if not cxx:
         raise RuntimeError("no C++ compiler found")
     cuda = os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(nvcc()))), "include")
-    tmp = BINDING + ".tmp"
+    out = binding_path()
+    tmp = out + ".tmp"
     cmd = [cxx, "-O2", "-std=c++17", "-fPIC", "-shared", "-I", sysconfig.get_paths()["include"],
            "-I", os.path.join(root, "include"), "-I", os.path.join(root, "include", "torch", "csrc", "api", "include"),
            "-I", cuda, "-I", INCLUDE, BINDING_SOURCE, "-o", tmp, "-L", os.path.join(root, "lib"),
@@ -65,13 +74,14 @@ def _compile_binding() -> None:
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"{cxx} failed for sage_binding.cpp:\n{r.stdout}\n{r.stderr}")
-    os.replace(tmp, BINDING)
+    os.replace(tmp, out)
 
 
 def _stale() -> bool:
-    if not os.path.exists(LIB) or not os.path.exists(BINDING):
+    made = (LIB, binding_path())
+    if not all(os.path.exists(m) for m in made):
         return True
-    t = min(os.path.getmtime(LIB), os.path.getmtime(BINDING))
+    t = min(os.path.getmtime(m) for m in made)
     deps = [os.path.join(CSRC, f) for f in os.listdir(CSRC)] + [os.path.join(INCLUDE, f) for f in os.listdir(INCLUDE)]
     return any(os.path.getmtime(d) > t for d in deps)
 
