@@ -3,7 +3,8 @@
 Each CUDA translation unit is compiled in parallel, then linked into one
 shared library next to this file.  Beside it the host compiler makes
 _sage_binding-torch<version><suffix>.so, the CPython module that hands torch
-tensors to the page-cache entries.  No cmake, no torch extension machinery.
+tensors to the page-cache entries; without torch there is no such module, and
+the C library is built alone.  No cmake, no torch extension machinery.
 """
 from __future__ import annotations
 
@@ -28,12 +29,16 @@ FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", 
          "--expt-relaxed-constexpr", "-I", INCLUDE, "-I", CSRC]
 
 
-def binding_path() -> str:
-    """The tensor-marshalling module of the torch and Python that run this.  It
-    reads tensors by the layout of one torch and links against one Python, so
-    its name holds both versions (and, in Python's suffix, the machine): after
-    a change of either, what was built before is not loaded."""
-    import torch
+def binding_path() -> str | None:
+    """The tensor-marshalling module of the torch and Python that run this (None
+    without torch, which users of the C library may lack).  It reads tensors by
+    the layout of one torch and links against one Python, so its name holds both
+    versions (and, in Python's suffix, the machine): after a change of either,
+    what was built before is not loaded."""
+    try:
+        import torch
+    except ImportError:
+        return None
     return os.path.join(PKG, f"_sage_binding-torch{torch.__version__}{sysconfig.get_config_var('EXT_SUFFIX')}")
 
 
@@ -78,7 +83,7 @@ def _compile_binding() -> None:
 
 
 def _stale() -> bool:
-    made = (LIB, binding_path())
+    made = [m for m in (LIB, binding_path()) if m is not None]
     if not all(os.path.exists(m) for m in made):
         return True
     t = min(os.path.getmtime(m) for m in made)
@@ -91,15 +96,16 @@ def build(force: bool = False, verbose: bool = False) -> str:
         return LIB
     os.makedirs(BUILD, exist_ok=True)
     with ThreadPoolExecutor(len(SOURCES) + 1) as ex:
-        binding = ex.submit(_compile_binding)
+        binding = ex.submit(_compile_binding) if binding_path() is not None else None
         objs = list(ex.map(lambda s: _compile(s, verbose), SOURCES))
-        binding.result()
     tmp = LIB + ".tmp"
     cmd = [nvcc(), *ARCH, "-shared", "-o", tmp, *objs]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB)
+    if binding is not None:
+        binding.result()                                   # raises what failed; the C library stands by itself
     return LIB
 
 

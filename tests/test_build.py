@@ -1,5 +1,7 @@
 """What the build makes for whom, without compiling anything."""
 import os
+import subprocess
+import sys
 import sysconfig
 
 import pytest
@@ -36,3 +38,40 @@ def test_a_binding_built_for_another_python_is_not_used(monkeypatch):
 def test_the_binding_of_this_torch_and_python_loads():
     B.build()
     assert S._paged_binding().__file__ == B.binding_path()
+
+
+@pytest.fixture()
+def stubbed(monkeypatch, tmp_path):
+    """A build into tmp_path whose compilers only leave their output files."""
+    def tool(cmd, **_):
+        with open(cmd[cmd.index("-o") + 1], "w") as f:
+            f.write("made")
+        return subprocess.CompletedProcess(cmd, 0, "", "")
+
+    for name in ("PKG", "BUILD"):
+        monkeypatch.setattr(B, name, str(tmp_path))
+    monkeypatch.setattr(B, "LIB", str(tmp_path / "libsage_gb300.so"))
+    monkeypatch.setattr(B.subprocess, "run", tool)
+    return tmp_path
+
+
+def test_the_c_library_is_built_without_torch(monkeypatch, stubbed):
+    monkeypatch.setitem(sys.modules, "torch", None)        # import torch raises
+    assert B.build(force=True) == str(stubbed / "libsage_gb300.so")
+    assert os.path.exists(B.LIB) and not B._stale()
+    assert not [f for f in os.listdir(stubbed) if "binding" in f]
+
+
+def test_a_binding_that_does_not_compile_leaves_the_c_library(monkeypatch, stubbed):
+    def no_compiler():
+        raise RuntimeError("no C++ compiler found")
+
+    monkeypatch.setattr(B, "_compile_binding", no_compiler)
+    with pytest.raises(RuntimeError, match="no C.. compiler"):
+        B.build(force=True)
+    assert os.path.exists(B.LIB) and B._stale()
+
+
+def test_a_build_makes_both(stubbed):
+    B.build(force=True)
+    assert os.path.exists(B.LIB) and os.path.exists(B.binding_path()) and not B._stale()
