@@ -399,7 +399,8 @@ int sage_paged_workspace(int B, int H, int Hkv, int Nq, int D, size_t* bytes);
  * The widths bound the lengths on the host and choose between kernels: rows no
  * wider than the requests may grow are served faster.
  * Cache rows behind a length are never used, whatever they hold; the rows
- * within the lengths must be finite, hidden ones included.  Scores, maxima,
+ * within the lengths must be finite, hidden ones included, and the scores
+ * (sm_scale * q.k) below 2^30 in magnitude.  Scores, maxima,
  * sums and the output up to its last rounding are FP32, the weights are
  * rounded to BF16 for the product with the values.  Results do not depend on the workspace or on earlier
  * calls: equal inputs and widths give equal bits on the same device. */

@@ -437,3 +437,23 @@ def test_the_widest_tables(D):
     with pytest.raises(S.SageError) as e:
         P.run(p)
     assert e.value.code == S.SAGE_ERR_UNSUPPORTED
+
+
+@pytest.mark.parametrize("Nq,wide_", [(1, 0), (1, 1), (40, 0), (300, 0), (300, 1)])
+@pytest.mark.parametrize("top", [2.0 ** 29, -2.0 ** 28])
+def test_scores_of_two_to_the_29(Nq, wide_, top):
+    """The largest score lies so far above the others that the output is its value: one
+    rounding of its weight and one of the output, whatever its distance to the rounded maximum."""
+    G.ensure_built()
+    D, n, at = 128, 230, 137                               # key `at` has the score `top`, the others half or twice that
+    p = P.make(B=1, H=4, Hkv=2, D=D, Nq=Nq, page=16, kv_len=[n], causal=False, sm_scale=1.0, seed=29, **pad(wide_))
+    rest = top / 2 if top > 0 else top * 2
+    p.q.fill_(2.0 ** 14)
+    for j in range(n):
+        pg, row = int(p.table[0, j // 16]), j % 16
+        p.cache_k[pg, :, row] = (top if j == at else rest) / 2.0 ** 14 / D
+    value = p.cache_v[int(p.table[0, at // 16]), :, at % 16].double().repeat_interleave(2, 0)[None, :, None]
+    o = P.run(p).double()
+    tol = ((1 + P.U_BF16) * (1 + P.U_BF16 + 2.0 ** -18) - 1) * value.abs()
+    assert bool(((o - value).abs() <= tol).all())
+    assert S.sage_get_device_status() == S.SAGE_OK
