@@ -37,9 +37,12 @@ namespace {
 // whole accumulator columns.  P is rounded to BF16 (relative error at most 2^-8) for
 // the second product, as its other operand V is BF16; l sums it unrounded.
 // A step never crosses a page: pages hold a multiple of 16 tokens.
-// Measured: 64 ragged requests of up to 8,192 keys (1,077 MB read) in 164 us,
-// 0.94 of the copy rate; one of 131,072 keys (537 MB) in 84 us with its join
-// behind it.
+// Measured, a call with its join: 64 ragged requests of up to 8,192 keys (1,077
+// MB read) in 166 to 171 us, 0.93 to 0.96 of the copy rate; one of 131,072 keys
+// (537 MB) in 89 to 91 us, 0.87 to 0.89.
+// Beside the prefix's kernel it reads lengths, pages and rows before its own
+// wait, behind a fence (128 requests behind 16,333 shared keys: 88 to 89 us a
+// call; with relaxed loads, which go past L1, in its place 92).
 // kWhole: for short sequences, bound by latency, a cluster of `split` CTAs
 // takes an item, shares its steps among its warps and joins them through
 // shared memory, so the call is one kernel (8 key heads, 60 keys: 3.9 us

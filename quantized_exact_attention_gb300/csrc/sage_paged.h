@@ -127,7 +127,7 @@ __device__ __forceinline__ int ld_gpu(const int32_t* a) {
 // split of an SM's memory (`max_shared`, set once per device): an SM drains
 // before it changes the split (a short decode call: 10.4 us, with the same
 // split 9.0 us).  The append moves its rows through L1 and keeps the default
-// (2 x 122 MB: 40.9 us; with little L1 51.3).
+// (2 x 122 MB: 37.9 us; with little L1 46.3).
 template <class... P, class... A>
 cudaError_t launch_pdl(void (*kernel)(P...), dim3 grid, dim3 block, size_t smem, cudaStream_t s, int cluster,
                        bool max_shared, bool (&ready)[64], const A&... args) {

@@ -32,8 +32,8 @@
 // scores are computed while the exponentials run, and the two groups fall into
 // turns by themselves.  (Each group's P over its own S, every unit a chain S,
 // softmax, PV: the groups fall into step and leave the tensor core idle
-// meanwhile, 2,250 cycles a unit.  An S for each group, at D = 64: 46.6 us
-// where the shared one takes 44.3.)  One group of D = 128, with 256 columns:
+// meanwhile, 2,250 cycles a unit.  An S for each group, at D = 64 and with
+// prompts from the list: 46.6 us where the shared one took 44.3.)  One group of D = 128, with 256 columns:
 // [S 128, its first half P | O 128].
 //
 // The reference of the exponentials follows the row maximum lazily: O is

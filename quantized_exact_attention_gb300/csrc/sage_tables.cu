@@ -50,7 +50,7 @@ constexpr int kTableThreads = 256;
 // kQuads: rows of the table and of the slots are 16-byte aligned and a multiple
 // of 4 long; they leave four entries a store.  A large batch is bound by
 // instructions: about 25 an entry one by one, half as many in fours (2,048 rows
-// of 1,024 pages and 1,024 slots: 8.0 us one by one, 6.65 in fours).
+// of 1,024 pages and 1,024 slots: 7.8 us one by one, 6.6 in fours).
 template <bool kQuads>
 __global__ void __launch_bounds__(kTableThreads, 8) page_tables_kernel(const __grid_constant__ TableParams p) {
     __shared__ int red[kTableThreads / 32];
@@ -144,9 +144,9 @@ __global__ void __launch_bounds__(kTableThreads, 8) page_tables_kernel(const __g
 // ---------------------------------------------------------------------------
 // Append: one warp copies the K and V rows of one token, 16 bytes a lane.
 // Reads and writes each row once; HBM bounds it (16 prompts of up to 2,048
-// tokens, 16 heads of 128 channels: 38 us, the copy's rate 36).  Four blocks an
-// SM, whose registers hold a warp's loads before its stores; with six it takes
-// 39.8 us, with eight 40.9, with eight that loop over the tokens 41.
+// tokens, 16 heads of 128 channels: 38 us, the copy's rate 36).  A lane loads
+// four chunks of K and of V before it stores them (one chunk: 41.5 us).  Four
+// blocks an SM, whose registers hold them; with six they spill (56 us).
 // ---------------------------------------------------------------------------
 struct AppendParams {
     const uint16_t* k;
