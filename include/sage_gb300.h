@@ -409,6 +409,113 @@ int sage_attn_paged(const sage_tensor* q, const sage_tensor* o, const sage_page_
                     const int32_t* kv_len, const int32_t* prefix_table, int prefix_width, const int32_t* prefix_len,
                     float sm_scale, int causal, void* workspace, size_t workspace_bytes, void* stream);
 
+/* ---------------------------------------------------------------------------
+ * A tree of drafted tokens, served from the page cache.  (The pages describe
+ * no drafts and no positions; these entries complete the serving path above.)
+ * A step's new tokens may be a tree: token i continues token parent[i] before
+ * it.  One step is sage_page_tables, sage_tree_tables (which tokens each sees,
+ * and how far behind the committed ones it stands), sage_rope (queries),
+ * sage_cache_append_rope (keys and values), sage_attn_paged_tree and, once the
+ * accepted path is known, sage_cache_keep.  sage_rope and
+ * sage_cache_append_rope serve any step, with or without a tree.
+ * ------------------------------------------------------------------------- */
+
+/* Rotary positions.  Pair j of a head's first rotary_dim channels is turned by
+ * pos * f_j radians:  y1 = A (x1 cos - x2 sin),  y2 = A (x1 sin + x2 cos).
+ *  turns : device [rotary_dim / 2], 16-byte aligned: f_j as sage_rotary_turns
+ *          gives it.
+ *  rotary_dim : a multiple of 16, up to D; the channels behind it are copied.
+ *  interleaved : 0: pair j is channels j and rotary_dim / 2 + j; else channels
+ *          2j and 2j + 1.
+ *  amplitude : A (1 for a plain rotation; some frequencies stretched for far
+ *          positions come with another). */
+typedef struct {
+    const uint64_t* turns;
+    int rotary_dim;
+    int interleaved;
+    float amplitude;
+} sage_rotary;
+
+/* On the host, without a GPU: turns[j] = frequencies[j] / (2 pi) modulo 1, in
+ * units of 2^-64, for n frequencies in radians a position (|f| < 2^20; any
+ * scaling for far positions is in them).  The angle of position pos is then
+ * pos * turns[j] modulo 2^64, an integer product: it is off by less than
+ * |pos| * 2^-64 + 2^-32 turns at any position of 32 bits. */
+int sage_rotary_turns(const double* frequencies, int n, uint64_t* turns);
+
+/* Rotate the rows of x into out.
+ *  x, out  : BF16 [B, H, N, D] views (device), D = 64 or 128.  out is x itself
+ *            (pointer and strides) or does not overlap it; it has no broadcast
+ *            axis (every stride at least D, but for an axis of one).
+ *  positions : device int32, B rows of N entries, positions_stride apart (0:
+ *            one row for all), or NULL: token i has position i.
+ *  start   : device int32 [B], added to request b's positions, or NULL.
+ *  n_len   : device int32 [B], or NULL for N: rows of out at or beyond it are
+ *            not written.
+ *  inverse : not 0: turned by the negative angle.  With the same amplitude
+ *            this is the transposed map, so it takes the gradient of out to the
+ *            gradient of x.
+ * Cosine, sine, products and sums are FP32, rounded to BF16 once.  B * N is
+ * below 2^31 (else SAGE_ERR_UNSUPPORTED).  One launch. */
+int sage_rope(const sage_tensor* x, const sage_tensor* out, int B, int H, int N, int D, const int32_t* positions,
+              int64_t positions_stride, const int32_t* start, const int32_t* n_len, const sage_rotary* rotary, int inverse,
+              void* stream);
+
+/* sage_cache_append with the keys rotated on the way: k, v, slots, the cache and
+ * the errors as there, positions and start as for sage_rope.  A key's row in the
+ * cache holds the bits that sage_rope gives. */
+int sage_cache_append_rope(const sage_tensor* k, const sage_tensor* v, int B, int N, const int32_t* slots,
+                           int64_t slots_stride, const int32_t* positions, int64_t positions_stride, const int32_t* start,
+                           const sage_rotary* rotary, const sage_page_cache* cache, void* stream);
+
+/* Which of a tree's tokens each of them sees, itself and its ancestors, and its
+ * depth, the number of its ancestors.
+ *  parents : device int32, B rows of N entries, parents_stride apart.  Token i's
+ *            parent is a token before it; a number that is negative or not below
+ *            i means none (a request may hold several roots).
+ *  n_len   : device int32 [B], the tokens each request has, or NULL for N.
+ *  mask    : device int32 [B][N] rows of (N + 31) / 32 words, mask_stride_b and
+ *            mask_stride_n apart: bit t % 32 of word t / 32 of row i is set when
+ *            token i sees token t.  Rows at or beyond n_len[b] are 0.
+ *  depth   : device int32, B rows of N entries, depth_stride apart (0 at or
+ *            beyond n_len[b]), or NULL.  With start = the committed tokens it is
+ *            what sage_rope and sage_cache_append_rope take as positions.
+ * The outputs overlap neither each other nor the parents.  N is at most 4096
+ * (else SAGE_ERR_UNSUPPORTED).  One launch. */
+int sage_tree_tables(const int32_t* parents, int64_t parents_stride, int B, int N, const int32_t* n_len, int32_t* mask,
+                     int64_t mask_stride_b, int64_t mask_stride_n, int32_t* depth, int64_t depth_stride, void* stream);
+
+/* sage_attn_paged for new tokens that see each other by a mask.  Request b's
+ * last q_len[b] own keys are its new tokens' (key kv_len[b] - q_len[b] + t is of
+ * token t; with kv_len[b] below q_len[b] the first tokens have none).  Row i sees
+ * the prefix, every own key before those, and the key of token t when bit t % 32
+ * of word t / 32 of its mask row is set; a row that sees no key is written as
+ * zero.  Any mask is served, not only a tree's.
+ *  mask    : device int32, rows of (Nq + 31) / 32 words, row (b, i) at
+ *            b * mask_stride_b + i * mask_stride_n (a stride of 0 shares rows).
+ *            Rows and bits at or beyond q_len[b] are not used.
+ * All else, workspace and limits included, as for sage_attn_paged. */
+int sage_attn_paged_tree(const sage_tensor* q, const sage_tensor* o, const sage_page_cache* cache, int B, int H, int Nq,
+                         const int32_t* q_len, const int32_t* table, int64_t table_stride, int table_width,
+                         const int32_t* kv_len, const int32_t* prefix_table, int prefix_width, const int32_t* prefix_len,
+                         const int32_t* mask, int64_t mask_stride_b, int64_t mask_stride_n, float sm_scale, void* workspace,
+                         size_t workspace_bytes, void* stream);
+
+/* Move the cache rows of accepted tokens to the front of a request's new ones:
+ * for i = 0, 1, ... K - 1 in this order, the rows in slot slots[b][kept[b][i]]
+ * are copied to slot slots[b][i].
+ *  kept    : device int32, B rows of K entries, kept_stride apart: numbers of new
+ *            tokens, an accepted path of the tree in its order.  An entry below 0
+ *            or at or beyond N moves nothing.
+ *  slots   : device int32, B rows of N entries, slots_stride apart, as for
+ *            sage_cache_append; K is at most N.  A move from or to a negative slot
+ *            is left out; a slot outside the cache too, which is recorded as
+ *            SAGE_ERR_PAGE in the device status.
+ * A move sees what the moves of its request before it wrote.  Slots that one
+ * request's moves write are not among another's.  One launch. */
+int sage_cache_keep(const int32_t* kept, int64_t kept_stride, int B, int K, const int32_t* slots, int64_t slots_stride, int N,
+                    const sage_page_cache* cache, void* stream);
+
 /* Synchronizes the device, returns the first error a kernel recorded since
  * the last call (SAGE_OK if none) and clears it. */
 int sage_get_device_status(void);

@@ -11,6 +11,7 @@ from __future__ import annotations
 import ctypes
 import functools
 import importlib.util
+import math
 import os
 from dataclasses import dataclass
 
@@ -41,7 +42,8 @@ EXPORTED = ("sage_buffer_sizes", "sage_prep_qkv", "sage_attn_fwd", "sage_attn_fw
             "sage_last_launch_count", "sage_debug_inject_fault", "sage_debug_prep_mode",
             "sage_debug_epilogue_mode", "sage_prep_qkv_noalloc",
             "sage_prep_noalloc_capacity", "sage_page_tables", "sage_cache_append",
-            "sage_paged_workspace", "sage_attn_paged")
+            "sage_paged_workspace", "sage_attn_paged", "sage_rotary_turns", "sage_rope", "sage_cache_append_rope",
+            "sage_tree_tables", "sage_attn_paged_tree", "sage_cache_keep")
 
 
 class SageError(RuntimeError):
@@ -80,6 +82,11 @@ class sage_copy(ctypes.Structure):
 class sage_page_cache(ctypes.Structure):
     _fields_ = [("k", sage_tensor), ("v", sage_tensor), ("num_pages", ctypes.c_int), ("page_size", ctypes.c_int),
                 ("heads", ctypes.c_int), ("D", ctypes.c_int)]
+
+
+class sage_rotary(ctypes.Structure):
+    _fields_ = [("turns", ctypes.c_void_p), ("rotary_dim", ctypes.c_int), ("interleaved", ctypes.c_int),
+                ("amplitude", ctypes.c_float)]
 
 
 _lib = None
@@ -130,6 +137,14 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.sage_paged_workspace.argtypes = [i, i, i, i, i, P(sz)]
     lib.sage_attn_paged.argtypes = [P(sage_tensor), P(sage_tensor), P(sage_page_cache), i, i, i, vp, vp, i64, i, vp,
                                     vp, i, vp, f, i, vp, sz, vp]
+    lib.sage_rotary_turns.argtypes = [P(ctypes.c_double), i, P(ctypes.c_uint64)]
+    lib.sage_rope.argtypes = [P(sage_tensor), P(sage_tensor), i, i, i, i, vp, i64, vp, vp, P(sage_rotary), i, vp]
+    lib.sage_cache_append_rope.argtypes = [P(sage_tensor), P(sage_tensor), i, i, vp, i64, vp, i64, vp, P(sage_rotary),
+                                           P(sage_page_cache), vp]
+    lib.sage_tree_tables.argtypes = [vp, i64, i, i, vp, vp, i64, i64, vp, i64, vp]
+    lib.sage_attn_paged_tree.argtypes = [P(sage_tensor), P(sage_tensor), P(sage_page_cache), i, i, i, vp, vp, i64, i,
+                                         vp, vp, i, vp, vp, i64, i64, f, vp, sz, vp]
+    lib.sage_cache_keep.argtypes = [vp, i64, i, i, vp, i64, i, P(sage_page_cache), vp]
     for name in EXPORTED:
         if name not in ("sage_status_string", "sage_prep_noalloc_capacity"):
             getattr(lib, name).restype = ctypes.c_int
@@ -491,7 +506,9 @@ def _paged_binding():
         _sage_binding = importlib.util.module_from_spec(spec)
         spec.loader.exec_module(_sage_binding)
         _sage_binding.bind(*[ctypes.cast(f, ctypes.c_void_p).value
-                             for f in (lib.sage_page_tables, lib.sage_cache_append, lib.sage_attn_paged)])
+                             for f in (lib.sage_page_tables, lib.sage_cache_append, lib.sage_attn_paged, lib.sage_rope,
+                                       lib.sage_cache_append_rope, lib.sage_tree_tables, lib.sage_attn_paged_tree,
+                                       lib.sage_cache_keep)])
         _paged = _sage_binding
     return _paged
 
@@ -545,13 +562,168 @@ def sage_attn_paged(q, o, cache: PageCache, table, workspace, q_len=None, kv_len
 
 
 def attention_paged(q, cache: PageCache, table, q_len=None, kv_len=None, prefix_table=None, prefix_len=None,
-                    sm_scale: float = 0.0, causal: bool = True, out=None, stream=None):
-    """sage_attn_paged with its own workspace and, unless `out` is given, output
-    (rows at or beyond q_len are zero); returns the output."""
+                    sm_scale: float = 0.0, causal: bool = True, out=None, stream=None, mask=None):
+    """sage_attn_paged (with a mask: sage_attn_paged_tree, for which `causal` has
+    no meaning) with its own workspace and, unless `out` is given, output (rows
+    at or beyond q_len are zero); returns the output."""
     B, H, Nq, D = q.shape
     with torch.cuda.stream(stream):                        # what is allocated here belongs to the stream that uses it
         if out is None:
             out = torch.zeros((B, Nq, H, D), dtype=torch.bfloat16, device=q.device).permute(0, 2, 1, 3)
         ws = alloc_paged_workspace(B, H, cache.heads, Nq, D, q.device)
-        sage_attn_paged(q, out, cache, table, ws, q_len, kv_len, prefix_table, prefix_len, sm_scale, causal)
+        if mask is None:
+            sage_attn_paged(q, out, cache, table, ws, q_len, kv_len, prefix_table, prefix_len, sm_scale, causal)
+        else:
+            sage_attn_paged_tree(q, out, cache, table, mask, ws, q_len, kv_len, prefix_table, prefix_len, sm_scale)
     return out
+
+
+# ---------------------------------------------------------------------------
+# Rotary positions, and a tree of drafted tokens
+# ---------------------------------------------------------------------------
+def rotary_frequencies(rotary_dim: int, base: float = 10000.0, scale: float = 1.0, method: str = "linear",
+                       trained: int = 4096, slow: float = 1.0, fast: float = 32.0):
+    """(frequencies in radians a position, amplitude) of rotary_dim / 2 pairs,
+    in 64 bits: f_j = base^(-2 j / rotary_dim), and for positions `scale` times
+    as far as those trained on
+      "linear"  f_j / scale (position interpolation);
+      "base"    base * scale^(R / (R - 2)) in place of base, R = rotary_dim, which
+                leaves the fastest pair and divides the slowest by scale;
+      "parts"   f_j / scale for pairs that turn up to `slow` times within `trained`
+                positions, f_j for those that turn `fast` times or more, a blend in
+                between that is linear in the turns; amplitude 0.1 ln(scale) + 1
+                (YaRN, Peng et al. 2023)."""
+    if rotary_dim <= 0 or rotary_dim % 2 or not base > 0 or not scale >= 1:
+        raise ValueError("rotary_dim is positive and even, base above 0, scale at least 1")
+    if method == "base":
+        if rotary_dim == 2:
+            raise ValueError("a single pair has no other base")
+        base = base * scale ** (rotary_dim / (rotary_dim - 2))
+    f = [base ** (-2.0 * j / rotary_dim) for j in range(rotary_dim // 2)]
+    if method == "base" or scale == 1:
+        return f, 1.0
+    if method == "linear":
+        return [x / scale for x in f], 1.0
+    if method != "parts" or not fast > slow:
+        raise ValueError('method is "linear", "base" or "parts", with fast above slow')
+    keep = [min(1.0, max(0.0, (trained * x / (2 * math.pi) - slow) / (fast - slow))) for x in f]
+    return [x * k + x / scale * (1 - k) for x, k in zip(f, keep)], 0.1 * math.log(scale) + 1.0
+
+
+@dataclass(frozen=True)
+class Rotary:
+    """Rotary positions as the kernels take them (sage_rotary in the header):
+    turns int64 [rotary_dim / 2], on the device of the calls.  Frozen: the C
+    struct is built once and reused by every call."""
+    turns: torch.Tensor
+    interleaved: bool = False
+    amplitude: float = 1.0
+
+    def __post_init__(self):
+        if self.turns.dim() != 1 or self.turns.dtype != torch.int64 or not self.turns.is_contiguous():
+            raise ValueError("turns of rotary positions are a contiguous int64 vector")
+        self._c
+
+    @property
+    def rotary_dim(self) -> int:
+        return 2 * self.turns.shape[0]
+
+    @functools.cached_property
+    def _c(self) -> sage_rotary:
+        return sage_rotary(self.turns.data_ptr(), self.rotary_dim, 1 if self.interleaved else 0, float(self.amplitude))
+
+    @functools.cached_property
+    def _address(self) -> int:
+        return ctypes.addressof(self._c)
+
+    @functools.cached_property
+    def _device(self) -> int:
+        return self.turns.get_device()
+
+
+def make_rotary(frequencies, interleaved: bool = False, amplitude: float = 1.0, device="cuda") -> Rotary:
+    """Rotary positions of these frequencies (radians a position, one for each
+    pair; see rotary_frequencies), laid out on the device."""
+    f = [float(x) for x in frequencies]
+    n = len(f)
+    turns = (ctypes.c_uint64 * max(n, 1))()
+    _check(load_library().sage_rotary_turns((ctypes.c_double * max(n, 1))(*f), n, turns), "sage_rotary_turns")
+    signed = [t - (1 << 64) if t >> 63 else t for t in turns]
+    return Rotary(torch.tensor(signed, dtype=torch.int64, device=device), bool(interleaved), float(amplitude))
+
+
+def sage_rope(x, out, rotary: Rotary, positions=None, start=None, n_len=None, inverse: bool = False, stream=None):
+    """Enqueue the rotation of the [B, H, N, D] BF16 view x into the view out
+    (x itself, or one that does not overlap it).  Token i of request b has
+    position positions[b, i] (int32 [B, N], or [N] for all requests; None: i)
+    plus start[b] (int32 [B]; None: 0); rows at or beyond n_len[b] are not
+    written.  inverse=True: the transposed map, which takes the gradient of out
+    to that of x."""
+    rc = (_paged or _paged_binding()).rope(x, out, rotary._address, rotary._device, positions, start, n_len, inverse,
+                                           None if stream is None else stream.cuda_stream)
+    if rc:
+        _check(rc, "sage_rope")
+
+
+def rope(x, rotary: Rotary, positions=None, start=None, n_len=None, inverse: bool = False, out=None, stream=None):
+    """sage_rope with its own output unless `out` is given (rows at or beyond
+    n_len are zero); returns the output."""
+    B, H, N, D = x.shape
+    with torch.cuda.stream(stream):                        # what is allocated here belongs to the stream that uses it
+        if out is None:
+            out = torch.zeros((B, N, H, D), dtype=torch.bfloat16, device=x.device).permute(0, 2, 1, 3)
+        sage_rope(x, out, rotary, positions, start, n_len, inverse)
+    return out
+
+
+def sage_cache_append_rope(k, v, slots, cache: PageCache, rotary: Rotary, positions=None, start=None, stream=None):
+    """sage_cache_append with the keys rotated on their way into the cache;
+    positions and start as for sage_rope."""
+    rc = (_paged or _paged_binding()).cache_append_rope(k, v, slots, cache._address, cache._device, rotary._address,
+                                                        rotary._device, positions, start,
+                                                        None if stream is None else stream.cuda_stream)
+    if rc:
+        _check(rc, "sage_cache_append_rope")
+
+
+def sage_tree_tables(parents, mask, depth=None, n_len=None, stream=None):
+    """Enqueue which tokens of a tree each of them sees: parents int32 [B, N]
+    (a token before it, or negative for none), mask int32 [B, N, W] with W at
+    least ceil(N / 32), depth int32 [B, N] or None, n_len int32 [B] or None."""
+    rc = (_paged or _paged_binding()).tree_tables(parents, mask, depth, n_len,
+                                                  None if stream is None else stream.cuda_stream)
+    if rc:
+        _check(rc, "sage_tree_tables")
+
+
+def tree_tables(parents, n_len=None, stream=None):
+    """sage_tree_tables into tensors of its own; returns (mask, depth)."""
+    B, N = parents.shape
+    with torch.cuda.stream(stream):
+        e = lambda *s: torch.empty(s, dtype=torch.int32, device=parents.device)  # noqa: E731
+        mask, depth = e(B, N, (N + 31) // 32), e(B, N)
+        sage_tree_tables(parents, mask, depth, n_len)
+    return mask, depth
+
+
+def sage_attn_paged_tree(q, o, cache: PageCache, table, mask, workspace, q_len=None, kv_len=None, prefix_table=None,
+                         prefix_len=None, sm_scale: float = 0.0, stream=None):
+    """sage_attn_paged for new tokens that see each other by a mask: int32
+    [B, Nq, W] of sage_tree_tables, or [Nq, W] for one that all requests share,
+    W at least ceil(Nq / 32).  Every token sees the prefix and the keys before
+    the new tokens'."""
+    rc = (_paged or _paged_binding()).attn_paged_tree(q, o, cache._address, cache._device, table, mask, workspace, q_len,
+                                                      kv_len, prefix_table, prefix_len, sm_scale,
+                                                      None if stream is None else stream.cuda_stream)
+    if rc:
+        _check(rc, "sage_attn_paged_tree")
+
+
+def sage_cache_keep(kept, slots, cache: PageCache, stream=None):
+    """Enqueue the move of accepted tokens to the front of the new ones: for i in
+    order, the cache rows in slots[b, kept[b, i]] go to slots[b, i] (kept int32
+    [B, K], negative: nothing moves; slots int32 [B, N], K at most N)."""
+    rc = (_paged or _paged_binding()).cache_keep(kept, slots, cache._address, cache._device,
+                                                 None if stream is None else stream.cuda_stream)
+    if rc:
+        _check(rc, "sage_cache_keep")

@@ -110,7 +110,15 @@ struct StepNote {
     int own, first;                      // own keys; first step of its item in this warp
 };
 
-template <int D, int NR, bool kWhole>
+// Whether row rr of a request sees new token t < n.  `first`: the row's first
+// word, which holds all of them unless a key head has more than 128 heads.
+__device__ __forceinline__ bool tree_sees(const PagedParams& p, const StepNote& nt, int rr, uint32_t first, int t) {
+    if (t < 32) return (first >> t) & 1;
+    const int i = fast_div(rr, p.by_G);
+    return i < nt.n && ((uint32_t)p.mask[nt.b * p.msb + i * p.msn + (t >> 5)] >> (t & 31)) & 1;
+}
+
+template <int D, int NR, bool kWhole, bool kTree>
 __global__ void __launch_bounds__(kRowWarps * 32, 2) paged_rows_kernel(const __grid_constant__ PagedParams p) {
     using Sh = RowsShape<D>;
     constexpr int M = 8 * NR, S = Sh::kStages;
@@ -216,6 +224,7 @@ __global__ void __launch_bounds__(kRowWarps * 32, 2) paged_rows_kernel(const __g
     float o[NR][D / 16][4];                               // O^T: channels x query rows
     float m[NR][2], l[NR][2];                             // of the two query rows this lane's columns are
     int lim[NR][2];                                       // own keys each of them sees
+    uint32_t sees[NR][2];                                 // kTree: which of the first 32 new tokens
     int item = -1, ib = 0, ih = 0, irt = 0, tokens = 0;   // the item these belong to, its request's query tokens
 
     // Leave the item's partial result.
@@ -269,9 +278,14 @@ __global__ void __launch_bounds__(kRowWarps * 32, 2) paged_rows_kernel(const __g
                 m[nr][e] = -INFINITY;
                 l[nr][e] = 0.f;
                 lim[nr][e] = len;
-                if (p.causal) {
+                if (kTree || p.causal) {
                     const int rr = irt * M + nr * 8 + (lane & 3) * 2 + e;
-                    lim[nr][e] = min(len, len - n + fast_div(rr, p.by_G) + 1);
+                    if constexpr (kTree) {
+                        const int i = fast_div(rr, p.by_G);
+                        sees[nr][e] = i < n ? (uint32_t)p.mask[ib * p.msb + i * p.msn] : 0u;
+                    } else {
+                        lim[nr][e] = min(len, len - n + fast_div(rr, p.by_G) + 1);
+                    }
                 }
             }
         }
@@ -320,6 +334,17 @@ __global__ void __launch_bounds__(kRowWarps * 32, 2) paged_rows_kernel(const __g
                 const int end = nt.own ? min(lim[nr][e], nt.key0 + nt.nkeys) : nt.key0 + nt.nkeys;
                 if (k0 >= end) sacc[nr][e] = -INFINITY;
                 if (k0 + 8 >= end) sacc[nr][2 + e] = -INFINITY;
+                if constexpr (kTree) {
+                    const int t0 = nt.key0 - (nt.len - nt.n);      // new token that the step's first key is of
+                    if (nt.own && t0 + kStep > 0) {
+#pragma unroll
+                        for (int x = 0; x < 2; ++x) {
+                            const int t = t0 + (lane >> 2) + 8 * x;
+                            if (t >= 0 && t < nt.n && !tree_sees(p, nt, irt * M + nr * 8 + (lane & 3) * 2 + e, sees[nr][e], t))
+                                sacc[nr][2 * x + e] = -INFINITY;
+                        }
+                    }
+                }
                 float mx = fmaxf(sacc[nr][e], sacc[nr][2 + e]);
                 mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
                 mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
@@ -714,45 +739,35 @@ cudaError_t launch_join(const PagedParams& p, cudaStream_t s) {
                       ready1, p);
 }
 
-template <int D, int NR>
+template <int D, int NR, bool kTree>
 cudaError_t launch_rows(const PagedParams& p, cudaStream_t s) {
     if (p.split > 0) {
         static bool whole_ready[64] = {};
-        return launch_pdl(paged_rows_kernel<D, NR, true>, dim3((unsigned)(p.B * p.rt * p.Hkv * p.split)), dim3(kRowWarps * 32),
+        return launch_pdl(paged_rows_kernel<D, NR, true, kTree>, dim3((unsigned)(p.B * p.rt * p.Hkv * p.split)), dim3(kRowWarps * 32),
                           RowsShape<D>::kSmem, s, p.split, true, whole_ready, p);
     }
     static bool ready[64] = {};
-    const cudaError_t e = launch_pdl(paged_rows_kernel<D, NR, false>, dim3((unsigned)(p.workers / kRowWarps)), dim3(kRowWarps * 32),
+    const cudaError_t e = launch_pdl(paged_rows_kernel<D, NR, false, kTree>, dim3((unsigned)(p.workers / kRowWarps)), dim3(kRowWarps * 32),
                                      RowsShape<D>::kSmem, s, 1, true, ready, p);
     return e != cudaSuccess ? e : launch_join<D, 8 * NR, kStep>(p, s);
 }
+template <bool kTree>
 cudaError_t launch_rows(const PagedParams& p, int D, int nr, cudaStream_t s) {
-    if (D == 64) return nr == 1 ? launch_rows<64, 1>(p, s) : launch_rows<64, 2>(p, s);
-    return nr == 1 ? launch_rows<128, 1>(p, s) : launch_rows<128, 2>(p, s);
+    if (D == 64) return nr == 1 ? launch_rows<64, 1, kTree>(p, s) : launch_rows<64, 2, kTree>(p, s);
+    return nr == 1 ? launch_rows<128, 1, kTree>(p, s) : launch_rows<128, 2, kTree>(p, s);
 }
 
-}  // namespace
-}  // namespace sage
+// Which new tokens a row sees.
+struct TreeMask {
+    const int32_t* words;
+    int64_t stride_b, stride_n;
+};
 
-using namespace sage;
-
-extern "C" {
-
-int sage_paged_workspace(int B, int H, int Hkv, int Nq, int D, size_t* bytes) {
-    if (bytes == nullptr) return SAGE_ERR_ARG;
-    const int rc = check_batch(B, H, Hkv, Nq, D);
-    if (rc != SAGE_OK) return rc;
-    // a prefix of any length may come: the form with a list of its own needs the most
-    *bytes = lists_bytes(make_lists(B, Hkv, H / Hkv, Nq, D, 0, INT32_MAX, 0), B, D);
-    const size_t alone = lists_bytes(make_lists(B, Hkv, H / Hkv, Nq, D, 0, 0, 0), B, D);
-    if (alone > *bytes) *bytes = alone;
-    return SAGE_OK;
-}
-
-int sage_attn_paged(const sage_tensor* q, const sage_tensor* o, const sage_page_cache* cache, int B, int H, int Nq,
-                    const int32_t* q_len, const int32_t* table, int64_t table_stride, int table_width,
-                    const int32_t* kv_len, const int32_t* prefix_table, int prefix_width, const int32_t* prefix_len,
-                    float sm_scale, int causal, void* workspace, size_t workspace_bytes, void* stream) {
+// sage_attn_paged, and with a tree's mask sage_attn_paged_tree.
+int attn_paged(const sage_tensor* q, const sage_tensor* o, const sage_page_cache* cache, int B, int H, int Nq,
+               const int32_t* q_len, const int32_t* table, int64_t table_stride, int table_width, const int32_t* kv_len,
+               const int32_t* prefix_table, int prefix_width, const int32_t* prefix_len, float sm_scale, int causal,
+               const TreeMask* tree, void* workspace, size_t workspace_bytes, void* stream) {
     int rc = check_page_cache(cache);
     if (rc != SAGE_OK) return rc;
     const int D = cache->D;
@@ -811,6 +826,11 @@ int sage_attn_paged(const sage_tensor* q, const sage_tensor* o, const sage_page_
     p.num_pages = cache->num_pages; p.page = cache->page_size;
     p.page_shift = 31 - __builtin_clz((unsigned)cache->page_size);
     p.causal = causal != 0;
+    if (tree != nullptr) {
+        p.mask = tree->words;
+        p.msb = tree->stride_b;
+        p.msn = tree->stride_n;
+    }
     const double scale = sm_scale > 0.f ? (double)sm_scale : 1.0 / std::sqrt((double)D);
     p.sc = (float)(scale * (1.0 / std::log(2.0)));
     p.rt = x.rt; p.join = x.join;
@@ -838,7 +858,7 @@ int sage_attn_paged(const sage_tensor* q, const sage_tensor* o, const sage_page_
     if (x.tiles) {
         p.workers = x.whole ? B * cache->heads * x.rt : tile_workers(sms, x.groups);
         if (x.pre) p.pre_rt = x.pre_items_rt;
-        e = launch_paged_tiles(p, D, x.groups, mq, mqp, mk, mv, s);
+        e = (tree != nullptr ? launch_paged_tiles_tree : launch_paged_tiles)(p, D, x.groups, mq, mqp, mk, mv, s);
         if (e == cudaSuccess && x.pre) e = D == 64 ? launch_join<64, 128, 128>(p, s) : launch_join<128, 128, 128>(p, s);
         launches = p.whole ? 1 : 2;
     } else {
@@ -851,12 +871,49 @@ int sage_attn_paged(const sage_tensor* q, const sage_tensor* o, const sage_page_
             p.beside = 1;
         }
         p.workers = std::min(2 * sms, kMaxRowWorkers / kRowWarps) * kRowWarps;
-        e = launch_rows(p, D, x.nr, s);
+        e = tree != nullptr ? launch_rows<true>(p, D, x.nr, s) : launch_rows<false>(p, D, x.nr, s);
         launches += p.split > 0 ? 1 : 2;
     }
     if (e != cudaSuccess) return SAGE_ERR_LAUNCH;
     set_last_launch_count(launches);
     return SAGE_OK;
+}
+
+}  // namespace
+}  // namespace sage
+
+using namespace sage;
+
+extern "C" {
+
+int sage_paged_workspace(int B, int H, int Hkv, int Nq, int D, size_t* bytes) {
+    if (bytes == nullptr) return SAGE_ERR_ARG;
+    const int rc = check_batch(B, H, Hkv, Nq, D);
+    if (rc != SAGE_OK) return rc;
+    // a prefix of any length may come: the form with a list of its own needs the most
+    *bytes = lists_bytes(make_lists(B, Hkv, H / Hkv, Nq, D, 0, INT32_MAX, 0), B, D);
+    const size_t alone = lists_bytes(make_lists(B, Hkv, H / Hkv, Nq, D, 0, 0, 0), B, D);
+    if (alone > *bytes) *bytes = alone;
+    return SAGE_OK;
+}
+
+int sage_attn_paged(const sage_tensor* q, const sage_tensor* o, const sage_page_cache* cache, int B, int H, int Nq,
+                    const int32_t* q_len, const int32_t* table, int64_t table_stride, int table_width,
+                    const int32_t* kv_len, const int32_t* prefix_table, int prefix_width, const int32_t* prefix_len,
+                    float sm_scale, int causal, void* workspace, size_t workspace_bytes, void* stream) {
+    return attn_paged(q, o, cache, B, H, Nq, q_len, table, table_stride, table_width, kv_len, prefix_table, prefix_width,
+                      prefix_len, sm_scale, causal, nullptr, workspace, workspace_bytes, stream);
+}
+
+int sage_attn_paged_tree(const sage_tensor* q, const sage_tensor* o, const sage_page_cache* cache, int B, int H, int Nq,
+                         const int32_t* q_len, const int32_t* table, int64_t table_stride, int table_width,
+                         const int32_t* kv_len, const int32_t* prefix_table, int prefix_width, const int32_t* prefix_len,
+                         const int32_t* mask, int64_t mask_stride_b, int64_t mask_stride_n, float sm_scale, void* workspace,
+                         size_t workspace_bytes, void* stream) {
+    if (mask == nullptr || mask_stride_b < 0 || mask_stride_n < 0) return SAGE_ERR_ARG;
+    const TreeMask tree{mask, mask_stride_b, mask_stride_n};
+    return attn_paged(q, o, cache, B, H, Nq, q_len, table, table_stride, table_width, kv_len, prefix_table, prefix_width,
+                      prefix_len, sm_scale, 0, &tree, workspace, workspace_bytes, stream);
 }
 
 }  // extern "C"

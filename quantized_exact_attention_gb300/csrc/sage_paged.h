@@ -46,6 +46,8 @@ struct PagedParams {
     const int32_t* table;                // device [B][table_stride], W entries used
     const int32_t* ptable;               // device [Wp]
     int64_t table_stride;
+    const int32_t* mask;                 // tree forms: which new tokens each row sees, 32 to a word
+    int64_t msb, msn;                    // request and row strides
     int B, H, Hkv, G, Nq;                // G = H / Hkv query heads to a key head
     int W, Wp;                           // table widths in pages (Wp = 0: no prefix)
     int num_pages, page, page_shift;     // tokens per page: a power of two
@@ -83,6 +85,9 @@ struct PagedParams {
 // tqp: of `pre_tok` requests (either may stand for one that no item uses).
 cudaError_t launch_paged_tiles(const PagedParams& p, int D, int groups, const CUtensorMap& tq, const CUtensorMap& tqp,
                                const CUtensorMap& tk, const CUtensorMap& tv, cudaStream_t s);
+// ... with a tree's mask (the shared prefix's items alone have none: either serves them).
+cudaError_t launch_paged_tiles_tree(const PagedParams& p, int D, int groups, const CUtensorMap& tq, const CUtensorMap& tqp,
+                                    const CUtensorMap& tk, const CUtensorMap& tv, cudaStream_t s);
 
 // Tensor map over one tensor of a page cache, box: one page of one head, 64 channels (sage_api.cu).
 int encode_pages(CUtensorMap* m, const sage_tensor& t, int D, int page, int heads, int pages);

@@ -175,7 +175,21 @@ __device__ __forceinline__ void stage_out(uint8_t* stage, const uint32_t (&w)[8]
 // the prefix's items in front, or an item for each CTA.
 enum TileForm { F_LIST, F_PREFIX, F_ITEM };
 
-template <int D, int kGroups, int kForm>
+// Bits t0 .. t0 + 63 of a row of a tree's mask (n new tokens): token t0 + k in
+// bit k of the two words.  The tokens before the first are seen, those behind
+// the last are not.
+__device__ __forceinline__ void tree_window(const int32_t* row, int t0, int n, uint32_t (&see)[2]) {
+    const int w = t0 >> 5, words = (n + 31) >> 5;
+    uint32_t x[3];
+#pragma unroll
+    for (int k = 0; k < 3; ++k) x[k] = w + k < 0 ? 0xffffffffu : w + k < words ? (uint32_t)row[w + k] : 0u;
+    see[0] = __funnelshift_r(x[0], x[1], t0 & 31);
+    see[1] = __funnelshift_r(x[1], x[2], t0 & 31);
+}
+// The lowest `many` bits.
+__device__ __forceinline__ uint32_t lowest(int many) { return many >= 32 ? 0xffffffffu : many <= 0 ? 0u : (1u << many) - 1u; }
+
+template <int D, int kGroups, int kForm, bool kTree>
 __global__ void __launch_bounds__(TilesShape<D, kGroups>::kThreads, TilesShape<D, kGroups>::kCtasPerSm)
 paged_tiles_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_qp,
                    const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
@@ -285,6 +299,16 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                 const PagedSpan span = paged_span(sched, ib, len, tile);
                 // keys of this half that this row sees (may be negative)
                 const int lim = (span.own ? min(span.nkeys, lim_own - span.key0) : span.nkeys) - half * 64;
+                uint32_t see[2] = {lowest(lim), lowest(lim - 32)};         // kTree: keys this row sees
+                if constexpr (kTree) {
+                    const int t0 = span.key0 + half * 64 - (len - nt.n);   // new token that the first key is of
+                    if (span.own && t0 > -64 && valid) {
+                        uint32_t bits[2];
+                        tree_window(p.mask + rb * p.msb + ri * p.msn, t0, nt.n, bits);
+                        see[0] &= bits[0];
+                        see[1] &= bits[1];
+                    }
+                }
                 if (!mbar_wait_warp(bar(L::B_S + X), t & 1, abort_flag)) { ok = false; break; }
                 tc_fence_after();
                 uint32_t s[2][32];
@@ -299,13 +323,13 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                 float f = 1.f;
                 bool rescale = false;
                 if (active) {
-                    if (!__all_sync(0xffffffffu, lim >= 64)) {
+                    if (!__all_sync(0xffffffffu, kTree ? (see[0] & see[1]) == 0xffffffffu : lim >= 64)) {
                         mx = -INFINITY;
 #pragma unroll
                         for (int a = 0; a < 2; ++a)
 #pragma unroll
                             for (int i = 0; i < 32; ++i) {
-                                if (a * 32 + i >= lim) s[a][i] = 0xFF800000u;      // -inf
+                                if (kTree ? !(see[a] >> i & 1) : a * 32 + i >= lim) s[a][i] = 0xFF800000u;     // -inf
                                 mx = fmaxf(mx, __uint_as_float(s[a][i]));
                             }
                     }
@@ -725,12 +749,12 @@ __global__ void __launch_bounds__(256) paged_cuts_kernel(const __grid_constant__
     }
 }
 
-template <int D, int kGroups, int kForm>
+template <int D, int kGroups, int kForm, bool kTree>
 cudaError_t launch_one(const PagedParams& p, const CUtensorMap& tq, const CUtensorMap& tqp, const CUtensorMap& tk,
                        const CUtensorMap& tv, cudaStream_t s) {
     using L = TilesShape<D, kGroups>;
     static bool ready[64] = {};
-    cudaError_t e = launch_pdl(paged_tiles_kernel<D, kGroups, kForm>, dim3((unsigned)p.workers), dim3(L::kThreads), L::kSmem, s, 1, true, ready,
+    cudaError_t e = launch_pdl(paged_tiles_kernel<D, kGroups, kForm, kTree>, dim3((unsigned)p.workers), dim3(L::kThreads), L::kSmem, s, 1, true, ready,
                                tq, tqp, tk, tv, p);
     if (e != cudaSuccess) return e;
     if (kForm == F_LIST && p.workers > 1) {
@@ -740,22 +764,37 @@ cudaError_t launch_one(const PagedParams& p, const CUtensorMap& tq, const CUtens
     return e;
 }
 
-template <int D, int kGroups>
+template <int D, int kGroups, bool kTree>
 cudaError_t launch_form(int form, const PagedParams& p, const CUtensorMap& tq, const CUtensorMap& tqp, const CUtensorMap& tk,
                         const CUtensorMap& tv, cudaStream_t s) {
-    if (form == F_ITEM) return launch_one<D, kGroups, F_ITEM>(p, tq, tqp, tk, tv, s);
-    if (form == F_PREFIX) return launch_one<D, kGroups, F_PREFIX>(p, tq, tqp, tk, tv, s);
-    return launch_one<D, kGroups, F_LIST>(p, tq, tqp, tk, tv, s);
+    if (form == F_ITEM) return launch_one<D, kGroups, F_ITEM, kTree>(p, tq, tqp, tk, tv, s);
+    if (form == F_PREFIX) return launch_one<D, kGroups, F_PREFIX, kTree>(p, tq, tqp, tk, tv, s);
+    return launch_one<D, kGroups, F_LIST, kTree>(p, tq, tqp, tk, tv, s);
+}
+
+template <bool kTree>
+cudaError_t launch_tiles(const PagedParams& p, int D, int groups, const CUtensorMap& tq, const CUtensorMap& tqp,
+                         const CUtensorMap& tk, const CUtensorMap& tv, cudaStream_t s) {
+    const int form = p.whole ? F_ITEM : p.pre_rt > 0 ? F_PREFIX : F_LIST;
+    if (D == 64)
+        return groups == 1 ? launch_form<64, 1, kTree>(form, p, tq, tqp, tk, tv, s)
+                           : launch_form<64, 2, kTree>(form, p, tq, tqp, tk, tv, s);
+    return groups == 1 ? launch_form<128, 1, kTree>(form, p, tq, tqp, tk, tv, s)
+                       : launch_form<128, 2, kTree>(form, p, tq, tqp, tk, tv, s);
 }
 
 }  // namespace
 
+#ifndef SAGE_PAGED_TILES_TREE
 cudaError_t launch_paged_tiles(const PagedParams& p, int D, int groups, const CUtensorMap& tq, const CUtensorMap& tqp,
                                const CUtensorMap& tk, const CUtensorMap& tv, cudaStream_t s) {
-    const int form = p.whole ? F_ITEM : p.pre_rt > 0 ? F_PREFIX : F_LIST;
-    if (D == 64)
-        return groups == 1 ? launch_form<64, 1>(form, p, tq, tqp, tk, tv, s) : launch_form<64, 2>(form, p, tq, tqp, tk, tv, s);
-    return groups == 1 ? launch_form<128, 1>(form, p, tq, tqp, tk, tv, s) : launch_form<128, 2>(form, p, tq, tqp, tk, tv, s);
+    return launch_tiles<false>(p, D, groups, tq, tqp, tk, tv, s);
 }
+#else
+cudaError_t launch_paged_tiles_tree(const PagedParams& p, int D, int groups, const CUtensorMap& tq, const CUtensorMap& tqp,
+                                    const CUtensorMap& tk, const CUtensorMap& tv, cudaStream_t s) {
+    return launch_tiles<true>(p, D, groups, tq, tqp, tk, tv, s);
+}
+#endif
 
 }  // namespace sage

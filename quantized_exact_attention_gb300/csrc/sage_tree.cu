@@ -1,0 +1,225 @@
+// sage_tree.cu - bookkeeping of a tree of drafted tokens on the GPU: which
+// tokens each of them sees, from the tree's parents, and the move of the
+// accepted tokens' cache rows to the front.
+#include <algorithm>
+
+#include "sage_gb300.h"
+#include "sage_internal.h"
+#include "sage_paged.h"
+
+namespace sage {
+namespace {
+
+// ---------------------------------------------------------------------------
+// Tree tables: see(i) = {i} u see(parent(i)), depth(i) = |see(i)| - 1.
+//
+// A thread walks from its token to the root.  Parents come before their
+// children, so the tokens fall, and a row's words are complete from the last to
+// the first.  A block holds the parents of its tokens in shared memory: those
+// of several requests where trees are small, up to its last token's of one
+// where they are large.
+// ---------------------------------------------------------------------------
+constexpr int kTreeThreads = 256;
+constexpr int kTreeTokens = 4096;        // of a request, at most: their parents take 16 KB
+
+struct TreeParams {
+    const int32_t* parents;
+    const int32_t* n_len;                // or null: N
+    int32_t* mask;
+    int32_t* depth;                      // or null
+    int64_t psb, msb, msn, dsb;
+    int B, N, W;
+    int pack;                            // requests of a block (1: a block takes 256 tokens of one)
+};
+
+__global__ void __launch_bounds__(kTreeThreads) tree_tables_kernel(const __grid_constant__ TreeParams p) {
+    __shared__ int up[kTreeTokens];
+    pdl_trigger();
+    pdl_wait();
+    const int t = threadIdx.x;
+    int b, i, base = 0;                                    // base: of the request's parents in `up`
+    if (p.pack > 1) {
+        const int r = t / p.N;
+        b = (int)blockIdx.x * p.pack + r;
+        i = t - r * p.N;
+        base = r * p.N;
+        if (r >= p.pack) b = p.B;
+    } else {
+        b = blockIdx.x;
+        i = (int)blockIdx.y * kTreeThreads + t;
+    }
+    const bool row = b < p.B && i < p.N;
+    const int n = row && p.n_len != nullptr ? p.n_len[b] : p.N;
+    // a token whose parent is not one before it has none
+    if (p.pack > 1) {
+        if (row) {
+            const int x = p.parents[b * p.psb + i];
+            up[t] = x < i ? x : -1;
+        }
+    } else {
+        const int last = min(p.N, ((int)blockIdx.y + 1) * kTreeThreads);
+        for (int j = t; j < last; j += kTreeThreads) {
+            const int x = p.parents[b * p.psb + j];
+            up[j] = x < j ? x : -1;
+        }
+    }
+    __syncthreads();
+    if (!row) return;
+    int32_t* m = p.mask + b * p.msb + i * p.msn;
+    int at = i < n ? i : -1, seen = 0;
+#pragma unroll 1
+    for (int w = p.W - 1; w >= 0; --w) {
+        uint32_t bits = 0;
+        while (at >= 32 * w && at >= 0) {
+            bits |= 1u << (at & 31);
+            ++seen;
+            at = up[base + at];
+        }
+        m[w] = (int32_t)bits;
+    }
+    if (p.depth != nullptr) p.depth[b * p.dsb + i] = max(seen - 1, 0);
+}
+
+// ---------------------------------------------------------------------------
+// Keep: the rows of token kept[b][i] move to the place of token i, for
+// i = 0, 1, ... in order.  A thread moves one 16-byte column of a K or V row
+// through all moves of its request, so the order holds without a barrier; eight
+// moves are in flight at a time where none of them reads what another of
+// them writes.
+// ---------------------------------------------------------------------------
+struct KeepParams {
+    const int32_t* kept;
+    const int32_t* slots;
+    uint16_t* ck;
+    uint16_t* cv;
+    int* status;
+    int64_t kept_stride, slots_stride, capacity;
+    int64_t ckp, ckh, ckt, cvp, cvh, cvt;
+    int N, K, columns, chunk_shift;      // columns: 16-byte columns of a token's K rows
+    int page, page_shift;
+};
+
+constexpr int kKeepThreads = 128;
+
+__global__ void __launch_bounds__(kKeepThreads) cache_keep_kernel(const __grid_constant__ KeepParams p) {
+    pdl_trigger();
+    pdl_wait();
+    const int b = blockIdx.x, lane = threadIdx.x & 31;
+    int col = (int)blockIdx.y * kKeepThreads + threadIdx.x;
+    const bool live = col < 2 * p.columns;
+    const bool is_v = col >= p.columns;
+    if (is_v) col -= p.columns;
+    const int h = col >> p.chunk_shift, c = (col - (h << p.chunk_shift)) * 8;
+    uint16_t* base = (is_v ? p.cv + h * p.cvh : p.ck + h * p.ckh) + c;
+    const int64_t sp = is_v ? p.cvp : p.ckp, st = is_v ? p.cvt : p.ckt;
+    const int32_t* slots = p.slots + b * p.slots_stride;
+    auto row = [&](int slot) -> uint16_t* {
+        return base + (int64_t)(slot >> p.page_shift) * sp + (int64_t)(slot & (p.page - 1)) * st;
+    };
+    constexpr int kFlight = 8;
+#pragma unroll 1
+    for (int i0 = 0; i0 < p.K; i0 += 32) {                 // a lane looks one move up
+        int src = -1, dst = -1;
+        if (i0 + lane < p.K) {
+            const int t = p.kept[b * p.kept_stride + i0 + lane];
+            if (t >= 0 && t < p.N) {
+                src = slots[t];
+                dst = slots[i0 + lane];
+            }
+        }
+        for (int s : {src, dst})
+            if (s >= p.capacity && atomicCAS(p.status, 0, kErrPage) == 0) p.status[3] = s >> p.page_shift;
+        if (src < 0 || dst < 0 || src >= p.capacity || dst >= p.capacity || src == dst) src = dst = -1;
+        const int many = min(32, p.K - i0);
+#pragma unroll 1
+        for (int g = 0; g < many; g += kFlight) {
+            // does a move of these eight read what one before it writes?
+            bool reads = false;
+#pragma unroll
+            for (int u = 0; u + 1 < kFlight; ++u) {
+                const int d = __shfl_sync(0xffffffffu, dst, g + u);
+                reads |= lane > g + u && lane < g + kFlight && src >= 0 && src == d;
+            }
+            if (__any_sync(0xffffffffu, reads)) {
+#pragma unroll 1
+                for (int u = 0; u < kFlight; ++u) {
+                    const int s = __shfl_sync(0xffffffffu, src, g + u), d = __shfl_sync(0xffffffffu, dst, g + u);
+                    if (live && s >= 0) *reinterpret_cast<uint4*>(row(d)) = *reinterpret_cast<const uint4*>(row(s));
+                }
+                continue;
+            }
+            uint4 x[kFlight];
+#pragma unroll
+            for (int u = 0; u < kFlight; ++u) {
+                const int s = __shfl_sync(0xffffffffu, src, g + u);
+                if (live && s >= 0) x[u] = *reinterpret_cast<const uint4*>(row(s));
+            }
+#pragma unroll
+            for (int u = 0; u < kFlight; ++u) {
+                const int d = __shfl_sync(0xffffffffu, dst, g + u);
+                if (live && d >= 0) *reinterpret_cast<uint4*>(row(d)) = x[u];
+            }
+        }
+    }
+}
+
+}  // namespace
+}  // namespace sage
+
+using namespace sage;
+
+extern "C" {
+
+int sage_tree_tables(const int32_t* parents, int64_t parents_stride, int B, int N, const int32_t* n_len, int32_t* mask,
+                     int64_t mask_stride_b, int64_t mask_stride_n, int32_t* depth, int64_t depth_stride, void* stream) {
+    if (B <= 0 || N <= 0 || parents == nullptr || mask == nullptr || parents_stride < 0) return SAGE_ERR_ARG;
+    if (N > kTreeTokens) return SAGE_ERR_UNSUPPORTED;
+    const int W = (N + 31) / 32;
+    // rows written once
+    if ((N > 1 && mask_stride_n < W) || (B > 1 && mask_stride_b < W) || (B > 1 && depth != nullptr && depth_stride < N))
+        return SAGE_ERR_ARG;
+    TreeParams p{};
+    p.parents = parents; p.psb = parents_stride; p.n_len = n_len;
+    p.mask = mask; p.msb = mask_stride_b; p.msn = mask_stride_n;
+    p.depth = depth; p.dsb = depth_stride;
+    p.B = B; p.N = N; p.W = W;
+    p.pack = std::max(1, kTreeThreads / N);
+    static bool ready[64] = {};
+    const dim3 grid((unsigned)ceil_div(B, p.pack), (unsigned)ceil_div(N, kTreeThreads));
+    if (launch_pdl(tree_tables_kernel, grid, dim3(kTreeThreads), 0, static_cast<cudaStream_t>(stream), 1, false, ready, p) !=
+        cudaSuccess)
+        return SAGE_ERR_LAUNCH;
+    set_last_launch_count(1);
+    return SAGE_OK;
+}
+
+int sage_cache_keep(const int32_t* kept, int64_t kept_stride, int B, int K, const int32_t* slots, int64_t slots_stride, int N,
+                    const sage_page_cache* cache, void* stream) {
+    const int rc = check_page_cache(cache);
+    if (rc != SAGE_OK) return rc;
+    if (B <= 0 || K <= 0 || N < K || kept == nullptr || slots == nullptr || kept_stride < 0 || slots_stride < 0)
+        return SAGE_ERR_ARG;
+    KeepParams p{};
+    p.status = device_status_ptr();
+    if (p.status == nullptr) return SAGE_ERR_LAUNCH;
+    p.kept = kept; p.kept_stride = kept_stride; p.slots = slots; p.slots_stride = slots_stride;
+    p.ck = static_cast<uint16_t*>(const_cast<void*>(cache->k.ptr));
+    p.cv = static_cast<uint16_t*>(const_cast<void*>(cache->v.ptr));
+    p.ckp = cache->k.stride_b; p.ckh = cache->k.stride_h; p.ckt = cache->k.stride_n;
+    p.cvp = cache->v.stride_b; p.cvh = cache->v.stride_h; p.cvt = cache->v.stride_n;
+    p.capacity = (int64_t)cache->num_pages * cache->page_size;
+    p.N = N; p.K = K;
+    p.chunk_shift = cache->D == 128 ? 4 : 3;
+    p.columns = cache->heads << p.chunk_shift;
+    p.page = cache->page_size;
+    p.page_shift = 31 - __builtin_clz((unsigned)cache->page_size);
+    static bool ready[64] = {};
+    const dim3 grid((unsigned)B, (unsigned)ceil_div(2 * (int64_t)p.columns, kKeepThreads));
+    if (launch_pdl(cache_keep_kernel, grid, dim3(kKeepThreads), 0, static_cast<cudaStream_t>(stream), 1, false, ready, p) !=
+        cudaSuccess)
+        return SAGE_ERR_LAUNCH;
+    set_last_launch_count(1);
+    return SAGE_OK;
+}
+
+}  // extern "C"

@@ -1,0 +1,284 @@
+"""Rotary positions and the append that rotates, against their definition in 64 bits."""
+import random
+
+import pytest
+import torch
+
+import quantized_exact_attention_gb300 as S
+from tests import gpu_support as G
+from tests import tree_support as T
+
+pytestmark = pytest.mark.gpu
+
+
+def randn(*shape, seed=0):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    return torch.randn(shape, device="cuda", generator=g).to(torch.bfloat16)
+
+
+def view(B, H, N, D, layout, seed=0):
+    """A [B, H, N, D] view in one of the memory orders."""
+    if layout == "nhd":
+        return randn(B, N, H, D, seed=seed).permute(0, 2, 1, 3)
+    if layout == "hnd":
+        return randn(B, H, N, D, seed=seed)
+    return randn(B, N, H, 3, D, seed=seed)[:, :, :, 1].permute(0, 2, 1, 3)     # one third of a fused projection
+
+
+def blank(B, H, N, D, fill=7.0):
+    return torch.full((B, N, H, D), fill, dtype=torch.bfloat16, device="cuda").permute(0, 2, 1, 3)
+
+
+def check_rope(x, out, r, f, positions, n_len=None, inverse=False, fill=7.0):
+    torch.cuda.synchronize()
+    B, H, N, D = x.shape
+    want, off = T.turned(x, T.angles(positions, f), 2 * len(f), r.interleaved, r.amplitude, inverse)
+    for b in range(B):
+        n = N if n_len is None else min(max(n_len[b], 0), N)
+        T.near(out[b, :, :n], want[b, :, :n], off[b, :, :n])
+        assert torch.equal(out[b, :, :n, 2 * len(f):], x[b, :, :n, 2 * len(f):])
+        assert bool((out[b, :, n:] == fill).all()), "rows behind n_len were written"
+
+
+@pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("inverse", [False, True])
+@pytest.mark.parametrize("D,rd", [(64, 64), (64, 16), (64, 48), (128, 128), (128, 64), (128, 16), (128, 112)])
+@pytest.mark.parametrize("layout", ["nhd", "hnd", "fused"])
+def test_parts_and_layouts(D, rd, interleaved, inverse, layout):
+    G.ensure_built()
+    B, H, N = 2, 5, 37
+    f = S.rotary_frequencies(rd)[0]
+    r = S.make_rotary(f, interleaved=interleaved, amplitude=1.25)
+    x, out = view(B, H, N, D, layout), blank(B, H, N, D)
+    S.sage_rope(x, out, r, inverse=inverse)
+    check_rope(x, out, r, f, [range(N)] * B, inverse=inverse)
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("B,H,N", [(1, 1, 1), (3, 1, 33), (1, 2, 7), (5, 3, 1), (2, 8, 19), (1, 24, 65), (2, 33, 3), (64, 32, 1),
+                                   (1, 9, 700), (130, 1, 17)])
+@pytest.mark.parametrize("interleaved", [False, True])
+def test_heads_and_tokens(B, H, N, D, interleaved):
+    G.ensure_built()
+    f = S.rotary_frequencies(D, 500000.0)[0]
+    r = S.make_rotary(f, interleaved=interleaved)
+    x, out = view(B, H, N, D, "nhd", seed=H), blank(B, H, N, D)
+    start = [(977 * b) % 5000 for b in range(B)]
+    S.sage_rope(x, out, r, start=T.i32(start))
+    check_rope(x, out, r, f, [range(s, s + N) for s in start])
+
+
+@pytest.mark.parametrize("interleaved", [False, True])
+def test_positions(interleaved):
+    """Given for each token, for all requests, strided, negative, far, with and without a start, rows behind n_len."""
+    G.ensure_built()
+    B, H, N, D = 4, 3, 21, 64
+    f = S.rotary_frequencies(D)[0]
+    r = S.make_rotary(f, interleaved=interleaved)
+    x = view(B, H, N, D, "nhd")
+    rnd = random.Random(1)
+    far = [2 ** 31 - 1, -2 ** 31, 2 ** 30 + 7, -1, 0, 1, 10 ** 6 + 3, 123456789]
+    pos = [[rnd.choice(far + [rnd.randrange(1 << 20)]) for _ in range(N)] for _ in range(B)]
+    start, n_len = [0, 100000, -5, 2 ** 31 - 1], [N, 0, N - 4, N + 9]
+    for at, shared in ((T.i32(pos), False), (T.i32(pos[1]), True),
+                       (torch.cat((T.i32(pos), T.i32(pos)), 1)[:, :N], False), (T.i32(pos[2])[None].expand(B, N), None)):
+        rows = pos if shared is False else [pos[1 if shared else 2]] * B
+        out = blank(B, H, N, D)
+        S.sage_rope(x, out, r, positions=at)
+        check_rope(x, out, r, f, rows)
+        out = blank(B, H, N, D)
+        S.sage_rope(x, out, r, positions=at, start=T.i32(start), n_len=T.i32(n_len))
+        check_rope(x, out, r, f, [[s + p for p in row] for s, row in zip(start, rows)], n_len)
+    out = S.rope(x, r, n_len=T.i32([-3, 1, 2, N]))
+    check_rope(x, out, r, f, [range(N)] * B, [-3, 1, 2, N], fill=0.0)
+
+
+@pytest.mark.parametrize("rd", [32, 64])
+@pytest.mark.parametrize("layout", ["nhd", "hnd"])
+def test_in_place(rd, layout):
+    G.ensure_built()
+    f = S.rotary_frequencies(rd)[0]
+    for interleaved in (False, True):
+        r = S.make_rotary(f, interleaved=interleaved)
+        x = view(3, 6, 50, 64, layout)
+        apart = blank(3, 6, 50, 64)
+        S.sage_rope(x, apart, r)
+        S.sage_rope(x, x, r)
+        torch.cuda.synchronize()
+        assert torch.equal(x, apart)
+
+
+def test_forms_of_one_call_agree_bit_for_bit():
+    """The split of heads among warps and the place of a token in its warp change nothing."""
+    G.ensure_built()
+    f = S.rotary_frequencies(128)[0]
+    r = S.make_rotary(f, interleaved=False)
+    x = view(2, 40, 300, 128, "nhd")
+    whole = S.rope(x, r)
+    for h in (1, 3, 40):
+        for n in (1, 7, 300):
+            part = S.rope(x[:, :h, :n], r)
+            assert torch.equal(part, whole[:, :h, :n])
+
+
+def test_special_values_stay_in_their_pair():
+    G.ensure_built()
+    f = S.rotary_frequencies(32)[0]
+    for interleaved in (False, True):
+        r = S.make_rotary(f, interleaved=interleaved)
+        x = view(1, 2, 4, 64, "nhd")
+        first, second = (6, 7) if interleaved else (3, 19)
+        x[0, 0, 1, first] = float("nan")
+        x[0, 1, 2, second] = float("inf")
+        x[0, 0, 3, 40] = float("nan")                       # behind the rotated channels
+        x[0, 1, 3, 41] = float("-inf")
+        clean = torch.where(torch.isfinite(x), x, torch.zeros_like(x))
+        y, z = S.rope(x, r), S.rope(clean, r)
+        touched = torch.zeros_like(x, dtype=torch.bool)
+        for h, n in ((0, 1), (1, 2)):
+            touched[0, h, n, first] = touched[0, h, n, second] = True
+        touched[0, 0, 3, 40] = touched[0, 1, 3, 41] = True
+        assert torch.equal(y[~touched], z[~touched])
+        assert not bool(torch.isfinite(y[touched]).any())
+        assert torch.equal(y[..., 32:].contiguous().view(torch.int16), x[..., 32:].contiguous().view(torch.int16))
+
+
+def test_gradient():
+    """The inverse is the gradient's map: against the formula's gradient, and against differences of the forward map."""
+    G.ensure_built()
+    B, H, N, D, rd = 2, 4, 30, 64, 48
+    f, a = S.rotary_frequencies(rd, scale=8.0, method="parts")
+    for interleaved in (False, True):
+        r = S.make_rotary(f, interleaved=interleaved, amplitude=a)
+        x, g = view(B, H, N, D, "nhd", seed=1), view(B, H, N, D, "hnd", seed=2)
+        pos = [range(1000, 1000 + N)] * B
+        dx = S.rope(g, r, start=T.i32([1000] * B), inverse=True)
+        angle = T.angles(pos, f)
+        leaf = x.double().requires_grad_()
+        R, half = rd, rd // 2
+        c, s = a * torch.cos(angle)[:, None], a * torch.sin(angle)[:, None]
+        p, q = (leaf[..., 0:R:2], leaf[..., 1:R:2]) if interleaved else (leaf[..., :half], leaf[..., half:R])
+        pair = (p * c - q * s, p * s + q * c)
+        y = torch.cat((torch.stack(pair, -1).flatten(-2) if interleaved else torch.cat(pair, -1), leaf[..., R:]), -1)
+        y.backward(g.double())
+        _, off = T.turned(g, angle, rd, interleaved, a, True)
+        T.near(dx, leaf.grad, off)
+        # <g, rope(x + e) - rope(x - e)> / 2 = <dx, e>, for steps e = one channel of one row that BF16 holds: each side is
+        # off by its roundings, of outputs below 2 * 8 in size here
+        for b, h, n, ch in ((0, 0, 0, 0), (1, 3, 29, 47), (0, 2, 11, 24), (1, 1, 5, 63)):
+            e = torch.zeros_like(x)
+            e[b, h, n, ch] = 4.0
+            base = torch.zeros_like(x)
+            up, down = S.rope(base + e, r, start=T.i32([1000] * B)), S.rope(base - e, r, start=T.i32([1000] * B))
+            assert torch.equal(up, -down)                   # the map is odd, so the differences are exact
+            slope = (g.double() * (up.double() - down.double())).sum() / 8.0
+            # two outputs of size up to 4 A, each rounded to BF16, times g; dx rounded itself
+            tol = 2.0 ** -8 * a * 2 * float(g[b, h, n].abs().max()) + float(dx[b, h, n, ch].abs()) * 2.0 ** -8 + 1e-4
+            assert abs(float(slope) - float(dx[b, h, n, ch])) <= tol
+        back = S.rope(S.rope(x, r, start=T.i32([1000] * B)), r, start=T.i32([1000] * B), inverse=True)
+        want = x.double().clone()
+        want[..., :rd] *= a * a
+        size = T.turned(x, angle, rd, interleaved, a)[1] * 2.0 ** 21          # A (|x1| + |x2|)
+        tol = (a * size + want.abs()) * (2.0 ** -8 * 1.02 + 2.0 ** -19)
+        assert bool(((back.double() - want).abs() <= tol).all())
+
+
+def test_far_strides():
+    """Rows over 2^31 elements apart, in the input and in the output."""
+    G.ensure_built()
+    apart = (1 << 31) + 1024
+    buf = torch.empty(apart + 4096, dtype=torch.bfloat16, device="cuda")
+    x = torch.as_strided(buf, (2, 2, 5, 128), (apart, 128, 256, 1))
+    src = randn(2, 2, 5, 128, seed=3)
+    x.copy_(src)
+    f = S.rotary_frequencies(128)[0]
+    r = S.make_rotary(f)
+    want = S.rope(src, r)
+    assert torch.equal(S.rope(x, r), want)
+    S.sage_rope(src, x, r)
+    torch.cuda.synchronize()
+    assert torch.equal(x, want)
+
+
+@pytest.mark.parametrize("layout", ["nhd", "hnd"])
+@pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("B,H,N,D,page,rd", [(1, 1, 1, 64, 16, 64), (64, 8, 1, 128, 16, 128), (5, 2, 40, 128, 32, 64),
+                                             (3, 16, 33, 64, 64, 16), (2, 3, 130, 128, 128, 96), (1, 24, 300, 128, 64, 128)])
+def test_append(B, H, N, D, page, rd, interleaved, layout):
+    """Keys land as sage_rope leaves them, values as they are; every other row of the cache stays."""
+    G.ensure_built()
+    f = S.rotary_frequencies(rd)[0]
+    r = S.make_rotary(f, interleaved=interleaved, amplitude=0.75)
+    n_pages = B * -(-N // page) + 3
+    shape = (n_pages, page, H, D) if layout == "nhd" else (n_pages, H, page, D)
+    ck, cv = randn(*shape, seed=1), randn(*shape, seed=2)
+    cache = S.PageCache(*(t.permute(0, 2, 1, 3) if layout == "nhd" else t for t in (ck, cv)))
+    kv = randn(B, N, 2, H, D, seed=3)
+    k, v = kv[:, :, 0].permute(0, 2, 1, 3), kv[:, :, 1].permute(0, 2, 1, 3)
+    slots = torch.randperm(n_pages * page, generator=torch.Generator().manual_seed(N))[:B * N].to(torch.int32).reshape(B, N)
+    slots[:, N // 2::5] = -1                               # tokens without a place
+    if N > 1:
+        slots[0, 0] = 5
+        slots[slots == 5] = 5
+    pos = torch.randint(0, 1 << 20, (B, N), dtype=torch.int32, device="cuda", generator=torch.Generator(device="cuda").manual_seed(N))
+    start = T.i32([3 * b for b in range(B)])
+    want_k, want_v = cache.k.clone(), cache.v.clone()
+    rot = S.rope(k, r, positions=pos, start=start)
+    for b in range(B):
+        for i in range(N):
+            s = int(slots[b, i])
+            if s >= 0 and not (s == 5 and (b, i) != (0, 0)):
+                want_k[s // page, :, s % page], want_v[s // page, :, s % page] = rot[b, :, i], v[b, :, i]
+    slots[(slots == 5).logical_and(torch.arange(B * N).reshape(B, N) > 0)] = -1
+    S.sage_cache_append_rope(k, v, slots.cuda(), cache, r, positions=pos, start=start)
+    torch.cuda.synchronize()
+    assert S.sage_get_device_status() == S.SAGE_OK
+    assert torch.equal(cache.k, want_k) and torch.equal(cache.v, want_v)
+
+
+def test_append_outside_the_cache_is_recorded():
+    G.ensure_built()
+    r = S.make_rotary(S.rotary_frequencies(64)[0])
+    cache = S.alloc_page_cache(4, 16, 2, 64)
+    cache.k.fill_(3.0)
+    cache.v.fill_(3.0)
+    k = randn(1, 2, 3, 64)
+    S.sage_cache_append_rope(k, k, T.i32([[7, 64, 2 ** 31 - 1]]), cache, r)
+    assert S.sage_get_device_status() == S.SAGE_ERR_PAGE
+    assert S.sage_get_device_status() == S.SAGE_OK
+    assert torch.equal(cache.v[0, :, 7], k[0, :, 0])
+    assert torch.equal(cache.k[0, :, 7], S.rope(k, r)[0, :, 0])
+    rest = torch.ones((4, 16), dtype=torch.bool, device="cuda")
+    rest[0, 7] = False
+    for t in (cache.k, cache.v):
+        assert bool((t.permute(0, 2, 1, 3)[rest] == 3.0).all())
+
+
+def test_other_streams_and_graphs():
+    """Calls on streams of their own, and one graph replayed with other positions."""
+    G.ensure_built()
+    B, H, N, D = 3, 8, 50, 128
+    r = S.make_rotary(S.rotary_frequencies(D)[0])
+    xs = [view(B, H, N, D, "nhd", seed=s) for s in range(4)]
+    starts = [T.i32([s * 100 + b for b in range(B)]) for s in range(4)]
+    want = [S.rope(x, r, start=s) for x, s in zip(xs, starts)]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in xs]
+    outs = [blank(B, H, N, D) for _ in xs]
+    torch.cuda.synchronize()
+    for _ in range(3):
+        for x, s, o, st in zip(xs, starts, outs, streams):
+            S.sage_rope(x, o, r, start=s, stream=st)
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(outs, want))
+    x, start, out = xs[0].clone(), starts[0].clone(), blank(B, H, N, D)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        S.sage_rope(x, out, r, start=start)
+    for k in (2, 1, 3):
+        x.copy_(xs[k])
+        start.copy_(starts[k])
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, want[k])
