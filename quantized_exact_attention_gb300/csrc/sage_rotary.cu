@@ -8,7 +8,7 @@
 // integer product that wraps by itself, so a far position loses nothing: the
 // error is below |pos| * 2^-65 turns from the frequency and 2^-32 from taking
 // the upper half, where an FP32 product pos * f_j would be off by 0.06 rad at
-// pos = 10^6.  sine and cosine are FP32 of that angle, the products and their
+// pos = 10^6.  Sine and cosine are FP32 of that angle, the products and their
 // sum FP32; the result is rounded to BF16 once.
 #include <algorithm>
 #include <cmath>
@@ -16,6 +16,7 @@
 #include "sage_gb300.h"
 #include "sage_internal.h"
 #include "sage_paged.h"
+#include "sage_paged_sched.cuh"
 
 namespace sage {
 namespace {
@@ -27,8 +28,12 @@ namespace {
 //   interleaved layout  pair j = channels 2j and 2j + 1: a chunk holds 4 pairs;
 //                       the same two chunks hold pairs 4u.. and 4(u + R/16)..
 //   channels >= R       units behind R/16 copy two chunks each
-// D/16 lanes hold a head, `slots` heads of a token lie beside each other, and
-// what is left of a warp's 32 lanes takes further tokens.
+// D/16 lanes hold a head, up to 2^slot_shift heads of a token lie beside each
+// other, and what is left of a warp's 32 lanes takes further tokens.  A lane has
+// the chunks of kFlight heads in flight: of one token, or where a token has too
+// few, of kTokens tokens (one head of 393,216 tokens, 201 MB: 62.6 us with a
+// token at a time, 51.7 so, and 44.6 with the sines below in place of
+// sincospif: 64 of them for every 512 bytes).
 struct Turn {
     const int32_t* positions;            // [B][pos_stride] or null: the token's number
     const int32_t* start;                // [B] or null: 0
@@ -41,57 +46,84 @@ struct Turn {
     int splits, heads_each;              // warps that share a token's heads, heads of one
     int64_t tokens;                      // B * N, below 2^31
     int N, H;
+    FastDiv by_N;
 };
 
 // What a lane has to do.
 struct LaneWork {
-    int b, i;                            // request and token
+    int64_t first;                       // its first token; the next one is `apart` behind
+    int apart;
     int unit, c0, c1;                    // its unit and the channels its two chunks begin at
     int h0, h1, step;                    // heads h0, h0 + step, ... below h1
-    bool live, rotates;
+    bool rotates;
 };
 
 constexpr int kRotaryThreads = 256;
 
-__device__ __forceinline__ LaneWork lane_work(const Turn& p, int64_t warp, int D) {
+template <int kTokens>
+__device__ __forceinline__ LaneWork lane_work(const Turn& p) {
     LaneWork x;
+    const int64_t warp = (int64_t)blockIdx.x * (kRotaryThreads / 32) + (threadIdx.x >> 5);
     const int lane = threadIdx.x & 31, slots = 1 << p.slot_shift, units = 1 << p.unit_shift;
     const uint32_t group = p.splits == 1 ? (uint32_t)warp : (uint32_t)warp / (uint32_t)p.splits;
     const int split = (int)((uint32_t)warp - group * (uint32_t)p.splits);
-    const int per_warp_shift = 5 - p.unit_shift - p.slot_shift;
-    const int64_t t = ((int64_t)group << per_warp_shift) + (lane >> (p.unit_shift + p.slot_shift));
-    x.live = t < p.tokens;
-    x.b = (int)((uint32_t)t / (uint32_t)p.N);
-    x.i = (int)(t - (int64_t)x.b * p.N);
+    x.apart = 32 >> (p.unit_shift + p.slot_shift);
+    x.first = (int64_t)group * kTokens * x.apart + (lane >> (p.unit_shift + p.slot_shift));
     x.unit = lane & (units - 1);
     x.rotates = x.unit < p.rot_units;
-    const int apart = x.rotates ? p.rot_units : units - p.rot_units;
-    const int first = x.rotates ? x.unit : p.rot_units + x.unit;         // chunks 2 rot_units.. are copied
-    x.c0 = first * 8;
-    x.c1 = (first + apart) * 8;
+    const int between = x.rotates ? p.rot_units : units - p.rot_units;
+    const int chunk = x.rotates ? x.unit : p.rot_units + x.unit;         // chunks 2 rot_units.. are copied
+    x.c0 = chunk * 8;
+    x.c1 = (chunk + between) * 8;
     x.h0 = split * p.heads_each + ((lane >> p.unit_shift) & (slots - 1));
     x.h1 = min(p.H, (split + 1) * p.heads_each);
     x.step = slots;
     return x;
 }
 
-// Cosines and sines (times the amplitude) of the lane's pairs.
+// Position of token i of request b.
+__device__ __forceinline__ int64_t position(const Turn& p, int b, int i) {
+    return (p.start == nullptr ? 0 : (int64_t)p.start[b]) +
+           (p.positions == nullptr ? (int64_t)i : (int64_t)p.positions[b * p.pos_stride + i]);
+}
+
+// Sine and cosine of an angle of phase * 2^-32 turns.  The angle is folded to x
+// in [-pi/4, pi/4] about the nearest quarter turn; there the Taylor series up to
+// x^9 and x^8 leave x^11 / 11! < 2e-9 and x^10 / 10! < 3e-8.  x is off by three
+// roundings (3 * 2^-24 of it, times a slope of cos x: 1.0e-7 at most), the sums
+// by one and what is left of those inside (4e-8): both within 2^-22 in all.
+__device__ __forceinline__ void sincos_turns(uint32_t phase, float& sn, float& cs) {
+    const uint32_t y = phase + 0x20000000u;                // upper two bits: the nearest quarter turn
+    const float x = (float)(int)((y & 0x3fffffffu) - 0x20000000u) * (float)(6.283185307179586 * 0x1p-32);
+    const float z = x * x;
+    float u = fmaf(z, 1.f / 362880.f, -1.f / 5040.f);
+    u = fmaf(z, u, 1.f / 120.f);
+    u = fmaf(z, u, -1.f / 6.f);
+    const float si = fmaf(x * z, u, x);
+    float v = fmaf(z, 1.f / 40320.f, -1.f / 720.f);
+    v = fmaf(z, v, 1.f / 24.f);
+    v = fmaf(z, v, -0.5f);
+    const float co = fmaf(z, v, 1.f);
+    const bool odd = y & 0x40000000u;
+    sn = __uint_as_float(__float_as_uint(odd ? co : si) ^ (y & 0x80000000u));
+    cs = __uint_as_float(__float_as_uint(odd ? si : co) ^ ((y + 0x40000000u) & 0x80000000u));
+}
+
+// Cosines and sines (times the amplitude) of the lane's pairs at a position.
 template <bool kInterleaved>
-__device__ __forceinline__ void lane_angles(const Turn& p, const LaneWork& x, float (&c)[8], float (&s)[8]) {
-    const int64_t pos = (p.start == nullptr ? 0 : (int64_t)p.start[x.b]) +
-                        (p.positions == nullptr ? (int64_t)x.i : (int64_t)p.positions[x.b * p.pos_stride + x.i]);
+__device__ __forceinline__ void lane_angles(const Turn& p, const LaneWork& x, int64_t pos, float (&c)[8], float (&s)[8]) {
 #pragma unroll
     for (int e = 0; e < 8; e += 2) {
         const int j = kInterleaved ? 4 * (e < 4 ? x.unit : x.unit + p.rot_units) + (e & 3) : 8 * x.unit + e;
         const ulonglong2 f = *reinterpret_cast<const ulonglong2*>(p.turns + j);
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
-            const uint64_t phase = (uint64_t)pos * (k == 0 ? f.x : f.y);
-            const float half_turns = (float)(int32_t)(phase >> 32) * 0x1p-31f;       // [-1, 1]
+            uint32_t phase = (uint32_t)(((uint64_t)pos * (k == 0 ? f.x : f.y)) >> 32);
+            if (p.inverse) phase = 0u - phase;
             float sn, cs;
-            sincospif(half_turns, &sn, &cs);
+            sincos_turns(phase, sn, cs);
             c[e + k] = cs * p.amplitude;
-            s[e + k] = (p.inverse ? -sn : sn) * p.amplitude;
+            s[e + k] = sn * p.amplitude;
         }
     }
 }
@@ -125,7 +157,7 @@ __device__ __forceinline__ void rotate(uint4& va, uint4& vb, const float (&c)[8]
 // ---------------------------------------------------------------------------
 // Rotation of a [B, H, N, D] view: each row read and written once, HBM bounds
 // it.  The first rows are on their way while the angles are computed (24 heads
-// of 16,384 tokens, 201 MB: 31.3 us, 0.95 of the copy rate; the angles first
+// of 16,384 tokens, 201 MB: 31.1 us, 0.95 of the copy rate; the angles first
 // 33.4).  Three blocks an SM hold eight chunks a lane in flight in registers
 // (four blocks with four chunks 31.5; eight chunks that spill 39.0).
 // ---------------------------------------------------------------------------
@@ -135,44 +167,60 @@ struct RopeParams {
     uint16_t* o;
     int64_t xsb, xsh, xsn, osb, osh, osn;
     const int32_t* n_len;                // or null: N
-    int D, in_place;
+    int in_place;
 };
 
-template <bool kInterleaved>
+template <bool kInterleaved, int kTokens>
 __global__ void __launch_bounds__(kRotaryThreads, 3) rope_kernel(const __grid_constant__ RopeParams p) {
+    constexpr int kFlight = 4, kHeads = kFlight / kTokens; // heads whose loads precede their stores, of a token
     pdl_trigger();
     pdl_wait();
-    const LaneWork w = lane_work(p.turn, (int64_t)blockIdx.x * (kRotaryThreads / 32) + (threadIdx.x >> 5), p.D);
-    if (!w.live || (p.in_place && !w.rotates)) return;
-    if (p.n_len != nullptr && w.i >= p.n_len[w.b]) return;
-    const uint16_t* x = p.x + w.b * p.xsb + w.i * p.xsn;
-    uint16_t* o = p.o + w.b * p.osb + w.i * p.osn;
-    constexpr int kFlight = 4;                             // heads whose loads precede their stores
-    float c[8], s[8];
+    const LaneWork w = lane_work<kTokens>(p.turn);
+    if (p.in_place && !w.rotates) return;
+    const uint16_t* x[kTokens];
+    uint16_t* o[kTokens];
+    int b0 = 0, i0 = 0;                                    // request and token (of one alone)
+    int64_t pos[kTokens];
+    bool live[kTokens];
+#pragma unroll
+    for (int t = 0; t < kTokens; ++t) {
+        const int64_t n = w.first + t * w.apart;
+        const int b = fast_div((int)min(n, p.turn.tokens - 1), p.turn.by_N), i = (int)(n - (int64_t)b * p.turn.N);
+        live[t] = n < p.turn.tokens && (p.n_len == nullptr || i < p.n_len[b]);
+        x[t] = p.x + b * p.xsb + i * p.xsn;
+        o[t] = p.o + b * p.osb + i * p.osn;
+        if (kTokens > 1) pos[t] = live[t] && w.rotates ? position(p.turn, b, i) : 0;
+        b0 = b; i0 = i;
+    }
+    if (kTokens == 1 && !live[0]) return;
     uint4 a[kFlight], b[kFlight];
     auto load = [&](int h0) {
 #pragma unroll
         for (int k = 0; k < kFlight; ++k) {
-            const int h = h0 + k * w.step;
-            if (h < w.h1) {
-                a[k] = *reinterpret_cast<const uint4*>(x + h * p.xsh + w.c0);
-                b[k] = *reinterpret_cast<const uint4*>(x + h * p.xsh + w.c1);
+            const int t = k / kHeads, h = h0 + (k % kHeads) * w.step;
+            if (live[t] && h < w.h1) {
+                a[k] = *reinterpret_cast<const uint4*>(x[t] + h * p.xsh + w.c0);
+                b[k] = *reinterpret_cast<const uint4*>(x[t] + h * p.xsh + w.c1);
             }
         }
     };
     load(w.h0);
-    if (w.rotates) lane_angles<kInterleaved>(p.turn, w, c, s);
+    float c[8], s[8];
+    // a token alone: its position is asked for behind its rows (before them: 32.7 us in place of 31.1)
+    if (kTokens == 1 && w.rotates) lane_angles<kInterleaved>(p.turn, w, position(p.turn, b0, i0), c, s);
 #pragma unroll 1
     for (int h0 = w.h0;;) {
 #pragma unroll
         for (int k = 0; k < kFlight; ++k) {
-            const int h = h0 + k * w.step;
-            if (h < w.h1) {
+            const int t = k / kHeads, h = h0 + (k % kHeads) * w.step;
+            if (kTokens > 1 && k % kHeads == 0 && live[t] && w.rotates) lane_angles<kInterleaved>(p.turn, w, pos[t], c, s);
+            if (live[t] && h < w.h1) {
                 if (w.rotates) rotate<kInterleaved>(a[k], b[k], c, s);
-                *reinterpret_cast<uint4*>(o + h * p.osh + w.c0) = a[k];
-                *reinterpret_cast<uint4*>(o + h * p.osh + w.c1) = b[k];
+                *reinterpret_cast<uint4*>(o[t] + h * p.osh + w.c0) = a[k];
+                *reinterpret_cast<uint4*>(o[t] + h * p.osh + w.c1) = b[k];
             }
         }
+        if (kTokens > 1) break;                            // they have no more heads
         h0 += kFlight * w.step;
         if (h0 >= w.h1) break;
         load(h0);
@@ -182,7 +230,7 @@ __global__ void __launch_bounds__(kRotaryThreads, 3) rope_kernel(const __grid_co
 // ---------------------------------------------------------------------------
 // Append with rotation: K rotated, V copied, into the cache rows of the slots.
 // HBM bounds it (16 ragged prompts of up to 2,048 tokens, 16 heads of 128
-// channels, 259 MB: 41.0 us, 0.93 of the copy rate; the angles before the first
+// channels, 259 MB: 40.6 us, 0.94 of the copy rate; the angles before the first
 // loads 42.9; four blocks an SM with half the chunks in flight 41.4).
 // ---------------------------------------------------------------------------
 struct AppendRopeParams {
@@ -196,66 +244,81 @@ struct AppendRopeParams {
     int64_t ksb, ksh, ksn, vsb, vsh, vsn;
     int64_t ckp, ckh, ckt, cvp, cvh, cvt;
     int64_t slots_stride, capacity;
-    int D, page, page_shift;
+    int page, page_shift;
 };
 
-template <bool kInterleaved>
+template <bool kInterleaved, int kTokens>
 __global__ void __launch_bounds__(kRotaryThreads, 3) append_rope_kernel(const __grid_constant__ AppendRopeParams p) {
+    constexpr int kFlight = 2, kHeads = kFlight / kTokens; // heads whose loads precede their stores, of a token
     pdl_trigger();
     pdl_wait();
-    const LaneWork w = lane_work(p.turn, (int64_t)blockIdx.x * (kRotaryThreads / 32) + (threadIdx.x >> 5), p.D);
-    if (!w.live) return;
-    const int slot = p.slots[w.b * p.slots_stride + w.i];
-    if (slot < 0) return;
-    if (slot >= p.capacity) {
-        if (w.unit == 0 && atomicCAS(p.status, 0, kErrPage) == 0) p.status[3] = slot >> p.page_shift;
-        return;
+    const LaneWork w = lane_work<kTokens>(p.turn);
+    int b0 = 0, i0 = 0, slot[kTokens];                     // request and token (of one alone), places in the cache
+    int64_t pos[kTokens];
+    const uint16_t* kr[kTokens];
+    const uint16_t* vr[kTokens];
+#pragma unroll
+    for (int t = 0; t < kTokens; ++t) {
+        const int64_t n = w.first + t * w.apart;
+        const int b = fast_div((int)min(n, p.turn.tokens - 1), p.turn.by_N), i = (int)(n - (int64_t)b * p.turn.N);
+        slot[t] = n < p.turn.tokens ? p.slots[b * p.slots_stride + i] : -1;
+        if (kTokens > 1) pos[t] = n < p.turn.tokens && w.rotates ? position(p.turn, b, i) : 0;
+        b0 = b; i0 = i;
+        kr[t] = p.k + b * p.ksb + i * p.ksn;
+        vr[t] = p.v + b * p.vsb + i * p.vsn;
     }
-    const int64_t pg = slot >> p.page_shift;
-    const int off = slot & (p.page - 1);
-    const uint16_t* k = p.k + w.b * p.ksb + w.i * p.ksn;
-    const uint16_t* v = p.v + w.b * p.vsb + w.i * p.vsn;
-    uint16_t* ck = p.ck + pg * p.ckp + off * p.ckt;
-    uint16_t* cv = p.cv + pg * p.cvp + off * p.cvt;
-    constexpr int kFlight = 2;                             // heads whose loads precede their stores
-    float c[8], s[8];
+#pragma unroll
+    for (int t = 0; t < kTokens; ++t)
+        if (slot[t] >= p.capacity) {
+            if (w.unit == 0 && atomicCAS(p.status, 0, kErrPage) == 0) p.status[3] = slot[t] >> p.page_shift;
+            slot[t] = -1;
+        }
+    if (kTokens == 1 && slot[0] < 0) return;
     uint4 a[kFlight], b[kFlight], d[kFlight], e[kFlight];
     auto load = [&](int h0) {
 #pragma unroll
         for (int u = 0; u < kFlight; ++u) {
-            const int h = h0 + u * w.step;
-            if (h < w.h1) {
-                a[u] = *reinterpret_cast<const uint4*>(k + h * p.ksh + w.c0);
-                b[u] = *reinterpret_cast<const uint4*>(k + h * p.ksh + w.c1);
-                d[u] = *reinterpret_cast<const uint4*>(v + h * p.vsh + w.c0);
-                e[u] = *reinterpret_cast<const uint4*>(v + h * p.vsh + w.c1);
+            const int t = u / kHeads, h = h0 + (u % kHeads) * w.step;
+            if (slot[t] >= 0 && h < w.h1) {
+                a[u] = *reinterpret_cast<const uint4*>(kr[t] + h * p.ksh + w.c0);
+                b[u] = *reinterpret_cast<const uint4*>(kr[t] + h * p.ksh + w.c1);
+                d[u] = *reinterpret_cast<const uint4*>(vr[t] + h * p.vsh + w.c0);
+                e[u] = *reinterpret_cast<const uint4*>(vr[t] + h * p.vsh + w.c1);
             }
         }
     };
     load(w.h0);
-    if (w.rotates) lane_angles<kInterleaved>(p.turn, w, c, s);
+    float c[8], s[8];
+    if (kTokens == 1 && w.rotates) lane_angles<kInterleaved>(p.turn, w, position(p.turn, b0, i0), c, s);
 #pragma unroll 1
     for (int h0 = w.h0;;) {
 #pragma unroll
         for (int u = 0; u < kFlight; ++u) {
-            const int h = h0 + u * w.step;
-            if (h < w.h1) {
-                *reinterpret_cast<uint4*>(cv + h * p.cvh + w.c0) = d[u];
-                *reinterpret_cast<uint4*>(cv + h * p.cvh + w.c1) = e[u];
+            const int t = u / kHeads, h = h0 + (u % kHeads) * w.step;
+            if (kTokens > 1 && slot[t] >= 0 && w.rotates) lane_angles<kInterleaved>(p.turn, w, pos[t], c, s);
+            if (slot[t] >= 0 && h < w.h1) {
+                const int64_t pg = slot[t] >> p.page_shift;
+                const int off = slot[t] & (p.page - 1);
+                uint16_t* ck = p.ck + pg * p.ckp + off * p.ckt + h * p.ckh;
+                uint16_t* cv = p.cv + pg * p.cvp + off * p.cvt + h * p.cvh;
+                *reinterpret_cast<uint4*>(cv + w.c0) = d[u];
+                *reinterpret_cast<uint4*>(cv + w.c1) = e[u];
                 if (w.rotates) rotate<kInterleaved>(a[u], b[u], c, s);
-                *reinterpret_cast<uint4*>(ck + h * p.ckh + w.c0) = a[u];
-                *reinterpret_cast<uint4*>(ck + h * p.ckh + w.c1) = b[u];
+                *reinterpret_cast<uint4*>(ck + w.c0) = a[u];
+                *reinterpret_cast<uint4*>(ck + w.c1) = b[u];
             }
         }
+        if (kTokens > 1) break;                            // they have no more heads
         h0 += kFlight * w.step;
         if (h0 >= w.h1) break;
         load(h0);
     }
 }
 
-// Fill `t`; the grid's warps in *warps.  SAGE_OK or why the call is refused.
-int make_turn(Turn& t, int64_t& warps, const sage_rotary* r, const int32_t* positions, int64_t positions_stride,
-              const int32_t* start, int B, int H, int N, int D, int inverse) {
+// Fill `t`; the grid's warps in *warps and how many tokens a lane has in flight
+// (of `flight` heads) in *together.  SAGE_OK or why the call is refused.
+int make_turn(Turn& t, int64_t& warps, int& together, int flight, const sage_rotary* r, const int32_t* positions,
+              int64_t positions_stride, const int32_t* start, int B, int H, int N, int D, int inverse) {
     if (r == nullptr || r->turns == nullptr || r->rotary_dim <= 0 || positions_stride < 0) return SAGE_ERR_ARG;
     if (r->rotary_dim > D || r->rotary_dim % 16 || !aligned16(r->turns)) return SAGE_ERR_UNSUPPORTED;
     if ((int64_t)B * N > INT32_MAX) return SAGE_ERR_UNSUPPORTED;
@@ -263,17 +326,37 @@ int make_turn(Turn& t, int64_t& warps, const sage_rotary* r, const int32_t* posi
     t.turns = r->turns; t.amplitude = r->amplitude; t.inverse = inverse != 0;
     t.rot_units = r->rotary_dim / 16;
     t.tokens = (int64_t)B * N; t.N = N; t.H = H;
+    t.by_N = make_fast_div((uint32_t)N);
     t.unit_shift = D == 128 ? 3 : 2;
     t.slot_shift = 0;
     while (t.slot_shift < 5 - t.unit_shift && (1 << t.slot_shift) < H) ++t.slot_shift;
-    const int64_t groups = ceil_div(t.tokens, 32 >> (t.unit_shift + t.slot_shift));
+    const int apart = 32 >> (t.unit_shift + t.slot_shift);
     const int passes = (int)ceil_div(H, 1 << t.slot_shift);
     constexpr int64_t kFill = 152 * 24;                    // warps that fill the GPU
+    together = 1;
+    while (2 * together * passes <= flight && ceil_div(t.tokens, apart * 2 * together) >= kFill) together *= 2;
+    const int64_t groups = ceil_div(t.tokens, apart * together);
     const int want = (int)std::min<int64_t>(passes, ceil_div(kFill, groups));
     t.heads_each = (int)ceil_div(passes, want) << t.slot_shift;
     t.splits = (int)ceil_div(H, t.heads_each);
     warps = groups * t.splits;
     return SAGE_OK;
+}
+
+template <bool kInterleaved>
+cudaError_t launch_rope(const RopeParams& p, int together, int64_t warps, cudaStream_t s) {
+    static bool ready[3][64] = {};
+    const dim3 grid((unsigned)ceil_div(warps, kRotaryThreads / 32)), block(kRotaryThreads);
+    if (together == 4) return launch_pdl(rope_kernel<kInterleaved, 4>, grid, block, 0, s, 1, false, ready[2], p);
+    if (together == 2) return launch_pdl(rope_kernel<kInterleaved, 2>, grid, block, 0, s, 1, false, ready[1], p);
+    return launch_pdl(rope_kernel<kInterleaved, 1>, grid, block, 0, s, 1, false, ready[0], p);
+}
+template <bool kInterleaved>
+cudaError_t launch_append(const AppendRopeParams& p, int together, int64_t warps, cudaStream_t s) {
+    static bool ready[2][64] = {};
+    const dim3 grid((unsigned)ceil_div(warps, kRotaryThreads / 32)), block(kRotaryThreads);
+    if (together == 2) return launch_pdl(append_rope_kernel<kInterleaved, 2>, grid, block, 0, s, 1, false, ready[1], p);
+    return launch_pdl(append_rope_kernel<kInterleaved, 1>, grid, block, 0, s, 1, false, ready[0], p);
 }
 
 }  // namespace
@@ -315,17 +398,16 @@ int sage_rope(const sage_tensor* x, const sage_tensor* out, int B, int H, int N,
         return SAGE_ERR_ARG;
     RopeParams p{};
     int64_t warps = 0;
-    if ((rc = make_turn(p.turn, warps, rotary, positions, positions_stride, start, B, H, N, D, inverse)) != SAGE_OK) return rc;
+    int together = 1;
+    if ((rc = make_turn(p.turn, warps, together, 4, rotary, positions, positions_stride, start, B, H, N, D, inverse)) != SAGE_OK)
+        return rc;
     p.x = static_cast<const uint16_t*>(x->ptr);
     p.o = static_cast<uint16_t*>(const_cast<void*>(out->ptr));
     p.xsb = x->stride_b; p.xsh = x->stride_h; p.xsn = x->stride_n;
     p.osb = out->stride_b; p.osh = out->stride_h; p.osn = out->stride_n;
-    p.n_len = n_len; p.D = D; p.in_place = in_place;
-    static bool ready[2][64] = {};
-    const dim3 grid((unsigned)ceil_div(warps, kRotaryThreads / 32)), block(kRotaryThreads);
+    p.n_len = n_len; p.in_place = in_place;
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
-    if ((rotary->interleaved ? launch_pdl(rope_kernel<true>, grid, block, 0, s, 1, false, ready[1], p)
-                             : launch_pdl(rope_kernel<false>, grid, block, 0, s, 1, false, ready[0], p)) != cudaSuccess)
+    if ((rotary->interleaved ? launch_rope<true>(p, together, warps, s) : launch_rope<false>(p, together, warps, s)) != cudaSuccess)
         return SAGE_ERR_LAUNCH;
     set_last_launch_count(1);
     return SAGE_OK;
@@ -340,7 +422,9 @@ int sage_cache_append_rope(const sage_tensor* k, const sage_tensor* v, int B, in
     if ((rc = check_view(k)) != SAGE_OK || (rc = check_view(v)) != SAGE_OK) return rc;
     AppendRopeParams p{};
     int64_t warps = 0;
-    if ((rc = make_turn(p.turn, warps, rotary, positions, positions_stride, start, B, cache->heads, N, cache->D, 0)) != SAGE_OK)
+    int together = 1;
+    if ((rc = make_turn(p.turn, warps, together, 2, rotary, positions, positions_stride, start, B, cache->heads, N, cache->D, 0)) !=
+        SAGE_OK)
         return rc;
     p.status = device_status_ptr();
     if (p.status == nullptr) return SAGE_ERR_LAUNCH;
@@ -354,13 +438,11 @@ int sage_cache_append_rope(const sage_tensor* k, const sage_tensor* v, int B, in
     p.ckp = cache->k.stride_b; p.ckh = cache->k.stride_h; p.ckt = cache->k.stride_n;
     p.cvp = cache->v.stride_b; p.cvh = cache->v.stride_h; p.cvt = cache->v.stride_n;
     p.capacity = (int64_t)cache->num_pages * cache->page_size;
-    p.D = cache->D; p.page = cache->page_size;
+    p.page = cache->page_size;
     p.page_shift = 31 - __builtin_clz((unsigned)cache->page_size);
-    static bool ready[2][64] = {};
-    const dim3 grid((unsigned)ceil_div(warps, kRotaryThreads / 32)), block(kRotaryThreads);
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
-    if ((rotary->interleaved ? launch_pdl(append_rope_kernel<true>, grid, block, 0, s, 1, false, ready[1], p)
-                             : launch_pdl(append_rope_kernel<false>, grid, block, 0, s, 1, false, ready[0], p)) != cudaSuccess)
+    if ((rotary->interleaved ? launch_append<true>(p, together, warps, s) : launch_append<false>(p, together, warps, s)) !=
+        cudaSuccess)
         return SAGE_ERR_LAUNCH;
     set_last_launch_count(1);
     return SAGE_OK;

@@ -1,4 +1,5 @@
 """Rotary positions and the append that rotates, against their definition in 64 bits."""
+import math
 import random
 
 import pytest
@@ -119,6 +120,19 @@ def test_forms_of_one_call_agree_bit_for_bit():
         for n in (1, 7, 300):
             part = S.rope(x[:, :h, :n], r)
             assert torch.equal(part, whole[:, :h, :n])
+
+
+@pytest.mark.parametrize("amplitude", [1.0, 2.0 ** -20, 2.0 ** 10])
+def test_sines_and_cosines(amplitude):
+    """Pairs (1, 0) give the cosine and the sine themselves, at every eighth of a turn and beside it too."""
+    G.ensure_built()
+    N = 4096
+    f = [2 * math.pi / n for n in (3, 5, 8, 16, 64, 100, 1000, 1024)] + [1.0, 0.5, 1e-3, 0.25, 3.0, 7e-5, 0.1, 0.01]
+    for interleaved in (False, True):
+        r = S.make_rotary(f, interleaved=interleaved, amplitude=amplitude)
+        x = torch.zeros((1, 1, N, 64), dtype=torch.bfloat16, device="cuda")
+        x[..., slice(0, 32, 2) if interleaved else slice(0, 16)] = 1.0
+        check_rope(x, S.rope(x, r), r, f, [range(N)])
 
 
 def test_special_values_stay_in_their_pair():

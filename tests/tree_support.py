@@ -31,10 +31,10 @@ def angles(positions, frequencies, device="cuda"):
 def turned(x, angle, rotary_dim, interleaved, amplitude=1.0, inverse=False):
     """(x rotated, bound of what the kernel may be off by before its one rounding to BF16), float64 [B, H, N, D].
 
-    The kernel's cosine and sine: the angle in half turns rounded to FP32 (pi 2^-25 rad) and cut at 2^-32 turns
-    (2^-29 rad), sincospif (2 ulp: 2^-23), the amplitude's product (2^-24): below 2.8e-7 together.  The two products and
-    their sum in FP32: 2^-24 of each once more for the product and once for the sum, below 1.2e-7 of |x1| + |x2|.
-    Together below 2^-21 A (|x1| + |x2|)."""
+    The kernel's cosine and sine: an angle x of up to pi / 4 in FP32, three roundings (3 * 2^-24 x, times the slope:
+    1.0e-7), cut at 2^-32 turns (2e-9); a Taylor series (3e-8) summed in FP32 (4e-8); the amplitude's product (2^-24): below
+    2.8e-7 together.  The two products and their sum in FP32: 2^-24 of each once more for the product and once for the sum,
+    below 1.2e-7 of |x1| + |x2|.  Together below 2^-21 A (|x1| + |x2|)."""
     R, half = rotary_dim, rotary_dim // 2
     x = x.double()
     c, s = amplitude * torch.cos(angle)[:, None], amplitude * torch.sin(angle)[:, None]
