@@ -510,7 +510,8 @@ int sage_attn_paged_tree(const sage_tensor* q, const sage_tensor* o, const sage_
  *  slots   : device int32, B rows of N entries, slots_stride apart, as for
  *            sage_cache_append; K is at most N.  A move from or to a negative slot
  *            is left out; a slot outside the cache too, which is recorded as
- *            SAGE_ERR_PAGE in the device status.
+ *            SAGE_ERR_PAGE in the device status.  A request's slots that are not
+ *            negative differ from each other.
  * A move sees what the moves of its request before it wrote.  Slots that one
  * request's moves write are not among another's.  One launch. */
 int sage_cache_keep(const int32_t* kept, int64_t kept_stride, int B, int K, const int32_t* slots, int64_t slots_stride, int N,
