@@ -88,16 +88,6 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
     asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
     return r;
 }
-__device__ __forceinline__ float4 ld_cluster4(uint32_t a) {
-    float4 v;
-    asm volatile("ld.shared::cluster.v4.f32 {%0,%1,%2,%3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(a) : "memory");
-    return v;
-}
-__device__ __forceinline__ float2 ld_cluster2(uint32_t a) {
-    float2 v;
-    asm volatile("ld.shared::cluster.v2.f32 {%0,%1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(a) : "memory");
-    return v;
-}
 __device__ __forceinline__ void record_page(const PagedParams& p, int page) {
     if (atomicCAS(p.status, 0, kErrPage) == 0) p.status[3] = page;
 }
@@ -608,6 +598,7 @@ __global__ void __launch_bounds__(256) paged_join_kernel(const __grid_constant__
 constexpr int kFewRows = 16;
 constexpr int64_t kReadAgain = int64_t(128) << 20;        // bytes of prefix read again that cost as much as its list
 constexpr int kWholeSteps = 12, kWholeItems = 4;          // few-rows kernel: a cluster takes an item up to these
+constexpr int kHalfRows = 64;                             // rows that the many-rows kernel takes with two lanes each
 constexpr double kOwnList = 12e6, kRowJoin = 6e3;         // many-rows kernel: ... as much as joining all rows, and one row
 
 struct Lists {
@@ -616,8 +607,9 @@ struct Lists {
     int groups;                          // ... 128-row groups of an item
     int tok;                             // ... tokens of a group
     int nr;                              // few-rows kernel: 8-row groups of an item
-    bool whole;                          // ... a CTA takes an item
-    int split;                           // few-rows kernel: CTAs of the cluster that takes an item (0: a list)
+    bool whole;                          // ... a CTA or a cluster takes an item
+    bool half;                           // ... of up to 64 rows, two lanes to each
+    int split;                           // CTAs of the cluster that takes an item (0: no clusters)
     int M, rt, join;                     // M: rows of a partial result
     int64_t slots;
     // items of the prefix for the rows of all requests (many-rows kernel): in the same list when `tiles`
@@ -652,11 +644,59 @@ int whole_split(int64_t items, int64_t steps, int sms) {
     return split;
 }
 
+// Items of a tree's call that clusters of the many-rows kernel take whole, each
+// CTA a share of the tiles, joined through shared memory: no list, no second
+// kernel.  Up to 64 rows have two lanes each (see there).  Sets x and returns
+// true where that is the faster form, by the table widths (own, pre: tiles):
+//  - `split` CTAs to an item, as many as run at a time, up to 8.  Clusters do not
+//    fill every SM: of 8 run 36 (30.5 us; 38 take 44), of 6 46 (28.1; 48: 41.5),
+//    of 5 55, of 4 72 (27.9; 75: 41.2), of 3 96, of 2 152; of 7 38, hardly more
+//    than of 8.
+//  - from 6 tiles on (16 items of 4 tiles, 64 rows: 8.8 us so, a CTA each 7.9);
+//  - up to 12 tiles a CTA, as a list evens out what a cluster does not (64 items
+//    of up to 48 tiles, 104 rows of 64 channels: 24.2 us, from the list 22.9; all
+//    of them 48 tiles long: 28.6 and 34.4).  A prefix is as long for all, so its
+//    tiles count two thirds (96 items of 52 rows, 33 shared tiles and up to 8 own:
+//    21.0 and 25.5).  Few items leave SMs idle, which a list does not (6 items
+//    behind 127 shared tiles: 22.1 and 16.8; 8 items of 96: 16.3 and 20.0);
+//  - over 128 rows from clusters of three on, since an item of 256 rows reads its
+//    tiles once (128 items of 24 tiles, 512 rows a request: 25.0 and 23.1; 64:
+//    18.6 and 22.8), below from two on (one CTA an item is the form above), with
+//    one at D = 64 (152 items of 12 tiles, 64 rows: 14.0 and 18.1; at D = 128, 6
+//    tiles: 19.4 and 17.4) and up to 16 rows (152 items of 8 tiles: 18.4 and 20.7);
+//  - against the few-rows kernel, whose time grows with each group of 8 rows, for
+//    9 to 16 rows (96 items of 32 tiles 25.2 and 30.9 us; 8 of 8 tiles 8.3 and
+//    8.6), and for 5 to 8 rows of 64 channels in clusters of up to 4 (96 items of
+//    16 tiles 11.5 and 12.4, of 36 17.4 and 24.5; in clusters of 8, 8 items of 8
+//    tiles 7.3 and 7.1; 128 channels, 64 items of 8: 9.9 and 9.2).
+bool cluster_items(Lists& x, int B, int Hkv, int G, int Nq, int D, int64_t own_keys, int64_t pre_keys, int sms) {
+    const int64_t rows = (int64_t)Nq * G, own = ceil_div(own_keys, 128), pre = ceil_div(pre_keys, 128);
+    if (G > 128) return false;
+    const bool few = rows <= kHalfRows;
+    const int tok = (few ? kHalfRows : 128) / G, rt = (int)ceil_div(Nq, tok);
+    const int64_t items = (int64_t)B * Hkv * rt;
+    int split = (int)std::min<int64_t>(8, own + pre);
+    while (split > 0 && (split == 7 || items * split * 10 > (split == 5 || split == 6 ? 18 : 19) * sms)) --split;
+    if (split == 0 || own + pre < 6 || 3 * own + 2 * pre > 36 * split || own + pre > 24 + 9 * items) return false;
+    const int least = rows > 128 ? 3 : rows > kHalfRows || (rows > kFewRows && D == 128) ? 2 : 1;
+    if (split < least || (rows <= kFewRows / 2 && (rows <= 4 || D == 128 || split > 4))) return false;
+    x.tiles = x.whole = true;
+    x.half = few;
+    x.groups = 1;
+    x.tok = tok;
+    x.M = 128;
+    x.rt = rt;
+    x.join = pre_keys > 0;
+    x.split = split;
+    return true;
+}
+
 // own_keys, pre_keys: by the table widths.  What a workspace has to hold does not
 // depend on own_keys or sms.
-Lists make_lists(int B, int Hkv, int G, int Nq, int D, int64_t own_keys, int64_t pre_keys, int sms) {
+Lists make_lists(int B, int Hkv, int G, int Nq, int D, int64_t own_keys, int64_t pre_keys, int sms, bool tree) {
     Lists x{};
     const int64_t rows = (int64_t)Nq * G;
+    if (tree && cluster_items(x, B, Hkv, G, Nq, D, own_keys, pre_keys, sms)) return x;
     x.tiles = rows > kFewRows && G <= 128;
     if (x.tiles && B > 1 && rows <= 64) {
         const int64_t tiles = ceil_div(pre_keys, 128), sets = ceil_div(B, 128 / rows);
@@ -787,7 +827,7 @@ int attn_paged(const sage_tensor* q, const sage_tensor* o, const sage_page_cache
     const int64_t pre_keys = (int64_t)prefix_width * cache->page_size;
     if (own_keys > INT32_MAX - 256 || pre_keys > INT32_MAX - 256) return SAGE_ERR_UNSUPPORTED;
     const int sms = sm_count();
-    const Lists x = make_lists(B, cache->heads, H / cache->heads, Nq, D, own_keys, pre_keys, sms);
+    const Lists x = make_lists(B, cache->heads, H / cache->heads, Nq, D, own_keys, pre_keys, sms, tree != nullptr);
     if (workspace == nullptr || !aligned16(workspace) || workspace_bytes < lists_bytes(x, B, D)) return SAGE_ERR_ARG;
     // list positions and slot numbers stay in int
     const int tk = x.tiles ? 128 : kStep;
@@ -851,12 +891,12 @@ int attn_paged(const sage_tensor* q, const sage_tensor* o, const sage_page_cache
     else p.start = reinterpret_cast<int32_t*>(w);
     p.pre_items_rt = x.pre_items_rt; p.pre_m = x.pre_M; p.pre_tok = x.pre_tok;
     p.pre_workers = tile_workers(sms, x.pre_groups);
-    p.whole = x.whole; p.split = x.split;
+    p.whole = x.whole; p.half = x.half; p.split = x.split;
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
     cudaError_t e;
     int launches = 0;
     if (x.tiles) {
-        p.workers = x.whole ? B * cache->heads * x.rt : tile_workers(sms, x.groups);
+        p.workers = x.whole ? B * cache->heads * x.rt * std::max(1, x.split) : tile_workers(sms, x.groups);
         if (x.pre) p.pre_rt = x.pre_items_rt;
         e = (tree != nullptr ? launch_paged_tiles_tree : launch_paged_tiles)(p, D, x.groups, mq, mqp, mk, mv, s);
         if (e == cudaSuccess && x.pre) e = D == 64 ? launch_join<64, 128, 128>(p, s) : launch_join<128, 128, 128>(p, s);
@@ -891,8 +931,8 @@ int sage_paged_workspace(int B, int H, int Hkv, int Nq, int D, size_t* bytes) {
     const int rc = check_batch(B, H, Hkv, Nq, D);
     if (rc != SAGE_OK) return rc;
     // a prefix of any length may come: the form with a list of its own needs the most
-    *bytes = lists_bytes(make_lists(B, Hkv, H / Hkv, Nq, D, 0, INT32_MAX, 0), B, D);
-    const size_t alone = lists_bytes(make_lists(B, Hkv, H / Hkv, Nq, D, 0, 0, 0), B, D);
+    *bytes = lists_bytes(make_lists(B, Hkv, H / Hkv, Nq, D, 0, INT32_MAX, 0, false), B, D);
+    const size_t alone = lists_bytes(make_lists(B, Hkv, H / Hkv, Nq, D, 0, 0, 0, false), B, D);
     if (alone > *bytes) *bytes = alone;
     return SAGE_OK;
 }

@@ -36,6 +36,19 @@
 // prompts from the list: 46.6 us where the shared one took 44.3.)  One group of D = 128, with 256 columns:
 // [S 128, its first half P | O 128].
 //
+// A cluster may take an item whole (F_CLUSTER): each CTA leaves its part in its
+// shared memory, where its rows, keys and values were, and the CTAs join all
+// parts of a share of the rows.
+// k64, items of up to 64 rows in clusters: the rows lie twice in the 128 of the
+// scores, and lane r has the keys 0-63 of row r, lane 64 + r the others.  The
+// weights of the other keys are zeros, so one product adds up both lanes' own
+// outputs, which are joined like those of two CTAs.  So all four quarters of
+// tensor memory, and the schedulers of their warps, have work (52 rows leave two
+// idle), no maxima are exchanged, and a CTA has 6 warps, whose registers hold a
+// tile without spills (24 requests of up to 13 tokens x 4 heads, 4 key heads of 64
+// channels, 4,099 shared keys, clusters of 3: 21.0 us; with two threads a row
+// 26.3, from the list 25.5).
+//
 // The reference of the exponentials follows the row maximum lazily: O is
 // rescaled only when the maximum has grown by more than 2^8 since the last
 // rescale.  The weights then reach 2^8 at most, which BF16 holds at the same
@@ -73,11 +86,13 @@ struct ItemNote {
     int pad[3];
 };
 
-template <int D, int kGroups>
+template <int D, int kGroups, bool k64 = false>
 struct TilesShape {
     static constexpr int M = 128 * kGroups;
-    static constexpr int kWarpLoad = 8 * kGroups, kWarpIssue = kWarpLoad + 1;     // + X
-    static constexpr int kThreads = kGroups == 2 ? 640 : 320;
+    // k64: one thread a lane; else two
+    static constexpr int kRowWarps = k64 ? 4 : 8;         // softmax warps of a group
+    static constexpr int kWarpLoad = kRowWarps * kGroups, kWarpIssue = kWarpLoad + 1;     // + X
+    static constexpr int kThreads = kGroups == 2 ? 640 : 32 * (kRowWarps + 2);
     static constexpr int kCtasPerSm = kGroups == 2 ? 1 : 2;
     static constexpr int kNB = D / 64;                    // 64-channel blocks of a row
     static constexpr uint32_t kTile = kNB * kBlk;         // bytes of a K (or V) tile, and of a group's Q
@@ -91,6 +106,10 @@ struct TilesShape {
     static constexpr uint32_t OFF_K = kGroups * kTile;
     static constexpr uint32_t OFF_V = OFF_K + kNS * kTile;
     static constexpr uint32_t OFF_STAGE = OFF_V + kNS * kTile;     // rows on their way out, 1 KB a warp
+    // a cluster's parts lie over rows, keys and values; a row's end is padded, so that rows lie in other banks
+    static constexpr int kPartRow = D + 4;
+    static constexpr uint32_t OFF_PART_ML = 128 * kPartRow * 4;
+    static_assert(kGroups == 2 || OFF_PART_ML + 128 * 8 <= OFF_STAGE);
     static constexpr uint32_t OFF_XM = OFF_STAGE + kGroups * 8 * 1024;            // float [2 turns][group][half][128]
     static constexpr uint32_t OFF_BAR = OFF_XM + kGroups * 2048;
     static constexpr int B_Q = 0, B_DRAIN = 1;            // B_DRAIN: + X
@@ -172,8 +191,8 @@ __device__ __forceinline__ void stage_out(uint8_t* stage, const uint32_t (&w)[8]
 }
 
 // What the kernel's work is: the list of the requests' own items, the list with
-// the prefix's items in front, or an item for each CTA.
-enum TileForm { F_LIST, F_PREFIX, F_ITEM };
+// the prefix's items in front, an item for each CTA, or an item for each cluster.
+enum TileForm { F_LIST, F_PREFIX, F_ITEM, F_CLUSTER };
 
 // Bits t0 .. t0 + 63 of a row of a tree's mask (n new tokens): token t0 + k in
 // bit k of the two words.  The tokens before the first are seen, those behind
@@ -189,14 +208,18 @@ __device__ __forceinline__ void tree_window(const int32_t* row, int t0, int n, u
 // The lowest `many` bits.
 __device__ __forceinline__ uint32_t lowest(int many) { return many >= 32 ? 0xffffffffu : many <= 0 ? 0u : (1u << many) - 1u; }
 
-template <int D, int kGroups, int kForm, bool kTree>
-__global__ void __launch_bounds__(TilesShape<D, kGroups>::kThreads, TilesShape<D, kGroups>::kCtasPerSm)
+// Tiles that each of `split` CTAs of a cluster takes.
+__device__ __forceinline__ int cluster_share(int tiles, int split) { return max(1, (tiles + split - 1) / split); }
+
+template <int D, int kGroups, int kForm, bool kTree, bool k64>
+__global__ void __launch_bounds__(TilesShape<D, kGroups, k64>::kThreads, TilesShape<D, kGroups, k64>::kCtasPerSm)
 paged_tiles_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_qp,
                    const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                    const __grid_constant__ PagedParams p) {
-    using L = TilesShape<D, kGroups>;
+    using L = TilesShape<D, kGroups, k64>;
+    static_assert(!k64 || (kGroups == 1 && kForm == F_CLUSTER));
     constexpr int M = L::M, NS = L::kNS;
-    constexpr bool kPre = kForm == F_PREFIX, kItem = kForm == F_ITEM;
+    constexpr bool kPre = kForm == F_PREFIX, kCluster = kForm == F_CLUSTER, kItem = kForm == F_ITEM || kCluster;
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw_base = smem_u32(smem_raw);
     const uint32_t sbase = (raw_base + 1023u) & ~1023u;
@@ -222,9 +245,9 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
         for (int i = 0; i < 2; ++i) {
             mbar_init(bar(L::B_DRAIN + i), 1);
             mbar_init(bar(L::B_S + i), 1);
-            mbar_init(bar(L::B_P + i), 8);                // one arrival a warp
+            mbar_init(bar(L::B_P + i), L::kRowWarps);     // one arrival a warp
             mbar_init(bar(L::B_ODONE + i), 1);
-            mbar_init(bar(L::B_SFREE + i), 8);
+            mbar_init(bar(L::B_SFREE + i), L::kRowWarps);
             mbar_init(bar(L::B_PV + i), 1);
         }
         for (int i = 0; i < 8; ++i) mbar_init(bar(L::B_X + i), 2);
@@ -262,15 +285,15 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
 
-    if (warp < 8 * kGroups) {
+    if (warp < L::kWarpLoad) {
         // ===================================================== softmax
         if constexpr (kGroups == 2) asm volatile("setmaxnreg.inc.sync.aligned.u32 104;");
-        const int X = warp >> 3, half = (warp >> 2) & 1, quarter = warp & 3;
-        const int row = quarter * 32 + lane;
+        const int X = k64 ? 0 : warp >> 3, quarter = warp & 3, half = k64 ? quarter >> 1 : (warp >> 2) & 1;
+        const int row = quarter * 32 + lane, query = k64 ? row & 63 : row;
         const uint32_t lane_base = (uint32_t)(quarter * 32) << 16;
         const uint32_t tS = tmem + lane_base + 64u * half;
         const uint32_t tP = tmem + lane_base + L::TM_P + 64u * X + 32u * half;
-        const uint32_t tO = tmem + lane_base + L::TM_O + (uint32_t)D * X + (uint32_t)half * (D / 2);
+        const uint32_t tO = tmem + lane_base + L::TM_O + (uint32_t)D * X + (k64 ? 0u : (uint32_t)half * (D / 2));
         const uint32_t bx = bar(L::B_X + 4 * X + quarter);
         // this row's place in the exchange, and its other half's
         float* xm = reinterpret_cast<float*>(sgen + L::OFF_XM) + (X * 2 + half) * 128 + row;
@@ -279,6 +302,17 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
         int turn = 0;                                     // exchanges so far
         int t = 0;
         bool ok = true;
+        auto zero_other_keys = [&]() {                    // k64: the weights of the keys that the row's other lane has
+            uint32_t z[16];
+#pragma unroll
+            for (int i = 0; i < 16; ++i) z[i] = 0u;
+            tmem_st16(tP + 32 - 64 * half, z);
+            tmem_st16(tP + 48 - 64 * half, z);
+        };
+        if (k64 && !L::kAlias) {
+            zero_other_keys();
+            tmem_wait_st();
+        }
         for (int k = 0; ok; ++k) {
             if (!mbar_wait_warp(bar(L::B_ITEM + k % kItemNotes), (k / kItemNotes) & 1, abort_flag)) {
                 if (lane == 0) fail(R_ROWS, t);
@@ -288,7 +322,7 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
             if (nt.run == 0) break;
             const int ib = nt.b, len = nt.len, end = t + nt.run;
             int lim_own, rb, ri, rh;
-            const bool valid = paged_row(sched, ib, nt.h, nt.rt, nt.n, X * 128 + row, rb, ri, rh);
+            const bool valid = paged_row(sched, ib, nt.h, nt.rt, nt.n, X * 128 + query, rb, ri, rh);
             const bool active = __any_sync(0xffffffffu, valid);        // some row of this warp exists
             lim_own = p.causal && !(kPre && ib < 0) ? min(len, len - nt.n + ri + 1) : len;   // own keys this row sees
             float m = -INFINITY, l = 0.f;                 // reference of the exponentials (log2 domain), sum of this half
@@ -333,14 +367,17 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                                 mx = fmaxf(mx, __uint_as_float(s[a][i]));
                             }
                     }
-                    float* at = xm + (turn & 1) * kTurn;
-                    *at = mx;
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(bx);
-                    if (!mbar_wait_warp(bx, turn & 1, abort_flag)) { ok = false; break; }
-                    tc_fence_after();                     // the other half has its scores: P may lie over S
-                    ++turn;
-                    const float mt = fmaxf(mx, at[other]) * p.sc;
+                    float mt = mx * p.sc;
+                    if constexpr (!k64) {
+                        float* at = xm + (turn & 1) * kTurn;
+                        *at = mx;
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(bx);
+                        if (!mbar_wait_warp(bx, turn & 1, abort_flag)) { ok = false; break; }
+                        tc_fence_after();                 // the other half has its scores: P may lie over S
+                        ++turn;
+                        mt = fmaxf(mx, at[other]) * p.sc;
+                    }
                     const bool grow = mt > m + kLazy;     // also the first visible key: m = -inf
                     if (grow) {
                         f = ex2_approx(m - mt);
@@ -372,7 +409,7 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                 if (active) {
                     if (rescale) {
 #pragma unroll 1
-                        for (int c = 0; c < D / 2; c += 16) {
+                        for (int c = 0; c < (k64 ? D : D / 2); c += 16) {
                             uint32_t o[16];
                             tmem_ld16(tO + c, o);
                             tmem_wait_ld();
@@ -388,13 +425,14 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                         for (int i = 0; i < 16; ++i) w[i] = s[a][i];
                         tmem_st16(tP + a * 16, w);
                     }
+                    if (k64 && L::kAlias) zero_other_keys();
                     tmem_wait_st();
                 }
                 fresh = false;
                 tc_fence_before();
                 // V rows behind the last key: whatever they hold times a weight of 0
                 // must be 0 (group 0's product is the first to read them)
-                if (span.nkeys < 128 && half == 0 && X == 0) {
+                if (span.nkeys < 128 && (k64 || half == 0) && X == 0) {
                     if (!mbar_wait_warp(bar(L::B_VF + t % NS), (t / NS) & 1, abort_flag)) { ok = false; break; }
                     if (row >= span.nkeys) {
                         uint8_t* vr = sgen + L::OFF_V + (t % NS) * L::kTile + row * 128;
@@ -410,7 +448,7 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
             if (!ok) break;
             // the item's end: the halves' sums together, the output from tensor memory
             float* at = xm + (turn & 1) * kTurn;
-            if (active) {
+            if (!k64 && active) {
                 *at = l;
                 __syncwarp();
                 if (lane == 0) mbar_arrive(bx);
@@ -418,11 +456,26 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
             if (!mbar_wait_warp(bar(L::B_ODONE + X), k & 1, abort_flag)) { ok = false; break; }
             tc_fence_after();
             if (active) {
-                if (!mbar_wait_warp(bx, turn & 1, abort_flag)) { ok = false; break; }
-                ++turn;
-                l += at[other];
+                if constexpr (!k64) {
+                    if (!mbar_wait_warp(bx, turn & 1, abort_flag)) { ok = false; break; }
+                    ++turn;
+                    l += at[other];
+                }
                 uint8_t* stage = sgen + L::OFF_STAGE + warp * 1024;
-                if (kItem || (!kPre && nt.whole)) {
+                if constexpr (kCluster) {
+                    // this CTA's part, in place of its rows, keys and values: all products are done
+                    float* part = reinterpret_cast<float*>(sgen) + row * L::kPartRow;
+                    if (k64 || half == 0) reinterpret_cast<float2*>(sgen + L::OFF_PART_ML)[row] = make_float2(m, l);
+#pragma unroll 1
+                    for (int c = 0; c < (k64 ? D : D / 2); c += 16) {
+                        uint32_t o[16];
+                        tmem_ld16(tO + c, o);
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int i = 0; i < 16; i += 4)
+                            *reinterpret_cast<uint4*>(part + (k64 ? 0 : half * (D / 2)) + c + i) = make_uint4(o[i], o[i + 1], o[i + 2], o[i + 3]);
+                    }
+                } else if (kItem || (!kPre && nt.whole)) {
                     const int64_t o_at = valid ? rb * p.osb + rh * p.osh + ri * p.osn + half * (D / 2) : -1;
                     const float inv = l == 0.f ? 0.f : __fdiv_rn(1.f, l);
 #pragma unroll 1
@@ -471,13 +524,19 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
         at.pos = t1;
         if constexpr (kItem) {
             // last row sets first: with a causal mask they are the longest
-            const int each = p.B * p.Hkv, set = worker / each, rest = worker - set * each;
+            const int item = kCluster ? worker / p.split : worker;
+            const int each = p.B * p.Hkv, set = item / each, rest = item - set * each;
             at.rt = p.rt - 1 - set;
             at.b = rest / p.Hkv;
             at.h = rest - at.b * p.Hkv;
             at.n = sched.q_rows(at.b);
             at.len = sched.own_keys(at.b);
             t1 = at.ntiles = sched.item_tiles(at.n, at.len, at.rt);
+            if constexpr (kCluster) {                     // this CTA's share of the item's tiles, maybe none
+                const int share = cluster_share(at.ntiles, p.split);
+                at.tile = at.pos = min((worker - item * p.split) * share, at.ntiles);
+                t1 = min(at.tile + share, at.ntiles);
+            }
         }
         else if (t0 < t1) at = paged_place(sched, found[0], t0);
         if (kForm == F_LIST && at.pos < t1 && at.tile > 0) {
@@ -540,7 +599,7 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                 if (lane == 0) {
                     const bool pre = kPre && at.b < 0;
                     const int tok = pre ? p.pre_tok : p.tok;
-                    mbar_arrive_expect_tx(bar(L::B_Q), (uint32_t)(kGroups * L::kNB * tok * (pre ? p.pre_unit : p.G)) * 128u);
+                    mbar_arrive_expect_tx(bar(L::B_Q), (uint32_t)((k64 ? 2 : kGroups) * L::kNB * tok * (pre ? p.pre_unit : p.G)) * 128u);
 #pragma unroll
                     for (int X = 0; X < kGroups; ++X)
 #pragma unroll
@@ -548,6 +607,9 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                             const int g = (at.rt * kGroups + X) * tok;
                             tma_load_4d(sbase + L::OFF_Q + X * L::kTile + hb * kBlk, pre ? &tm_qp : &tm_q, hb * 64,
                                         at.h * p.G, pre ? 0 : g, pre ? g : at.b, bar(L::B_Q));
+                            if (k64)                      // the same rows once more, for the other keys
+                                tma_load_4d(sbase + L::OFF_Q + hb * kBlk + 64 * 128, &tm_q, hb * 64, at.h * p.G, g, at.b,
+                                            bar(L::B_Q));
                         }
                 }
                 ++items;
@@ -675,6 +737,44 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
         tc_fence_after();
         tmem_dealloc(tmem, L::kCols);
     }
+    if constexpr (kCluster) {
+        // Join the CTAs' parts: a thread takes four channels of a row at a time.
+        __syncwarp();
+        cluster_sync_all();
+        const int item = worker / p.split, rank = worker - item * p.split;
+        const int each = p.B * p.Hkv, set = item / each, rest = item - set * each;
+        const int rt = p.rt - 1 - set, b = rest / p.Hkv, h = rest - b * p.Hkv, n = sched.q_rows(b);
+        const int tiles = sched.item_tiles(n, sched.own_keys(b), rt), share = cluster_share(tiles, p.split);
+        const int parts = (tiles + share - 1) / share;
+#pragma unroll 1
+        for (int v = rank * L::kThreads + (int)threadIdx.x; v < (k64 ? 64 : M) * D / 4; v += p.split * L::kThreads) {
+            const int r = v / (D / 4), c = (v - r * (D / 4)) * 4;
+            int rb, ri, rh;
+            if (!paged_row(sched, b, h, rt, n, r, rb, ri, rh)) continue;
+            const uint32_t at = sbase + (uint32_t)(r * L::kPartRow + c) * 4, ml_at = sbase + L::OFF_PART_ML + (uint32_t)r * 8;
+            float mx = -INFINITY, l = 0.f;
+            float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+            for (int w = 0; w < (k64 ? 2 * parts : parts); ++w) {
+                const uint32_t cta = k64 ? (uint32_t)w >> 1 : (uint32_t)w, lower = k64 ? (w & 1) * 64 : 0;
+                const float2 ml = ld_cluster2(mapa_rank(ml_at + lower * 8, cta));
+                const float4 x = ld_cluster4(mapa_rank(at + lower * L::kPartRow * 4, cta));
+                const float mn = fmaxf(mx, ml.x), ms = mn == -INFINITY ? 0.f : mn;
+                const float fa = ex2_approx(mx - ms), fb = ex2_approx(ml.x - ms);
+                l = l * fa + ml.y * fb;
+                acc.x = acc.x * fa + x.x * fb;
+                acc.y = acc.y * fa + x.y * fb;
+                acc.z = acc.z * fa + x.z * fb;
+                acc.w = acc.w * fa + x.w * fb;
+                mx = mn;
+            }
+            const float inv = l == 0.f ? 0.f : __fdiv_rn(1.f, l);
+            uint16_t* dst = p.o + rb * p.osb + rh * p.osh + ri * p.osn + c;
+            *reinterpret_cast<uint2*>(dst) = make_uint2(pack2(acc.x * inv, acc.y * inv), pack2(acc.z * inv, acc.w * inv));
+        }
+        __syncwarp();
+        cluster_sync_all();                               // the parts stay until all have read them
+    }
 }
 
 // ---------------------------------------------------------------------------
@@ -749,12 +849,13 @@ __global__ void __launch_bounds__(256) paged_cuts_kernel(const __grid_constant__
     }
 }
 
-template <int D, int kGroups, int kForm, bool kTree>
+template <int D, int kGroups, int kForm, bool kTree, bool k64 = false>
 cudaError_t launch_one(const PagedParams& p, const CUtensorMap& tq, const CUtensorMap& tqp, const CUtensorMap& tk,
                        const CUtensorMap& tv, cudaStream_t s) {
-    using L = TilesShape<D, kGroups>;
+    using L = TilesShape<D, kGroups, k64>;
     static bool ready[64] = {};
-    cudaError_t e = launch_pdl(paged_tiles_kernel<D, kGroups, kForm, kTree>, dim3((unsigned)p.workers), dim3(L::kThreads), L::kSmem, s, 1, true, ready,
+    cudaError_t e = launch_pdl(paged_tiles_kernel<D, kGroups, kForm, kTree, k64>, dim3((unsigned)p.workers), dim3(L::kThreads), L::kSmem, s,
+                               kForm == F_CLUSTER ? p.split : 1, true, ready,
                                tq, tqp, tk, tv, p);
     if (e != cudaSuccess) return e;
     if (kForm == F_LIST && p.workers > 1) {
@@ -767,6 +868,10 @@ cudaError_t launch_one(const PagedParams& p, const CUtensorMap& tq, const CUtens
 template <int D, int kGroups, bool kTree>
 cudaError_t launch_form(int form, const PagedParams& p, const CUtensorMap& tq, const CUtensorMap& tqp, const CUtensorMap& tk,
                         const CUtensorMap& tv, cudaStream_t s) {
+    if constexpr (kTree && kGroups == 1)
+        if (form == F_CLUSTER)
+            return p.half ? launch_one<D, kGroups, F_CLUSTER, kTree, true>(p, tq, tqp, tk, tv, s)
+                                     : launch_one<D, kGroups, F_CLUSTER, kTree>(p, tq, tqp, tk, tv, s);
     if (form == F_ITEM) return launch_one<D, kGroups, F_ITEM, kTree>(p, tq, tqp, tk, tv, s);
     if (form == F_PREFIX) return launch_one<D, kGroups, F_PREFIX, kTree>(p, tq, tqp, tk, tv, s);
     return launch_one<D, kGroups, F_LIST, kTree>(p, tq, tqp, tk, tv, s);
@@ -775,7 +880,7 @@ cudaError_t launch_form(int form, const PagedParams& p, const CUtensorMap& tq, c
 template <bool kTree>
 cudaError_t launch_tiles(const PagedParams& p, int D, int groups, const CUtensorMap& tq, const CUtensorMap& tqp,
                          const CUtensorMap& tk, const CUtensorMap& tv, cudaStream_t s) {
-    const int form = p.whole ? F_ITEM : p.pre_rt > 0 ? F_PREFIX : F_LIST;
+    const int form = p.split > 0 ? F_CLUSTER : p.whole ? F_ITEM : p.pre_rt > 0 ? F_PREFIX : F_LIST;
     if (D == 64)
         return groups == 1 ? launch_form<64, 1, kTree>(form, p, tq, tqp, tk, tv, s)
                            : launch_form<64, 2, kTree>(form, p, tq, tqp, tk, tv, s);

@@ -105,6 +105,24 @@ def test_long_sequences(B, H, Hkv, Nq, n, D):
     go(trees(B, Nq, 12, n), B=B, H=H, Hkv=Hkv, D=D, Nq=Nq, page=64, kv_len=kv, seed=n, table_pad=0)
 
 
+# Items that clusters of 1 to 8 CTAs take whole: up to 64 rows (two lanes each), to 128, and several sets of rows;
+# requests much shorter than the table is wide, without keys and without rows.
+@pytest.mark.parametrize("B,H,Hkv,Nq,n,D", [
+    (1, 4, 1, 16, 3000, 64), (1, 8, 8, 9, 900, 128), (3, 24, 12, 20, 1200, 64), (5, 32, 8, 13, 800, 128), (6, 16, 8, 5, 1500, 64),
+    (16, 8, 4, 32, 1000, 128), (70, 1, 1, 60, 2000, 64), (24, 16, 4, 4, 2500, 128), (36, 8, 4, 16, 1500, 64),
+    (140, 2, 1, 40, 1400, 64), (140, 2, 1, 40, 1400, 128), (270, 2, 1, 7, 1000, 64), (36, 4, 4, 2, 1600, 64), (47, 6, 2, 3, 900, 64),
+    (2, 32, 8, 26, 5000, 64), (9, 32, 8, 26, 900, 128), (2, 16, 2, 100, 2000, 128), (1, 8, 4, 250, 4000, 64), (1, 100, 1, 7, 1100, 64)])
+@pytest.mark.parametrize("prefix", [0, 700])
+def test_clusters(B, H, Hkv, Nq, n, D, prefix):
+    kv = [max(0, n - 397 * b % (n + 1)) for b in range(B)]
+    q = [Nq if b % 4 else max(0, Nq - 3 * b % (Nq + 1)) for b in range(B)]
+    kv[-1], q[0] = (kv[-1], Nq) if B == 1 else (0, Nq)
+    kv[0] = n
+    deep = 3 if B < 100 else 0
+    sees = trees(1, Nq, deep, n) * B if B > 20 else trees(B, Nq, deep, n)
+    go(sees, B=B, H=H, Hkv=Hkv, D=D, Nq=Nq, page=(16, 64, 128)[B % 3], q_len=q, kv_len=kv, prefix=prefix, seed=n, table_pad=0)
+
+
 def test_layouts_scale_and_shared_masks():
     G.ensure_built()
     B, Nq = 3, 21
@@ -118,17 +136,15 @@ def test_layouts_scale_and_shared_masks():
 
 @wide
 @pytest.mark.parametrize("Nq,G", [(1, 1), (5, 2), (30, 4), (200, 1)])
-def test_equal_to_the_unmasked_form_where_all_is_seen(Nq, G, wide):
-    """All bits set: the same arithmetic as sage_attn_paged without a causal mask, bit for bit; bits and rows behind
-    q_len do not matter."""
-    _ = wide
+def test_where_all_is_seen(Nq, G, wide):
+    """All bits set: attention without a mask; bits and rows behind q_len do not matter, to the last bit."""
     p = P.make(B=3, H=2 * G, Hkv=2, D=128, Nq=Nq, page=32, q_len=[Nq, max(1, Nq - 2), Nq], kv_len=[Nq + 50, Nq, 700],
                causal=False, **pad(wide))
-    want = P.run(p)
     ones = torch.full((3, Nq, -(-Nq // 32)), -1, dtype=torch.int32, device="cuda")
-    assert torch.equal(T.run(p, ones), want)
+    o = T.run(p, ones)
+    P.check(p, o)
     exact = mask_of([[set(range(n))] * n + [set()] * (Nq - n) for n in p.q_len], Nq)
-    assert torch.equal(T.run(p, exact), want)
+    assert torch.equal(T.run(p, exact), o)
 
 
 def test_chain_is_the_causal_mask():
@@ -140,13 +156,14 @@ def test_chain_is_the_causal_mask():
         assert depth[0].tolist() == list(range(Nq))
 
 
-def test_streams_graphs_and_repeats():
+@pytest.mark.parametrize("pages,far", [(40, 50), (100, 350), (1300, 400)])     # an item a CTA, a cluster, the list
+def test_streams_graphs_and_repeats(pages, far):
     """Two calls in flight on their own streams and workspaces; a captured call that serves later lengths, masks and
     tables; equal bits for equal inputs."""
     G.ensure_built()
     B, Nq = 5, 18
-    ps = [P.make(B=B, H=8, Hkv=2, D=128, Nq=Nq, page=16, kv_len=[Nq + 50 * b + s for b in range(B)], causal=False, seed=s,
-                 table_pad=40 - (Nq + 200 + s + 15) // 16) for s in range(2)]
+    ps = [P.make(B=B, H=8, Hkv=2, D=128, Nq=Nq, page=16, kv_len=[Nq + far * b + s for b in range(B)], causal=False, seed=s,
+                 table_pad=pages - (Nq + 4 * far + s + 15) // 16) for s in range(2)]
     sees = [trees(B, Nq, 3, s) for s in range(2)]
     masks = [mask_of(s, Nq) for s in sees]
     want = [T.run(p, m) for p, m in zip(ps, masks)]
@@ -190,6 +207,47 @@ def test_an_unlisted_page_is_recorded():
         assert S.sage_get_device_status() == S.SAGE_ERR_PAGE
         assert S.sage_get_device_status() == S.SAGE_OK
         assert bool(torch.isfinite(o).all())
+
+
+def test_a_withheld_copy_runs_out():
+    """The bounded waits of every form of the many-rows kernel: the call ends, says so, and the next one is right."""
+    G.ensure_built()
+    for D, Nq, n, list_ in ((128, 40, 100, 0), (64, 40, 100, 1), (128, 40, 900, 0), (64, 40, 900, 0), (128, 100, 900, 0)):
+        p = P.make(B=1, H=2, Hkv=1, D=D, Nq=Nq, page=64, kv_len=[Nq + n], seed=D, causal=False, **pad(list_))
+        sees = trees(1, Nq, 3, D)
+        S.sage_debug_inject_fault(1)
+        T.run(p, mask_of(sees, Nq))
+        torch.cuda.synchronize()
+        assert S.sage_get_device_status() == S.SAGE_ERR_TIMEOUT
+        T.check(p, sees, T.run(p, mask_of(sees, Nq)))
+
+
+def test_cache_offsets_behind_two_to_the_32_elements():
+    G.ensure_built()
+    heads, D, page = 32, 128, 128
+    pages = 2 ** 32 // (heads * D * page) + 4
+    k = torch.zeros((pages, page, heads, D), dtype=torch.bfloat16, device="cuda").permute(0, 2, 1, 3)
+    v = torch.zeros((pages, page, heads, D), dtype=torch.bfloat16, device="cuda").permute(0, 2, 1, 3)
+    g = torch.Generator(device="cuda").manual_seed(5)
+    last = torch.tensor([[pages - 1, pages - 3, pages - 2, 0, pages - 4, 5, 7]], dtype=torch.int32, device="cuda")
+    for pg in last.unique().tolist():
+        k[pg] = torch.randn((heads, page, D), device="cuda", generator=g).to(torch.bfloat16)
+        v[pg] = torch.randn((heads, page, D), device="cuda", generator=g).to(torch.bfloat16)
+    for Nq, n, width in ((3, 300, 3), (20, 300, 3), (20, 850, 7)):
+        q = torch.randn((1, heads, Nq, D), device="cuda", generator=g).to(torch.bfloat16)
+        sees = trees(1, Nq, 3, Nq)
+        p = P.Paged(q, k, v, last[:, :width].contiguous(), [Nq], [n], None, 0, False)
+        T.check(p, sees, T.run(p, mask_of(sees, Nq)))
+    # rows of the append and of the move there
+    from_, to = (pages - 1) * page + 5, (pages - 2) * page + 100
+    r = S.make_rotary(S.rotary_frequencies(D)[0])
+    new = torch.randn((1, heads, 1, D), device="cuda", generator=g).to(torch.bfloat16)
+    S.sage_cache_append_rope(new, new, T.i32([[from_]]), S.PageCache(k, v), r, start=T.i32([77]))
+    S.sage_cache_keep(T.i32([[1]]), T.i32([[to, from_]]), S.PageCache(k, v))
+    turned = S.rope(new, r, start=T.i32([77]))
+    torch.cuda.synchronize()
+    for pg, off in ((pages - 1, 5), (pages - 2, 100)):
+        assert torch.equal(k[pg, :, off], turned[0, :, 0]) and torch.equal(v[pg, :, off], new[0, :, 0])
 
 
 def test_refusals_of_the_binding():
