@@ -46,7 +46,8 @@ namespace {
 // kWhole: for short sequences, bound by latency, a cluster of `split` CTAs
 // takes an item, shares its steps among its warps and joins them through
 // shared memory, so the call is one kernel (8 key heads, 60 keys: 3.9 us
-// against 6.6 with the join behind it; 777 keys: 6.7 against 7.4).
+// against 6.6 with the join behind it; 777 keys: 6.7 against 7.4; eight parts'
+// loads in flight in the join: 6.4 -> 6.1, sixteen 6.9).
 // ---------------------------------------------------------------------------
 constexpr int kRowWarps = 4;             // warps of a CTA
 constexpr int kStep = 16;                // keys of a step
@@ -383,7 +384,7 @@ __global__ void __launch_bounds__(kRowWarps * 32, 2) paged_rows_kernel(const __g
             const uint32_t ml0 = smem_u32(&part_ml[0][r]), o0 = smem_u32(smem) + (uint32_t)(r * kPartRow + c) * 4;
             float mx = -INFINITY, l = 0.f;
             float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
+#pragma unroll 8
             for (int w = 0; w < parts; ++w) {
                 const uint32_t cta = (uint32_t)w / kRowWarps, in = (uint32_t)w % kRowWarps;
                 const float2 ml = ld_cluster2(mapa_rank(ml0 + in * (uint32_t)sizeof(part_ml[0]), cta));
