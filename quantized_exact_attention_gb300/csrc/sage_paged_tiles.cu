@@ -781,8 +781,7 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
 // Join the items that a worker boundary cuts (list without shared prefix
 // items; whole items were written by the kernel above).  blockIdx.x + 1 is
 // the worker behind the boundary, blockIdx.y a group of 16 rows.  Bound by
-// latency, so kFlight parts of each of a warp's rows are loaded together (a call
-// that cuts most of 256 items: 105.4 us with a row after the other, 103.6 so).
+// latency, so kFlight parts of a row are loaded together.
 // ---------------------------------------------------------------------------
 template <int D, int M>
 __global__ void __launch_bounds__(256) paged_cuts_kernel(const __grid_constant__ PagedParams p) {
@@ -795,72 +794,57 @@ __global__ void __launch_bounds__(256) paged_cuts_kernel(const __grid_constant__
     if (cut.b < 0) return;
     const PagedSched<M, 128, false> s(p);
     const int r0 = ((int)blockIdx.y * 8 + warp) * kRows;
-    int64_t out[kRows];                                    // where a row goes (< 0: no such row)
-    float acc[kRows][V], m[kRows], l[kRows];
-    bool any = false;
 #pragma unroll
     for (int k = 0; k < kRows; ++k) {
         int b, i, hq;
-        out[k] = paged_row(s, cut.b, cut.h, cut.rt, cut.n, r0 + k, b, i, hq) ? b * p.osb + hq * p.osh + i * p.osn : -1;
-        any |= out[k] >= 0;
-        m[k] = -INFINITY;
-        l[k] = 0.f;
+        if (!paged_row(s, cut.b, cut.h, cut.rt, cut.n, r0 + k, b, i, hq)) continue;
+        float acc[V], m = -INFINITY, l = 0.f;
 #pragma unroll
-        for (int v = 0; v < V; ++v) acc[k][v] = 0.f;
-    }
-    if (!any) return;
+        for (int v = 0; v < V; ++v) acc[v] = 0.f;
 #pragma unroll 1
-    for (int j0 = 0; j0 < cut.parts; j0 += kFlight) {
-        float2 ml[kRows][kFlight];
-        float y[kRows][kFlight][V];
-#pragma unroll
-        for (int k = 0; k < kRows; ++k)
+        for (int j0 = 0; j0 < cut.parts; j0 += kFlight) {
+            float2 ml[kFlight];
+            float y[kFlight][V];
 #pragma unroll
             for (int f = 0; f < kFlight; ++f) {            // part 0: the second slot of worker w - 1
                 const int j = j0 + f;
                 const int64_t q = (int64_t)(j == 0 ? 2 * (w - 1) + 1 : 2 * (w - 1 + j)) * M + r0 + k;
-                ml[k][f] = make_float2(-INFINITY, 0.f);
+                ml[f] = make_float2(-INFINITY, 0.f);
 #pragma unroll
-                for (int v = 0; v < V; ++v) y[k][f][v] = 0.f;
-                if (j < cut.parts && out[k] >= 0) {
-                    ml[k][f] = p.part_ml[q];
+                for (int v = 0; v < V; ++v) y[f][v] = 0.f;
+                if (j < cut.parts) {
+                    ml[f] = p.part_ml[q];
                     const float* src = p.part_o + q * D + lane * V;
                     if constexpr (V == 4) {
                         const float4 x = *reinterpret_cast<const float4*>(src);
-                        y[k][f][0] = x.x; y[k][f][1] = x.y; y[k][f][2] = x.z; y[k][f][3] = x.w;
+                        y[f][0] = x.x; y[f][1] = x.y; y[f][2] = x.z; y[f][3] = x.w;
                     } else {
                         const float2 x = *reinterpret_cast<const float2*>(src);
-                        y[k][f][0] = x.x; y[k][f][1] = x.y;
+                        y[f][0] = x.x; y[f][1] = x.y;
                     }
                 }
             }
+            float mn = m;
 #pragma unroll
-        for (int k = 0; k < kRows; ++k) {
-            float mn = m[k];
-#pragma unroll
-            for (int f = 0; f < kFlight; ++f) mn = fmaxf(mn, ml[k][f].x);
+            for (int f = 0; f < kFlight; ++f) mn = fmaxf(mn, ml[f].x);
             const float ms = mn == -INFINITY ? 0.f : mn;
-            const float fa = ex2_approx(m[k] - ms);
-            l[k] *= fa;
+            const float fa = ex2_approx(m - ms);
+            l *= fa;
 #pragma unroll
-            for (int v = 0; v < V; ++v) acc[k][v] *= fa;
+            for (int v = 0; v < V; ++v) acc[v] *= fa;
 #pragma unroll
             for (int f = 0; f < kFlight; ++f) {
-                const float fb = ex2_approx(ml[k][f].x - ms);
-                l[k] += ml[k][f].y * fb;
+                const float fb = ex2_approx(ml[f].x - ms);
+                l += ml[f].y * fb;
 #pragma unroll
-                for (int v = 0; v < V; ++v) acc[k][v] += y[k][f][v] * fb;
+                for (int v = 0; v < V; ++v) acc[v] += y[f][v] * fb;
             }
-            m[k] = mn;
+            m = mn;
         }
-    }
-#pragma unroll
-    for (int k = 0; k < kRows; ++k) {
-        if (out[k] < 0) continue;
-        const float inv = l[k] == 0.f ? 0.f : __fdiv_rn(1.f, l[k]);
-        uint16_t* dst = p.o + out[k] + lane * V;
-        const uint32_t lo = pack2(acc[k][0] * inv, acc[k][1] * inv);
-        if constexpr (V == 4) *reinterpret_cast<uint2*>(dst) = make_uint2(lo, pack2(acc[k][V - 2] * inv, acc[k][V - 1] * inv));
+        const float inv = l == 0.f ? 0.f : __fdiv_rn(1.f, l);
+        uint16_t* dst = p.o + b * p.osb + hq * p.osh + i * p.osn + lane * V;
+        const uint32_t lo = pack2(acc[0] * inv, acc[1] * inv);
+        if constexpr (V == 4) *reinterpret_cast<uint2*>(dst) = make_uint2(lo, pack2(acc[V - 2] * inv, acc[V - 1] * inv));
         else *reinterpret_cast<uint32_t*>(dst) = lo;
     }
 }
