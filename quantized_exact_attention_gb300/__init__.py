@@ -595,7 +595,9 @@ def rotary_frequencies(rotary_dim: int, base: float = 10000.0, scale: float = 1.
                 (YaRN, Peng et al. 2023)."""
     if rotary_dim <= 0 or rotary_dim % 2 or not base > 0 or not scale >= 1:
         raise ValueError("rotary_dim is positive and even, base above 0, scale at least 1")
-    if method == "base":
+    if method not in ("linear", "base", "parts") or not fast > slow:
+        raise ValueError('method is "linear", "base" or "parts", with fast above slow')
+    if method == "base" and scale > 1:
         if rotary_dim == 2:
             raise ValueError("a single pair has no other base")
         base = base * scale ** (rotary_dim / (rotary_dim - 2))
@@ -604,8 +606,6 @@ def rotary_frequencies(rotary_dim: int, base: float = 10000.0, scale: float = 1.
         return f, 1.0
     if method == "linear":
         return [x / scale for x in f], 1.0
-    if method != "parts" or not fast > slow:
-        raise ValueError('method is "linear", "base" or "parts", with fast above slow')
     keep = [min(1.0, max(0.0, (trained * x / (2 * math.pi) - slow) / (fast - slow))) for x in f]
     return [x * k + x / scale * (1 - k) for x, k in zip(f, keep)], 0.1 * math.log(scale) + 1.0
 

@@ -1,5 +1,5 @@
-// sage_binding.cpp - CPython module that hands torch tensors to the page-cache
-// entries of the C ABI.
+// sage_binding.cpp - CPython module that hands torch tensors to the entries of
+// the C ABI that serve from a page cache.
 //
 // A serving loop makes these calls once per layer and token, so their host
 // time is part of their latency: reading a tensor's attributes from Python

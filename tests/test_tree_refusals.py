@@ -153,7 +153,7 @@ def test_frequencies():
     for method in ("linear", "base", "parts"):
         assert S.rotary_frequencies(64, method=method) == (plain, 1.0)
     for bad in (dict(rotary_dim=0), dict(rotary_dim=7), dict(rotary_dim=8, base=0.0), dict(rotary_dim=8, scale=0.5),
-                dict(rotary_dim=8, scale=2.0, method="other"), dict(rotary_dim=2, scale=2.0, method="base"),
+                dict(rotary_dim=8, scale=2.0, method="other"), dict(rotary_dim=8, method="other"), dict(rotary_dim=2, scale=2.0, method="base"),
                 dict(rotary_dim=8, scale=2.0, method="parts", slow=3.0, fast=3.0)):
         with pytest.raises(ValueError):
             S.rotary_frequencies(**bad)
