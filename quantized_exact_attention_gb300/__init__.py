@@ -671,7 +671,8 @@ def rope(x, rotary: Rotary, positions=None, start=None, n_len=None, inverse: boo
     B, H, N, D = x.shape
     with torch.cuda.stream(stream):                        # what is allocated here belongs to the stream that uses it
         if out is None:
-            out = torch.zeros((B, N, H, D), dtype=torch.bfloat16, device=x.device).permute(0, 2, 1, 3)
+            make = torch.empty if n_len is None else torch.zeros
+            out = make((B, N, H, D), dtype=torch.bfloat16, device=x.device).permute(0, 2, 1, 3)
         sage_rope(x, out, rotary, positions, start, n_len, inverse)
     return out
 

@@ -42,11 +42,11 @@
 // k64, items of up to 64 rows in clusters: the rows lie twice in the 128 of the
 // scores, and lane r has the keys 0-63 of row r, lane 64 + r the others.  The
 // weights of the other keys are zeros, so one product adds up both lanes' own
-// outputs, which are joined like those of two CTAs.  So all four quarters of
+// outputs, which are joined like those of two CTAs.  K and V have a loader each.  So all four quarters of
 // tensor memory, and the schedulers of their warps, have work (52 rows leave two
-// idle), no maxima are exchanged, and a CTA has 6 warps, whose registers hold a
+// idle), no maxima are exchanged, and a CTA has 7 warps, whose registers hold a
 // tile without spills (24 requests of up to 13 tokens x 4 heads, 4 key heads of 64
-// channels, 4,099 shared keys, clusters of 3: 21.0 us; with two threads a row
+// channels, 4,099 shared keys, clusters of 3: 20.3 us; with two threads a row
 // 26.3, from the list 25.5).
 //
 // The reference of the exponentials follows the row maximum lazily: O is
@@ -92,7 +92,8 @@ struct TilesShape {
     // k64: one thread a lane; else two
     static constexpr int kRowWarps = k64 ? 4 : 8;         // softmax warps of a group
     static constexpr int kWarpLoad = kRowWarps * kGroups, kWarpIssue = kWarpLoad + 1;     // + X
-    static constexpr int kThreads = kGroups == 2 ? 640 : 32 * (kRowWarps + 2);
+    static constexpr int kWarpLoadV = kWarpLoad + 2;      // k64 only
+    static constexpr int kThreads = kGroups == 2 ? 640 : 32 * (kRowWarps + (k64 ? 3 : 2));
     static constexpr int kCtasPerSm = kGroups == 2 ? 1 : 2;
     static constexpr int kNB = D / 64;                    // 64-channel blocks of a row
     static constexpr uint32_t kTile = kNB * kBlk;         // bytes of a K (or V) tile, and of a group's Q
@@ -514,7 +515,86 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
     } else if constexpr (kGroups == 2) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
     }
-    if (warp == L::kWarpLoad) {
+    if (k64 && (warp == L::kWarpLoad || warp == L::kWarpLoadV)) {
+        // ===================================================== TMA producers of K and of V
+        // One item, of which this CTA has a run of tiles, so the loop is short.  Its
+        // instructions are fetched anew for each tile, which is what they cost: one
+        // loader for K and V in turn, with the list's walk, was the longest chain of a
+        // tile (8 items of 94 tiles of 64 channels, clusters of 8: 18.3 us, so 16.5;
+        // in pages of 16 20.4 and 16.7; two issuers besides 16.2, but 25.4 in place of
+        // 24.8 for 32 items).
+        const bool for_v = warp == L::kWarpLoadV;
+        const int item = worker / p.split;
+        const int each = p.B * p.Hkv, set = item / each, rest = item - set * each;
+        const int rt = p.rt - 1 - set, b = rest / p.Hkv, h = rest - b * p.Hkv;
+        const int n = sched.q_rows(b), len = sched.own_keys(b);
+        const int tiles = sched.item_tiles(n, len, rt), share = cluster_share(tiles, p.split);
+        const int first = min((worker - item * p.split) * share, tiles), run = min(share, tiles - first);
+        if (!for_v && lane == 0) {
+            ItemNote& nt = notes[0];
+            nt.b = b; nt.h = h; nt.rt = rt; nt.n = n; nt.len = len;
+            nt.tile = first; nt.run = run;
+            mbar_arrive(bar(L::B_ITEM));
+            if (run > 0) {                                // and none behind it
+                notes[1].run = 0;
+                mbar_arrive(bar(L::B_ITEM + 1));
+            }
+        }
+        const int pre_tiles = p.join ? sched.pre_tiles() : 0;
+        const CUtensorMap* map = for_v ? &tm_v : &tm_k;
+        const uint32_t dst = sbase + (for_v ? L::OFF_V : L::OFF_K) + (uint32_t)(lane * p.page) * 128u;
+        const int full = for_v ? L::B_VF : L::B_KF, empty = for_v ? L::B_VE : L::B_KE;
+        const int32_t* table = p.table + (int64_t)b * p.table_stride;
+        const int key = lane << p.page_shift;             // this lane's page begins here in a tile
+        int nkeys = 0, page = 0;                          // of the tile to load next
+        auto look_up = [&](int tile) {
+            const bool own = tile >= pre_tiles;
+            const int key0 = (own ? tile - pre_tiles : tile) * 128;
+            nkeys = min(128, (own ? len : sched.lp) - key0);
+            page = 0;
+            if (key < nkeys) page = (own ? table : p.ptable)[(key0 + key) >> p.page_shift];
+        };
+        if (run > 0) look_up(first);
+        if (for_v && run > 0 && lane == 0) {
+            mbar_arrive_expect_tx(bar(L::B_Q), (uint32_t)(2 * L::kNB * p.tok * p.G) * 128u);
+#pragma unroll
+            for (int hb = 0; hb < L::kNB; ++hb)
+#pragma unroll
+                for (int copy = 0; copy < 2; ++copy)      // the same rows twice, for the two halves of the keys
+                    tma_load_4d(sbase + L::OFF_Q + hb * kBlk + copy * (64 * 128), &tm_q, hb * 64, h * p.G, rt * p.tok, b,
+                                bar(L::B_Q));
+        }
+        __syncwarp();
+        bool ok = true;
+        int t = 0;
+#pragma unroll 1
+        for (; t < run; ++t) {
+            const int st = t % NS;
+            if (t >= NS && !mbar_wait_warp(bar(empty + st), ((t / NS) & 1) ^ 1, abort_flag)) { ok = false; break; }
+            if (lane == 0)
+                mbar_arrive_expect_tx(bar(full + st), (uint32_t)((nkeys + p.page - 1) >> p.page_shift) * (uint32_t)(p.page * 128 * L::kNB));
+            __syncwarp();
+            if (key < nkeys) {
+                // a page outside the cache: the copy reads zeros there
+                if ((unsigned)page >= (unsigned)p.num_pages && atomicCAS(p.status, 0, kErrPage) == 0) p.status[3] = page;
+                if (!for_v || p.fault_mode != 1) {
+#pragma unroll
+                    for (int hb = 0; hb < L::kNB; ++hb)
+                        tma_load_4d(dst + st * L::kTile + hb * kBlk, map, hb * 64, 0, h, page, bar(full + st));
+                }
+            }
+            if (t + 1 < run) look_up(first + t + 1);
+        }
+        if (!ok && lane == 0) fail(R_LOAD, t);
+        __syncwarp();
+        // every copy issued lands before the CTA may exit
+        const int zero = 0;
+        if (for_v && run > 0) mbar_wait_warp(bar(L::B_Q), 0, &zero);
+        for (int i = 0; i < NS; ++i) {
+            const int u = t - 1 - i;
+            if (u >= 0 && (!for_v || p.fault_mode != 1)) mbar_wait_warp(bar(full + u % NS), (u / NS) & 1, &zero);
+        }
+    } else if (!k64 && warp == L::kWarpLoad) {
         // ===================================================== TMA producer
         // Whether this worker's run opens inside an item and is the first to do
         // so: then the item is joined from its parts afterwards.
@@ -599,7 +679,7 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                 if (lane == 0) {
                     const bool pre = kPre && at.b < 0;
                     const int tok = pre ? p.pre_tok : p.tok;
-                    mbar_arrive_expect_tx(bar(L::B_Q), (uint32_t)((k64 ? 2 : kGroups) * L::kNB * tok * (pre ? p.pre_unit : p.G)) * 128u);
+                    mbar_arrive_expect_tx(bar(L::B_Q), (uint32_t)(kGroups * L::kNB * tok * (pre ? p.pre_unit : p.G)) * 128u);
 #pragma unroll
                     for (int X = 0; X < kGroups; ++X)
 #pragma unroll
@@ -607,9 +687,6 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                             const int g = (at.rt * kGroups + X) * tok;
                             tma_load_4d(sbase + L::OFF_Q + X * L::kTile + hb * kBlk, pre ? &tm_qp : &tm_q, hb * 64,
                                         at.h * p.G, pre ? 0 : g, pre ? g : at.b, bar(L::B_Q));
-                            if (k64)                      // the same rows once more, for the other keys
-                                tma_load_4d(sbase + L::OFF_Q + hb * kBlk + 64 * 128, &tm_q, hb * 64, at.h * p.G, g, at.b,
-                                            bar(L::B_Q));
                         }
                 }
                 ++items;
