@@ -137,3 +137,102 @@ def run(B, H, Hkv, D, page, N, steps, interleaved, captured):
                                                           (2, 16, 2, 128, 64, 40, True)])
 def test_drafting_loop(B, H, Hkv, D, page, N, interleaved, captured):
     run(B, H, Hkv, D, page, N, 6, interleaved, captured)
+
+
+def test_calls_that_allocate_their_outputs():
+    """rope, tree_tables and attention_paged with a mask, on the current stream and on one of their own; one launch each."""
+    G.ensure_built()
+    B, H, Hkv, D, page, N, base = 3, 8, 2, 128, 16, 20, 150
+    g = torch.Generator(device="cuda").manual_seed(3)
+    randn = lambda *s: torch.randn(s, device="cuda", generator=g).to(torch.bfloat16)  # noqa: E731
+    rotary = S.make_rotary(S.rotary_frequencies(D)[0])
+    r = random.Random(3)
+    parents = T.i32([T.random_parents(r, N, 3) for _ in range(B)])
+    n = [N, 0, 7]
+    cache = S.alloc_page_cache(B * 11, page, Hkv, D)
+    cache.k.copy_(randn(*cache.k.shape))
+    cache.v.copy_(randn(*cache.v.shape))
+    table = torch.randperm(B * 11, generator=torch.Generator().manual_seed(1)).to(torch.int32).reshape(B, 11).cuda()
+    q, kv = randn(B, H, N, D), T.i32([base + x for x in n])
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    outs = []
+    for stream in (None, side):
+        mask, depth = S.tree_tables(parents, n_len=T.i32(n), stream=stream)
+        assert S.sage_last_launch_count() == 1
+        torch.cuda.synchronize()
+        turned = S.rope(q, rotary, positions=depth, start=T.i32([base] * B), n_len=T.i32(n), stream=stream)
+        assert S.sage_last_launch_count() == 1
+        torch.cuda.synchronize()
+        o = S.attention_paged(turned, cache, table, q_len=T.i32(n), kv_len=kv, mask=mask, stream=stream)
+        torch.cuda.synchronize()
+        outs.append((mask, depth, turned, o))
+        for b in range(B):
+            assert int(turned[b, :, n[b]:].count_nonzero()) == 0 and int(o[b, :, n[b]:].count_nonzero()) == 0
+            assert int(mask[b, n[b]:].count_nonzero()) == 0
+    assert all(torch.equal(x, y) for x, y in zip(*outs))
+    mask, _, turned, o = outs[0]
+    p = P.Paged(turned, cache.k, cache.v, table, n, [base + x for x in n], None, 0, False)
+    T.check(p, [T.sees_of(row) for row in parents.tolist()], o, fill=0.0)
+
+
+def test_appends_and_moves_on_their_own_streams():
+    """Steps of four requests' caches in flight together, each on its own stream, then all as one captured graph."""
+    G.ensure_built()
+    B, Hkv, D, page, N, K, count = 5, 4, 64, 32, 30, 9, 4
+    rotary = S.make_rotary(S.rotary_frequencies(32)[0], interleaved=True)
+    g = torch.Generator(device="cuda").manual_seed(5)
+    randn = lambda *s: torch.randn(s, device="cuda", generator=g).to(torch.bfloat16)  # noqa: E731
+    r = random.Random(4)
+    first = [[randn(B * 2, page, Hkv, D).permute(0, 2, 1, 3) for _ in range(2)] for _ in range(count)]
+    caches = [S.PageCache(*(t.clone() for t in pair)) for pair in first]
+    slots = [torch.randperm(B * 2 * page, generator=torch.Generator().manual_seed(i))[:B * N].to(torch.int32).reshape(B, N).cuda()
+             for i in range(count)]
+    kept = [T.i32([sorted(r.sample(range(N), K)) for _ in range(B)]) for _ in range(count)]
+    new = [[randn(B, Hkv, N, D) for _ in range(2)] for _ in range(count)]
+
+    def step(i, stream=None):
+        S.sage_cache_append_rope(*new[i], slots[i], caches[i], rotary, stream=stream)
+        S.sage_cache_keep(kept[i], slots[i], caches[i], stream=stream)
+
+    def reset():
+        for c, pair in zip(caches, first):
+            c.k.copy_(pair[0])
+            c.v.copy_(pair[1])
+        torch.cuda.synchronize()
+
+    def left():
+        torch.cuda.synchronize()
+        assert S.sage_get_device_status() == S.SAGE_OK
+        return [t.clone() for c in caches for t in (c.k, c.v)]
+
+    reset()
+    for i in range(count):
+        step(i)
+        torch.cuda.synchronize()
+    want = left()
+    streams = [torch.cuda.Stream() for _ in range(count)]
+    for _ in range(3):
+        reset()
+        for i in range(count):
+            step(i, streams[i])
+        assert all(torch.equal(a, b) for a, b in zip(left(), want))
+    graph = torch.cuda.CUDAGraph()
+    reset()
+    with torch.cuda.graph(graph):
+        for i in range(count):
+            step(i)
+    graph.replay()
+    assert all(torch.equal(a, b) for a, b in zip(left(), want))
+
+
+def test_a_plan_that_is_not_aligned_is_refused():
+    G.ensure_built()
+    whole = S.make_rotary(S.rotary_frequencies(64)[0])
+    odd = S.Rotary(whole.turns[1:17])                      # 16 pairs that begin 8 bytes behind an aligned address
+    x = torch.zeros((1, 1, 1, 64), dtype=torch.bfloat16, device="cuda")
+    with pytest.raises(S.SageError) as e:
+        S.sage_rope(x, x, odd)
+    assert e.value.code == S.SAGE_ERR_UNSUPPORTED
+    with pytest.raises(S.SageError):
+        S.sage_rope(x, x, S.make_rotary(S.rotary_frequencies(40)[0]))
