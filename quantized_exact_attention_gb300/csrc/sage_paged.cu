@@ -131,11 +131,11 @@ __global__ void __launch_bounds__(kRowWarps * 32, 2) paged_rows_kernel(const __g
     int parts = 0;                                        // kWhole: workers that share the item
     PagedPlace at{};
     if constexpr (kWhole) {
-        const int all = (int)blockIdx.x / p.split;        // a cluster takes an item
+        const int all = fast_div((int)blockIdx.x, p.by_split);       // a cluster takes an item
         worker = ((int)blockIdx.x - all * p.split) * kRowWarps + warp;
-        const int pair = all / p.Hkv;
+        const int pair = fast_div(all, p.by_Hkv);
         at.h = all - pair * p.Hkv;
-        at.b = pair / p.rt;
+        at.b = fast_div(pair, p.by_rt);
         at.rt = pair - at.b * p.rt;
         at.n = sched.q_rows(at.b);
         at.len = sched.own_keys(at.b);
@@ -376,7 +376,7 @@ __global__ void __launch_bounds__(kRowWarps * 32, 2) paged_rows_kernel(const __g
         __syncwarp();
         cluster_sync_all();
         // Join the workers' parts: a thread takes four channels of a row at a time.
-        const int rank = (int)blockIdx.x % p.split;
+        const int rank = (int)blockIdx.x - fast_div((int)blockIdx.x, p.by_split) * p.split;
         for (int v = rank * (int)blockDim.x + (int)threadIdx.x; v < M * D / 4; v += p.split * (int)blockDim.x) {
             const int r = v / (D / 4), c = (v - r * (D / 4)) * 4;
             int b, i, hq;
@@ -878,6 +878,9 @@ int attn_paged(const sage_tensor* q, const sage_tensor* o, const sage_page_cache
     p.tok = x.tok; p.part_m = x.M;
     p.by_G = make_fast_div(p.G);
     p.by_rt = make_fast_div(x.rt);
+    p.by_split = make_fast_div(std::max(1, x.split));
+    p.by_pairs = make_fast_div((uint32_t)B * (uint32_t)cache->heads);
+    p.by_Hkv = make_fast_div(cache->heads);
     char* w = static_cast<char*>(workspace);
     auto take = [&](size_t n) { char* at = w; w += padded(n); return at; };
     p.part_o = reinterpret_cast<float*>(take((size_t)x.slots * x.M * D * 4));

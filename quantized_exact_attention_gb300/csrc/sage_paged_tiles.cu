@@ -209,8 +209,21 @@ __device__ __forceinline__ void tree_window(const int32_t* row, int t0, int n, u
 // The lowest `many` bits.
 __device__ __forceinline__ uint32_t lowest(int many) { return many >= 32 ? 0xffffffffu : many <= 0 ? 0u : (1u << many) - 1u; }
 
-// Tiles that each of `split` CTAs of a cluster takes.
-__device__ __forceinline__ int cluster_share(int tiles, int split) { return max(1, (tiles + split - 1) / split); }
+// The item that a CTA or a cluster takes.  The last row sets come first: with a
+// causal mask they are the longest.
+struct WholeItem {
+    int b, h, rt, rank;                                   // rank of this CTA in the cluster
+};
+template <bool kCluster>
+__device__ __forceinline__ WholeItem whole_item(const PagedParams& p, int worker) {
+    const int item = kCluster ? fast_div(worker, p.by_split) : worker;
+    const int set = fast_div(item, p.by_pairs), rest = item - set * (p.B * p.Hkv), b = fast_div(rest, p.by_Hkv);
+    return WholeItem{b, rest - b * p.Hkv, p.rt - 1 - set, worker - item * p.split};
+}
+// Tiles that each CTA of a cluster takes.
+__device__ __forceinline__ int cluster_share(const PagedParams& p, int tiles) {
+    return max(1, fast_div(tiles + p.split - 1, p.by_split));
+}
 
 template <int D, int kGroups, int kForm, bool kTree, bool k64>
 __global__ void __launch_bounds__(TilesShape<D, kGroups, k64>::kThreads, TilesShape<D, kGroups, k64>::kCtasPerSm)
@@ -524,12 +537,10 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
         // in pages of 16 20.4 and 16.7; two issuers besides 16.2, but 25.4 in place of
         // 24.8 for 32 items).
         const bool for_v = warp == L::kWarpLoadV;
-        const int item = worker / p.split;
-        const int each = p.B * p.Hkv, set = item / each, rest = item - set * each;
-        const int rt = p.rt - 1 - set, b = rest / p.Hkv, h = rest - b * p.Hkv;
-        const int n = sched.q_rows(b), len = sched.own_keys(b);
-        const int tiles = sched.item_tiles(n, len, rt), share = cluster_share(tiles, p.split);
-        const int first = min((worker - item * p.split) * share, tiles), run = min(share, tiles - first);
+        const WholeItem item = whole_item<kCluster>(p, worker);
+        const int b = item.b, h = item.h, rt = item.rt, n = sched.q_rows(b), len = sched.own_keys(b);
+        const int tiles = sched.item_tiles(n, len, rt), share = cluster_share(p, tiles);
+        const int first = min(item.rank * share, tiles), run = min(share, tiles - first);
         if (!for_v && lane == 0) {
             ItemNote& nt = notes[0];
             nt.b = b; nt.h = h; nt.rt = rt; nt.n = n; nt.len = len;
@@ -603,18 +614,16 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
         PagedPlace at{};
         at.pos = t1;
         if constexpr (kItem) {
-            // last row sets first: with a causal mask they are the longest
-            const int item = kCluster ? worker / p.split : worker;
-            const int each = p.B * p.Hkv, set = item / each, rest = item - set * each;
-            at.rt = p.rt - 1 - set;
-            at.b = rest / p.Hkv;
-            at.h = rest - at.b * p.Hkv;
+            const WholeItem item = whole_item<kCluster>(p, worker);
+            at.rt = item.rt;
+            at.b = item.b;
+            at.h = item.h;
             at.n = sched.q_rows(at.b);
             at.len = sched.own_keys(at.b);
             t1 = at.ntiles = sched.item_tiles(at.n, at.len, at.rt);
             if constexpr (kCluster) {                     // this CTA's share of the item's tiles, maybe none
-                const int share = cluster_share(at.ntiles, p.split);
-                at.tile = at.pos = min((worker - item * p.split) * share, at.ntiles);
+                const int share = cluster_share(p, at.ntiles);
+                at.tile = at.pos = min(item.rank * share, at.ntiles);
                 t1 = min(at.tile + share, at.ntiles);
             }
         }
@@ -818,13 +827,13 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
         // Join the CTAs' parts: a thread takes four channels of a row at a time.
         __syncwarp();
         cluster_sync_all();
-        const int item = worker / p.split, rank = worker - item * p.split;
-        const int each = p.B * p.Hkv, set = item / each, rest = item - set * each;
-        const int rt = p.rt - 1 - set, b = rest / p.Hkv, h = rest - b * p.Hkv, n = sched.q_rows(b);
-        const int tiles = sched.item_tiles(n, sched.own_keys(b), rt), share = cluster_share(tiles, p.split);
-        const int parts = (tiles + share - 1) / share;
+        const WholeItem item = whole_item<kCluster>(p, worker);
+        const int b = item.b, h = item.h, rt = item.rt, n = sched.q_rows(b);
+        const int tiles = sched.item_tiles(n, sched.own_keys(b), rt), share = cluster_share(p, tiles);
+        int parts = 0;                                    // CTAs that have tiles
+        while (parts * share < tiles) ++parts;
 #pragma unroll 1
-        for (int v = rank * L::kThreads + (int)threadIdx.x; v < (k64 ? 64 : M) * D / 4; v += p.split * L::kThreads) {
+        for (int v = item.rank * L::kThreads + (int)threadIdx.x; v < (k64 ? 64 : M) * D / 4; v += p.split * L::kThreads) {
             const int r = v / (D / 4), c = (v - r * (D / 4)) * 4;
             int rb, ri, rh;
             if (!paged_row(sched, b, h, rt, n, r, rb, ri, rh)) continue;
