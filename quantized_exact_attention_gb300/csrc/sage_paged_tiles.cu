@@ -46,7 +46,7 @@
 // tensor memory, and the schedulers of their warps, have work (52 rows leave two
 // idle), no maxima are exchanged, and a CTA has 7 warps, whose registers hold a
 // tile without spills (24 requests of up to 13 tokens x 4 heads, 4 key heads of 64
-// channels, 4,099 shared keys, clusters of 3: 20.3 us; with two threads a row
+// channels, 4,099 shared keys, clusters of 3: 19.8 us; with two threads a row
 // 26.3, from the list 25.5).
 //
 // The reference of the exponentials follows the row maximum lazily: O is
