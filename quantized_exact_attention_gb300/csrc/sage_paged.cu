@@ -658,8 +658,11 @@ int whole_split(int64_t items, int64_t steps, int sms) {
 //    of up to 48 tiles, 104 rows of 64 channels: 24.2 us, from the list 22.9; all
 //    of them 48 tiles long: 28.6 and 34.4).  A prefix is as long for all, so its
 //    tiles count two thirds (96 items of 52 rows, 33 shared tiles and up to 8 own:
-//    21.0 and 25.5).  Few items leave SMs idle, which a list does not (6 items
-//    behind 127 shared tiles: 22.1 and 16.8; 8 items of 96: 16.3 and 20.0);
+//    21.0 and 25.5).  Few key sequences leave SMs idle, which a list does not (8 of
+//    64 rows of 128 channels, 36 tiles: 15.1 and 16.4, 64: 20.2 and 19.8, 96: 26.4
+//    and 22.5; one of 104 rows, 24 tiles: 13.4 and 14.9, 48: 17.8 and 15.0; against
+//    the few-rows kernel, one of 16 rows, 36 tiles: 11.9 and 12.5, 64: 15.5 and
+//    15.4; 6 of 64 channels, 127 tiles: 22.1 and 16.8);
 //  - over 128 rows from clusters of three on, since an item of 256 rows reads its
 //    tiles once (128 items of 24 tiles, 512 rows a request: 25.0 and 23.1; 64:
 //    18.6 and 22.8), below from two on (one CTA an item is the form above), with
@@ -678,7 +681,8 @@ bool cluster_items(Lists& x, int B, int Hkv, int G, int Nq, int D, int64_t own_k
     const int64_t items = (int64_t)B * Hkv * rt;
     int split = (int)std::min<int64_t>(8, own + pre);
     while (split > 0 && (split == 7 || items * split * 10 > (split == 5 || split == 6 ? 18 : 19) * sms)) --split;
-    if (split == 0 || own + pre < 6 || 3 * own + 2 * pre > 36 * split || own + pre > 24 + 9 * items) return false;
+    if (split == 0 || own + pre < 6 || 3 * own + 2 * pre > 36 * split) return false;
+    if (own + pre > (rows <= kFewRows ? 40 + 12 * (int64_t)B * Hkv : 32 + 3 * (int64_t)B * Hkv)) return false;
     const int least = rows > 128 ? 3 : rows > kHalfRows || (rows > kFewRows && D == 128) ? 2 : 1;
     if (split < least || (rows <= kFewRows / 2 && (rows <= 4 || D == 128 || split > 4))) return false;
     x.tiles = x.whole = true;

@@ -61,6 +61,8 @@
 // Waits are bounded as in sage_attn.cu: one that runs out records
 // SAGE_ERR_TIMEOUT, raises the CTA's abort flag, and every role leaves its
 // loop, lets its copies and products land, and returns.
+#include <algorithm>
+
 #include "sage_gb300.h"
 #include "sage_internal.h"
 #include "sage_paged.h"
@@ -71,6 +73,7 @@ namespace sage {
 namespace {
 
 constexpr int kItemNotes = 16;
+constexpr int kManyParts = 12;                            // workers to an item from which on four warps share a row's parts
 constexpr float kLazy = 8.f;                              // log2 of the weights' bound
 constexpr uint32_t kBlk = 128 * 128;                      // 128 rows x 64 channels
 
@@ -935,6 +938,107 @@ __global__ void __launch_bounds__(256) paged_cuts_kernel(const __grid_constant__
     }
 }
 
+// The same for few items of many parts each: four warps share a row's parts, and
+// the blocks of an item (blockIdx.x) look its cut up in the list of them, so that
+// all its rows are joined at a time (one request of 40,000 keys, 8 key heads of 64
+// rows, 38 parts an item: 53.0 us, so 43.0; from 12 parts on, as 9 take the same either way).
+template <int D, int M>
+__global__ void __launch_bounds__(256) paged_items_join_kernel(const __grid_constant__ PagedParams p) {
+    constexpr int V = D / 32, kShare = 4, kFlight = 4;     // channels of a lane, warps of a row, parts in flight
+    __shared__ int cut_at[3];                              // the worker behind the first boundary (0: none), its note's n and parts
+    __shared__ float red_o[8][D];
+    __shared__ float2 red_ml[8];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int sub = warp % kShare, r = (int)blockIdx.y * (8 / kShare) + warp / kShare;
+    const int pair = fast_div((int)blockIdx.x, p.by_Hkv), h = (int)blockIdx.x - pair * p.Hkv;
+    const int ib = fast_div(pair, p.by_rt), rt = pair - ib * p.rt;
+    if (threadIdx.x == 0) cut_at[0] = 0;
+    __syncthreads();
+    pdl_trigger();
+    pdl_wait();
+    for (int w = 1 + (int)threadIdx.x; w < p.workers; w += 256) {
+        const PagedCut c = p.cuts[w];
+        if (c.b == ib && c.h == h && c.rt == rt) {         // one at most
+            cut_at[0] = w;
+            cut_at[1] = c.n;
+            cut_at[2] = c.parts;
+        }
+    }
+    __syncthreads();
+    const int w = cut_at[0], n = cut_at[1], parts = cut_at[2];
+    if (w == 0) return;
+    const PagedSched<M, 128, false> s(p);
+    int b, i, hq;
+    const bool live = paged_row(s, ib, h, rt, n, r, b, i, hq);
+    float acc[V], m = -INFINITY, l = 0.f;
+#pragma unroll
+    for (int v = 0; v < V; ++v) acc[v] = 0.f;
+#pragma unroll 1
+    for (int j0 = sub; live && j0 < parts; j0 += kShare * kFlight) {
+        float2 ml[kFlight];
+        float y[kFlight][V];
+#pragma unroll
+        for (int f = 0; f < kFlight; ++f) {                // part 0: the second slot of worker w - 1
+            const int j = j0 + f * kShare;
+            const int64_t q = (int64_t)(j == 0 ? 2 * (w - 1) + 1 : 2 * (w - 1 + j)) * M + r;
+            ml[f] = make_float2(-INFINITY, 0.f);
+#pragma unroll
+            for (int v = 0; v < V; ++v) y[f][v] = 0.f;
+            if (j < parts) {
+                ml[f] = p.part_ml[q];
+                const float* src = p.part_o + q * D + lane * V;
+                if constexpr (V == 4) {
+                    const float4 x = *reinterpret_cast<const float4*>(src);
+                    y[f][0] = x.x; y[f][1] = x.y; y[f][2] = x.z; y[f][3] = x.w;
+                } else {
+                    const float2 x = *reinterpret_cast<const float2*>(src);
+                    y[f][0] = x.x; y[f][1] = x.y;
+                }
+            }
+        }
+        float mn = m;
+#pragma unroll
+        for (int f = 0; f < kFlight; ++f) mn = fmaxf(mn, ml[f].x);
+        const float ms = mn == -INFINITY ? 0.f : mn;
+        const float fa = ex2_approx(m - ms);
+        l *= fa;
+#pragma unroll
+        for (int v = 0; v < V; ++v) acc[v] *= fa;
+#pragma unroll
+        for (int f = 0; f < kFlight; ++f) {
+            const float fb = ex2_approx(ml[f].x - ms);
+            l += ml[f].y * fb;
+#pragma unroll
+            for (int v = 0; v < V; ++v) acc[v] += y[f][v] * fb;
+        }
+        m = mn;
+    }
+#pragma unroll
+    for (int v = 0; v < V; ++v) red_o[warp][lane * V + v] = acc[v];
+    if (lane == 0) red_ml[warp] = make_float2(m, l);
+    __syncthreads();
+    if (sub != 0 || !live) return;
+    float mn = m;
+#pragma unroll
+    for (int x = 1; x < kShare; ++x) mn = fmaxf(mn, red_ml[warp + x].x);
+    const float ms = mn == -INFINITY ? 0.f : mn;
+    l = 0.f;
+#pragma unroll
+    for (int v = 0; v < V; ++v) acc[v] = 0.f;
+#pragma unroll
+    for (int x = 0; x < kShare; ++x) {
+        const float fb = ex2_approx(red_ml[warp + x].x - ms);
+        l += red_ml[warp + x].y * fb;
+#pragma unroll
+        for (int v = 0; v < V; ++v) acc[v] += red_o[warp + x][lane * V + v] * fb;
+    }
+    const float inv = l == 0.f ? 0.f : __fdiv_rn(1.f, l);
+    uint16_t* dst = p.o + b * p.osb + hq * p.osh + i * p.osn + lane * V;
+    const uint32_t lo = pack2(acc[0] * inv, acc[1] * inv);
+    if constexpr (V == 4) *reinterpret_cast<uint2*>(dst) = make_uint2(lo, pack2(acc[V - 2] * inv, acc[V - 1] * inv));
+    else *reinterpret_cast<uint32_t*>(dst) = lo;
+}
+
 template <int D, int kGroups, int kForm, bool kTree, bool k64 = false>
 cudaError_t launch_one(const PagedParams& p, const CUtensorMap& tq, const CUtensorMap& tqp, const CUtensorMap& tk,
                        const CUtensorMap& tv, cudaStream_t s) {
@@ -944,6 +1048,13 @@ cudaError_t launch_one(const PagedParams& p, const CUtensorMap& tq, const CUtens
                                kForm == F_CLUSTER ? p.split : 1, true, ready,
                                tq, tqp, tk, tv, p);
     if (e != cudaSuccess) return e;
+    const int64_t items = (int64_t)p.B * p.Hkv * p.rt;
+    if (kTree && kForm == F_LIST && items * kManyParts <= p.workers) {
+        static bool items_ready[64] = {};
+        const unsigned rows = (unsigned)std::min<int64_t>(L::M, (int64_t)p.Nq * p.G + (128 - p.tok * p.G) * (kGroups - 1));
+        return launch_pdl(paged_items_join_kernel<D, L::M>, dim3((unsigned)items, (rows + 1) / 2), dim3(256), 0, s, 1, true, items_ready,
+                          p);
+    }
     if (kForm == F_LIST && p.workers > 1) {
         static bool cuts_ready[64] = {};
         e = launch_pdl(paged_cuts_kernel<D, L::M>, dim3((unsigned)p.workers - 1, L::M / 16), dim3(256), 0, s, 1, true, cuts_ready, p);
