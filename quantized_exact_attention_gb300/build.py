@@ -22,7 +22,7 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libsage_gb300.so")
 SOURCES = ["sage_api.cu", "sage_prep.cu", "sage_attn.cu", "sage_noalloc.cu", "sage_tables.cu", "sage_paged.cu",
-           "sage_paged_tiles.cu", "sage_paged_tiles_tree.cu", "sage_rotary.cu", "sage_tree.cu"]
+           "sage_paged_tiles.cu", "sage_paged_tiles_tree.cu", "sage_paged_tiles_half.cu", "sage_rotary.cu", "sage_tree.cu"]
 BINDING_SOURCE = os.path.join(CSRC, "sage_binding.cpp")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-O2",

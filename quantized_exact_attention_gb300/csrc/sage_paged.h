@@ -90,6 +90,9 @@ cudaError_t launch_paged_tiles(const PagedParams& p, int D, int groups, const CU
 // ... with a tree's mask (the shared prefix's items alone have none: either serves them).
 cudaError_t launch_paged_tiles_tree(const PagedParams& p, int D, int groups, const CUtensorMap& tq, const CUtensorMap& tqp,
                                     const CUtensorMap& tk, const CUtensorMap& tv, cudaStream_t s);
+// ... items of up to 64 rows of 64 channels from the list, two lanes to each row.
+cudaError_t launch_paged_tiles_half(const PagedParams& p, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
+                                    cudaStream_t s);
 
 // Tensor map over one tensor of a page cache, box: one page of one head, 64 channels (sage_api.cu).
 int encode_pages(CUtensorMap* m, const sage_tensor& t, int D, int page, int heads, int pages);

@@ -39,10 +39,11 @@
 // A cluster may take an item whole (F_CLUSTER): each CTA leaves its part in its
 // shared memory, where its rows, keys and values were, and the CTAs join all
 // parts of a share of the rows.
-// k64, items of up to 64 rows in clusters: the rows lie twice in the 128 of the
+// k64, items of up to 64 rows in clusters or from a tree's list: the rows lie twice in the 128 of the
 // scores, and lane r has the keys 0-63 of row r, lane 64 + r the others.  The
 // weights of the other keys are zeros, so one product adds up both lanes' own
-// outputs, which are joined like those of two CTAs.  K and V have a loader each.  So all four quarters of
+// outputs, which are joined like those of two CTAs (from the list, D = 64: the
+// upper lanes hand theirs down through shared memory).  K and V have a loader each.  So all four quarters of
 // tensor memory, and the schedulers of their warps, have work (52 rows leave two
 // idle), no maxima are exchanged, and a CTA has 7 warps, whose registers hold a
 // tile without spills (24 requests of up to 13 tokens x 4 heads, 4 key heads of 64
@@ -63,6 +64,9 @@
 // loop, lets its copies and products land, and returns.
 #include <algorithm>
 
+#ifndef SAGE_PAGED_TILES_TREE
+#define SAGE_PAGED_TILES_TREE 0      // 0: forms without a tree's mask; 1: with one; 2: its list of items with two lanes a row
+#endif
 #include "sage_gb300.h"
 #include "sage_internal.h"
 #include "sage_paged.h"
@@ -89,7 +93,7 @@ struct ItemNote {
     int pad[3];
 };
 
-template <int D, int kGroups, bool k64 = false>
+template <int D, int kGroups, bool k64 = false, bool k64List = false>
 struct TilesShape {
     static constexpr int M = 128 * kGroups;
     // k64: one thread a lane; else two
@@ -110,11 +114,14 @@ struct TilesShape {
     static constexpr uint32_t OFF_K = kGroups * kTile;
     static constexpr uint32_t OFF_V = OFF_K + kNS * kTile;
     static constexpr uint32_t OFF_STAGE = OFF_V + kNS * kTile;     // rows on their way out, 1 KB a warp
+    // k64, list: the upper lanes' maxima, sums and outputs on their way to the lower ones
+    static constexpr uint32_t OFF_MERGE = OFF_STAGE + (k64List ? kWarpLoad : kGroups * 8) * 1024;
+    static constexpr uint32_t kMerge = k64List ? 64 * (D + 4) * 4 + 64 * 8 : 0;
     // a cluster's parts lie over rows, keys and values; a row's end is padded, so that rows lie in other banks
     static constexpr int kPartRow = D + 4;
     static constexpr uint32_t OFF_PART_ML = 128 * kPartRow * 4;
     static_assert(kGroups == 2 || OFF_PART_ML + 128 * 8 <= OFF_STAGE);
-    static constexpr uint32_t OFF_XM = OFF_STAGE + kGroups * 8 * 1024;            // float [2 turns][group][half][128]
+    static constexpr uint32_t OFF_XM = OFF_MERGE + kMerge;            // float [2 turns][group][half][128]
     static constexpr uint32_t OFF_BAR = OFF_XM + kGroups * 2048;
     static constexpr int B_Q = 0, B_DRAIN = 1;            // B_DRAIN: + X
     static constexpr int B_S = 3, B_P = 5, B_ODONE = 7;   // + X
@@ -229,12 +236,14 @@ __device__ __forceinline__ int cluster_share(const PagedParams& p, int tiles) {
 }
 
 template <int D, int kGroups, int kForm, bool kTree, bool k64>
-__global__ void __launch_bounds__(TilesShape<D, kGroups, k64>::kThreads, TilesShape<D, kGroups, k64>::kCtasPerSm)
+__global__ void __launch_bounds__(TilesShape<D, kGroups, k64, k64 && kForm == F_LIST>::kThreads,
+                                  TilesShape<D, kGroups, k64, k64 && kForm == F_LIST>::kCtasPerSm)
 paged_tiles_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_qp,
                    const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                    const __grid_constant__ PagedParams p) {
-    using L = TilesShape<D, kGroups, k64>;
-    static_assert(!k64 || (kGroups == 1 && kForm == F_CLUSTER));
+    using L = TilesShape<D, kGroups, k64, k64 && kForm == F_LIST>;
+    static_assert(!k64 || (kGroups == 1 && (kForm == F_CLUSTER || (kForm == F_LIST && D == 64))));
+    constexpr bool k64List = k64 && kForm == F_LIST;
     constexpr int M = L::M, NS = L::kNS;
     constexpr bool kPre = kForm == F_PREFIX, kCluster = kForm == F_CLUSTER, kItem = kForm == F_ITEM || kCluster;
     extern __shared__ uint8_t smem_raw[];
@@ -316,7 +325,7 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
         float* xm = reinterpret_cast<float*>(sgen + L::OFF_XM) + (X * 2 + half) * 128 + row;
         const int other = half ? -128 : 128;
         constexpr int kTurn = kGroups * 256;
-        int turn = 0;                                     // exchanges so far
+        int turn = 0;                                     // exchanges so far (k64, list: items handed down)
         int t = 0;
         bool ok = true;
         auto zero_other_keys = [&]() {                    // k64: the weights of the keys that the row's other lane has
@@ -492,6 +501,69 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                         for (int i = 0; i < 16; i += 4)
                             *reinterpret_cast<uint4*>(part + (k64 ? 0 : half * (D / 2)) + c + i) = make_uint4(o[i], o[i + 1], o[i + 2], o[i + 3]);
                     }
+                } else if constexpr (k64List) {
+                    // the upper lanes hand their part down, the lower ones join both and write
+                    float* part = reinterpret_cast<float*>(sgen + L::OFF_MERGE) + query * L::kPartRow;
+                    float2* part_ml = reinterpret_cast<float2*>(sgen + L::OFF_MERGE + 64 * L::kPartRow * 4) + query;
+                    const uint32_t ready = bar(L::B_X + 2 * (quarter & 1)), taken = ready + 8;
+                    if (half == 1) {
+                        if (turn > 0 && !mbar_wait_warp(taken, (turn - 1) & 1, abort_flag)) { ok = false; break; }
+                        *part_ml = make_float2(m, l);
+#pragma unroll 1
+                        for (int c = 0; c < D; c += 16) {
+                            uint32_t o[16];
+                            tmem_ld16(tO + c, o);
+                            tmem_wait_ld();
+#pragma unroll
+                            for (int i = 0; i < 16; i += 4)
+                                *reinterpret_cast<uint4*>(part + c + i) = make_uint4(o[i], o[i + 1], o[i + 2], o[i + 3]);
+                        }
+                        __syncwarp();
+                        if (lane < 2) mbar_arrive(ready);
+                    } else {
+                        if (!mbar_wait_warp(ready, turn & 1, abort_flag)) { ok = false; break; }
+                        const float2 ml = *part_ml;
+                        const float mn = fmaxf(m, ml.x), ms = mn == -INFINITY ? 0.f : mn;
+                        float fa = ex2_approx(m - ms), fb = ex2_approx(ml.x - ms);
+                        l = l * fa + ml.y * fb;
+                        const int64_t o_at = valid ? rb * p.osb + rh * p.osh + ri * p.osn : -1;
+                        const int64_t part_at = valid ? ((int64_t)nt.slot * p.part_m + query) * D : -1;
+                        if (nt.whole) {
+                            const float inv = l == 0.f ? 0.f : __fdiv_rn(1.f, l);
+                            fa *= inv;
+                            fb *= inv;
+                        } else if (valid) {
+                            p.part_ml[(int64_t)nt.slot * p.part_m + query] = make_float2(mn, l);
+                        }
+                        uint8_t* out = sgen + L::OFF_STAGE + warp * 1024;
+#pragma unroll 1
+                        for (int c = 0; c < D; c += 8) {
+                            uint32_t o[8];
+                            tmem_ld8(tO + c, o);
+                            tmem_wait_ld();
+                            float x[8];
+#pragma unroll
+                            for (int i = 0; i < 8; i += 4) {
+                                const float4 y = *reinterpret_cast<const float4*>(part + c + i);
+                                x[i] = y.x; x[i + 1] = y.y; x[i + 2] = y.z; x[i + 3] = y.w;
+                            }
+#pragma unroll
+                            for (int i = 0; i < 8; ++i) x[i] = __uint_as_float(o[i]) * fa + x[i] * fb;
+                            if (nt.whole) {
+                                if (o_at >= 0)
+                                    *reinterpret_cast<uint4*>(p.o + o_at + c) =
+                                        make_uint4(pack2(x[0], x[1]), pack2(x[2], x[3]), pack2(x[4], x[5]), pack2(x[6], x[7]));
+                                __syncwarp();
+                            } else {
+#pragma unroll
+                                for (int i = 0; i < 8; ++i) o[i] = __float_as_uint(x[i]);
+                                stage_out(out, o, part_at, p.part_o + c, lane);
+                            }
+                        }
+                        __syncwarp();
+                        if (lane < 2) mbar_arrive(taken);
+                    }
+                    ++turn;
                 } else if (kItem || (!kPre && nt.whole)) {
                     const int64_t o_at = valid ? rb * p.osb + rh * p.osh + ri * p.osn + half * (D / 2) : -1;
                     const float inv = l == 0.f ? 0.f : __fdiv_rn(1.f, l);
@@ -531,7 +603,7 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
     } else if constexpr (kGroups == 2) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
     }
-    if (k64 && (warp == L::kWarpLoad || warp == L::kWarpLoadV)) {
+    if (k64 && kCluster && (warp == L::kWarpLoad || warp == L::kWarpLoadV)) {
         // ===================================================== TMA producers of K and of V
         // One item, of which this CTA has a run of tiles, so the loop is short.  Its
         // instructions are fetched anew for each tile, which is what they cost: one
@@ -608,8 +680,9 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
             const int u = t - 1 - i;
             if (u >= 0 && (!for_v || p.fault_mode != 1)) mbar_wait_warp(bar(full + u % NS), (u / NS) & 1, &zero);
         }
-    } else if (!k64 && warp == L::kWarpLoad) {
-        // ===================================================== TMA producer
+    } else if (!(k64 && kCluster) && (warp == L::kWarpLoad || (k64List && warp == L::kWarpLoadV))) {
+        // ===================================================== TMA producer (k64: one for K, with notes and rows, one for V)
+        const bool do_k = !k64List || warp == L::kWarpLoad, do_v = !k64List || warp == L::kWarpLoadV;
         // Whether this worker's run opens inside an item and is the first to do
         // so: then the item is joined from its parts afterwards.
         PagedCut cut{};
@@ -635,7 +708,7 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
             const int start = at.pos - at.tile, w0 = start / per;
             if (w0 == worker - 1) cut = PagedCut{at.b, at.h, at.rt, at.n, (start + at.ntiles - 1) / per - w0 + 1, {}};
         }
-        if (kForm == F_LIST && lane == 0) p.cuts[worker] = cut;
+        if (kForm == F_LIST && do_k && lane == 0) p.cuts[worker] = cut;
         const int per_tile = 128 >> p.page_shift;         // pages of a whole tile
         PagedSpan span{};
         int page = 0;
@@ -659,67 +732,74 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
             const bool mine = lane < per_tile && (lane << p.page_shift) < span.nkeys;
             const uint32_t bytes = (uint32_t)((span.nkeys + p.page - 1) >> p.page_shift) * (uint32_t)(p.page * 128 * L::kNB);
             const uint32_t off = (uint32_t)(lane * p.page) * 128u;
-            if (t >= NS && !mbar_wait_warp(bar(L::B_KE + st), ph ^ 1, abort_flag)) { ok = false; break; }
-            if (lane == 0) {
-                if (first) {
-                    // Slots of notes are not overrun: item k + 16 begins 16 tiles or more
-                    // behind item k, and the stages keep the loader that close.
-                    ItemNote& nt = notes[items % kItemNotes];
-                    nt.b = at.b; nt.h = at.h; nt.rt = at.rt;
-                    nt.n = at.n; nt.len = at.len;
-                    nt.tile = at.tile; nt.run = min(at.ntiles - at.tile, t1 - at.pos);
-                    nt.slot = kPre ? worker + at.item : 2 * worker + (at.tile == 0 ? 1 : 0);
-                    nt.whole = nt.run == at.ntiles;
-                    mbar_arrive(bar(L::B_ITEM + items % kItemNotes));
-                }
-                mbar_arrive_expect_tx(bar(L::B_KF + st), bytes);
-            }
-            __syncwarp();
-            // a page outside the cache: the copy reads zeros there
-            if (mine && (unsigned)page >= (unsigned)p.num_pages && atomicCAS(p.status, 0, kErrPage) == 0) p.status[3] = page;
-            if (mine) {
-#pragma unroll
-                for (int hb = 0; hb < L::kNB; ++hb)
-                    tma_load_4d(sbase + L::OFF_K + st * L::kTile + hb * kBlk + off, &tm_k, hb * 64, 0, at.h, page,
-                                bar(L::B_KF + st));
-            }
-            loaded_k = t + 1;
-            if (first) {
-                // The item's rows: their place is free once the scores of the tile
-                // before are computed, well before that item's output is written.
-                if (t > 0 && !mbar_wait_warp(bar(L::B_KE + (t - 1) % NS), ((t - 1) / NS) & 1, abort_flag)) { ok = false; break; }
+            if (do_k) {
+                if (t >= NS && !mbar_wait_warp(bar(L::B_KE + st), ph ^ 1, abort_flag)) { ok = false; break; }
                 if (lane == 0) {
-                    const bool pre = kPre && at.b < 0;
-                    const int tok = pre ? p.pre_tok : p.tok;
-                    mbar_arrive_expect_tx(bar(L::B_Q), (uint32_t)(kGroups * L::kNB * tok * (pre ? p.pre_unit : p.G)) * 128u);
-#pragma unroll
-                    for (int X = 0; X < kGroups; ++X)
-#pragma unroll
-                        for (int hb = 0; hb < L::kNB; ++hb) {
-                            const int g = (at.rt * kGroups + X) * tok;
-                            tma_load_4d(sbase + L::OFF_Q + X * L::kTile + hb * kBlk, pre ? &tm_qp : &tm_q, hb * 64,
-                                        at.h * p.G, pre ? 0 : g, pre ? g : at.b, bar(L::B_Q));
-                        }
+                    if (first) {
+                        // Slots of notes are not overrun: item k + 16 begins 16 tiles or more
+                        // behind item k, and the stages keep the loader that close.
+                        ItemNote& nt = notes[items % kItemNotes];
+                        nt.b = at.b; nt.h = at.h; nt.rt = at.rt;
+                        nt.n = at.n; nt.len = at.len;
+                        nt.tile = at.tile; nt.run = min(at.ntiles - at.tile, t1 - at.pos);
+                        nt.slot = kPre ? worker + at.item : 2 * worker + (at.tile == 0 ? 1 : 0);
+                        nt.whole = nt.run == at.ntiles;
+                        mbar_arrive(bar(L::B_ITEM + items % kItemNotes));
+                    }
+                    mbar_arrive_expect_tx(bar(L::B_KF + st), bytes);
                 }
-                ++items;
-            }
-            if (t >= NS && !mbar_wait_warp(bar(L::B_VE + st), ph ^ 1, abort_flag)) { ok = false; break; }
-            if (lane == 0) mbar_arrive_expect_tx(bar(L::B_VF + st), bytes);
-            __syncwarp();
-            if (mine && p.fault_mode != 1) {
+                __syncwarp();
+                // a page outside the cache: the copy reads zeros there
+                if (mine && (unsigned)page >= (unsigned)p.num_pages && atomicCAS(p.status, 0, kErrPage) == 0) p.status[3] = page;
+                if (mine) {
 #pragma unroll
-                for (int hb = 0; hb < L::kNB; ++hb)
-                    tma_load_4d(sbase + L::OFF_V + st * L::kTile + hb * kBlk + off, &tm_v, hb * 64, 0, at.h, page,
-                                bar(L::B_VF + st));
+                    for (int hb = 0; hb < L::kNB; ++hb)
+                        tma_load_4d(sbase + L::OFF_K + st * L::kTile + hb * kBlk + off, &tm_k, hb * 64, 0, at.h, page,
+                                    bar(L::B_KF + st));
+                }
+                loaded_k = t + 1;
+                if (first) {
+                    // The item's rows: their place is free once the scores of the tile
+                    // before are computed, well before that item's output is written.
+                    if (t > 0 && !mbar_wait_warp(bar(L::B_KE + (t - 1) % NS), ((t - 1) / NS) & 1, abort_flag)) { ok = false; break; }
+                    if (lane == 0) {
+                        const bool pre = kPre && at.b < 0;
+                        const int tok = pre ? p.pre_tok : p.tok;
+                        mbar_arrive_expect_tx(bar(L::B_Q), (uint32_t)((k64 ? 2 : kGroups) * L::kNB * tok * (pre ? p.pre_unit : p.G)) * 128u);
+#pragma unroll
+                        for (int X = 0; X < kGroups; ++X)
+#pragma unroll
+                            for (int hb = 0; hb < L::kNB; ++hb) {
+                                const int g = (at.rt * kGroups + X) * tok;
+                                tma_load_4d(sbase + L::OFF_Q + X * L::kTile + hb * kBlk, pre ? &tm_qp : &tm_q, hb * 64,
+                                            at.h * p.G, pre ? 0 : g, pre ? g : at.b, bar(L::B_Q));
+                                if (k64)                      // the same rows once more, for the other keys
+                                    tma_load_4d(sbase + L::OFF_Q + hb * kBlk + 64 * 128, &tm_q, hb * 64, at.h * p.G, g, at.b,
+                                                bar(L::B_Q));
+                            }
+                    }
+                    ++items;
+                }
             }
-            loaded_v = t + 1;
+            if (do_v) {
+                if (t >= NS && !mbar_wait_warp(bar(L::B_VE + st), ph ^ 1, abort_flag)) { ok = false; break; }
+                if (lane == 0) mbar_arrive_expect_tx(bar(L::B_VF + st), bytes);
+                __syncwarp();
+                if (mine && p.fault_mode != 1) {
+#pragma unroll
+                    for (int hb = 0; hb < L::kNB; ++hb)
+                        tma_load_4d(sbase + L::OFF_V + st * L::kTile + hb * kBlk + off, &tm_v, hb * 64, 0, at.h, page,
+                                    bar(L::B_VF + st));
+                }
+                loaded_v = t + 1;
+            }
             if constexpr (kItem) ++at.pos, ++at.tile;
             else paged_next(sched, at);
             first = at.tile == 0;
             if (at.pos < t1) look_up();
         }
         if (!ok && lane == 0) fail(R_LOAD, loaded_v);
-        if (ok && lane == 0) {                            // no more items
+        if (ok && do_k && lane == 0) {                    // no more items
             notes[items % kItemNotes].run = 0;
             mbar_arrive(bar(L::B_ITEM + items % kItemNotes));
         }
@@ -1042,7 +1122,7 @@ __global__ void __launch_bounds__(256) paged_items_join_kernel(const __grid_cons
 template <int D, int kGroups, int kForm, bool kTree, bool k64 = false>
 cudaError_t launch_one(const PagedParams& p, const CUtensorMap& tq, const CUtensorMap& tqp, const CUtensorMap& tk,
                        const CUtensorMap& tv, cudaStream_t s) {
-    using L = TilesShape<D, kGroups, k64>;
+    using L = TilesShape<D, kGroups, k64, k64 && kForm == F_LIST>;
     static bool ready[64] = {};
     cudaError_t e = launch_pdl(paged_tiles_kernel<D, kGroups, kForm, kTree, k64>, dim3((unsigned)p.workers), dim3(L::kThreads), L::kSmem, s,
                                kForm == F_CLUSTER ? p.split : 1, true, ready,
@@ -1062,6 +1142,7 @@ cudaError_t launch_one(const PagedParams& p, const CUtensorMap& tq, const CUtens
     return e;
 }
 
+#if SAGE_PAGED_TILES_TREE != 2
 template <int D, int kGroups, bool kTree>
 cudaError_t launch_form(int form, const PagedParams& p, const CUtensorMap& tq, const CUtensorMap& tqp, const CUtensorMap& tk,
                         const CUtensorMap& tv, cudaStream_t s) {
@@ -1077,6 +1158,7 @@ cudaError_t launch_form(int form, const PagedParams& p, const CUtensorMap& tq, c
 template <bool kTree>
 cudaError_t launch_tiles(const PagedParams& p, int D, int groups, const CUtensorMap& tq, const CUtensorMap& tqp,
                          const CUtensorMap& tk, const CUtensorMap& tv, cudaStream_t s) {
+    if (kTree && p.half && p.split == 0) return launch_paged_tiles_half(p, tq, tk, tv, s);
     const int form = p.split > 0 ? F_CLUSTER : p.whole ? F_ITEM : p.pre_rt > 0 ? F_PREFIX : F_LIST;
     if (D == 64)
         return groups == 1 ? launch_form<64, 1, kTree>(form, p, tq, tqp, tk, tv, s)
@@ -1084,13 +1166,19 @@ cudaError_t launch_tiles(const PagedParams& p, int D, int groups, const CUtensor
     return groups == 1 ? launch_form<128, 1, kTree>(form, p, tq, tqp, tk, tv, s)
                        : launch_form<128, 2, kTree>(form, p, tq, tqp, tk, tv, s);
 }
+#endif
 
 }  // namespace
 
-#ifndef SAGE_PAGED_TILES_TREE
+#if SAGE_PAGED_TILES_TREE == 0
 cudaError_t launch_paged_tiles(const PagedParams& p, int D, int groups, const CUtensorMap& tq, const CUtensorMap& tqp,
                                const CUtensorMap& tk, const CUtensorMap& tv, cudaStream_t s) {
     return launch_tiles<false>(p, D, groups, tq, tqp, tk, tv, s);
+}
+#elif SAGE_PAGED_TILES_TREE == 2
+cudaError_t launch_paged_tiles_half(const PagedParams& p, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
+                                    cudaStream_t s) {
+    return launch_one<64, 1, F_LIST, true, true>(p, tq, tq, tk, tv, s);
 }
 #else
 cudaError_t launch_paged_tiles_tree(const PagedParams& p, int D, int groups, const CUtensorMap& tq, const CUtensorMap& tqp,

@@ -98,6 +98,20 @@ def test_many_heads_to_a_key_head(G, Nq, wide):
        **pad(wide))
 
 
+# Lists: two lanes a row (up to 64 rows of 64 channels) with whole and cut items, few items of many parts, and others.
+@pytest.mark.parametrize("B,H,Hkv,Nq,n,D", [
+    (150, 4, 2, 12, 500, 64), (40, 32, 8, 16, 900, 64), (1, 2, 1, 32, 30000, 64), (3, 8, 2, 16, 9000, 64), (2, 4, 2, 20, 20000, 128),
+    (1, 6, 2, 100, 15000, 128), (1, 4, 4, 40, 12000, 64)])
+@pytest.mark.parametrize("page", [16, 128])
+def test_lists(B, H, Hkv, Nq, n, D, page):
+    kv = [max(0, n - 397 * b % (n + 1)) for b in range(B)]
+    q = [Nq if b % 4 else max(0, Nq - 3 * b % (Nq + 1)) for b in range(B)]
+    sees = trees(1, Nq, 3, n) * B
+    p = go(sees, B=B, H=H, Hkv=Hkv, D=D, Nq=Nq, page=page, q_len=q, kv_len=kv, seed=n, table_pad=3000 // page)
+    first = T.run(p, mask_of(sees, Nq))
+    assert all(torch.equal(first, T.run(p, mask_of(sees, Nq))) for _ in range(3))
+
+
 @pytest.mark.parametrize("B,H,Hkv,Nq,n,D", [(1, 8, 8, 8, 777, 128), (32, 32, 8, 26, 3000, 128), (4, 24, 8, 251, 5000, 128),
                                             (50, 32, 8, 32, 500, 128), (3, 6, 3, 500, 1100, 64), (1, 8, 2, 64, 40000, 128)])
 def test_long_sequences(B, H, Hkv, Nq, n, D):

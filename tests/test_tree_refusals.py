@@ -185,7 +185,7 @@ def test_python_checks_name_the_argument():
         S.sage_rope(x.float(), x, r)
 
 
-@pytest.mark.parametrize("name", ["sage_rotary.cu", "sage_tree.cu", "sage_paged_tiles_tree.cu"])
+@pytest.mark.parametrize("name", ["sage_rotary.cu", "sage_tree.cu", "sage_paged_tiles_tree.cu", "sage_paged_tiles_half.cu"])
 def test_no_load_may_pass_the_wait(name):
     with open(os.path.join(B.CSRC, name)) as f:
         assert unordered_loads(f.read()) == []
