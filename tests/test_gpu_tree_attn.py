@@ -226,7 +226,7 @@ def test_an_unlisted_page_is_recorded():
 def test_a_withheld_copy_runs_out():
     """The bounded waits of every form of the many-rows kernel: the call ends, says so, and the next one is right."""
     G.ensure_built()
-    for D, Nq, n, list_ in ((128, 40, 100, 0), (64, 40, 100, 1), (128, 40, 900, 0), (64, 40, 900, 0), (128, 100, 900, 0)):
+    for D, Nq, n, list_ in ((128, 40, 100, 0), (64, 40, 100, 1), (64, 20, 100, 1), (128, 20, 900, 0), (64, 20, 900, 0), (128, 100, 900, 0)):
         p = P.make(B=1, H=2, Hkv=1, D=D, Nq=Nq, page=64, kv_len=[Nq + n], seed=D, causal=False, **pad(list_))
         sees = trees(1, Nq, 3, D)
         S.sage_debug_inject_fault(1)
