@@ -417,7 +417,10 @@ int sage_attn_paged(const sage_tensor* q, const sage_tensor* o, const sage_page_
  * and how far behind the committed ones it stands), sage_rope (queries),
  * sage_cache_append_rope (keys and values), sage_attn_paged_tree and, once the
  * accepted path is known, sage_cache_keep.  sage_rope and
- * sage_cache_append_rope serve any step, with or without a tree.
+ * sage_cache_append_rope serve any step, with or without a tree.  Lengths,
+ * positions, parents, masks and slots are read on the device, so captured calls
+ * serve later ones; make the first call of an entry on a device before any
+ * capture.
  * ------------------------------------------------------------------------- */
 
 /* Rotary positions.  Pair j of a head's first rotary_dim channels is turned by

@@ -120,11 +120,11 @@ __global__ void __launch_bounds__(kTreeThreads) tree_tables_kernel(const __grid_
 // through all moves of its request, so the order holds without a barrier.  A
 // move reads what one before it wrote only where kept[b][i] < i, which an
 // accepted path, ascending, never has; then all moves go one by one, else six
-// are in flight at a time.  Bound by HBM behind three dependent loads (512
-// requests, 16 heads of 128 channels, up to 20 kept of 61, 82 MB: 16.8 us, 0.72
-// of the copy rate; with up to 6 kept, 21 MB, 4.6 us, with four in flight 5.3,
-// and 5.8 where a thread has a column of either K or V and looks at all
-// entries, eight in flight).
+// are in flight at a time.  Bound by HBM behind dependent loads (512 requests,
+// 16 heads of 128 channels, up to 20 kept of 61, 82 MB: 16.5 us, 0.73 of the copy
+// rate; with up to 6 kept, 21 MB, 4.3 us; slots asked for behind the entries 16.8
+// and 4.6, with four in flight 5.3, and 5.8 where a thread has a column of either
+// K or V and looks at all entries, eight in flight).
 // ---------------------------------------------------------------------------
 struct KeepParams {
     const int32_t* kept;
@@ -154,16 +154,27 @@ __global__ void __launch_bounds__(kKeepThreads) cache_keep_kernel(const __grid_c
         return reinterpret_cast<uint4*>(base + (int64_t)(slot >> p.page_shift) * sp + (int64_t)(slot & (p.page - 1)) * st);
     };
     constexpr int kFlight = 6;
+    // up to 64 slots are asked for beside the entries that name them
+    const bool held = p.N <= 64;
+    int slot0 = -1, slot1 = -1;
+    if (held) {
+        if (lane < p.N) slot0 = slots[lane];
+        if (lane + 32 < p.N) slot1 = slots[lane + 32];
+    }
 #pragma unroll 1
     for (int i0 = 0; i0 < p.K; i0 += 32) {                 // a lane looks one move up
         const int i = i0 + lane;
-        int src = -1, dst = -1, t = -1;
-        if (i < p.K) {
-            t = p.kept[b * p.kept_stride + i];
-            if (t >= 0 && t < p.N && t != i) {
-                src = slots[t];
-                dst = slots[i];
+        int src = -1, dst = -1, t = i < p.K ? p.kept[b * p.kept_stride + i] : -1;
+        const bool names = t >= 0 && t < p.N && t != i;
+        if (held) {
+            const int lower = __shfl_sync(0xffffffffu, slot0, t & 31), upper = __shfl_sync(0xffffffffu, slot1, t & 31);
+            if (names) {
+                src = t < 32 ? lower : upper;
+                dst = i0 == 0 ? slot0 : slot1;
             }
+        } else if (names) {
+            src = slots[t];
+            dst = slots[i];
         }
         for (int s : {src, dst})
             if (s >= p.capacity && atomicCAS(p.status, 0, kErrPage) == 0) p.status[3] = s >> p.page_shift;
