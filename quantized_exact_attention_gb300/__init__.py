@@ -648,8 +648,7 @@ def make_rotary(frequencies, interleaved: bool = False, amplitude: float = 1.0, 
     n = len(f)
     turns = (ctypes.c_uint64 * max(n, 1))()
     _check(load_library().sage_rotary_turns((ctypes.c_double * max(n, 1))(*f), n, turns), "sage_rotary_turns")
-    signed = [t - (1 << 64) if t >> 63 else t for t in turns]
-    return Rotary(torch.tensor(signed, dtype=torch.int64, device=device), bool(interleaved), float(amplitude))
+    return Rotary(torch.frombuffer(turns, dtype=torch.int64).clone().to(device), bool(interleaved), float(amplitude))
 
 
 def sage_rope(x, out, rotary: Rotary, positions=None, start=None, n_len=None, inverse: bool = False, stream=None):

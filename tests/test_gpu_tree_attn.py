@@ -125,7 +125,8 @@ def test_long_sequences(B, H, Hkv, Nq, n, D):
     (1, 4, 1, 16, 3000, 64), (1, 8, 8, 9, 900, 128), (3, 24, 12, 20, 1200, 64), (5, 32, 8, 13, 800, 128), (6, 16, 8, 5, 1500, 64),
     (16, 8, 4, 32, 1000, 128), (70, 1, 1, 60, 2000, 64), (24, 16, 4, 4, 2500, 128), (36, 8, 4, 16, 1500, 64),
     (140, 2, 1, 40, 1400, 64), (140, 2, 1, 40, 1400, 128), (270, 2, 1, 7, 1000, 64), (36, 4, 4, 2, 1600, 64), (47, 6, 2, 3, 900, 64),
-    (2, 32, 8, 26, 5000, 64), (9, 32, 8, 26, 900, 128), (2, 16, 2, 100, 2000, 128), (1, 8, 4, 250, 4000, 64), (1, 100, 1, 7, 1100, 64)])
+    (2, 32, 8, 26, 5000, 64), (9, 32, 8, 26, 900, 128), (2, 16, 2, 100, 2000, 128), (1, 8, 4, 250, 4000, 64), (1, 100, 1, 7, 1100, 64),
+    (3, 66, 2, 1, 1500, 64), (2, 64, 1, 1, 1800, 128), (9, 64, 2, 2, 1000, 128)])
 @pytest.mark.parametrize("prefix", [0, 700])
 def test_clusters(B, H, Hkv, Nq, n, D, prefix):
     kv = [max(0, n - 397 * b % (n + 1)) for b in range(B)]
