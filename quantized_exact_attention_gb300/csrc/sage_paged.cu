@@ -150,7 +150,7 @@ __global__ void __launch_bounds__(kRowWarps * 32, 2) paged_rows_kernel(const __g
         worker = warp * gridDim.x + blockIdx.x;
         const int total = paged_scan<M, kStep, false, kRowWarps * 32, kRowWarps>(sched, blockIdx.x, gridDim.x, found,
                                                                                  warp_sums, blockIdx.x == 0);
-        const int per = sched.share(total, p.workers, p.B * p.rt * p.Hkv), t0 = min(worker * per, total);
+        const int per = sched.share(total, p.by_workers, p.workers, p.B * p.rt * p.Hkv), t0 = min(worker * per, total);
         t1 = min(t0 + per, total);
         at.pos = t1;
         if (t0 < t1) at = paged_place(sched, found[warp], t0);
@@ -425,7 +425,7 @@ struct RowParts {
 __device__ __forceinline__ RowParts parts_of(int start, int nt, int per, int item) {
     RowParts r{0, 0};
     if (nt > 0) {
-        const int w0 = start / per, w1 = (start + nt - 1) / per;
+        const int w0 = small_div(start, per), w1 = small_div(start + nt - 1, per);
         r.slot0 = (int64_t)w0 + item;
         r.n = w1 - w0 + 1;
     }
@@ -454,7 +454,7 @@ __global__ void __launch_bounds__(256) paged_join_kernel(const __grid_constant__
 #pragma unroll
     for (int v = 0; v < V; ++v) acc[v] = 0.f;
     if (live) {
-        const int per = s.share(p.start[p.B * p.rt], p.workers, p.B * p.rt * p.Hkv);
+        const int per = s.share(p.start[p.B * p.rt], p.by_workers, p.workers, p.B * p.rt * p.Hkv);
         const int nt = s.item_tiles(n, len, rt), pair = b * p.rt + rt;
         const RowParts own = parts_of(p.start[pair] + h * s.places(nt) + s.kItemCost, nt, per, pair * p.Hkv + h);
         const int64_t own_q = own.slot0 * p.part_m + (r - rt * M);
@@ -468,7 +468,7 @@ __global__ void __launch_bounds__(256) paged_join_kernel(const __grid_constant__
             const int it = set * p.Hkv + h;
             // ... in the same list, or in one of its own
             const int pre_per = kTiles ? per
-                                : Tiles::share(p.Hkv * p.pre_items_rt * Tiles::places(pt), p.pre_workers, 0);
+                                : Tiles::share(p.Hkv * p.pre_items_rt * Tiles::places(pt), p.by_pre_workers, p.pre_workers, 0);
             pre = parts_of(it * Tiles::places(pt) + Tiles::kItemCost, pt, pre_per, it);
             pre_q = pre.slot0 * p.pre_m + place;
         }
@@ -906,12 +906,14 @@ int attn_paged(const sage_tensor* q, const sage_tensor* o, const sage_page_cache
     else p.start = reinterpret_cast<int32_t*>(w);
     p.pre_items_rt = x.pre_items_rt; p.pre_m = x.pre_M; p.pre_tok = x.pre_tok;
     p.pre_workers = tile_workers(sms, x.pre_groups);
+    p.by_pre_workers = make_fast_div(p.pre_workers);
     p.whole = x.whole; p.half = x.half; p.split = x.split;
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
     cudaError_t e;
     int launches = 0;
     if (x.tiles) {
         p.workers = x.whole ? B * cache->heads * x.rt * std::max(1, x.split) : tile_workers(sms, x.groups);
+        p.by_workers = make_fast_div(p.workers);
         if (x.pre) p.pre_rt = x.pre_items_rt;
         e = (tree != nullptr ? launch_paged_tiles_tree : launch_paged_tiles)(p, D, x.groups, mq, mqp, mk, mv, s);
         if (e == cudaSuccess && x.pre) e = D == 64 ? launch_join<64, 128, 128>(p, s) : launch_join<128, 128, 128>(p, s);
@@ -921,11 +923,13 @@ int attn_paged(const sage_tensor* q, const sage_tensor* o, const sage_page_cache
             PagedParams pp = p;
             pp.start = nullptr;
             pp.rt = 0; pp.pre_rt = x.pre_items_rt; pp.workers = p.pre_workers;
+            pp.by_workers = p.by_pre_workers;
             if (launch_paged_tiles(pp, D, x.pre_groups, mq, mqp, mk, mv, s) != cudaSuccess) return SAGE_ERR_LAUNCH;
             ++launches;
             p.beside = 1;
         }
         p.workers = std::min(2 * sms, kMaxRowWorkers / kRowWarps) * kRowWarps;
+        p.by_workers = make_fast_div(p.workers);
         e = tree != nullptr ? launch_rows<true>(p, D, x.nr, s) : launch_rows<false>(p, D, x.nr, s);
         launches += p.split > 0 ? 1 : 2;
     }

@@ -59,6 +59,7 @@ struct PagedParams {
     int pre_rt;                          // row sets of all requests against the prefix (0: a list of own keys)
     int tok;                             // tiles kernel: tokens of a 128-row group
     FastDiv by_G, by_rt;                 // G, rt
+    FastDiv by_workers, by_pre_workers;  // workers, pre_workers
     FastDiv by_split, by_pairs, by_Hkv;  // whole items of the many-rows kernel: split, B Hkv, Hkv
     int join;                            // 1: a request's key sequence is the prefix followed by its own keys
     int workers;                         // workers the list is shared among

@@ -46,6 +46,13 @@ __device__ __forceinline__ int fast_div(int n, const FastDiv& f) {
     return (int)((__umulhi((uint32_t)n, f.m) + (uint32_t)n) >> f.s);
 }
 
+// n / d for 0 <= n < 2^30, 0 < d, and a quotient below 2^20, which the
+// approximation misses by one at most.
+__device__ __forceinline__ int small_div(int n, int d) {
+    const int q = (int)__fdividef((float)n, (float)d), r = n - q * d;
+    return q + (r >= d ? 1 : 0) - (r < 0 ? 1 : 0);
+}
+
 // kPre: the list holds items of the shared prefix.
 template <int M, int TK, bool kPre>
 struct PagedSched {
@@ -64,9 +71,9 @@ struct PagedSched {
     // places of an item of nt tiles
     __device__ static int places(int nt) { return nt > 0 ? nt + kItemCost : 0; }
     // Places of each of `workers` runs of a list of `total` places, `items` items.
-    __device__ static int share(int total, int workers, int items) {
+    __device__ static int share(int total, const FastDiv& workers, int count, int items) {
         const int least = kTiles ? kItemCost : 1 + (int)sqrtf(kPartCost * (float)total / (float)items);
-        return max(least, (total + workers - 1) / workers);
+        return max(least, fast_div(total + count - 1, workers));
     }
     __device__ int pre_total() const { return kPre ? p.pre_rt * p.Hkv * places(pre_tiles()) : 0; }
     // Tiles of row set rt of a request with n query tokens and len own keys.
@@ -129,7 +136,7 @@ __device__ __forceinline__ int paged_scan(const PagedSched<M, TK, kPre>& s, int 
         total += red[i];
     }
     base += inc - mine;
-    const int per = s.share(total, p.workers, pairs * p.Hkv);
+    const int per = s.share(total, p.by_workers, p.workers, pairs * p.Hkv);
     int b = b0, rt = u0 - b0 * p.rt;
 #pragma unroll 1
     for (int u = u0; u < u1; ++u) {
@@ -176,7 +183,7 @@ __device__ __forceinline__ PagedPlace paged_place(const PagedSched<M, TK, kPre>&
         x.n = s.q_rows(x.b);
         x.len = s.own_keys(x.b);
         x.ntiles = s.item_tiles(x.n, x.len, x.rt);
-        x.h = (t - found.y) / s.places(x.ntiles);
+        x.h = small_div(t - found.y, s.places(x.ntiles));
         o = t - found.y - x.h * s.places(x.ntiles);
         x.item = found.x * p.Hkv + x.h;
     }

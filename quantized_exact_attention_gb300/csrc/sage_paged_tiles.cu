@@ -304,7 +304,7 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
     } else {
         const int total = paged_scan<M, 128, kPre, L::kThreads, 1>(sched, worker, 0, found, red,      // ends with a barrier
                                                                    kPre && worker == 0 && p.start != nullptr);
-        per = sched.share(total, p.workers, 0);
+        per = sched.share(total, p.by_workers, p.workers, 0);
         t0 = min(worker * per, total);
         t1 = min(t0 + per, total);
     }
@@ -705,8 +705,8 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
         }
         else if (t0 < t1) at = paged_place(sched, found[0], t0);
         if (kForm == F_LIST && at.pos < t1 && at.tile > 0) {
-            const int start = at.pos - at.tile, w0 = start / per;
-            if (w0 == worker - 1) cut = PagedCut{at.b, at.h, at.rt, at.n, (start + at.ntiles - 1) / per - w0 + 1, {}};
+            const int start = at.pos - at.tile, w0 = small_div(start, per);
+            if (w0 == worker - 1) cut = PagedCut{at.b, at.h, at.rt, at.n, small_div(start + at.ntiles - 1, per) - w0 + 1, {}};
         }
         if (kForm == F_LIST && do_k && lane == 0) p.cuts[worker] = cut;
         const int per_tile = 128 >> p.page_shift;         // pages of a whole tile
