@@ -117,14 +117,18 @@ __global__ void __launch_bounds__(kTreeThreads) tree_tables_kernel(const __grid_
 // ---------------------------------------------------------------------------
 // Keep: the rows of token kept[b][i] move to the place of token i, for
 // i = 0, 1, ... in order.  A thread moves one 16-byte column of K and of V
-// through all moves of its request, so the order holds without a barrier.  A
-// move reads what one before it wrote only where kept[b][i] < i, which an
-// accepted path, ascending, never has; then all moves go one by one, else six
-// are in flight at a time.  Bound by HBM behind dependent loads (512 requests,
-// 16 heads of 128 channels, up to 20 kept of 61, 82 MB: 16.5 us, 0.73 of the copy
-// rate; with up to 6 kept, 21 MB, 4.3 us; slots asked for behind the entries 16.8
-// and 4.6, with four in flight 5.3, and 5.8 where a thread has a column of either
-// K or V and looks at all entries, eight in flight).
+// through the moves of its request, so with one group of threads the order holds
+// without a barrier.  A move reads what one before it wrote only where kept[b][i]
+// < i, which an accepted path, ascending, never has; then the moves of the 32 go
+// one by one.  Else no move reads what an earlier one writes, and six are in
+// flight at a time, or four groups take every fourth of 32, all loaded before the
+// first is stored (a later window reads nothing that an earlier one writes
+// either, so one barrier a window does).
+// Bound by HBM behind dependent loads (512 requests, 16 heads of 128 channels, up
+// to 20 kept of 61, 82 MB: 16.5 us, 0.73 of the copy rate; with up to 6 kept, 21
+// MB, 4.4 us; slots asked for behind the entries 16.8 and 4.6, with four in flight
+// 5.3, and 5.8 where a thread has a column of either K or V and looks at all
+// entries, eight in flight).
 // ---------------------------------------------------------------------------
 struct KeepParams {
     const int32_t* kept;
@@ -138,13 +142,14 @@ struct KeepParams {
     int page, page_shift;
 };
 
-constexpr int kKeepThreads = 64;
+constexpr int kKeepColumns = 64;         // of a block
 
-__global__ void __launch_bounds__(kKeepThreads) cache_keep_kernel(const __grid_constant__ KeepParams p) {
+template <int kGroups>
+__global__ void __launch_bounds__(kKeepColumns * kGroups) cache_keep_kernel(const __grid_constant__ KeepParams p) {
     pdl_trigger();
     pdl_wait();
     const int b = blockIdx.x, lane = threadIdx.x & 31;
-    const int col = (int)blockIdx.y * kKeepThreads + threadIdx.x;
+    const int group = threadIdx.x / kKeepColumns, col = (int)blockIdx.y * kKeepColumns + threadIdx.x % kKeepColumns;
     const bool live = col < p.columns;
     const int h = col >> p.chunk_shift, c = (col - (h << p.chunk_shift)) * 8;
     uint16_t* k = p.ck + h * p.ckh + c;
@@ -153,7 +158,6 @@ __global__ void __launch_bounds__(kKeepThreads) cache_keep_kernel(const __grid_c
     auto row = [&](uint16_t* base, int slot, int64_t sp, int64_t st) -> uint4* {
         return reinterpret_cast<uint4*>(base + (int64_t)(slot >> p.page_shift) * sp + (int64_t)(slot & (p.page - 1)) * st);
     };
-    constexpr int kFlight = 6;
     // up to 64 slots are asked for beside the entries that name them
     const bool held = p.N <= 64;
     int slot0 = -1, slot1 = -1;
@@ -179,24 +183,48 @@ __global__ void __launch_bounds__(kKeepThreads) cache_keep_kernel(const __grid_c
         for (int s : {src, dst})
             if (s >= p.capacity && atomicCAS(p.status, 0, kErrPage) == 0) p.status[3] = s >> p.page_shift;
         const bool moves = src >= 0 && dst >= 0 && src < p.capacity && dst < p.capacity;
-        const int flight = __any_sync(0xffffffffu, moves && t < i) ? 1 : kFlight;
         uint32_t left = __ballot_sync(0xffffffffu, moves);
+        const bool in_turn = __any_sync(0xffffffffu, moves && t < i);      // the same in every warp
+        constexpr int kFlight = kGroups == 1 ? 6 : 32 / kGroups;
+        uint4 x[kFlight], y[kFlight];
+        int to[kFlight];
+        if (kGroups == 1 || in_turn) {                     // the next moves that are left, by the first group
+            if (kGroups > 1) __syncthreads();
+            const int flight = in_turn ? 1 : kFlight;
 #pragma unroll 1
-        while (left != 0) {
-            uint4 x[kFlight], y[kFlight];
-            int to[kFlight];
+            while (left != 0) {
+#pragma unroll
+                for (int u = 0; u < kFlight; ++u) {
+                    const bool one = left != 0 && u < flight;
+                    const int from = one ? __ffs((int)left) - 1 : 0;
+                    const int s = __shfl_sync(0xffffffffu, src, from), d = __shfl_sync(0xffffffffu, dst, from);
+                    to[u] = one && live && group == 0 ? d : -1;
+                    if (one) left &= left - 1;
+                    if (to[u] >= 0) {
+                        x[u] = *row(k, s, p.ckp, p.ckt);
+                        y[u] = *row(v, s, p.cvp, p.cvt);
+                    }
+                }
+#pragma unroll
+                for (int u = 0; u < kFlight; ++u)
+                    if (to[u] >= 0) {
+                        *row(k, to[u], p.ckp, p.ckt) = x[u];
+                        *row(v, to[u], p.cvp, p.cvt) = y[u];
+                    }
+            }
+            if (kGroups > 1) __syncthreads();
+        } else {                                           // a group takes every kGroups-th entry
 #pragma unroll
             for (int u = 0; u < kFlight; ++u) {
-                const bool one = left != 0 && u < flight;
-                const int from = one ? __ffs((int)left) - 1 : 0;
+                const int from = u * kGroups + group;
                 const int s = __shfl_sync(0xffffffffu, src, from), d = __shfl_sync(0xffffffffu, dst, from);
-                to[u] = one && live ? d : -1;
-                if (one) left &= left - 1;
+                to[u] = (left >> from) & 1 && live ? d : -1;
                 if (to[u] >= 0) {
                     x[u] = *row(k, s, p.ckp, p.ckt);
                     y[u] = *row(v, s, p.cvp, p.cvt);
                 }
             }
+            __syncthreads();                               // all have read what others write
 #pragma unroll
             for (int u = 0; u < kFlight; ++u)
                 if (to[u] >= 0) {
@@ -259,10 +287,15 @@ int sage_cache_keep(const int32_t* kept, int64_t kept_stride, int B, int K, cons
     p.columns = cache->heads << p.chunk_shift;
     p.page = cache->page_size;
     p.page_shift = 31 - __builtin_clz((unsigned)cache->page_size);
-    static bool ready[64] = {};
-    const dim3 grid((unsigned)B, (unsigned)ceil_div(p.columns, kKeepThreads));
-    if (launch_pdl(cache_keep_kernel, grid, dim3(kKeepThreads), 0, static_cast<cudaStream_t>(stream), 1, false, ready, p) !=
-        cudaSuccess)
+    static bool ready[2][64] = {};
+    const dim3 grid((unsigned)B, (unsigned)ceil_div(p.columns, kKeepColumns));
+    const cudaStream_t st = static_cast<cudaStream_t>(stream);
+    // More than one round of moves, and no more blocks than run at a time: four groups
+    // share them (64 requests, 16 heads, up to 20 kept: 3.5 us, one group 5.8; 16
+    // requests, 4 heads of 64, up to 91: 5.9 and 16.3; but 512 requests 19.3 and 16.5).
+    const bool one = K <= 6 || (int64_t)grid.x * grid.y > 4 * 152;
+    if ((one ? launch_pdl(cache_keep_kernel<1>, grid, dim3(kKeepColumns), 0, st, 1, false, ready[0], p)
+               : launch_pdl(cache_keep_kernel<4>, grid, dim3(kKeepColumns * 4), 0, st, 1, false, ready[1], p)) != cudaSuccess)
         return SAGE_ERR_LAUNCH;
     set_last_launch_count(1);
     return SAGE_OK;

@@ -98,7 +98,8 @@ def fresh(n_pages, page, H, D, layout, seed=0):
 
 @pytest.mark.parametrize("layout", ["nhd", "hnd"])
 @pytest.mark.parametrize("B,H,D,page,N,K", [(1, 1, 64, 16, 1, 1), (64, 8, 128, 16, 26, 6), (7, 3, 64, 32, 40, 40),
-                                            (5, 2, 128, 64, 100, 70), (3, 16, 128, 128, 9, 8), (2, 5, 64, 16, 300, 33)])
+                                            (5, 2, 128, 64, 100, 70), (3, 16, 128, 128, 9, 8), (2, 5, 64, 16, 300, 33),
+                                            (700, 2, 64, 16, 20, 12), (2, 40, 128, 64, 80, 64)])
 def test_keep_accepted_paths(B, H, D, page, N, K, layout):
     """Paths of random trees: moves to the front, whose sources may be destinations of others."""
     G.ensure_built()
@@ -116,11 +117,12 @@ def test_keep_accepted_paths(B, H, D, page, N, K, layout):
     assert torch.equal(cache.k, want[0]) and torch.equal(cache.v, want[1])
 
 
-@pytest.mark.parametrize("N,K", [(4, 4), (9, 8), (33, 33), (80, 64)])
-def test_keep_in_any_order(N, K):
+@pytest.mark.parametrize("B", [6, 650])                   # several groups of threads to a block, and one
+@pytest.mark.parametrize("N,K", [(4, 4), (9, 8), (33, 33), (80, 64), (100, 97)])
+def test_keep_in_any_order(N, K, B):
     """Entries in any order, repeated, out of range, and tokens without a place: one move after another."""
     G.ensure_built()
-    B, page = 6, 16
+    page = 16
     r = random.Random(N)
     cache = fresh(B * -(-N // page) + 2, page, 2, 64, "nhd")
     order = torch.randperm(cache.num_pages * page, generator=torch.Generator().manual_seed(K))[:B * N].reshape(B, N).tolist()
