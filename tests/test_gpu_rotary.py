@@ -296,3 +296,100 @@ def test_other_streams_and_graphs():
         graph.replay()
         torch.cuda.synchronize()
         assert torch.equal(out, want[k])
+
+
+# Few heads and so many tokens that a lane holds rows of 2 or 4 tokens at a time: of 4 tokens from 14,589 tokens on where
+# heads fill a warp's lanes (4 of 128 channels, 8 of 64), later where they are fewer; of 2 from 7,295 on, up to twice as
+# many heads.  The same rows in calls of a thousand tokens take the form with one.
+def whole_and_parts(B, N):
+    """Request and token ranges of calls small enough for the form with a token at a time."""
+    if N >= 1000:
+        return [(slice(b, b + 1), slice(i, i + 1000)) for b in range(B) for i in range(0, N, 1000)]
+    many = max(1, 1000 // N)
+    return [(slice(b, b + many), slice(0, N)) for b in range(0, B, many)]
+
+
+@pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("B,H,N,D,rd,together", [
+    (7, 1, 16801, 128, 128, 4), (1, 1, 65536, 128, 64, 4), (3, 3, 5333, 128, 48, 4), (40, 2, 777, 128, 128, 4), (15001, 4, 1, 128, 128, 4),
+    (5, 1, 7001, 128, 16, 2), (9, 4, 1001, 128, 112, 2), (1, 8, 8003, 128, 128, 2), (2, 7, 5001, 128, 64, 2),
+    (3, 1, 41001, 64, 64, 4), (1, 8, 15001, 64, 16, 4), (4, 5, 3777, 64, 64, 4), (5001, 6, 3, 64, 48, 4),
+    (1, 7, 8001, 64, 64, 2), (3, 16, 2500, 64, 32, 2), (2500, 11, 3, 64, 64, 2)])
+def test_several_tokens_of_a_lane(B, H, N, D, rd, together, interleaved):
+    """Tokens of different requests in one lane, a count that its tokens do not divide, rows behind n_len, in place: the bits
+    of the form with one token, and the definition."""
+    G.ensure_built()
+    apart = 32 // (D // 16) // min(32 // (D // 16), 1 << (H - 1).bit_length())       # tokens beside each other in a warp
+    assert -(-B * N // (apart * together)) >= 24 * torch.cuda.get_device_properties(0).multi_processor_count
+    r_ = random.Random(B + N)
+    f = S.rotary_frequencies(rd, 500000.0)[0]
+    r = S.make_rotary(f, interleaved=interleaved, amplitude=1.25)
+    x = view(B, H, N, D, "nhd", seed=H)
+    gen = torch.Generator(device="cuda").manual_seed(N)
+    pos = torch.randint(-(1 << 30), 1 << 30, (B, N), dtype=torch.int32, device="cuda", generator=gen)
+    start = torch.randint(0, 1 << 20, (B,), dtype=torch.int32, device="cuda", generator=gen)
+    lens = [r_.choice((N, N, N - 1, 0, -1, N + 3, r_.randrange(N + 1))) for _ in range(B)]
+    n_len = T.i32(lens)
+    live = torch.arange(N, device="cuda")[None] < n_len[:, None]                      # [B, N]
+    for inverse in (False, True):
+        for at, first in ((None, None), (pos, start)):
+            out, parts = blank(B, H, N, D), blank(B, H, N, D)
+            S.sage_rope(x, out, r, positions=at, start=first, n_len=n_len, inverse=inverse)
+            for bs, ns in whole_and_parts(B, N):
+                n = len(range(*ns.indices(N)))
+                off = torch.arange(ns.start, ns.start + n, dtype=torch.int32, device="cuda")
+                S.sage_rope(x[bs, :, ns], parts[bs, :, ns], r, positions=off if at is None else at[bs, ns],
+                            start=None if first is None else first[bs], n_len=n_len[bs] - ns.start, inverse=inverse)
+            torch.cuda.synchronize()
+            assert torch.equal(out, parts)
+            assert bool((out.permute(0, 2, 1, 3)[~live] == 7.0).all()), "rows behind n_len were written"
+            there = x.clone(memory_format=torch.preserve_format)
+            S.sage_rope(there, there, r, positions=at, start=first, n_len=n_len, inverse=inverse)
+            want = torch.where(live[:, None, :, None], out, x)
+            assert torch.equal(there, want)
+    # and some rows from their definition: the first, the last, those about a border of requests
+    for b, i in {(0, 0), (B - 1, max(0, N - 20)), (B // 2, 0), (B // 2, N // 2)}:
+        S.sage_rope(x, out, r, positions=pos, start=start)
+        some = slice(i, min(N, i + 20))
+        p = [[int(start[b]) + int(v) for v in pos[b, some].tolist()]]
+        check_rope(x[b:b + 1, :, some], out[b:b + 1, :, some], r, f, p)
+
+
+@pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("B,H,N,D,page,rd", [(9, 4, 1001, 128, 16, 128), (3, 1, 11003, 128, 64, 64), (8001, 3, 1, 128, 32, 128),
+                                             (2, 8, 4001, 64, 128, 64), (2501, 5, 3, 64, 16, 16), (20, 2, 777, 128, 16, 48)])
+def test_append_several_tokens_of_a_lane(B, H, N, D, page, rd, interleaved):
+    """Tokens without a place or with one outside the cache beside tokens that have one, in one lane."""
+    G.ensure_built()
+    f = S.rotary_frequencies(rd)[0]
+    r = S.make_rotary(f, interleaved=interleaved)
+    n_pages = -(-B * N // page) + 2
+    c0 = S.PageCache(*(randn(n_pages, page, H, D, seed=s).permute(0, 2, 1, 3) for s in (1, 2)))
+    c1 = S.PageCache(c0.k.clone(memory_format=torch.preserve_format), c0.v.clone(memory_format=torch.preserve_format))
+    kv = randn(B, N, 2, H, D, seed=3)
+    k, v = kv[:, :, 0].permute(0, 2, 1, 3), kv[:, :, 1].permute(0, 2, 1, 3)
+    cpu = torch.Generator().manual_seed(N)
+    slots = torch.randperm(n_pages * page, generator=cpu)[:B * N].to(torch.int32).reshape(B, N)
+    kind = torch.randint(0, 6, (B, N), generator=cpu)
+    slots[kind == 0] = -1
+    slots[kind == 1] = n_pages * page                                                # the first behind the cache
+    slots[0, 0] = 2 ** 31 - 1
+    gen = torch.Generator(device="cuda").manual_seed(N)
+    pos = torch.randint(0, 1 << 20, (B, N), dtype=torch.int32, device="cuda", generator=gen)
+    start = torch.randint(0, 1 << 20, (B,), dtype=torch.int32, device="cuda", generator=gen)
+    there = slots.cuda()
+    S.sage_cache_append_rope(k, v, there, c0, r, positions=pos, start=start)
+    assert S.sage_get_device_status() == S.SAGE_ERR_PAGE
+    for bs, ns in whole_and_parts(B, N):
+        S.sage_cache_append_rope(k[bs, :, ns], v[bs, :, ns], there[bs, ns], c1, r, positions=pos[bs, ns], start=start[bs])
+    assert S.sage_get_device_status() == S.SAGE_ERR_PAGE
+    assert S.sage_get_device_status() == S.SAGE_OK
+    assert torch.equal(c0.k, c1.k) and torch.equal(c0.v, c1.v)
+    # and against the rotation of the same rows; all other rows of the cache as they were
+    want_k, want_v = (randn(n_pages, page, H, D, seed=s).reshape(-1, H, D) for s in (1, 2))
+    held = (there >= 0) & (there < n_pages * page)
+    rot = S.rope(k, r, positions=pos, start=start)
+    want_k[there[held].long()] = rot.permute(0, 2, 1, 3)[held]
+    want_v[there[held].long()] = v.permute(0, 2, 1, 3)[held]
+    assert torch.equal(c0.k.permute(0, 2, 1, 3).reshape(-1, H, D), want_k)
+    assert torch.equal(c0.v.permute(0, 2, 1, 3).reshape(-1, H, D), want_v)
