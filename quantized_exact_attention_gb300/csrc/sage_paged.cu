@@ -22,6 +22,15 @@
 #include "sage_quant.cuh"
 
 namespace sage {
+
+int sm_count() {
+    static int n[64] = {};
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
+    if (n[dev] == 0 && cudaDeviceGetAttribute(&n[dev], cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 0;
+    return n[dev];
+}
+
 namespace {
 
 // ---------------------------------------------------------------------------
@@ -768,14 +777,6 @@ int check_batch(int B, int H, int Hkv, int Nq, int D) {
     // row numbers stay in int
     if ((int64_t)B * Nq * (H / Hkv) > INT32_MAX / 2 || (int64_t)H * Nq > INT32_MAX / 2) return SAGE_ERR_UNSUPPORTED;
     return SAGE_OK;
-}
-
-int sm_count() {
-    static int n[64] = {};
-    int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
-    if (n[dev] == 0 && cudaDeviceGetAttribute(&n[dev], cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 0;
-    return n[dev];
 }
 
 // Join after a list of items of M rows and TK-key tiles.

@@ -332,11 +332,11 @@ int make_turn(Turn& t, int64_t& warps, int& together, int flight, const sage_rot
     while (t.slot_shift < 5 - t.unit_shift && (1 << t.slot_shift) < H) ++t.slot_shift;
     const int apart = 32 >> (t.unit_shift + t.slot_shift);
     const int passes = (int)ceil_div(H, 1 << t.slot_shift);
-    constexpr int64_t kFill = 152 * 24;                    // warps that fill the GPU
+    const int64_t fill = 24 * std::max(1, sm_count());     // warps that fill the GPU
     together = 1;
-    while (2 * together * passes <= flight && ceil_div(t.tokens, apart * 2 * together) >= kFill) together *= 2;
+    while (2 * together * passes <= flight && ceil_div(t.tokens, apart * 2 * together) >= fill) together *= 2;
     const int64_t groups = ceil_div(t.tokens, apart * together);
-    const int want = (int)std::min<int64_t>(passes, ceil_div(kFill, groups));
+    const int want = (int)std::min<int64_t>(passes, ceil_div(fill, groups));
     t.heads_each = (int)ceil_div(passes, want) << t.slot_shift;
     t.splits = (int)ceil_div(H, t.heads_each);
     warps = groups * t.splits;

@@ -293,7 +293,7 @@ int sage_cache_keep(const int32_t* kept, int64_t kept_stride, int B, int K, cons
     // More than one round of moves, and no more blocks than run at a time: four groups
     // share them (64 requests, 16 heads, up to 20 kept: 3.5 us, one group 5.8; 16
     // requests, 4 heads of 64, up to 91: 5.9 and 16.3; but 512 requests 19.3 and 16.5).
-    const bool one = K <= 6 || (int64_t)grid.x * grid.y > 4 * 152;
+    const bool one = K <= 6 || (int64_t)grid.x * grid.y > 4 * sm_count();
     if ((one ? launch_pdl(cache_keep_kernel<1>, grid, dim3(kKeepColumns), 0, st, 1, false, ready[0], p)
                : launch_pdl(cache_keep_kernel<4>, grid, dim3(kKeepColumns * 4), 0, st, 1, false, ready[1], p)) != cudaSuccess)
         return SAGE_ERR_LAUNCH;

@@ -3,6 +3,7 @@ CUDA call; the frequencies and their turns; how the kernels load."""
 import ctypes
 import math
 import os
+import re
 from fractions import Fraction
 
 import pytest
@@ -189,3 +190,12 @@ def test_python_checks_name_the_argument():
 def test_no_load_may_pass_the_wait(name):
     with open(os.path.join(B.CSRC, name)) as f:
         assert unordered_loads(f.read()) == []
+
+
+@pytest.mark.parametrize("name", ["sage_rotary.cu", "sage_tree.cu"])
+def test_the_device_says_how_many_sms_it_has(name):
+    """Rules of the host that go by the size of the GPU ask for it."""
+    with open(os.path.join(B.CSRC, name)) as f:
+        code = re.sub(r"//[^\n]*", "", f.read())
+    assert not re.search(r"\b15[02]\b", code)
+    assert "sm_count()" in code
