@@ -290,10 +290,19 @@ int sage_cache_keep(const int32_t* kept, int64_t kept_stride, int B, int K, cons
     static bool ready[2][64] = {};
     const dim3 grid((unsigned)B, (unsigned)ceil_div(p.columns, kKeepColumns));
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
-    // More than one round of moves, and no more blocks than run at a time: four groups
-    // share them (64 requests, 16 heads, up to 20 kept: 3.5 us, one group 5.8; 16
-    // requests, 4 heads of 64, up to 91: 5.9 and 16.3; but 512 requests 19.3 and 16.5).
-    const bool one = K <= 6 || (int64_t)grid.x * grid.y > 4 * sm_count();
+    // Four groups of a block share the moves of a call of few blocks and several entries.
+    // Such a block holds 256 threads of 104 registers, and two run on an SM at a time:
+    //  - up to two blocks an SM, from the seventh entry on, as one group has six moves in
+    //    flight (16 heads of 128, 256 blocks, 8 entries: 2.9 us, one group 3.2; 7 entries
+    //    2.9 and 2.9; 20: 3.5 and 5.9; 16 requests, 4 heads of 64, up to 91: 5.9 and 16.3);
+    //  - up to four, in two rounds, from the eleventh on (336 blocks, 7 entries: 3.5 and
+    //    2.9; 10: 3.7 and 3.8; 12: 3.9 and 4.15; 608 blocks, 7: 3.9 and 3.1; 10: 4.3 and
+    //    4.3; 12: 4.5 and 4.8; 20: 5.8 and 8.1);
+    //  - beyond, one group, whose blocks hide each other's waits (704 blocks, 12 entries:
+    //    5.4 and 4.7; 2,048, 20: 19.3 and 16.4; but 920, 20: 9.2 and 10.3).
+    const int64_t blocks = (int64_t)grid.x * grid.y;
+    const int sms = sm_count();
+    const bool one = blocks > 4 * sms || K <= (blocks > 2 * sms ? 10 : 6);
     if ((one ? launch_pdl(cache_keep_kernel<1>, grid, dim3(kKeepColumns), 0, st, 1, false, ready[0], p)
                : launch_pdl(cache_keep_kernel<4>, grid, dim3(kKeepColumns * 4), 0, st, 1, false, ready[1], p)) != cudaSuccess)
         return SAGE_ERR_LAUNCH;

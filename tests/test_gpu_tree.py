@@ -153,3 +153,22 @@ def test_keep_outside_the_cache_is_recorded():
     S.sage_cache_keep(T.i32(kept), T.i32(slots), cache)
     assert S.sage_get_device_status() == S.SAGE_ERR_PAGE
     assert torch.equal(cache.k, k) and torch.equal(cache.v, v)
+
+
+@pytest.mark.parametrize("B,K", [(300, 6), (300, 8), (400, 8), (400, 10), (400, 11), (400, 33), (600, 12), (700, 12), (700, 40)])
+def test_keep_on_all_sides_of_its_rule(B, K):
+    """Up to two, four and more blocks an SM (a block for each request here), few entries and many: paths and any order."""
+    G.ensure_built()
+    page, N = 16, K + 9
+    r = random.Random(B + K)
+    cache = fresh(B * -(-N // page) + 2, page, 3, 64, "nhd")
+    order = torch.randperm(cache.num_pages * page, generator=torch.Generator().manual_seed(K))[:B * N].reshape(B, N).tolist()
+    kept = []
+    for b in range(B):
+        path = sorted(r.sample(range(N), r.randint(0, K))) if b % 3 else [r.randrange(-2, N + 1) for _ in range(K)]
+        kept.append(path + [-1] * (K - len(path)))
+    want = moved(kept, order, cache)
+    S.sage_cache_keep(T.i32(kept), T.i32(order), cache)
+    torch.cuda.synchronize()
+    assert S.sage_get_device_status() == S.SAGE_OK
+    assert torch.equal(cache.k, want[0]) and torch.equal(cache.v, want[1])
