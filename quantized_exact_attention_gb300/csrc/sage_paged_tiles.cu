@@ -1151,7 +1151,8 @@ cudaError_t launch_form(int form, const PagedParams& p, const CUtensorMap& tq, c
             return p.half ? launch_one<D, kGroups, F_CLUSTER, kTree, true>(p, tq, tqp, tk, tv, s)
                                      : launch_one<D, kGroups, F_CLUSTER, kTree>(p, tq, tqp, tk, tv, s);
     if (form == F_ITEM) return launch_one<D, kGroups, F_ITEM, kTree>(p, tq, tqp, tk, tv, s);
-    if (form == F_PREFIX) return launch_one<D, kGroups, F_PREFIX, kTree>(p, tq, tqp, tk, tv, s);
+    if constexpr (!kTree || kGroups == 1)                 // a tree's list with the prefix's items is of single groups
+        if (form == F_PREFIX) return launch_one<D, kGroups, F_PREFIX, kTree>(p, tq, tqp, tk, tv, s);
     return launch_one<D, kGroups, F_LIST, kTree>(p, tq, tqp, tk, tv, s);
 }
 

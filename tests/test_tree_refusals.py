@@ -4,6 +4,7 @@ import ctypes
 import math
 import os
 import re
+import subprocess
 from fractions import Fraction
 
 import pytest
@@ -199,3 +200,19 @@ def test_the_device_says_how_many_sms_it_has(name):
         code = re.sub(r"//[^\n]*", "", f.read())
     assert not re.search(r"\b15[02]\b", code)
     assert "sm_count()" in code
+
+
+def test_no_form_is_built_that_no_call_reaches(lib):
+    """paged_tiles_kernel<channels, groups, form, tree, two lanes a row> (forms: 0 the list, 1 with the prefix's items, 2 an
+    item to a CTA, 3 to a cluster), as the library's symbols name them."""
+    names = subprocess.run(["nm", "-C", B.LIB], capture_output=True, text=True, check=True).stdout
+    built = set(re.findall(r" t void sage::\(anonymous namespace\)::paged_tiles_kernel<(\d+), (\d), (\d), (\w+), (\w+)>\(", names))
+    want = set()
+    for D in ("64", "128"):
+        for tree in ("false", "true"):
+            want |= {(D, g, form, tree, "false") for g in "12" for form in "02"}
+            want.add((D, "1", "1", tree, "false"))
+        want.add((D, "2", "1", "false", "false"))          # the prefix's own list, which needs no mask
+        want |= {(D, "1", "3", "true", "false"), (D, "1", "3", "true", "true")}
+    want.add(("64", "1", "0", "true", "true"))
+    assert built == want
