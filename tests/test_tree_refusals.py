@@ -216,3 +216,11 @@ def test_no_form_is_built_that_no_call_reaches(lib):
         want |= {(D, "1", "3", "true", "false"), (D, "1", "3", "true", "true")}
     want.add(("64", "1", "0", "true", "true"))
     assert built == want
+
+
+@pytest.mark.parametrize("name,form", [("sage_paged_tiles_tree.cu", "1"), ("sage_paged_tiles_half.cu", "2")])
+def test_units_of_the_other_forms_hold_nothing_else(name, form):
+    """So the checks of sage_paged_tiles.cu's text cover what they compile."""
+    with open(os.path.join(B.CSRC, name)) as f:
+        code = [x for x in (re.sub(r"//.*", "", line).strip() for line in f) if x]
+    assert code == [f"#define SAGE_PAGED_TILES_TREE {form}", '#include "sage_paged_tiles.cu"']
