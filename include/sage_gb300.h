@@ -443,7 +443,7 @@ typedef struct {
  * units of 2^-64, for n frequencies in radians a position (|f| < 2^20; any
  * scaling for far positions is in them).  The angle of position pos is then
  * pos * turns[j] modulo 2^64, an integer product: it is off by less than
- * |pos| * 2^-64 + 2^-32 turns at any position of 32 bits. */
+ * |pos| * 2^-64 + 2^-32 turns, at any position of 32 bits by less than 2^-31. */
 int sage_rotary_turns(const double* frequencies, int n, uint64_t* turns);
 
 /* Rotate the rows of x into out.

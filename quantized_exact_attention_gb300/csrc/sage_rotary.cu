@@ -5,10 +5,10 @@
 //     y1 = A (x1 cos a - x2 sin a),   y2 = A (x1 sin a + x2 cos a)
 // (inverse: -a, which is the transposed matrix and so the gradient).  The angle
 // is held in turns of 2^-64: pos * round(f_j / (2 pi) * 2^64) modulo 2^64 is an
-// integer product that wraps by itself, so a far position loses nothing: the
-// error is below |pos| * 2^-65 turns from the frequency and 2^-32 from taking
-// the upper half, where an FP32 product pos * f_j would be off by 0.06 rad at
-// pos = 10^6.  Sine and cosine are FP32 of that angle, the products and their
+// integer product that wraps by itself: the error is below |pos| * 2^-64 turns
+// from the frequency and 2^-32 from taking the upper half, so below 2^-31 turns
+// at every position of 32 bits, where an FP32 product pos * f_j would be off by
+// 0.06 rad at pos = 10^6.  Sine and cosine are FP32 of that angle, the products and their
 // sum FP32; the result is rounded to BF16 once.
 #include <algorithm>
 #include <cmath>

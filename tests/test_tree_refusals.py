@@ -224,3 +224,15 @@ def test_units_of_the_other_forms_hold_nothing_else(name, form):
     with open(os.path.join(B.CSRC, name)) as f:
         code = [x for x in (re.sub(r"//.*", "", line).strip() for line in f) if x]
     assert code == [f"#define SAGE_PAGED_TILES_TREE {form}", '#include "sage_paged_tiles.cu"']
+
+
+def test_angles_of_far_positions(lib):
+    """The upper 32 bits of pos * turns: off by less than |pos| * 2^-64 + 2^-32 turns, which is 2^-31 at most for positions
+    of 32 bits and for the sum of two."""
+    f = S.rotary_frequencies(128, 500000.0)[0] + [3.0, -0.25, 1e-12, 77777.7]
+    for pos in (1, -1, 12345, 10 ** 6, 2 ** 31 - 1, -2 ** 31, 2 ** 32 - 2, -2 ** 32):
+        for x, t in zip(f, S.make_rotary(f, device="cpu").turns.tolist()):
+            phase = (pos * t) % 2 ** 64 >> 32
+            off = (Fraction(phase, 2 ** 32) - pos * Fraction(x) / TWO_PI) % 1
+            off = min(off, 1 - off)
+            assert off < abs(pos) * Fraction(1, 2 ** 64) + Fraction(1, 2 ** 32) <= Fraction(1, 2 ** 31), (x, pos)
