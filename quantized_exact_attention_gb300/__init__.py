@@ -657,21 +657,48 @@ def sage_rope(x, out, rotary: Rotary, positions=None, start=None, n_len=None, in
     position positions[b, i] (int32 [B, N], or [N] for all requests; None: i)
     plus start[b] (int32 [B]; None: 0); rows at or beyond n_len[b] are not
     written.  inverse=True: the transposed map, which takes the gradient of out
-    to that of x."""
+    to that of x.  Autograd does not see what is written here; rope's result
+    carries the gradient."""
     rc = (_paged or _paged_binding()).rope(x, out, rotary._address, rotary._device, positions, start, n_len, inverse,
                                            None if stream is None else stream.cuda_stream)
     if rc:
         _check(rc, "sage_rope")
 
 
+class _Rope(torch.autograd.Function):
+    """rope for an x that requires a gradient.  The map is linear and its inverse
+    form the transposed one, so backward is rope again (and differentiable too);
+    rows behind n_len, zeros of the output, have gradients of zero."""
+
+    @staticmethod
+    def forward(ctx, x, rotary, positions, start, n_len, inverse):
+        ctx.save_for_backward(positions, start, n_len)
+        ctx.rotary, ctx.inverse = rotary, inverse
+        return rope(x, rotary, positions, start, n_len, inverse)
+
+    @staticmethod
+    def backward(ctx, g):
+        positions, start, n_len = ctx.saved_tensors
+        if g.stride(3) != 1 or g.data_ptr() % 16 or any(s % 8 for s in g.stride()[:3]):
+            g = g.clone(memory_format=torch.contiguous_format)       # such as the gradient of a sum, one value expanded
+        return rope(g, ctx.rotary, positions, start, n_len, not ctx.inverse), None, None, None, None, None
+
+
 def rope(x, rotary: Rotary, positions=None, start=None, n_len=None, inverse: bool = False, out=None, stream=None):
     """sage_rope with its own output unless `out` is given (rows at or beyond
-    n_len are zero); returns the output."""
+    n_len are zero); returns the output.  Without `out` the result carries x's
+    gradient, if x requires one: positions, start and n_len then stay as they are
+    until the backward pass, as for any saved tensor, and as with any operator a
+    backward pass is captured while no eager result of the same leaves is alive.
+    `out`, like the memory that sage_rope writes, is nothing that autograd sees."""
     B, H, N, D = x.shape
     with torch.cuda.stream(stream):                        # what is allocated here belongs to the stream that uses it
         if out is None:
-            make = torch.empty if n_len is None else torch.zeros
-            out = make((B, N, H, D), dtype=torch.bfloat16, device=x.device).permute(0, 2, 1, 3)
+            if x.requires_grad and torch.is_grad_enabled():
+                return _Rope.apply(x, rotary, positions, start, n_len, inverse)
+            out = torch.empty_strided((B, H, N, D), (N * H * D, D, H * D, 1), dtype=torch.bfloat16, device=x.device)
+            if n_len is not None:
+                out.zero_()
         sage_rope(x, out, rotary, positions, start, n_len, inverse)
     return out
 

@@ -393,3 +393,103 @@ def test_append_several_tokens_of_a_lane(B, H, N, D, page, rd, interleaved):
     want_v[there[held].long()] = v.permute(0, 2, 1, 3)[held]
     assert torch.equal(c0.k.permute(0, 2, 1, 3).reshape(-1, H, D), want_k)
     assert torch.equal(c0.v.permute(0, 2, 1, 3).reshape(-1, H, D), want_v)
+
+
+@pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("inverse", [False, True])
+def test_the_result_carries_the_gradient(interleaved, inverse):
+    """rope of an x that requires a gradient: the bits of a call without, and backward is the inverse form."""
+    G.ensure_built()
+    B, H, N, D, rd = 3, 4, 29, 64, 48
+    f, a = S.rotary_frequencies(rd, scale=8.0, method="parts")
+    r = S.make_rotary(f, interleaved=interleaved, amplitude=a)
+    x, g = view(B, H, N, D, "fused", seed=1), view(B, H, N, D, "hnd", seed=2)
+    start, lens = T.i32([1000, 5, 70000]), [N, 0, N - 3]
+    for n_len in (None, T.i32(lens)):
+        plain = S.rope(x, r, start=start, n_len=n_len, inverse=inverse)
+        assert not plain.requires_grad
+        leaf = x.clone().requires_grad_()
+        y = S.rope(leaf, r, start=start, n_len=n_len, inverse=inverse)
+        assert torch.equal(y, plain)
+        y.backward(g)
+        want = S.rope(g, r, start=start, n_len=n_len, inverse=not inverse)
+        assert torch.equal(leaf.grad, want)
+        pos = [range(s, s + N) for s in (1000, 5, 70000)]
+        check_rope(g, leaf.grad, r, f, pos, None if n_len is None else lens, not inverse, fill=0.0)
+        with torch.no_grad():
+            assert not S.rope(leaf, r, start=start, n_len=n_len).requires_grad
+    # into another tensor, and further on: the gradient of an expression of it
+    leaf = x.clone().requires_grad_()
+    (S.rope(leaf, r, start=start, inverse=inverse) * g).float().pow(2).sum().backward()
+    y = S.rope(x, r, start=start, inverse=inverse)
+    want = S.rope((2 * (y * g).float()).to(torch.bfloat16) * g, r, start=start, inverse=not inverse)
+    assert torch.equal(leaf.grad, want)
+
+
+def test_gradients_of_other_forms():
+    """A gradient that is one value expanded, one of other strides, of a gradient, on a stream, in a graph; and differences."""
+    G.ensure_built()
+    B, H, N, D = 2, 3, 17, 128
+    f = S.rotary_frequencies(D)[0]
+    r = S.make_rotary(f)
+    x = view(B, H, N, D, "nhd", seed=4)
+    ones = torch.ones_like(x)
+    want = S.rope(ones, r, inverse=True)
+    leaf = x.clone().requires_grad_()
+    S.rope(leaf, r).sum().backward()
+    assert torch.equal(leaf.grad, want)
+    g = randn(B, H, D, N, seed=5).transpose(2, 3)          # channels apart
+    odd = randn(B * H * N * D + 1, seed=6)[1:].view(B, H, N, D)                       # not on 16 bytes
+    for grad in (g, odd, randn(H, N, D, seed=7).expand(B, H, N, D)):
+        leaf = x.clone().requires_grad_()
+        S.rope(leaf, r).backward(grad)
+        assert torch.equal(leaf.grad, S.rope(grad.clone(memory_format=torch.contiguous_format), r, inverse=True))
+    # of a gradient: the map is linear, so the gradient's gradient is the map again
+    leaf, v = x.clone().requires_grad_(), view(B, H, N, D, "nhd", seed=8).requires_grad_()
+    (dx,) = torch.autograd.grad(S.rope(leaf, r), leaf, v, create_graph=True)
+    u = view(B, H, N, D, "nhd", seed=9)
+    (dv,) = torch.autograd.grad(dx, v, u)
+    assert torch.equal(dv, S.rope(u, r))
+    # differences of one channel by a step that BF16 holds, from 0: both sides within their roundings
+    leaf = torch.zeros_like(x).requires_grad_()
+    S.rope(leaf, r).backward(u)
+    for b, h, n, c in ((0, 0, 3, 1), (1, 2, 16, 127), (0, 1, 9, 64)):
+        e = torch.zeros_like(x)
+        e[b, h, n, c] = 4.0
+        slope = (u.double() * (S.rope(e, r).double() - S.rope(-e, r).double())).sum() / 8.0
+        # two outputs of size up to 4, rounded by 2^-8 of it at most, times u, over 4; the gradient rounded itself
+        tol = 2.0 ** -8 * 2 * float(u[b, h, n].abs().max()) + float(leaf.grad[b, h, n, c].abs()) * 2.0 ** -8 + 1e-4
+        assert abs(float(slope) - float(leaf.grad[b, h, n, c])) <= tol
+    # on a stream of its own
+    st = torch.cuda.Stream()
+    leaf = x.clone().requires_grad_()
+    torch.cuda.synchronize()
+    y = S.rope(leaf, r, stream=st)
+    st.synchronize()
+    y.backward(u)
+    torch.cuda.synchronize()
+    assert torch.equal(y, S.rope(x, r)) and torch.equal(leaf.grad, S.rope(u, r, inverse=True))
+    # positions changed in between: refused, as for any saved tensor
+    start = T.i32([3, 4])
+    y = S.rope(x.clone().requires_grad_(), r, start=start)
+    start += 1
+    with pytest.raises(RuntimeError, match="modified"):
+        y.backward(u)
+    # forward and backward in one graph, replayed with other values
+    leaf, grad, start = x.clone().requires_grad_(), u.clone(), T.i32([0, 0])
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        torch.autograd.grad(S.rope(leaf, r, start=start), leaf, grad)
+    torch.cuda.current_stream().wait_stream(side)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        y = S.rope(leaf, r, start=start)
+        (dx,) = torch.autograd.grad(y, leaf, grad)
+    for k in (7, 100000):
+        grad.copy_(view(B, H, N, D, "nhd", seed=k))
+        start.copy_(T.i32([k, 2 * k]))
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(y, S.rope(x, r, start=start)) and torch.equal(dx, S.rope(grad, r, start=start, inverse=True))
