@@ -665,9 +665,14 @@ int whole_split(int64_t items, int64_t steps, int sms) {
 //  - from 6 tiles on (16 items of 4 tiles, 64 rows: 8.8 us so, a CTA each 7.9);
 //  - up to 12 tiles a CTA, as a list evens out what a cluster does not (64 items
 //    of up to 48 tiles, 104 rows of 64 channels: 24.2 us, from the list 22.9; all
-//    of them 48 tiles long: 28.6 and 34.4).  A prefix is as long for all, so its
-//    tiles count two thirds (96 items of 52 rows, 33 shared tiles and up to 8 own:
-//    21.0 and 25.5).  Few key sequences leave SMs idle, which a list does not (8 of
+//    of them 48 tiles long: 28.6 and 34.4).  A prefix is as long for all, so at 64
+//    channels its tiles count two thirds (33 shared tiles and up to 8 own, 96 items of
+//    52 rows: 19.8 and 24.6; 64 and 8, 48 of 52: 19.6 and 23.0; 16 and 1, 192 of 32:
+//    19.1 and 22.3; beyond, 33 and 8, 192 of 32: 37.8 and 30.3).  At 128 channels a CTA
+//    waits for twice the bytes, which the list reads once for several requests, and
+//    they count whole (64 and 8, 48 of 52: 31.7 and 29.4; 47 and 1, 96 of 32: 36.5 and
+//    27.9; within the bound, 33 and 1, 48 of 52: 21.1 and 23.2).  Few key sequences
+//    leave SMs idle, which a list does not (8 of
 //    64 rows of 128 channels, 36 tiles: 15.1 and 16.4, 64: 20.2 and 19.8, 96: 26.4
 //    and 22.5; one of 104 rows, 24 tiles: 13.4 and 14.9, 48: 17.8 and 15.0; against
 //    the few-rows kernel, one of 16 rows, 36 tiles: 11.9 and 12.5, 64: 15.5 and
@@ -690,7 +695,7 @@ bool cluster_items(Lists& x, int B, int Hkv, int G, int Nq, int D, int64_t own_k
     const int64_t items = (int64_t)B * Hkv * rt;
     int split = (int)std::min<int64_t>(8, own + pre);
     while (split > 0 && (split == 7 || items * split * 10 > (split == 5 || split == 6 ? 18 : 19) * sms)) --split;
-    if (split == 0 || own + pre < 6 || 3 * own + 2 * pre > 36 * split) return false;
+    if (split == 0 || own + pre < 6 || 3 * own + (D == 64 ? 2 : 3) * pre > 36 * split) return false;
     if (own + pre > (rows <= kFewRows ? 40 + 12 * (int64_t)B * Hkv : 32 + 3 * (int64_t)B * Hkv)) return false;
     const int least = rows > 128 ? 3 : rows > kHalfRows || (rows > kFewRows && D == 128) ? 2 : 1;
     if (split < least || (rows <= kFewRows / 2 && (rows <= 4 || D == 128 || split > 4))) return false;

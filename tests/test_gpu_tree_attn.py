@@ -272,3 +272,36 @@ def test_refusals_of_the_binding():
     for bad in (good[:, :39], good[:1], good[..., :1], good.float(), good.transpose(1, 2), good[0, 0], good.cpu()):
         with pytest.raises(ValueError):
             T.run(p, bad)
+
+
+# Which form a call takes, by the widths of its tables in tiles of 128 keys: one launch where clusters or CTAs take whole
+# items, two from a list with its join, three where the prefix has a list of its own besides.  Both sides of each bound.
+@pytest.mark.parametrize("B,H,Hkv,D,Nq,own,pre,launches", [
+    (24, 16, 4, 64, 13, 36, 0, 1), (24, 16, 4, 64, 13, 37, 0, 2),                     # 12 tiles a CTA of clusters of 3
+    (24, 16, 4, 128, 13, 36, 0, 1), (24, 16, 4, 128, 13, 37, 0, 2),
+    (24, 16, 4, 64, 13, 8, 42, 1), (24, 16, 4, 64, 13, 8, 43, 2),                     # 64 channels: a prefix's count 2 / 3
+    (24, 16, 4, 128, 13, 8, 28, 1), (24, 16, 4, 128, 13, 8, 29, 2), (24, 16, 4, 128, 13, 8, 42, 2),        # 128: whole
+    (24, 16, 4, 64, 13, 64, 33, 2),                        # a table far wider than its requests
+    (1, 4, 1, 64, 16, 35, 0, 1), (1, 4, 1, 64, 16, 36, 0, 2),                         # few key sequences
+    (1, 4, 1, 128, 4, 52, 0, 1), (1, 4, 1, 128, 4, 53, 0, 2),                         # ... of up to 16 rows
+    (2, 16, 2, 128, 100, 24, 0, 1), (2, 16, 2, 128, 100, 45, 0, 2),                   # several sets of rows
+    (6, 16, 8, 64, 5, 12, 0, 1), (150, 4, 2, 64, 12, 200, 0, 2), (3, 6, 3, 64, 500, 48, 0, 1), (3, 6, 3, 64, 500, 49, 0, 2),
+    (16, 8, 8, 128, 4, 2, 33, 3), (2, 4, 2, 128, 40, 1, 0, 1)])
+def test_which_form_a_call_takes(B, H, Hkv, D, Nq, own, pre, launches):
+    G.ensure_built()
+    if torch.cuda.get_device_properties(0).multi_processor_count != 152:
+        pytest.skip("the bounds are those of 152 SMs")
+    page = 128
+    p = P.make(B=B, H=H, Hkv=Hkv, D=D, Nq=Nq, page=page, kv_len=[min(own * page, Nq + 50 * (b % 4)) for b in range(B)],
+               prefix=300 if pre else 0, causal=False, seed=own, table_pad=0)
+
+    def widened(t, width):
+        return torch.cat((t, t.new_full(t.shape[:-1] + (width - t.shape[-1],), p.cache_k.shape[0] + 9)), -1)
+
+    p.table = widened(p.table, own)
+    if pre:
+        p.prefix_table = widened(p.prefix_table, pre)
+    sees = trees(1, Nq, 3, own) * B
+    o = T.run(p, mask_of(sees, Nq))
+    assert S.sage_last_launch_count() == launches
+    T.check(p, sees, o)
