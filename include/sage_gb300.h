@@ -397,7 +397,8 @@ int sage_paged_workspace(int B, int H, int Hkv, int Nq, int D, size_t* bytes);
  * Lengths, tables and prefix are read on the device, so a captured call
  * serves later lengths; make the first call on a device before any capture.
  * The widths bound the lengths on the host and choose between kernels: rows no
- * wider than the requests may grow are served faster.
+ * wider than the requests may grow are served faster, and so is a narrower
+ * table_width over rows that are wider (table_stride).
  * Cache rows behind a length are never used, whatever they hold; the rows
  * within the lengths must be finite, hidden ones included, and the scores
  * (sm_scale * q.k) below 2^30 in magnitude.  Scores, maxima,

@@ -64,9 +64,9 @@ struct PagedParams {
     int join;                            // 1: a request's key sequence is the prefix followed by its own keys
     int workers;                         // workers the list is shared among
     int fault_mode;                      // test hook: 0 = none
-    int split;                           // whole items: CTAs of the cluster that takes one (many-rows kernel: above 1)
+    int split;                           // whole items: CTAs of the cluster that takes one (0: no clusters)
     int whole;                           // many-rows kernel: a CTA or a cluster takes an item
-    int half;                            // many-rows kernel, clusters: items of up to 64 rows, two lanes to each
+    int half;                            // many-rows kernel, clusters and a tree's list: items of up to 64 rows, two lanes to each
     int beside;                          // runs beside the kernel before it, which it does not depend on
     // workspace
     float* part_o;                       // [slot][part_m][D]
