@@ -12,6 +12,7 @@
 // which is what lets one request's keys be split among workers and the
 // prefix be read once for the rows of all requests.
 #include <algorithm>
+#include <atomic>
 #include <cmath>
 
 #include "sage_gb300.h"
@@ -24,11 +25,12 @@
 namespace sage {
 
 int sm_count() {
-    static int n[64] = {};
-    int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
-    if (n[dev] == 0 && cudaDeviceGetAttribute(&n[dev], cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 0;
-    return n[dev];
+    static std::atomic<int> known{0};
+    int n = known.load(std::memory_order_relaxed), dev = 0;
+    if (n == 0 && cudaGetDevice(&dev) == cudaSuccess &&
+        cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) == cudaSuccess)
+        known.store(n, std::memory_order_relaxed);
+    return n;
 }
 
 namespace {

@@ -100,7 +100,10 @@ int encode_pages(CUtensorMap* m, const sage_tensor& t, int D, int page, int head
 // Tensor map over q [B, H, Nq, D] as (channel, head, token, request), box: 64
 // channels of `heads` heads, `tokens` tokens and `requests` requests.
 int encode_rows(CUtensorMap* m, const sage_tensor& t, int D, int H, int Nq, int B, int heads, int tokens, int requests);
-// SMs of the current device, 0 where there is none (sage_paged.cu).
+// SMs of a device, 0 where there is none; asked for once, of the first that is used,
+// as the GPUs of a process are of one kind and only the choice of forms goes by it:
+// asking for the current device each time costs a small call 0.1 of its 2.6 us
+// (sage_paged.cu).
 int sm_count();
 // The fault the next launch has to make (test hook), taken once (sage_api.cu).
 int take_fault_mode();
